@@ -386,6 +386,120 @@ tms_status tms_decode_k_pointers_noalloc(const tms_trie* trie, const void* emb, 
                                          int32_t* tokens, int32_t* len, int32_t* entries, int32_t* status,
                                          void* stream);
 
+/* ------------------------------------------------- paged key/value cache -- */
+
+/* The model around the decode step: sequences of a batch keep their keys and
+ * values in pages of one pool, share the pages of a common prompt (the catalog
+ * prompt that all answers start from), attend from the new tokens of a step
+ * over their pages, and keep only the drafted tokens that were accepted.  A
+ * catalog trie gives the drafts: below a node every legal continuation is
+ * known, so a tree of them can be verified in one pass of the model.
+ *
+ * The descriptor holds caller-owned device memory; the calls read it on the
+ * host only for its pointers and sizes, allocate nothing and enqueue kernels
+ * on the caller's stream.  Sequence s owns the rows [0, length[s]) (its
+ * committed tokens): row r is slot r % page_tokens of page
+ * table[s][r / page_tokens].  A page's reference count is the number of
+ * sequences whose table holds it; a page with none is free.  A new cache is
+ * table = -1 and length = held = refs = status = 0.
+ *
+ * Device-detected errors are per sequence and sticky (status[s], a
+ * tms_status): the calls leave a sequence in error unchanged until tms_kv_fork
+ * gives it new content.  Calls on one descriptor share its work memory and its
+ * tables: on several streams the caller orders them. */
+typedef struct {
+  void* kv;         /* dev [layers][pages][2][kv_heads][page_tokens][head_dim]: keys, then values, of a page */
+  int32_t* table;   /* dev [seqs][max_pages]: pages of every sequence, -1 past held */
+  int32_t* length;  /* dev [seqs]: committed rows */
+  int32_t* held;    /* dev [seqs]: pages held (reserved ones included) */
+  int32_t* refs;    /* dev [pages]: reference counts */
+  int32_t* status;  /* dev [seqs]: tms_status */
+  void* work;       /* dev, 256-byte aligned: at least tms_kv_work_bytes */
+  int64_t work_bytes;
+  int32_t dtype;    /* tms_dtype of kv, queries, outputs and norm weights */
+  int32_t layers, pages, kv_heads, page_tokens, head_dim, seqs, max_pages;
+} tms_kv;
+
+/* Sizes: head_dim 64, 128 or 256; page_tokens a power of two in [8, 1024];
+ * seqs in [1, 4096]; kv_heads in [1, 256]; layers and pages at least 1;
+ * max_pages * page_tokens below 2^31.  kv, the rows of q, k, v and the outputs
+ * are 16-byte aligned.  tms_kv_work_bytes needs the sizes and dtype only. */
+tms_status tms_kv_work_bytes(const tms_kv* c, int64_t* bytes);
+
+/* Forking, reordering and freeing: sequence s becomes what sequence src[s] was
+ * before the call (dev int32 [seqs]); src[s] = s leaves it, -1 empties it (its
+ * pages are given back).  All sequences change at once, so any reordering of
+ * a beam is one call.  The committed rows' pages are shared, not copied;
+ * reserved pages are not taken over.  The status follows the source (OK where
+ * emptied).  A src outside [-1, seqs) sets INVALID_ARG and leaves s unchanged. */
+tms_status tms_kv_fork(const tms_kv* c, const int32_t* src, void* stream);
+
+/* Pages for the rows [length, length + n_new[s]) of every sequence (dev int32
+ * [seqs]; 0 or less: nothing).  Where the first of them lies in a page that
+ * other sequences hold too, that page is copied (its committed rows, in all
+ * layers) and the copy takes its place.  Free pages are taken in ascending
+ * order, for sequence 0 first (the copy before the further pages), among those
+ * that were free before the call.  A sequence whose demand, with those of the
+ * sequences before it, exceeds them gets OOM; rows past max_pages: INVALID_ARG. */
+tms_status tms_kv_reserve(const tms_kv* c, const int32_t* n_new, void* stream);
+
+/* Keys and values of the new tokens into reserved rows of one layer, and the
+ * queries beside them, in one pass over the projections.  Tokens are packed:
+ * sequence s has the tokens start[s] .. start[s+1]-1 (dev int32 [seqs+1],
+ * ascending, T in all; host T), which become its rows length[s], length[s]+1,
+ * ...  For every query and key head
+ *     x <- x * rsqrt(mean(x^2) + eps) * weight       (weight null: x as it is)
+ *     (x_a, x_b) <- (x_a cos t - x_b sin t, x_b cos t + x_a sin t)
+ * with t = pos * inv_freq[i], (a, b) = (i, i + n_freq), or (2i, 2i+1) if
+ * interleaved, for i < n_freq; the values past 2 n_freq are not rotated, and
+ * n_freq = 0 rotates nothing.  Values are copied.
+ * q dev [T][q_heads][D] with rows of ldq elements between tokens, q_out dev
+ * [T][q_heads][D]; q null: keys and values only.  k, v dev [T][kv_heads][D],
+ * rows ldk, ldv apart.  q_weight, k_weight dev [D] or null; pos dev int32 [T]
+ * and inv_freq dev fp32 [n_freq] (null with n_freq = 0).  The row strides are
+ * multiples of 16 bytes; n_freq a multiple of 8, at most D/2.  Sums, angles
+ * (reduced in fp64) and rotation are fp32 or wider, rounded once.  A row past
+ * the pages held sets the sequence's status to INVALID_ARG and is not written
+ * (reserving is also what makes a shared last page the sequence's own: reserve
+ * after every fork, before writing). */
+tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, int32_t T, const void* q, int64_t ldq,
+                        int32_t q_heads, void* q_out, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                        const void* q_weight, const void* k_weight, float eps, const int32_t* pos,
+                        const float* inv_freq, int32_t n_freq, int32_t interleaved, void* stream);
+
+/* Attention of the new tokens over one layer: out = softmax(scale q k^T) v
+ * over the rows a token sees, query head h with kv head h / (q_heads /
+ * kv_heads).  Tokens packed as in tms_kv_write, their rows written.  Token i
+ * of sequence s sees the committed rows and, of the new ones,
+ *   parent null: the tokens 0 .. i (single tokens, whole prompts);
+ *   parent dev int32 [T]: itself and its ancestors, parent[t] being the index
+ *     among its sequence's new tokens of the token it follows, -1 where it
+ *     follows the committed rows (a tree of drafts; what is not the index of
+ *     an earlier token counts as -1; max_new at most 1024).
+ * q, out dev [T][q_heads][D], q's rows ldq elements apart.  max_new: the most
+ * tokens any sequence has (host; the launch is chosen by it).  Scores and sums
+ * are fp32; bf16 weights of the second product are rounded to bf16
+ * unnormalised, relative to their running maximum.  The outputs of a sequence
+ * in error, with rows not reserved or with more than max_new tokens are NaN. */
+tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                            const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
+                            void* out, void* stream);
+
+/* The accepted ones of the new tokens: keep[s][0 .. n_keep[s]) (dev int32
+ * [seqs][keep_stride], ascending indices among the sequence's reserved rows)
+ * become the rows length, length+1, ..., moved together in every layer;
+ * keep null: the first n_keep[s].  length grows by n_keep[s] (dev int32
+ * [seqs]; 0: all drafts dropped; negative: sequence left as it is) and the
+ * pages past it are given back.  Indices that are not ascending or not
+ * reserved set INVALID_ARG and leave the sequence unchanged. */
+tms_status tms_kv_commit(const tms_kv* c, const int32_t* n_keep, const int32_t* keep, int32_t keep_stride,
+                         void* stream);
+
+/* Synchronise stream, copy the per-sequence status to host_status [seqs] (may
+ * be NULL) and return the status of the lowest-numbered sequence in error, or
+ * TMS_OK. */
+tms_status tms_kv_sync_status(const tms_kv* c, int32_t* host_status, void* stream);
+
 const char* tms_status_str(tms_status s);
 const char* tms_last_error(void);
 

@@ -1,0 +1,452 @@
+"""The paged key/value cache on the GPU against plain 64-bit forms
+(kv_util.py, which also derives the bounds): attention of single tokens, trees
+of drafts and prompts, cache writes, page operations, and their refusals."""
+import numpy as np
+import pytest
+import torch
+
+import trie_masked_sparse_amd as tms
+from kv_util import Pages, attention, head
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+
+
+def dev32(a):
+    return torch.tensor(np.asarray(a, dtype=np.int32), device="cuda")
+
+
+def offsets(n):
+    return np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+
+
+def tree(rng, n, back=5):
+    return [-1 if i == 0 or rng.random() < 0.1 else int(rng.integers(max(0, i - back), i)) for i in range(n)]
+
+
+def filled(rng, dtype, kv_heads, dim, page, lens, new, layers=1, layer=0, spare=2, fill=float("nan")):
+    """A cache whose sequences hold lens committed and new further rows of
+    normal values, in pages of random order; every other value is `fill`.
+    Returns (cache, [k of every sequence], [v ...]) in fp64."""
+    need = [-(-(a + b) // page) for a, b in zip(lens, new)]
+    total, width = sum(need) + spare, max(max(need), 1)
+    order = list(rng.permutation(total))
+    kv = torch.full((layers, total, 2, kv_heads, page, dim), fill, dtype=dtype)
+    table, refs = np.full((len(lens), width), -1, np.int32), np.zeros(total, np.int32)
+    ks, vs = [], []
+    for s, (a, b) in enumerate(zip(lens, new)):
+        both = torch.from_numpy(rng.standard_normal((2, kv_heads, a + b, dim)).astype(np.float32)).to(dtype)
+        for j in range(need[s]):
+            p = int(order.pop())
+            table[s, j], refs[p] = p, 1
+            rows = both[:, :, j * page:(j + 1) * page]
+            kv[layer, p, :, :, :rows.shape[2]] = rows
+        ks.append(both[0].transpose(0, 1).double().numpy())
+        vs.append(both[1].transpose(0, 1).double().numpy())
+    cache = tms.PagedCache(kv.cuda(), dev32(table), dev32(lens), dev32(need), dev32(refs), dev32([0] * len(lens)))
+    return cache, ks, vs
+
+
+def run_attention(cache, q, new, parents=None, max_new=None, scale=None, layer=0, stream=None):
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    par = None if parents is None else dev32([p for t in parents for p in t])
+    tms.kv_attention(cache, layer, q, dev32(offsets(new)), out, scale, parent=par,
+                     max_new=max_new or max(max(new), 1), stream=stream)
+    return out
+
+
+def check_attention(q, out, ks, vs, lens, new, scale, parents, bf16, where=""):
+    q, out = q.double().cpu().numpy(), out.double().cpu().numpy()
+    at = offsets(new)
+    for s, (a, b) in enumerate(zip(lens, new)):
+        if b:
+            want, bound = attention(q[at[s]:at[s + 1]], ks[s], vs[s], a, scale, None if parents is None else parents[s],
+                                    bf16)
+            err = np.abs(out[at[s]:at[s + 1]] - want)
+            assert (err <= bound).all(), (where, s, a, b, float(np.nanmax(err / bound)), int((~(err <= bound)).sum()))
+
+
+SHAPES = [
+    # lens, new
+    ([0], [1]), ([1], [1]), ([63], [1]), ([64], [1]), ([517], [1]),
+    ([0, 1, 0, 130], [0, 1, 3, 2]), ([33, 0, 700, 15, 16, 17], [5, 31, 1, 0, 13, 64]),
+    ([2000, 3], [63, 100]), ([0, 90], [257, 129]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (16, 8, 128), (8, 1, 128), (3, 3, 64), (10, 2, 256)],
+                         ids=lambda h: "x".join(map(str, h)))
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_attention_matches_the_64_bit_form(dtype, heads, kind):
+    hq, hkv, D = heads
+    for n, (lens, new) in enumerate(SHAPES):
+        page = [16, 64, 8, 128][n % 4]
+        print(f"attention {dtype} {heads} {kind} lens {lens} new {new} page {page}", flush=True)
+        rng = np.random.default_rng(100 * n + D + hq)
+        # rows past the end of a sequence and pages of nobody hold NaN
+        cache, ks, vs = filled(rng, dtype, hkv, D, page, lens, new, layers=2, layer=1)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+        parents = [tree(rng, b) for b in new] if kind == "tree" else None
+        out = run_attention(cache, q, new, parents, layer=1)
+        check_attention(q, out, ks, vs, lens, new, D ** -0.5, parents, dtype == BF, (n, kind))
+        assert (cache.status() == tms.OK).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_attention_many_sequences_and_long_contexts(dtype):
+    """Work split over the context: many ragged sequences, and one long one."""
+    rng = np.random.default_rng(5)
+    for lens, new in (([int(x) for x in rng.integers(0, 900, 70)], [int(x) for x in rng.integers(0, 4, 70)]),
+                      ([20011], [1]), ([9001, 0, 12], [37, 2, 20])):
+        print(f"attention long {dtype} {len(lens)} sequences, longest {max(lens)}", flush=True)
+        cache, ks, vs = filled(rng, dtype, 2, 128, 32, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), 8, 128)).astype(np.float32)).to(dtype).cuda()
+        for parents in (None, [tree(rng, b) for b in new]):
+            out = run_attention(cache, q, new, parents)
+            check_attention(q, out, ks, vs, lens, new, 128 ** -0.5, parents, dtype == BF)
+            again = run_attention(cache, q, new, parents)
+            assert torch.equal(out, again)  # no order depends on timing
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_attention_scores_far_apart(dtype):
+    """Scores of several thousand, positive and negative, infinities in the
+    keys of rows nobody sees, negative and zero scale."""
+    rng = np.random.default_rng(11)
+    lens, new = [100, 5], [6, 9]
+    for scale in (8.0, -3.0, 0.0):
+        cache, ks, vs = filled(rng, dtype, 2, 64, 16, lens, new, fill=float("inf"))
+        q = torch.from_numpy(20 * rng.standard_normal((sum(new), 4, 64)).astype(np.float32)).to(dtype).cuda()
+        parents = [tree(rng, b) for b in new]
+        for p in (None, parents):
+            out = run_attention(cache, q, new, p, scale=scale)
+            assert torch.isfinite(out.float()).all()
+            check_attention(q, out, ks, vs, lens, new, scale, p, dtype == BF, scale)
+
+
+def test_attention_parents_that_are_not_earlier_tokens_count_as_none():
+    rng = np.random.default_rng(12)
+    lens, new = [20], [6]
+    cache, ks, vs = filled(rng, BF, 2, 64, 16, lens, new)
+    q = torch.from_numpy(rng.standard_normal((6, 4, 64)).astype(np.float32)).to(BF).cuda()
+    odd = [[-5, 0, 2, 9, 3, 2 ** 31 - 1]]
+    out = run_attention(cache, q, new, odd)
+    check_attention(q, out, ks, vs, lens, new, 64 ** -0.5, [[-1, 0, -1, -1, 3, -1]], True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_attention_strided_queries_and_another_stream(dtype):
+    rng = np.random.default_rng(13)
+    lens, new = [40, 300], [3, 1]
+    cache, ks, vs = filled(rng, dtype, 2, 128, 64, lens, new)
+    wide = torch.from_numpy(rng.standard_normal((4, 11, 128)).astype(np.float32)).to(dtype).cuda()
+    q = wide[:, 2:10]
+    assert not q.is_contiguous()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty((4, 8, 128), dtype=dtype, device="cuda")
+    start = dev32(offsets(new))
+    side.wait_stream(torch.cuda.current_stream())
+    tms.kv_attention(cache, 0, q, start, out, max_new=3, stream=side)
+    side.synchronize()
+    check_attention(q, out, ks, vs, lens, new, 128 ** -0.5, None, dtype == BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_attention_sequences_in_error_give_nan(dtype):
+    rng = np.random.default_rng(14)
+    lens, new = [10, 20, 30, 40], [2, 3, 2, 2]
+    cache, ks, vs = filled(rng, dtype, 2, 64, 16, lens, new)
+    cache.status_codes[0] = tms.ERR_OOM
+    cache.held[2] = 1  # 16 rows held, 32 needed
+    q = torch.from_numpy(rng.standard_normal((sum(new), 4, 64)).astype(np.float32)).to(dtype).cuda()
+    out = run_attention(cache, q, new, max_new=2)  # sequence 1 has more than max_new tokens
+    assert torch.isnan(out[:7].float()).all()
+    check_attention(q[7:], out[7:], ks[3:], vs[3:], lens[3:], new[3:], 64 ** -0.5, None, dtype == BF)
+
+
+def test_caches_past_32_bits():
+    """A pool of more than 2^32 bytes and 2^31 elements, pages at its end."""
+    rng = np.random.default_rng(15)
+    hkv, D, page, pages = 8, 128, 64, 17000  # 262144 bytes a page: 4.4 GB a layer of bf16, two layers
+    kv = torch.empty((2, pages, 2, hkv, page, D), dtype=BF, device="cuda")
+    assert kv.numel() > 2 ** 31 and kv.numel() * 2 > 2 ** 33
+    lens, new = [100], [5]
+    table, refs = np.array([[pages - 1, 0]], np.int32), np.zeros(pages, np.int32)
+    refs[[pages - 1, 0]] = 1
+    cache = tms.PagedCache(kv, dev32(table), dev32([0]), dev32([2]), dev32(refs), dev32([0]))
+    k = torch.from_numpy(rng.standard_normal((2, 105, hkv, D)).astype(np.float32)).to(BF).cuda()
+    tms.kv_write(cache, 1, k[0], k[1], dev32([0, 105]))
+    assert torch.equal(kv[1, pages - 1, 0].transpose(0, 1), k[0, :64]) and torch.equal(kv[1, 0, 1, :, :41].transpose(0, 1), k[1, 64:])
+    cache.length.fill_(100)
+    q = torch.from_numpy(rng.standard_normal((5, 16, D)).astype(np.float32)).to(BF).cuda()
+    out = run_attention(cache, q, new, layer=1)
+    ks, vs = ([k[i].double().cpu().numpy()] for i in (0, 1))
+    check_attention(q, out, ks, vs, lens, new, D ** -0.5, None, True)
+    # a fork and its copy, from and to pages past 2^31 elements
+    cache2 = tms.PagedCache(kv, torch.cat([cache.table, torch.full_like(cache.table, -1)]), dev32([40, 0]), dev32([1, 0]),
+                            cache.refs, dev32([0, 0]))
+    cache2.refs.fill_(1)
+    cache2.refs[pages - 2] = 0
+    tms.kv_fork(cache2, dev32([0, 0]))
+    tms.kv_reserve(cache2, dev32([0, 3]))
+    assert cache2.table[1, 0].item() == pages - 2
+    assert torch.equal(kv[1, pages - 2, :, :, :40], kv[1, pages - 1, :, :, :40])
+    tms.kv_write(cache2, 1, k[0, 60:63], k[1, 60:63], dev32([0, 0, 3]))
+    tms.kv_commit(cache2, dev32([0, 2]), dev32([[0, 0], [0, 2]]))
+    assert torch.equal(kv[1, pages - 2, 0, :, 40:42].transpose(0, 1), k[0, [60, 62]])
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim,n_freq,interleaved", [(64, 32, False), (64, 32, True), (128, 64, False), (128, 16, False),
+                                                    (128, 16, True), (256, 128, False), (64, 0, False), (256, 8, True)])
+def test_write_matches_the_64_bit_form(dtype, dim, n_freq, interleaved):
+    rng = np.random.default_rng(dim + n_freq)
+    hq, hkv, page = 5, 3, 16
+    for lens, new in (([0], [1]), ([5, 0, 31, 16], [0, 17, 33, 1]), (list(range(70)), [i % 3 for i in range(70)])):
+        print(f"write {dtype} D={dim} n_freq={n_freq} {interleaved} {len(lens)} sequences", flush=True)
+        for norm in (True, False):
+            cache, _, _ = filled(rng, dtype, hkv, dim, page, lens, new, layers=3, layer=1, fill=3.0)
+            before, T = cache.kv.clone(), sum(new)
+            fused = torch.from_numpy(rng.standard_normal((T, hq + 2 * hkv, dim)).astype(np.float32)).to(dtype).cuda()
+            q, k, v = fused.split([hq, hkv, hkv], 1)
+            w = [torch.from_numpy((1 + 0.3 * rng.standard_normal(dim)).astype(np.float32)).to(dtype).cuda() for _ in range(2)]
+            pos = rng.integers(0, 200000, T)
+            inv = (10000.0 ** -(np.arange(n_freq) / max(n_freq, 1))).astype(np.float32)
+            q_out = torch.empty((T, hq, dim), dtype=dtype, device="cuda")
+            tms.kv_write(cache, 1, k, v, dev32(offsets(new)), q=q, q_out=q_out, q_weight=w[0] if norm else None,
+                         k_weight=w[1] if norm else None, eps=1e-5, pos=dev32(pos),
+                         inv_freq=torch.from_numpy(inv).cuda() if n_freq else None, interleaved=interleaved)
+            assert (cache.status() == tms.OK).all()
+            got = {"q": q_out}
+            seq = np.repeat(np.arange(len(lens)), new)
+            row = np.concatenate([a + np.arange(b) for a, b in zip(lens, new)]).astype(np.int64)
+            page_of = cache.table.cpu().numpy()[seq, row // page]
+            at = (torch.from_numpy(page_of).long().cuda(), torch.from_numpy(row % page).cuda())
+            got["k"], got["v"] = cache.kv[1][at[0], 0, :, at[1]], cache.kv[1][at[0], 1, :, at[1]]
+            for name, x, weight in (("q", q, w[0]), ("k", k, w[1])):
+                want, bound = head(x.double().cpu().numpy(), weight.double().cpu().numpy() if norm else None, 1e-5, pos,
+                                   inv, interleaved, dtype == BF)
+                err = np.abs(got[name].double().cpu().numpy() - want)
+                assert (err <= bound).all(), (name, float((err / np.maximum(bound, 1e-30)).max()))
+            assert torch.equal(got["v"], v)
+            # nothing else moved
+            before[1][at[0], 0, :, at[1]], before[1][at[0], 1, :, at[1]] = got["k"], got["v"]
+            assert torch.equal(before, cache.kv)
+
+
+def test_write_refuses_rows_that_are_not_reserved():
+    cache = tms.PagedCache.empty(1, 4, 1, 16, 64, 2, 2, dtype=F)
+    k = torch.ones((5, 1, 64), device="cuda")
+    tms.kv_reserve(cache, dev32([3, 0]))
+    tms.kv_write(cache, 0, k, k, dev32([0, 3, 5]))
+    assert cache.status().tolist() == [tms.OK, tms.ERR_INVALID_ARG]
+    with pytest.raises(tms.TmsError) as ei:
+        tms.kv_reserve(cache, dev32([1, 1]))
+    assert ei.value.code == tms.ERR_INVALID_ARG
+    tms.kv_fork(cache, dev32([0, -1]))  # new content clears the error
+    assert (cache.status() == tms.OK).all()
+
+
+def _live_rows(cache, s):
+    page = cache.page_tokens
+    n = int(cache.length[s])
+    t = cache.table[s].tolist()
+    return [float(cache.kv[0, t[r // page], 0, 0, r % page, 0]) for r in range(n)]
+
+
+@pytest.mark.parametrize("seqs,pages,page,max_pages,seed", [(1, 3, 8, 3, 0), (5, 12, 8, 4, 1), (7, 64, 16, 5, 2),
+                                                            (70, 300, 8, 6, 3), (300, 5000, 8, 9, 4)])
+def test_page_operations_follow_the_model(seqs, pages, page, max_pages, seed):
+    """Random forks, reorderings, reservations (some past the pool), writes and
+    commits: tables, counts, statuses and the rows of every sequence after each."""
+    rng = np.random.default_rng(seed)
+    cache = tms.PagedCache.empty(1, pages, 1, page, 64, seqs, max_pages, dtype=F)
+    cache.kv.fill_(-1.0)
+    model, mark = Pages(seqs, pages, page, max_pages), 0
+    for step in range(12 if seqs > 100 else 40):
+        print(f"pages {seqs}/{pages} step {step}", flush=True)
+        src = np.arange(seqs)
+        kind = rng.integers(4)
+        if kind == 0:
+            src = rng.integers(0, seqs, seqs)
+        elif kind == 1:
+            some = rng.random(seqs) < 0.3
+            src = np.where(some, rng.integers(-1, seqs, seqs), src)
+        if step % 7 == 5:
+            src[rng.integers(seqs)] = seqs + 3
+        tms.kv_fork(cache, dev32(src), check=False)
+        model.fork(src.tolist())
+        n_new = np.where(rng.random(seqs) < 0.7, rng.integers(0, 2 * page, seqs), -1)
+        tms.kv_reserve(cache, dev32(n_new), check=False)
+        model.reserve(n_new.tolist())
+        ok = [n if n > 0 and not model.status[s] else 0 for s, n in enumerate(n_new.tolist())]
+        drafts = []
+        for n in ok:
+            drafts.append([float(mark + i + 1) for i in range(n)])
+            mark += n
+        rows = torch.tensor([x for d in drafts for x in d], device="cuda")
+        k = rows[:, None, None].expand(-1, 1, 64).contiguous()
+        tms.kv_write(cache, 0, k, -k, dev32(offsets(ok)))
+        keep = np.zeros((seqs, 2 * page), np.int32)
+        n_keep = np.zeros(seqs, np.int32)
+        for s, n in enumerate(ok):
+            idx = np.sort(rng.permutation(n)[: rng.integers(0, n + 1)])
+            n_keep[s] = len(idx)
+            keep[s, :len(idx)] = idx
+        if step % 5 == 3:
+            s = int(rng.integers(seqs))
+            if n_keep[s] >= 2:
+                keep[s, :2] = keep[s, 1::-1]  # not ascending
+        if step % 6 == 2:
+            n_keep = np.where(rng.random(seqs) < 0.5, np.minimum(n_keep, 1), n_keep).astype(np.int32)
+            tms.kv_commit(cache, dev32(n_keep), check=False)
+            model.commit(n_keep.tolist(), None, drafts)
+        else:
+            tms.kv_commit(cache, dev32(n_keep), dev32(keep), check=False)
+            model.commit(n_keep.tolist(), keep, drafts)
+        table = np.full((seqs, max_pages), -1)
+        for s, t in enumerate(model.table):
+            table[s, :len(t)] = t
+        assert cache.status().tolist() == model.status, step
+        assert np.array_equal(cache.table.cpu().numpy(), table), step
+        assert cache.refs.tolist() == model.refs(), step
+        assert cache.held.tolist() == [len(t) for t in model.table], step
+        assert cache.length.tolist() == [len(r) for r in model.rows], step
+        kv = cache.kv.cpu()
+        for s in range(seqs):
+            r = np.arange(len(model.rows[s]))
+            at = table[s][r // page], r % page
+            want = np.array(model.rows[s])
+            assert np.array_equal(kv[0][at[0], 0, 0, at[1]].numpy(), np.repeat(want[:, None], 64, 1)), (step, s)
+            assert np.array_equal(kv[0][at[0], 1, 0, at[1]].numpy(), np.repeat(-want[:, None], 64, 1)), (step, s)
+        if any(model.status) and step % 3 == 0:  # errors stay until new content comes
+            clear = [-1 if x else s for s, x in enumerate(model.status)]
+            tms.kv_fork(cache, dev32(clear), check=False)
+            model.fork(clear)
+
+
+def test_commit_moves_long_keep_lists_in_place():
+    """Several hundred rows that overlap their targets, in every layer and head."""
+    rng = np.random.default_rng(21)
+    for dtype, dim in ((BF, 128), (F, 256)):
+        n = 700
+        cache = tms.PagedCache.empty(2, 60, 2, 16, dim, 2, 50, dtype=dtype)
+        tms.kv_reserve(cache, dev32([n, 5]))
+        k = torch.from_numpy(rng.standard_normal((2, n + 5, 2, dim)).astype(np.float32)).to(dtype).cuda()
+        for layer in (0, 1):
+            tms.kv_write(cache, layer, k[layer], k[1 - layer], dev32([0, n, n + 5]))
+        idx = np.sort(rng.permutation(n)[:650])
+        idx[0] = 0
+        keep = np.zeros((2, 660), np.int32)
+        keep[0, :650] = idx
+        tms.kv_commit(cache, dev32([650, 0]), dev32(keep))
+        t = cache.table[0].tolist()
+        r = np.arange(650)
+        at = torch.tensor([t[i // 16] for i in r]).cuda(), torch.tensor(r % 16).cuda()
+        for layer in (0, 1):
+            assert torch.equal(cache.kv[layer][at[0], 0, :, at[1]], k[layer][idx])
+            assert torch.equal(cache.kv[layer][at[0], 1, :, at[1]], k[1 - layer][idx])
+        assert cache.length.tolist() == [650, 0] and cache.held.tolist() == [41, 0]
+
+
+def test_a_whole_step_replays_in_a_graph():
+    """Fork, reserve, write, attend and commit recorded once: every replay
+    gives the eager results (the branches start from the same root each time)."""
+    rng = np.random.default_rng(22)
+    seqs, page, hq, hkv, D = 6, 16, 4, 2, 64
+    lens = [45] + [0] * 5
+    new = [0, 3, 1, 7, 0, 5]
+    cache, _, _ = filled(rng, BF, hkv, D, page, lens, [0] * seqs, spare=30, fill=0.0)
+    cache = tms.PagedCache(cache.kv, torch.cat([cache.table, torch.full((seqs, 3), -1, dtype=torch.int32, device="cuda")], 1).contiguous(),
+                           cache.length, cache.held, cache.refs, cache.status_codes)
+    T = sum(new)
+    fused = torch.from_numpy(rng.standard_normal((T, hq + 2 * hkv, D)).astype(np.float32)).to(BF).cuda()
+    q, k, v = fused.split([hq, hkv, hkv], 1)
+    start, src, n_new = dev32(offsets(new)), dev32([0] * seqs), dev32(new)
+    parent = dev32([p for n in new for p in tree(rng, n)])
+    n_keep, keep = dev32([0, 2, 1, 3, 0, 0]), dev32([[0, 0, 0], [0, 2, 0], [0, 0, 0], [1, 4, 6], [0, 0, 0], [0, 0, 0]])
+    pos, inv = dev32(rng.integers(0, 99, T)), torch.tensor([1.0 / (i + 1) for i in range(32)], device="cuda")
+    q_out, out = torch.empty((T, hq, D), dtype=BF, device="cuda"), torch.empty((T, hq, D), dtype=BF, device="cuda")
+
+    def step():
+        tms.kv_fork(cache, src, check=False)
+        tms.kv_reserve(cache, n_new, check=False)
+        tms.kv_write(cache, 0, k, v, start, q=q, q_out=q_out, pos=pos, inv_freq=inv)
+        tms.kv_attention(cache, 0, q_out, start, out, parent=parent, max_new=7)
+        tms.kv_commit(cache, n_keep, keep, check=False)
+
+    def results():
+        torch.cuda.synchronize()
+        assert (cache.status() == tms.OK).all()
+        return [t.clone() for t in (out, q_out, cache.kv, cache.table, cache.length, cache.held, cache.refs)]
+
+    step()
+    want = results()
+    assert torch.isfinite(want[0].float()).all()
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        out.fill_(9.0)
+        q_out.fill_(9.0)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    with torch.cuda.stream(side):
+        g2 = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g2, stream=side):
+            with pytest.raises(tms.TmsError) as ei:
+                tms.kv_fork(cache, src)
+            assert "recorded" in str(ei.value)
+
+
+def test_binding_refusals():
+    cache = tms.PagedCache.empty(2, 8, 2, 16, 64, 3, 4)
+    start, q = dev32([0, 1, 1, 2]), torch.zeros((2, 4, 64), dtype=BF, device="cuda")
+    k, out = q[:, :2].contiguous(), torch.empty_like(q)
+    for call, what in (
+            (lambda: tms.kv_attention(cache, 2, q, start, out), "layer"),
+            (lambda: tms.kv_attention(cache, -1, q, start, out), "layer"),
+            (lambda: tms.kv_attention(cache, 0, q[:, :3].contiguous(), start, out), "kv_heads"),
+            (lambda: tms.kv_attention(cache, 0, q, start, out, max_new=0), "max_new"),
+            (lambda: tms.kv_write(cache, 5, k, k, start), "layer"),
+            (lambda: tms.kv_write(cache, 0, k, k, start, pos=dev32([0, 1]), inv_freq=torch.ones(40, device="cuda")), "n_freq"),
+            (lambda: tms.kv_write(cache, 0, k, k, start, pos=dev32([0, 1]), inv_freq=torch.ones(4, device="cuda")), "n_freq")):
+        with pytest.raises(tms.TmsError) as ei:
+            call()
+        assert ei.value.code == tms.ERR_INVALID_ARG and what in str(ei.value)
+    big = torch.zeros((1100, 4, 64), dtype=BF, device="cuda")
+    with pytest.raises(tms.TmsError) as ei:
+        tms.kv_attention(cache, 0, big, dev32([0, 1100, 1100, 1100]), torch.empty_like(big), parent=dev32([0] * 1100))
+    assert "1024" in str(ei.value)
+    for call in (
+            lambda: tms.kv_attention(cache, 0, q, start[:3].contiguous(), out),
+            lambda: tms.kv_attention(cache, 0, q, start, out[:1]),
+            lambda: tms.kv_attention(cache, 0, q.float(), start, out),
+            lambda: tms.kv_attention(cache, 0, q.transpose(0, 1), start, out),
+            lambda: tms.kv_attention(cache, 0, q, start, out, parent=dev32([0])),
+            lambda: tms.kv_write(cache, 0, k, k[:1], start),
+            lambda: tms.kv_write(cache, 0, q, q, start),
+            lambda: tms.kv_write(cache, 0, k, k, start, q=q),
+            lambda: tms.kv_write(cache, 0, k, k, start, inv_freq=torch.ones(8, device="cuda")),
+            lambda: tms.kv_write(cache, 0, k, k, start, q_weight=None, k_weight=torch.ones(64, device="cuda")),
+            lambda: tms.kv_fork(cache, dev32([0, 1])),
+            lambda: tms.kv_fork(cache, torch.zeros(3, dtype=torch.int32)),
+            lambda: tms.kv_commit(cache, dev32([0, 0, 0]), dev32([[0], [0]])),
+            lambda: tms.PagedCache(cache.kv.half(), cache.table, cache.length, cache.held, cache.refs, cache.status_codes),
+            lambda: tms.PagedCache(cache.kv, cache.table, cache.length, cache.held, cache.refs[:4], cache.status_codes)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    # no tokens at all: nothing to do
+    none = torch.empty((0, 4, 64), dtype=BF, device="cuda")
+    tms.kv_attention(cache, 0, none, dev32([0, 0, 0, 0]), none, max_new=1)
+    tms.kv_write(cache, 0, none[:, :2], none[:, :2], dev32([0, 0, 0, 0]))
+    assert (cache.status() == tms.OK).all()

@@ -46,7 +46,10 @@ EXPORTS = (
     "tms_debug_set_live",
     "tms_state_set_split", "tms_state_set_loop", "tms_state_set_norepeat", "tms_state_set_step_grouping",
     "tms_state_get_launch",
-    "tms_decode_k_pointers_noalloc", "tms_read_reference", "tms_status_str", "tms_last_error",
+    "tms_decode_k_pointers_noalloc", "tms_read_reference",
+    "tms_kv_work_bytes", "tms_kv_fork", "tms_kv_reserve", "tms_kv_write", "tms_kv_attention", "tms_kv_commit",
+    "tms_kv_sync_status",
+    "tms_status_str", "tms_last_error",
 )
 NOREPEAT_LIVE, NOREPEAT_BITMASK = 0, 1
 STEP_GROUP_AUTO, STEP_GROUP_OFF, STEP_GROUP_ROOT, STEP_GROUP_NODES = 0, 1, 2, 3
@@ -62,6 +65,14 @@ class TmsError(RuntimeError):
 class TrieInfo(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("n_nodes", "n_edges", "n_entries", "cap", "max_depth", "sep", "stop",
                                          "vocab", "path")] + [("device_bytes", C.c_int64)]
+
+
+class KvDescriptor(C.Structure):
+    """tms_kv"""
+    _fields_ = [(n, C.c_void_p) for n in ("kv", "table", "length", "held", "refs", "status", "work")] + \
+        [("work_bytes", C.c_int64)] + \
+        [(n, C.c_int32) for n in ("dtype", "layers", "pages", "kv_heads", "page_tokens", "head_dim", "seqs",
+                                  "max_pages")]
 
 
 _lib = None
@@ -105,6 +116,14 @@ def lib():
             "tms_read_reference": [P, C.c_int64, P, i32, i32, P],
             "tms_decode_k_pointers_noalloc": [P, P, C.c_int, i32, i32, i32, P, i32, P, P, P, P, P],
             "tms_state_get_launch": [P, P, P],
+            "tms_kv_work_bytes": [P, P],
+            "tms_kv_fork": [P, P, P],
+            "tms_kv_reserve": [P, P, P],
+            "tms_kv_write": [P, i32, P, i32, P, C.c_int64, i32, P, P, C.c_int64, P, C.c_int64, P, P, C.c_float, P, P,
+                             i32, i32, P],
+            "tms_kv_attention": [P, i32, P, C.c_int64, i32, P, i32, i32, P, C.c_float, P, P],
+            "tms_kv_commit": [P, P, P, i32, P],
+            "tms_kv_sync_status": [P, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -437,6 +456,190 @@ def read_reference(src, out, grid: int = 0, unroll: int = 0, nbytes: int | None 
 
 def debug_set_live(st, s: int, edge: int, value: int, stream=None):
     _check(lib().tms_debug_set_live(_handle(st), s, edge, value, _stream(stream)), "debug_set_live")
+
+
+# --------------------------------------------------------------------------- paged key/value cache
+
+def _sized(t, dtype, numel: int, name: str):
+    """Data pointer of a contiguous GPU tensor of at least numel values."""
+    p = _dev(t, dtype, name)
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} values, {numel} are needed")
+    return p
+
+
+def _token_rows(t, dtype, dim: int, name: str):
+    """(pointer, row stride in elements) of a GPU tensor [T][heads][dim] whose
+    tokens are contiguous (a slice of a wider projection may hold them)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T][heads][{dim}]")
+    if t.shape[0] == 0:  # no tokens: strides say nothing
+        return None, t.shape[1] * dim
+    s = t.stride()
+    if s[2] != 1 or (s[1] != dim and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * dim)
+
+
+class PagedCache:
+    """Keys and values of a batch of sequences in shared pages: the caller's
+    tensors, kept alive and changed in place by the kv_* calls, and the work
+    memory those share (calls on several streams have to be ordered by the
+    caller, as for one State).
+
+    kv [layers][pages][2][kv_heads][page_tokens][head_dim] (float32 or
+    bfloat16); int32 table [seqs][max_pages], length, held, status [seqs] and
+    refs [pages].  PagedCache.empty() makes an empty one."""
+
+    def __init__(self, kv, table, length, held, refs, status):
+        if kv.dim() != 6 or kv.shape[2] != 2:
+            raise ValueError("kv must be [layers][pages][2][kv_heads][page_tokens][head_dim]")
+        if kv.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("kv must be float32 or bfloat16")
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs][max_pages]")
+        self.layers, self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = kv.shape
+        self.seqs, self.max_pages = table.shape
+        for name, t, n in (("length", length, self.seqs), ("held", held, self.seqs), ("status", status, self.seqs),
+                           ("refs", refs, self.pages)):
+            if t.numel() != n:
+                raise ValueError(f"{name} has {t.numel()} values, expected {n}")
+        for t in (kv, table, length, held, refs, status):
+            if t.device != kv.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.kv, self.table, self.length, self.held, self.refs, self.status_codes = kv, table, length, held, refs, status
+        d = KvDescriptor(_dev(kv, name="kv"), _dev(table, torch.int32, "table"), _dev(length, torch.int32, "length"),
+                         _dev(held, torch.int32, "held"), _dev(refs, torch.int32, "refs"),
+                         _dev(status, torch.int32, "status"), None, 0, F32 if kv.dtype == torch.float32 else BF16,
+                         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim, self.seqs,
+                         self.max_pages)
+        need = C.c_int64()
+        _check(lib().tms_kv_work_bytes(C.byref(d), C.byref(need)), "PagedCache")
+        self.work = torch.empty(need.value, dtype=torch.uint8, device=kv.device)
+        self._made_on = torch.cuda.current_stream(kv.device).cuda_stream
+        d.work, d.work_bytes = self.work.data_ptr(), need.value
+        self.d = d
+        self.ref = C.byref(d)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int, seqs: int, max_pages: int,
+              dtype=torch.bfloat16, device="cuda"):
+        def ints(*shape, value=0):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+        return cls(torch.empty((layers, pages, 2, kv_heads, page_tokens, head_dim), dtype=dtype, device=device),
+                   ints(seqs, max_pages, value=-1), ints(seqs), ints(seqs), ints(pages), ints(seqs))
+
+    def status(self, stream=None, check: bool = False) -> np.ndarray:
+        out = np.zeros(self.seqs, np.int32)
+        rc = lib().tms_kv_sync_status(self.ref, out.ctypes.data, _stream(stream))
+        if rc not in (OK, ERR_OOM, ERR_INVALID_ARG) or (check and rc != OK):
+            _check(rc, "kv_sync_status")
+        return out
+
+
+def _kv_stream(cache: PagedCache, stream):
+    """The stream of a call; the work memory is told of streams other than the
+    one it was allocated on, so that it is not handed on while they use it."""
+    s = torch.cuda.current_stream(cache.kv.device) if stream is None else stream
+    if not isinstance(s, torch.cuda.Stream):
+        s = torch.cuda.ExternalStream(int(s), device=cache.kv.device)
+    if s.cuda_stream != cache._made_on:
+        cache.work.record_stream(s)
+    return s.cuda_stream
+
+
+def _raise_kv_errors(cache: PagedCache, stream, where: str):
+    buf = np.zeros(cache.seqs, np.int32)
+    rc = lib().tms_kv_sync_status(cache.ref, buf.ctypes.data, _stream(stream))
+    if rc != OK:
+        bad = {i: int(x) for i, x in enumerate(buf) if x != OK}
+        raise TmsError(rc, where, f"{lib().tms_last_error().decode()}; {len(bad)} of {cache.seqs} sequences in error: "
+                                  f"{dict(list(bad.items())[:16])}")
+
+
+def kv_fork(cache: PagedCache, src, stream=None, check: bool = True):
+    """Sequence s becomes what src[s] was (int32 [seqs]; itself: unchanged,
+    -1: emptied).  check: synchronise and raise on device errors."""
+    _refuse_check_while_recording(check, stream, "kv_fork")
+    _check(lib().tms_kv_fork(cache.ref, _sized(src, torch.int32, cache.seqs, "src"), _kv_stream(cache, stream)),
+           "kv_fork")
+    if check:
+        _raise_kv_errors(cache, stream, "kv_fork")
+
+
+def kv_reserve(cache: PagedCache, n_new, stream=None, check: bool = True):
+    """Pages for n_new[s] more rows of every sequence (int32 [seqs])."""
+    _refuse_check_while_recording(check, stream, "kv_reserve")
+    _check(lib().tms_kv_reserve(cache.ref, _sized(n_new, torch.int32, cache.seqs, "n_new"), _kv_stream(cache, stream)),
+           "kv_reserve")
+    if check:
+        _raise_kv_errors(cache, stream, "kv_reserve")
+
+
+def kv_write(cache: PagedCache, layer: int, k, v, start, q=None, q_out=None, q_weight=None, k_weight=None,
+             eps: float = 1e-6, pos=None, inv_freq=None, interleaved: bool = False, stream=None):
+    """Norm, rotation and cache rows of the packed new tokens (tms_kv_write).
+    k, v, q: [T][heads][head_dim], the tokens' rows any multiple of 16 bytes
+    apart; start: int32 [seqs+1].  Asynchronous: PagedCache.status() reports."""
+    dt, D, T = cache.kv.dtype, cache.head_dim, k.shape[0]
+    kp, ldk = _token_rows(k, dt, D, "k")
+    vp, ldv = _token_rows(v, dt, D, "v")
+    if k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads or v.shape[0] != T:
+        raise ValueError("k and v must be [T][kv_heads][head_dim]")
+    qp, ldq, hq, qo = None, 0, 0, None
+    if q is not None:
+        qp, ldq = _token_rows(q, dt, D, "q")
+        hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q must have the tokens of k")
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        qo = _sized(q_out, dt, T * hq * D, "q_out")
+    n_freq = 0 if inv_freq is None else inv_freq.numel()
+    if n_freq and pos is None:
+        raise ValueError("inv_freq needs pos")
+    _check(lib().tms_kv_write(cache.ref, layer, _sized(start, torch.int32, cache.seqs + 1, "start"), T, qp, ldq, hq, qo,
+                              kp, ldk, vp, ldv, None if q_weight is None else _sized(q_weight, dt, D, "q_weight"),
+                              None if k_weight is None else _sized(k_weight, dt, D, "k_weight"), eps,
+                              _sized(pos, torch.int32, T, "pos") if n_freq else None,
+                              _dev(inv_freq, torch.float32, "inv_freq") if n_freq else None, n_freq, int(interleaved),
+                              _kv_stream(cache, stream)), "kv_write")
+
+
+def kv_attention(cache: PagedCache, layer: int, q, start, out, scale: float | None = None, parent=None,
+                 max_new: int | None = None, stream=None):
+    """Attention of the packed new tokens over the cache (tms_kv_attention):
+    parent (int32 [T]) makes them a tree of drafts, without it they are causal.
+    q, out: [T][q_heads][head_dim]; scale: head_dim ** -0.5 by default;
+    max_new: the most tokens of a sequence (T if not given).  Asynchronous."""
+    dt, D = cache.kv.dtype, cache.head_dim
+    qp, ldq = _token_rows(q, dt, D, "q")
+    T, hq = q.shape[0], q.shape[1]
+    _check(lib().tms_kv_attention(cache.ref, layer, qp, ldq, hq, _sized(start, torch.int32, cache.seqs + 1, "start"), T,
+                                  T if max_new is None else max_new,
+                                  None if parent is None else _sized(parent, torch.int32, T, "parent"),
+                                  D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"),
+                                  _kv_stream(cache, stream)), "kv_attention")
+
+
+def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = True):
+    """Keep the accepted new rows: n_keep int32 [seqs], keep int32
+    [seqs][stride] ascending indices (None: the first n_keep), and give the
+    pages past them back."""
+    _refuse_check_while_recording(check, stream, "kv_commit")
+    stride = 0
+    if keep is not None:
+        if keep.dim() != 2 or keep.shape[0] != cache.seqs:
+            raise ValueError("keep must be [seqs][stride]")
+        stride = keep.shape[1]
+    _check(lib().tms_kv_commit(cache.ref, _sized(n_keep, torch.int32, cache.seqs, "n_keep"),
+                               _dev(keep, torch.int32, "keep"), stride, _kv_stream(cache, stream)), "kv_commit")
+    if check:
+        _raise_kv_errors(cache, stream, "kv_commit")
 
 
 # --------------------------------------------------------------------------- handles

@@ -1,0 +1,185 @@
+// Norm of queries and keys for each head, rotation, and the keys and values
+// into their pages, for gfx950.
+//
+// Every value is read once and written once, so memory bounds it: a wavefront
+// takes one token and a few of its heads, a lane 16 bytes of a head, and
+// nothing but the sum of squares (over a head's lanes) and the rotation's
+// partner values (one exchange between lanes) leaves the registers.  The
+// angles depend on the token and on the lane's place in the head only, so they
+// are computed once for all heads of the wavefront, reduced to a turn in fp64:
+// pos * inv_freq passes 10^5 and its fp32 product would be off by 10^-2.
+#include <hip/hip_runtime.h>
+
+#include "kv_cache.h"
+#include "tms.h"
+
+namespace tms {
+namespace {
+
+constexpr int kWave = 64;
+
+__device__ inline float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ inline float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two floats rounded to nearest even into one word of bf16.
+__device__ inline uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int DT>
+struct Chunk;  // the values of 16 bytes
+template <>
+struct Chunk<0> {
+  static constexpr int N = 4;
+  static __device__ inline void unpack(const uint4& r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
+  }
+  static __device__ inline uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+template <>
+struct Chunk<1> {
+  static constexpr int N = 8;
+  static __device__ inline void unpack(const uint4& r, float (&x)[8]) {
+    x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
+    x[4] = bf16_lo(r.z), x[5] = bf16_hi(r.z), x[6] = bf16_lo(r.w), x[7] = bf16_hi(r.w);
+  }
+  static __device__ inline uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+};
+
+// Sequence of token t: the number of offsets start[1..seqs] at or below t, in
+// two reads of the wavefront (blocks of 64, then within the block; seqs is at
+// most 4096).
+__device__ inline int sequence_of(const int32_t* __restrict__ start, int seqs, int t, int lane) {
+  const int coarse = (lane + 1) * kWave;  // last offset of block `lane`
+  const int block = __popcll(__ballot(coarse <= seqs && start[min(coarse, seqs)] <= t));
+  const int fine = block * kWave + lane + 1;
+  return block * kWave + __popcll(__ballot(fine <= seqs && start[min(fine, seqs)] <= t));
+}
+
+// DT: 0 fp32, 1 bf16.  LPR: lanes of a head.  One wavefront: token t, the
+// groups of 64 / LPR heads g0, g0 + step, ...; heads are the queries', then
+// the keys', then the values'.
+template <int DT, int LPR>
+__global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int waves_per_token) {
+  constexpr int N = Chunk<DT>::N, D = LPR * N, RPW = kWave / LPR;
+  const int lane = threadIdx.x % kWave, wave = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+  const int t = __builtin_amdgcn_readfirstlane(wave / waves_per_token);
+  if (t >= a.T) return;
+  const int col = lane % LPR, sub = lane / LPR;  // chunk of the head, head of the group
+  const int heads = a.q_heads + 2 * c.kv_heads;
+  const uint4* q = static_cast<const uint4*>(a.q) + int64_t(t) * (a.ldq / N);
+  const uint4* k = static_cast<const uint4*>(a.k) + int64_t(t) * (a.ldk / N);
+  const uint4* v = static_cast<const uint4*>(a.v) + int64_t(t) * (a.ldv / N);
+  // the angles of the lane's values
+  const int first = col * N, turned = 2 * a.n_freq;
+  const bool rotate = first < turned;
+  float cs[N], sn[N];
+  if (rotate) {
+    const double pos = a.pos[t] * 0.15915494309189533577;  // in turns for a frequency of 1
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = first + i, f = a.interleaved ? e / 2 : (e < a.n_freq ? e : e - a.n_freq);
+      double turn = pos * static_cast<double>(a.inv_freq[f]);
+      turn -= rint(turn);
+      const float r = 2.f * static_cast<float>(turn);
+      sincospif(r, &sn[i], &cs[i]);
+    }
+  }
+  const int s = sequence_of(a.start, c.seqs, t, lane);
+  // where the token's keys and values go; null where they may not
+  uint4* kv_row = nullptr;
+  if (s < c.seqs && c.status[s] == TMS_OK) {
+    const int64_t row = int64_t(c.length[s]) + (t - a.start[s]);
+    if (t >= a.start[s] && row < int64_t(min(c.held[s], c.max_pages)) << c.page_shift) {
+      const int32_t p = c.table[int64_t(s) * c.max_pages + (row >> c.page_shift)];
+      if (p >= 0 && p < c.pages)
+        kv_row = static_cast<uint4*>(c.kv) +
+                 ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR;
+    }
+    if (!kv_row && lane == 0) c.status[s] = TMS_ERR_INVALID_ARG;
+  }
+  for (int g = (wave % waves_per_token) * RPW; g < heads; g += waves_per_token * RPW) {
+    const int h = g + sub;
+    const bool is_q = h < a.q_heads, is_k = !is_q && h < a.q_heads + c.kv_heads;
+    if (h >= heads) continue;  // whole heads: the lanes that exchange values leave together
+    const int kh = h - a.q_heads, vh = kh - c.kv_heads;
+    uint4 raw = is_q ? q[h * LPR + col] : is_k ? k[kh * LPR + col] : v[vh * LPR + col];
+    const void* weight = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+    if (is_q || is_k) {
+      float x[N];
+      Chunk<DT>::unpack(raw, x);
+      if (weight) {
+        float ss = 0.f, w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int d = 1; d < LPR; d *= 2) ss += __shfl_xor(ss, d);
+        const float r = 1.f / sqrtf(ss / D + a.eps);
+        Chunk<DT>::unpack(static_cast<const uint4*>(weight)[col], w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = x[i] * r * w[i];
+      }
+      if (a.n_freq) {
+        if (a.interleaved) {
+          if (rotate) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+              const float lo = x[i], hi = x[i + 1];
+              x[i] = lo * cs[i] - hi * sn[i];
+              x[i + 1] = hi * cs[i] + lo * sn[i];
+            }
+          }
+        } else {
+          const int half = a.n_freq / N, lower = first < a.n_freq;
+          const int other = lane + (rotate ? (lower ? half : -half) : 0);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float y = __shfl(x[i], other);
+            if (rotate) x[i] = lower ? x[i] * cs[i] - y * sn[i] : x[i] * cs[i] + y * sn[i];
+          }
+        }
+      }
+      raw = Chunk<DT>::pack(x);
+    }
+    if (is_q) {
+      static_cast<uint4*>(a.q_out)[(int64_t(t) * a.q_heads + h) * LPR + col] = raw;
+    } else if (kv_row) {
+      const int part = is_k ? kh : c.kv_heads + vh;
+      kv_row[int64_t(part) * c.page_tokens * LPR + col] = raw;
+    }
+  }
+}
+
+template <int DT>
+hipError_t launch(const KvCache& c, const KvWrite& a, hipStream_t s) {
+  const int lpr = c.head_dim / Chunk<DT>::N, rpw = kWave / lpr;
+  const int groups = (a.q_heads + 2 * c.kv_heads + rpw - 1) / rpw;
+  int per = 1;
+  while (per < groups && int64_t(a.T) * per < 4096) per *= 2;
+  const int64_t grid = (int64_t(a.T) * per + 3) / 4;
+  if (grid > (int64_t(1) << 24) - 1) return hipErrorInvalidValue;
+  auto run = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(c, a, per);
+    return hipGetLastError();
+  };
+  switch (lpr) {
+    case 8: return run(write_kernel<DT, 8>);
+    case 16: return run(write_kernel<DT, 16>);
+    case 32: return run(write_kernel<DT, 32>);
+    default: return run(write_kernel<DT, 64>);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const KvCache& c, const KvWrite& a, hipStream_t s) {
+  return c.dtype == TMS_F32 ? launch<0>(c, a, s) : launch<1>(c, a, s);
+}
+
+}  // namespace tms
