@@ -30,10 +30,19 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Workgroup barrier that orders LDS only: global loads stay in flight across it.
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 // Maximum and sum over the 4 lanes of a query row (lane % 16).
 __device__ inline float row_max(float x) {
@@ -53,6 +62,15 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
   return __builtin_bit_cast(uint32_t, v);
+}
+
+// 4 values at element i of an output.
+template <int DT>
+__device__ inline void store4(void* out, int64_t i, f32x4 x) {
+  if constexpr (DT == 1)
+    *reinterpret_cast<u32x2*>(static_cast<char*>(out) + i * 2) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+  else
+    *reinterpret_cast<f32x4*>(static_cast<char*>(out) + i * 4) = x;
 }
 
 // ------------------------------------------------------------------ plan --
@@ -84,8 +102,9 @@ __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, in
   return q;
 }
 
-__device__ inline int64_t tiles_of(const KvCache& c, const Seq& q) {
-  return int64_t(q.rows_tiles) * q.key_tiles * c.kv_heads;
+// Units of work of a sequence: its key tiles, or whole segments.
+__device__ inline int64_t tiles_of(const KvCache& c, const Seq& q, bool split) {
+  return int64_t(q.rows_tiles) * (split ? q.key_tiles : 1) * c.kv_heads;
 }
 
 // A segment that several workgroups share, written by the one it starts in.
@@ -99,8 +118,8 @@ struct Join {
 __host__ __device__ inline int64_t round256(int64_t x) { return (x + 255) & ~int64_t(255); }
 __host__ __device__ inline int64_t part_floats(int rows, int dim) { return int64_t(rows) * (dim + 2); }
 
-constexpr int kShares = 512;
-constexpr int64_t kPartFloats = 64 * (128 + 2) > 32 * (256 + 2) ? 64 * (128 + 2) : 32 * (256 + 2);
+constexpr int kShares = 512;  // few rows: two workgroups for each compute unit
+constexpr int kManyShares = 256;
 
 __device__ inline Join* joins(const KvCache& c) { return static_cast<Join*>(c.work); }
 __device__ inline float* part(const KvCache& c, int share, int which, int64_t floats) {
@@ -114,6 +133,90 @@ __device__ inline int share_of(int64_t total, int shares, int64_t tile) {
   int w = static_cast<int>(tile * shares / total);
   while (w + 1 < shares && share_begin(total, shares, w + 1) <= tile) ++w;
   return w;
+}
+
+// The share [*lo, *hi) of this workgroup among all units, the sequence *s that
+// it starts in and that sequence's first unit *base: a prefix sum over the
+// sequences (*shares is cut so that a share has at least `least` units).
+// Returns whether there is work.
+template <int M, int KW, int W>
+__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, int& shares, int least, int64_t* lo,
+                                int64_t* hi, int* s_out, int64_t* base_out, int64_t* total_out) {
+  __shared__ int64_t scan[W];
+  __shared__ int found_s;
+  __shared__ int64_t found_base;
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  int64_t mine = 0, total = 0, before = 0;
+  const int each = (c.seqs + W * kWave - 1) / (W * kWave);
+  for (int i = 0; i < each; ++i) {
+    const int s = tid * each + i;
+    if (s < c.seqs) mine += tiles_of(c, sequence(c, a, s, M, KW), split);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int64_t o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == kWave - 1) scan[wave] = incl;
+  __syncthreads();
+  for (int i = 0; i < W; ++i) {
+    if (i < wave) before += scan[i];
+    total += scan[i];
+  }
+  before += incl - mine;
+  if (split) shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / least)));
+  const int me = blockIdx.x;
+  if (split && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
+  *lo = split ? share_begin(total, shares, me) : me;
+  *hi = split ? share_begin(total, shares, me + 1) : me + 1;
+  if (total == 0 || (split ? me >= shares : me >= total)) return false;
+  if (*lo >= before && *lo < before + mine) {
+    int64_t base = before;
+    for (int s = tid * each;; ++s) {
+      const int64_t t = tiles_of(c, sequence(c, a, s, M, KW), split);
+      if (*lo < base + t) {
+        found_s = s;
+        found_base = base;
+        break;
+      }
+      base += t;
+    }
+  }
+  __syncthreads();
+  *s_out = found_s;
+  *base_out = found_base;
+  *total_out = total;
+  return true;
+}
+
+// Drafts of the tokens tok0 .. tok1 of a sequence: for each one bit a key from
+// key (len & ~31) on, set for committed rows and for the drafts on its walk to
+// the root.  Ends with a barrier.
+template <int Threads>
+__device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, int tok1, int32_t* par,
+                                 uint32_t (*seen)[kTreeWords]) {
+  const int tid = threadIdx.x, low = q.len & 31;
+  for (int i = tid; i < q.n; i += Threads) par[i] = a.parent[q.begin + i];
+  for (int i = tid; i < (tok1 - tok0 + 1) * kTreeWords; i += Threads)
+    seen[i / kTreeWords][i % kTreeWords] = i % kTreeWords ? 0 : (1u << low) - 1;
+  __syncthreads();
+  if (tid <= tok1 - tok0)
+    for (int j = tok0 + tid; j >= 0;) {
+      const int bit = low + j, p = par[j];
+      seen[tid][bit >> 5] |= 1u << (bit & 31);
+      j = p < j ? p : -1;
+    }
+  __syncthreads();
+}
+
+// Keys first .. first+31 (first a multiple of 32 in the tree's region) that
+// token tok sees, one bit each.
+__device__ inline uint32_t sees(const KvAttention& a, const Seq& q, int tok, int tok0, int first,
+                                const uint32_t (*seen)[kTreeWords]) {
+  if (a.parent) return seen[max(tok - tok0, 0)][(first - (q.len & ~31)) >> 5];
+  const int count = q.len + tok + 1 - first;
+  return count >= 32 ? ~0u : (1u << max(count, 0)) - 1;
 }
 
 // ------------------------------------------------- few rows: token, drafts --
@@ -155,9 +258,6 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   __shared__ float stat[kWaves][2][M];
   __shared__ uint32_t seen[M][kTreeWords];
   __shared__ int32_t par[kTree];
-  __shared__ int64_t scan[kWaves];
-  __shared__ int found_s;
-  __shared__ int64_t found_base;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int col = lane % 16, g = lane / 16;
   const int group = a.q_heads / c.kv_heads;
@@ -165,55 +265,15 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
   const uint32_t flip = a.scale < 0.f ? (DT == 0 ? 0x80000000u : 0x80008000u) : 0u, on = a.scale == 0.f ? 0u : ~0u;
 
-  // share: prefix sums of the sequences' tiles
-  int64_t mine = 0, total = 0, before = 0;
-  const int each = (c.seqs + kBlock - 1) / kBlock;
-  for (int i = 0; i < each; ++i) {
-    const int s = tid * each + i;
-    if (s < c.seqs) mine += tiles_of(c, sequence(c, a, s, M, KW));
-  }
-  {
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-      const int64_t o = __shfl_up(incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == kWave - 1) scan[wave] = incl;
-    __syncthreads();
-    for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) before += scan[i];
-      total += scan[i];
-    }
-    before += incl - mine;
-  }
-  // at least one tile for every wavefront
-  shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / kWaves)));
+  int64_t lo, hi, base, total;
+  int s;
+  if (!my_share<M, KW, kWaves>(c, a, true, shares, kWaves, &lo, &hi, &s, &base, &total)) return;
   const int me = blockIdx.x;
-  if (tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
-  if (me >= shares || total == 0) return;
-  int64_t lo = share_begin(total, shares, me);
-  const int64_t hi = share_begin(total, shares, me + 1);
-  if (lo >= before && lo < before + mine) {
-    int64_t base = before;
-    for (int s = tid * each;; ++s) {
-      const int64_t t = tiles_of(c, sequence(c, a, s, M, KW));
-      if (lo < base + t) {
-        found_s = s;
-        found_base = base;
-        break;
-      }
-      base += t;
-    }
-  }
-  __syncthreads();
-  int s = found_s;
-  int64_t base = found_base;
   Seq q = sequence(c, a, s, M, KW);
 
   while (lo < hi) {
-    while (lo >= base + tiles_of(c, q)) {
-      base += tiles_of(c, q);
+    while (lo >= base + tiles_of(c, q, true)) {
+      base += tiles_of(c, q, true);
       q = sequence(c, a, ++s, M, KW);
     }
     const int64_t off = lo - base;
@@ -239,22 +299,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // tokens of the tile
     const int limit = a.parent ? all : q.len + tok1 + 1;                             // keys that any row sees
     const int end = min(kt1, (limit + KW - 1) / KW);
-    const int base32 = q.len & ~31;  // key of bit 0 of the words of `seen`
-    if (a.parent && !q.bad && end * KW > q.len) {
-      // who sees whom: for each token of the tile one bit a key from base32
-      // on, set for committed rows and for the drafts on its walk to the root
-      for (int i = tid; i < q.n; i += kBlock) par[i] = a.parent[q.begin + i];
-      for (int i = tid; i < (tok1 - tok0 + 1) * kTreeWords; i += kBlock)
-        seen[i / kTreeWords][i % kTreeWords] = i % kTreeWords ? 0 : (1u << (q.len - base32)) - 1;
-      __syncthreads();
-      if (tid <= tok1 - tok0)
-        for (int j = tok0 + tid; j >= 0;) {
-          const int bit = q.len - base32 + j, p = par[j];
-          seen[tid][bit >> 5] |= 1u << (bit & 31);
-          j = p < j ? p : -1;
-        }
-      __syncthreads();
-    }
+    if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen);
 
     f32x4 o[MT][DB];
     float mx[MT], sum[MT];
@@ -330,9 +375,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         const int first = kt * KW, at = first & 31;  // key and bit of the tile's first key
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const int count = q.len + tok[m] + 1 - (first & ~31);  // causal: keys seen from the word's first on
-          uint32_t word = count >= 32 ? ~0u : (1u << max(count, 0)) - 1;
-          if (a.parent) word = seen[max(tok[m] - tok0, 0)][(first - base32) >> 5];
+          uint32_t word = sees(a, q, tok[m], tok0, first & ~31, seen);
           word >>= at + 4 * g;
 #pragma unroll
           for (int i = 0; i < T::Sub; ++i)
@@ -378,9 +421,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
           const char* p1 = reinterpret_cast<const char*>(vt + T::at(16 + r, 2 * d + half)) + col % 2 * 8;
           const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
           const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
-          const short v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-          bf16x8 va;
-          __builtin_memcpy(&va, v, 16);
+          const bf16x8 va = __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)));
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             o[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, __builtin_bit_cast(bf16x8, pw[m]), o[m][d], 0, 0, 0);
@@ -436,13 +477,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         } else if (r < rows) {
           if (q.bad) x = f32x4{NAN, NAN, NAN, NAN}, l = 1.f;
           const int64_t at_out = (int64_t(q.begin + r / group) * a.q_heads + h * group + r % group) * D + 16 * d + 4 * g;
-          x *= 1.f / l;
-          if constexpr (DT == 1) {
-            *reinterpret_cast<u32x2*>(static_cast<char*>(a.out) + at_out * 2) =
-                u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-          } else {
-            *reinterpret_cast<f32x4*>(static_cast<char*>(a.out) + at_out * 4) = x;
-          }
+          store4<DT>(a.out, at_out, x * (1.f / l));
         }
       }
     }
@@ -453,55 +488,285 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   }
 }
 
+// ------------------------------------------ many rows: drafts, whole prompts --
+
+// Workgroup of W wavefronts with 32 rows each over a segment (whole prompts:
+// the heaviest first) or over a share of the key tiles (drafts over a long
+// context).  64-key tiles of K and V in LDS, two buffers: the loads of the next
+// tile are in flight during the products of this one.
+template <int D, int W>
+__global__ __launch_bounds__(W * kWave, 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split) {
+  constexpr int M = 32 * W, KT = 64, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
+  constexpr int RPP = Threads / CH, P = KT / RPP;  // rows of a pass of loads, passes
+  __shared__ u32x4 kt_lds[2][KT * CH], vt_lds[2][KT * CH];
+  __shared__ uint32_t seen[M][kTreeWords];
+  __shared__ int32_t par[kTree];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int col = lane % 32, hi2 = lane / 32;
+  const int group = a.q_heads / c.kv_heads;
+  const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, on = a.scale == 0.f ? 0u : ~0u;
+  // places in LDS: K is read 16 bytes of 32 rows at a time, V 32 bytes of 8
+  auto k_at = [](int r, int ch) { return r * CH + (ch ^ (r & (CH - 1))); };
+  auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << 1 & (CH - 1))); };
+
+  int64_t lo, hi, base, total;
+  int s;
+  if (!my_share<M, KT, W>(c, a, split, shares, 1, &lo, &hi, &s, &base, &total)) return;
+  Seq q = sequence(c, a, s, M, KT);
+  while (lo < hi) {
+    while (lo >= base + tiles_of(c, q, split)) {
+      base += tiles_of(c, q, split);
+      q = sequence(c, a, ++s, M, KT);
+    }
+    const int64_t off = lo - base;
+    int h, rt, kt0 = 0, kt1 = q.key_tiles;
+    if (split) {
+      const int seg = static_cast<int>(off / q.key_tiles);
+      kt0 = static_cast<int>(off % q.key_tiles);
+      kt1 = static_cast<int>(min(int64_t(q.key_tiles), kt0 + hi - lo));
+      h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
+    } else {  // heads of a row tile next to each other (each on its own XCD's cache), long rows first
+      h = static_cast<int>(off) % c.kv_heads, rt = q.rows_tiles - 1 - static_cast<int>(off) / c.kv_heads;
+    }
+    const int rows = q.n * group, all = q.len + q.n;
+    const int r = rt * M + wave * 32 + col, tok = r < rows ? r / group : -1;
+    bf16x8 qr[KK];
+    {
+      const int64_t at = int64_t(q.begin + max(tok, 0)) * a.ldq + int64_t(h * group + (r < rows ? r % group : 0)) * D;
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + at * 2);
+#pragma unroll
+      for (int i = 0; i < KK; ++i) qr[i] = __builtin_bit_cast(bf16x8, (p[2 * i + hi2] ^ flip) & on);
+    }
+    const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // of the workgroup
+    const int limit = a.parent ? all : q.len + tok1 + 1;
+    const int end = q.bad ? kt0 : min(kt1, (limit + KT - 1) / KT);
+    // of the wavefront: keys that all its rows see, keys that any sees
+    const int w0 = rt * M + wave * 32;
+    const int clear = a.parent ? q.len : q.len + min(w0 / group, q.n - 1) + 1;
+    const int some = w0 >= rows ? 0 : a.parent ? all : q.len + min((w0 + 31) / group, q.n - 1) + 1;
+    if (a.parent && !q.bad && end * KT > q.len) walk_tree<Threads>(a, q, tok0, tok1, par, seen);
+
+    f32x16 o[DB];
+    float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    const int32_t* table = c.table + int64_t(s) * c.max_pages;
+    const int64_t head_stride = int64_t(c.page_tokens) * CH;  // 16-byte words
+    const u32x4* kv = static_cast<const u32x4*>(c.kv) + (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
+    const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
+    const int my_row = tid / CH, my_ch = tid % CH;
+    u32x4 kr[P], vr[P];
+    int32_t pg[P];
+    // keys past the end are read from the last row: in bounds, and masked
+#define TMS_PAGES(kt)                                                                                  \
+  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
+    const int32_t p_ = table[min((kt) * KT + i * RPP + my_row, all - 1) >> c.page_shift];              \
+    pg[i] = max(0, min(p_, c.pages - 1));                                                              \
+  }
+#define TMS_LOAD(kt)                                                                                   \
+  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
+    const int r_ = min((kt) * KT + i * RPP + my_row, all - 1);                                         \
+    const u32x4* p_ = kv + pg[i] * page_stride + int64_t(r_ & (c.page_tokens - 1)) * CH + my_ch;       \
+    kr[i] = p_[0];                                                                                     \
+    vr[i] = p_[v_off];                                                                                 \
+  }
+#define TMS_STAGE(b)                                                                                   \
+  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
+    kt_lds[b][k_at(i * RPP + my_row, my_ch)] = kr[i];                                                  \
+    vt_lds[b][v_at(i * RPP + my_row, my_ch)] = vr[i];                                                  \
+  }
+    if (kt0 < end) {
+      TMS_PAGES(kt0);
+      TMS_LOAD(kt0);
+      TMS_PAGES(min(kt0 + 1, end - 1));
+      TMS_STAGE(0);
+    }
+    lds_barrier();
+    for (int kt = kt0; kt < end; ++kt) {
+      const int b = (kt - kt0) & 1;
+      if (kt + 1 < end) {
+        TMS_LOAD(kt + 1);
+        TMS_PAGES(min(kt + 2, end - 1));
+      }
+      if (kt * KT < some) {
+        f32x16 sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < KK; ++j)
+            sc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, kt_lds[b][k_at(i * 32 + col, 2 * j + hi2)]), qr[j], sc[i], 0, 0, 0);
+        }
+        if ((kt + 1) * KT > clear) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int first = kt * KT + 32 * i;
+            uint32_t word = 0;
+            if (a.parent ? first + 32 > q.len && first < all : true) word = sees(a, q, tok, tok0, first, seen);
+            else word = first < q.len ? ~0u : 0u;
+            word >>= 4 * hi2;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[i][e] = word >> (8 * (e / 4) + e % 4) & 1 ? sc[i][e] : -INFINITY;
+          }
+        }
+        float top = fmaxf(sc[0][0], sc[1][0]);
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(sc[0][e], sc[1][e]));
+        {
+          auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+          top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * scale;
+        }
+        // the maximum is moved only when a row has outgrown it by 2^8: weights
+        // stay below 256, and most tiles need no rescaling
+        if (__any(top > mx + 8.f)) {
+          const float next = fmaxf(mx, top), turn = next == -INFINITY ? 1.f : exp2_fast(mx - next);
+          mx = next;
+          sum *= turn;
+#pragma unroll
+          for (int d = 0; d < DB; ++d) o[d] *= turn;
+        }
+        const float at = mx == -INFINITY ? 0.f : mx;
+        u32x4 pw[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            sc[i][e] = exp2_fast(fmaf(sc[i][e], scale, -at));
+            sum += sc[i][e];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            pw[2 * i + j] = u32x4{pack_bf16(sc[i][8 * j], sc[i][8 * j + 1]), pack_bf16(sc[i][8 * j + 2], sc[i][8 * j + 3]),
+                                  pack_bf16(sc[i][8 * j + 4], sc[i][8 * j + 5]), pack_bf16(sc[i][8 * j + 6], sc[i][8 * j + 7])};
+        }
+        // V^T: lane (d = lane % 32 of the block, keys 4 hi2 .. +3 of two
+        // groups of 8) as the weights have them
+        const int vrow = 4 * hi2 + lane % 16 / 4, vch = 2 * (lane % 32 / 16) + lane % 4 / 2, vb = lane % 2 * 8;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const char* p0 = reinterpret_cast<const char*>(&vt_lds[b][v_at(16 * j + vrow, 4 * d + vch)]) + vb;
+            const char* p1 = reinterpret_cast<const char*>(&vt_lds[b][v_at(16 * j + 8 + vrow, 4 * d + vch)]) + vb;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
+            const s16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                           __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
+          }
+      }
+      if (kt + 1 < end) TMS_STAGE(b ^ 1);
+      lds_barrier();
+    }
+#undef TMS_PAGES
+#undef TMS_LOAD
+#undef TMS_STAGE
+    {
+      auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+      sum = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+    if (kt0 == 0 && kt1 == q.key_tiles) {
+      if (r < rows) {
+        const float inv = 1.f / sum;
+        const int64_t at = (int64_t(q.begin + tok) * a.q_heads + h * group + r % group) * D + 4 * hi2;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 x{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+            store4<1>(a.out, at + 32 * d + 8 * j, q.bad ? f32x4{NAN, NAN, NAN, NAN} : x * inv);
+          }
+      }
+    } else {
+      float* to = part(c, blockIdx.x, kt0 == 0, part_floats(M, D));
+      if (hi2 == 0) to[wave * 32 + col] = mx, to[M + wave * 32 + col] = sum;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          reinterpret_cast<f32x4*>(to + 2 * M)[((wave * DB + d) * 4 + j) * kWave + lane] =
+              f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, lo + q.key_tiles - 1)};
+    }
+    lo += split ? kt1 - kt0 : 1;
+  }
+}
+
+// Row and column of value 4 i of a part's outputs: the lanes' order of the
+// 16-row (few rows) and of the 32-row products (many rows).
+template <int D>
+__device__ inline void part_place(int i, int wide, int* row, int* column) {
+  const int lane = i % kWave, block = i / kWave;
+  if (wide) {
+    *row = block / (D / 8) * 32 + lane % 32;
+    *column = block % (D / 8) * 8 + lane / 32 * 4;
+  } else {
+    *row = block / (D / 16) * 16 + lane % 16;
+    *column = block % (D / 16) * 16 + lane / 16 * 4;
+  }
+}
+
 // Joins the parts of a segment that starts in share blockIdx.x and ends in a
-// later one.  blockIdx.y: 16 of its rows.
+// later one; a thread takes 4 values of a row.
 template <int DT, int D>
-__global__ __launch_bounds__(kBlock) void combine_kernel(KvCache c, KvAttention a, int M) {
-  constexpr int DB = D / 16, Q = DB / kWaves;
+__global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, int M, int wide) {
   const Join j = joins(c)[blockIdx.x];
   if (j.last < 0) return;
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16, m = blockIdx.y;
   const int group = a.q_heads / c.kv_heads, begin = a.start[j.s], rows = (a.start[j.s + 1] - begin) * group;
+  const int i = blockIdx.y * 256 + threadIdx.x;
+  int row, column;
+  part_place<D>(i, wide, &row, &column);
+  const int r = j.rt * M + row;
+  if (row >= M || r >= rows) return;
   const int64_t floats = part_floats(M, D);
-  f32x4 x[Q] = {};
+  f32x4 x{0.f, 0.f, 0.f, 0.f};
   float top = -INFINITY, l = 0.f;
   for (int w = blockIdx.x; w <= j.last; ++w) {
     const float* p = part(c, w, w == static_cast<int>(blockIdx.x), floats);
-    const float t = p[m * 16 + col], k = p[M + m * 16 + col];
+    const float t = p[row], k = p[M + row];
+    const f32x4 y = reinterpret_cast<const f32x4*>(p + 2 * M)[i];
     const float next = fmaxf(top, t), at = next == -INFINITY ? 0.f : next;
     const float old = exp2_fast(top - at), now = exp2_fast(t - at);
     top = next;
     l = l * old + k * now;
-#pragma unroll
-    for (int i = 0; i < Q; ++i)
-      x[i] = x[i] * old + reinterpret_cast<const f32x4*>(p + 2 * M)[(m * DB + wave * Q + i) * kWave + lane] * now;
+    x = x * old + y * now;
   }
-  const int r = j.rt * M + m * 16 + col;
-  if (r >= rows) return;
-#pragma unroll
-  for (int i = 0; i < Q; ++i) {
-    const int64_t at = (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + 16 * (wave * Q + i) + 4 * g;
-    x[i] *= 1.f / l;
-    if constexpr (DT == 1) {
-      *reinterpret_cast<u32x2*>(static_cast<char*>(a.out) + at * 2) =
-          u32x2{pack_bf16(x[i][0], x[i][1]), pack_bf16(x[i][2], x[i][3])};
-    } else {
-      *reinterpret_cast<f32x4*>(static_cast<char*>(a.out) + at * 4) = x[i];
-    }
-  }
+  const int64_t at = (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + column;
+  store4<DT>(a.out, at, x * (1.f / l));
 }
 
 template <int DT, int D, int MT>
 hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   few_rows_kernel<DT, D, MT><<<kShares, kBlock, 0, s>>>(c, a, kShares);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  combine_kernel<DT, D><<<dim3(kShares, MT), kBlock, 0, s>>>(c, a, 16 * MT);
+  combine_kernel<DT, D><<<dim3(kShares, (16 * MT * D / 4 + 255) / 256), 256, 0, s>>>(c, a, 16 * MT, 0);
+  return hipGetLastError();
+}
+
+template <int D, int W>
+hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
+  constexpr int M = 32 * W;
+  // row tiles of all sequences, at most
+  const int64_t segments = (int64_t(a.T) * (a.q_heads / c.kv_heads) / M + c.seqs) * c.kv_heads;
+  if (segments >= (int64_t(1) << 31) / (W * kWave)) return hipErrorInvalidValue;
+  const int split = segments < 2 * kManyShares;
+  many_rows_kernel<D, W><<<split ? kManyShares : int(segments), W * kWave, 0, s>>>(c, a, kManyShares, split);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
+  combine_kernel<1, D><<<dim3(kManyShares, M * D / 4 / 256), 256, 0, s>>>(c, a, M, 1);
   return hipGetLastError();
 }
 
 template <int DT, int D>
 hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
   const int64_t rows = int64_t(a.max_new) * (a.q_heads / c.kv_heads);
+  if constexpr (DT == 1 && D <= 128) {
+    if (rows > 64) return many_rows<D, 8>(c, a, s);
+  }
   constexpr int kMost = DT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);
   if constexpr (kMost >= 4)
     if (rows > 32) return few_rows<DT, D, 4>(c, a, s);
@@ -519,8 +784,10 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
 
 }  // namespace
 
-int64_t kv_attention_work_bytes(const KvCache&) {
-  return round256(kShares * int64_t(sizeof(Join))) + 2 * kShares * kPartFloats * 4;
+int64_t kv_attention_work_bytes(const KvCache& c) {
+  // two parts of a share: 64 rows for each of the few-row shares, 256 for each of the many-row shares
+  const int64_t few = kShares * part_floats(64, c.head_dim), many = kManyShares * part_floats(256, c.head_dim);
+  return round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * (many > few ? many : few);
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, hipStream_t s) {
