@@ -24,6 +24,7 @@ namespace tms {
 namespace {
 
 constexpr int kWave = 64, kWaves = 4, kBlock = kWave * kWaves;
+constexpr int kAhead = 4;  // products of 32 rows that the reads of LDS run ahead
 constexpr int kTree = 1024, kTreeWords = kTree / 32 + 1;  // drafts of a tree; words of 32 keys they may touch
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -34,6 +35,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef const __attribute__((address_space(3))) u32x4* lds_u32x4;
+typedef const __attribute__((address_space(4))) int32_t* const_i32;  // read through the scalar cache
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -42,6 +45,27 @@ __device__ inline void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ inline int64_t uniform(int64_t x) {
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+  return static_cast<int64_t>(uint64_t(hi) << 32 | uint32_t(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x))));
+}
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// 16 bytes for each lane from address `from` + `offset` (per lane) to LDS: lane i's go
+// to byte `to` + 16 i.  The compiler does not see the copy: wait_copies, then
+// a barrier, before LDS is read.
+__device__ inline void copy_to_lds(int64_t from, int offset, int to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(to)), "v"(offset),
+               "s"(uniform(from))
+               : "memory", "m0");
+}
+// All copies but the last N of this wavefront are in LDS.
+template <int N>
+__device__ inline void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // Maximum and sum over the 4 lanes of a query row (lane % 16).
@@ -102,9 +126,18 @@ __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, in
   return q;
 }
 
-// Units of work of a sequence: its key tiles, or whole segments.
-__device__ inline int64_t tiles_of(const KvCache& c, const Seq& q, bool split) {
-  return int64_t(q.rows_tiles) * (split ? q.key_tiles : 1) * c.kv_heads;
+__device__ inline Seq uniform(const Seq& q) {
+  return Seq{uniform(q.begin), uniform(q.n), uniform(q.len), uniform(q.rows_tiles), uniform(q.key_tiles), uniform(int(q.bad)) != 0};
+}
+
+// Units of work of a sequence: its key tiles and kOpen more for every segment,
+// or whole segments.  A segment's start (queries, page numbers, the first keys,
+// the join of the wavefronts) is a chain of memory latencies that a share pays
+// for each of its segments: without kOpen a share of many short contexts takes
+// several times as long as one of a long context.
+constexpr int kOpen = 4;
+__device__ inline int64_t units_of(const KvCache& c, const Seq& q, bool split) {
+  return int64_t(q.rows_tiles) * (split ? q.key_tiles + kOpen : 1) * c.kv_heads;
 }
 
 // A segment that several workgroups share, written by the one it starts in.
@@ -150,7 +183,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   const int each = (c.seqs + W * kWave - 1) / (W * kWave);
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
-    if (s < c.seqs) mine += tiles_of(c, sequence(c, a, s, M, KW), split);
+    if (s < c.seqs) mine += units_of(c, sequence(c, a, s, M, KW), split);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -165,6 +198,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
     total += scan[i];
   }
   before += incl - mine;
+  total = uniform(total);
   if (split) shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / least)));
   const int me = blockIdx.x;
   if (split && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
@@ -174,7 +208,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   if (*lo >= before && *lo < before + mine) {
     int64_t base = before;
     for (int s = tid * each;; ++s) {
-      const int64_t t = tiles_of(c, sequence(c, a, s, M, KW), split);
+      const int64_t t = units_of(c, sequence(c, a, s, M, KW), split);
       if (*lo < base + t) {
         found_s = s;
         found_base = base;
@@ -184,8 +218,8 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
     }
   }
   __syncthreads();
-  *s_out = found_s;
-  *base_out = found_base;
+  *s_out = __builtin_amdgcn_readfirstlane(found_s);
+  *base_out = uniform(found_base);
   *total_out = total;
   return true;
 }
@@ -193,18 +227,18 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
 // Drafts of the tokens tok0 .. tok1 of a sequence: for each one bit a key from
 // key (len & ~31) on, set for committed rows and for the drafts on its walk to
 // the root.  Ends with a barrier.
+// words: of a token, at least (drafts + 31) / 32 + 1.
 template <int Threads>
-__device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, int tok1, int32_t* par,
-                                 uint32_t (*seen)[kTreeWords]) {
+__device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, int tok1, int32_t* par, uint32_t* seen,
+                                 int words) {
   const int tid = threadIdx.x, low = q.len & 31;
   for (int i = tid; i < q.n; i += Threads) par[i] = a.parent[q.begin + i];
-  for (int i = tid; i < (tok1 - tok0 + 1) * kTreeWords; i += Threads)
-    seen[i / kTreeWords][i % kTreeWords] = i % kTreeWords ? 0 : (1u << low) - 1;
+  for (int i = tid; i < (tok1 - tok0 + 1) * words; i += Threads) seen[i] = i % words ? 0 : (1u << low) - 1;
   __syncthreads();
   if (tid <= tok1 - tok0)
     for (int j = tok0 + tid; j >= 0;) {
       const int bit = low + j, p = par[j];
-      seen[tid][bit >> 5] |= 1u << (bit & 31);
+      seen[tid * words + (bit >> 5)] |= 1u << (bit & 31);
       j = p < j ? p : -1;
     }
   __syncthreads();
@@ -212,9 +246,9 @@ __device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, i
 
 // Keys first .. first+31 (first a multiple of 32 in the tree's region) that
 // token tok sees, one bit each.
-__device__ inline uint32_t sees(const KvAttention& a, const Seq& q, int tok, int tok0, int first,
-                                const uint32_t (*seen)[kTreeWords]) {
-  if (a.parent) return seen[max(tok - tok0, 0)][(first - (q.len & ~31)) >> 5];
+__device__ inline uint32_t sees(const KvAttention& a, const Seq& q, int tok, int tok0, int first, const uint32_t* seen,
+                                int words) {
+  if (a.parent) return seen[max(tok - tok0, 0) * words + ((first - (q.len & ~31)) >> 5)];
   const int count = q.len + tok + 1 - first;
   return count >= 32 ? ~0u : (1u << max(count, 0)) - 1;
 }
@@ -256,7 +290,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   constexpr int kLds = kWaves * kVWords > kWaves * M * D / 4 ? kWaves * kVWords : kWaves * M * D / 4;
   __shared__ u32x4 lds[kLds];
   __shared__ float stat[kWaves][2][M];
-  __shared__ uint32_t seen[M][kTreeWords];
+  __shared__ uint32_t seen[M * kTreeWords];
   __shared__ int32_t par[kTree];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int col = lane % 16, g = lane / 16;
@@ -269,17 +303,20 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   int s;
   if (!my_share<M, KW, kWaves>(c, a, true, shares, kWaves, &lo, &hi, &s, &base, &total)) return;
   const int me = blockIdx.x;
-  Seq q = sequence(c, a, s, M, KW);
+  Seq q = uniform(sequence(c, a, s, M, KW));
 
   while (lo < hi) {
-    while (lo >= base + tiles_of(c, q, true)) {
-      base += tiles_of(c, q, true);
-      q = sequence(c, a, ++s, M, KW);
+    while (lo >= base + units_of(c, q, true)) {
+      base += units_of(c, q, true);
+      q = uniform(sequence(c, a, ++s, M, KW));
     }
-    const int64_t off = lo - base;
-    const int seg = static_cast<int>(off / q.key_tiles), kt0 = static_cast<int>(off % q.key_tiles);
+    const int units = q.key_tiles + kOpen, seg = static_cast<int>((lo - base) / units);
+    const int u0 = static_cast<int>((lo - base) % units), u1 = static_cast<int>(min(int64_t(units), u0 + hi - lo));
+    const int64_t last = lo + units - u0 - 1;  // unit of the segment's last tile
+    lo += u1 - u0;
+    if (u1 <= kOpen) break;  // the share ends before the segment's first tile
+    const int kt0 = max(u0 - kOpen, 0), kt1 = u1 - kOpen;
     const int h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
-    const int kt1 = static_cast<int>(min(int64_t(q.key_tiles), kt0 + hi - lo));
     const int rows = q.n * group;  // of the sequence and key head
     const int all = q.len + q.n;
     // the queries: B operand, row = lane % 16
@@ -299,7 +336,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // tokens of the tile
     const int limit = a.parent ? all : q.len + tok1 + 1;                             // keys that any row sees
     const int end = min(kt1, (limit + KW - 1) / KW);
-    if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen);
+    if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen, kTreeWords);
 
     f32x4 o[MT][DB];
     float mx[MT], sum[MT];
@@ -375,7 +412,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         const int first = kt * KW, at = first & 31;  // key and bit of the tile's first key
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          uint32_t word = sees(a, q, tok[m], tok0, first & ~31, seen);
+          uint32_t word = sees(a, q, tok[m], tok0, first & ~31, seen, kTreeWords);
           word >>= at + 4 * g;
 #pragma unroll
           for (int i = 0; i < T::Sub; ++i)
@@ -482,30 +519,53 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       }
     }
     if (kt0 == 0 && !whole && tid == 0)
-      joins(c)[me] = Join{s, h, rt, share_of(total, shares, lo + q.key_tiles - 1)};
+      joins(c)[me] = Join{s, h, rt, share_of(total, shares, last)};
     __syncthreads();
-    lo += kt1 - kt0;
   }
 }
 
 // ------------------------------------------ many rows: drafts, whole prompts --
 
-// Workgroup of W wavefronts with 32 rows each over a segment (whole prompts:
-// the heaviest first) or over a share of the key tiles (drafts over a long
-// context).  64-key tiles of K and V in LDS, two buffers: the loads of the next
-// tile are in flight during the products of this one.
-template <int D, int W>
-__global__ __launch_bounds__(W * kWave, 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split) {
-  constexpr int M = 32 * W, KT = 64, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
-  constexpr int RPP = Threads / CH, P = KT / RPP;  // rows of a pass of loads, passes
-  __shared__ u32x4 kt_lds[2][KT * CH], vt_lds[2][KT * CH];
-  __shared__ uint32_t seen[M][kTreeWords];
-  __shared__ int32_t par[kTree];
+// Words of the table of drafts that a workgroup of 32 RW rows has, and of a
+// token's row in it: a tree fits in one row tile below 8 x 32 rows; there, the
+// rows are of at most 128 tokens with two query heads or more to a key head
+// (any tree), and of 256 with one (trees of up to 512 drafts).
+template <int RW>
+constexpr int kSeen = RW == 8 ? 256 * 17 : 32 * RW * (RW + 1);
+template <int RW>
+int tree_words(int group) {
+  return RW < 8 ? RW + 1 : group > 1 ? kTreeWords : 17;
+}
+
+// Workgroup of RW x KS wavefronts over a segment (whole prompts: the heaviest
+// first) or over a share of the key tiles (drafts over a long context).  A
+// wavefront holds 32 rows and takes 1 / KS of the keys of every tile; the tiles
+// of K and V are in LDS, two buffers each.
+//
+// A tile is two phases: the products (scores of this tile, output of the one
+// before) and the softmax with the copies of later tiles into LDS.  With 8
+// wavefronts, two on a SIMD, the second four run one phase behind: while one
+// wavefront of a SIMD feeds the matrix cores the other has the vector units.
+template <int D, int RW, int KS>
+__global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
+  constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
+  constexpr bool Behind = W == 8;
+  constexpr int KT = 64, TileWords = KT * CH;       // keys of a tile, its 16-byte words
+  constexpr int NB = KT / 32 / KS;                  // 32-key blocks of a tile for each wavefront
+  constexpr int Ahead = Behind ? 2 : 1;             // tiles that the copies run ahead
+  constexpr int Bufs = Behind ? Ahead + 2 : Ahead + 1;
+  constexpr int RPI = kWave / CH, P = KT / RPI / W;  // rows of a copying instruction, instructions of a wavefront
+  // K tiles, then V tiles; the outputs of the second half of the keys at the end
+  __shared__ u32x4 tiles[2 * Bufs * TileWords];
+  __shared__ float stat[KS == 2 ? 2 * M : 1];
+  __shared__ uint32_t seen[kSeen<RW>];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-  const int col = lane % 32, hi2 = lane / 32;
+  const int rw = wave % RW, ks = wave / RW, col = lane % 32, hi2 = lane / 32;
+  const bool behind = Behind && wave >= 4;
   const int group = a.q_heads / c.kv_heads;
   const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, on = a.scale == 0.f ? 0u : ~0u;
+  const int tiles_at = static_cast<int>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)tiles));
   // places in LDS: K is read 16 bytes of 32 rows at a time, V 32 bytes of 8
   auto k_at = [](int r, int ch) { return r * CH + (ch ^ (r & (CH - 1))); };
   auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << 1 & (CH - 1))); };
@@ -513,24 +573,30 @@ __global__ __launch_bounds__(W * kWave, 2) void many_rows_kernel(KvCache c, KvAt
   int64_t lo, hi, base, total;
   int s;
   if (!my_share<M, KT, W>(c, a, split, shares, 1, &lo, &hi, &s, &base, &total)) return;
-  Seq q = sequence(c, a, s, M, KT);
+  Seq q = uniform(sequence(c, a, s, M, KT));
   while (lo < hi) {
-    while (lo >= base + tiles_of(c, q, split)) {
-      base += tiles_of(c, q, split);
-      q = sequence(c, a, ++s, M, KT);
+    while (lo >= base + units_of(c, q, split)) {
+      base += units_of(c, q, split);
+      q = uniform(sequence(c, a, ++s, M, KT));
     }
-    const int64_t off = lo - base;
     int h, rt, kt0 = 0, kt1 = q.key_tiles;
+    int64_t last = 0;  // unit of the segment's last tile
     if (split) {
-      const int seg = static_cast<int>(off / q.key_tiles);
-      kt0 = static_cast<int>(off % q.key_tiles);
-      kt1 = static_cast<int>(min(int64_t(q.key_tiles), kt0 + hi - lo));
+      const int units = q.key_tiles + kOpen, seg = static_cast<int>((lo - base) / units);
+      const int u0 = static_cast<int>((lo - base) % units), u1 = static_cast<int>(min(int64_t(units), u0 + hi - lo));
+      last = lo + units - u0 - 1;
+      lo += u1 - u0;
+      if (u1 <= kOpen) break;  // the share ends before the segment's first tile
+      kt0 = max(u0 - kOpen, 0), kt1 = u1 - kOpen;
       h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
     } else {  // heads of a row tile next to each other (each on its own XCD's cache), long rows first
-      h = static_cast<int>(off) % c.kv_heads, rt = q.rows_tiles - 1 - static_cast<int>(off) / c.kv_heads;
+      const int off = static_cast<int>(lo - base);
+      h = off % c.kv_heads, rt = q.rows_tiles - 1 - off / c.kv_heads;
+      ++lo;
     }
+    h = uniform(h), rt = uniform(rt), kt0 = uniform(kt0), kt1 = uniform(kt1);
     const int rows = q.n * group, all = q.len + q.n;
-    const int r = rt * M + wave * 32 + col, tok = r < rows ? r / group : -1;
+    const int r = rt * M + rw * 32 + col, tok = r < rows ? r / group : -1;
     bf16x8 qr[KK];
     {
       const int64_t at = int64_t(q.begin + max(tok, 0)) * a.ldq + int64_t(h * group + (r < rows ? r % group : 0)) * D;
@@ -541,135 +607,234 @@ __global__ __launch_bounds__(W * kWave, 2) void many_rows_kernel(KvCache c, KvAt
     const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // of the workgroup
     const int limit = a.parent ? all : q.len + tok1 + 1;
     const int end = q.bad ? kt0 : min(kt1, (limit + KT - 1) / KT);
-    // of the wavefront: keys that all its rows see, keys that any sees
-    const int w0 = rt * M + wave * 32;
-    const int clear = a.parent ? q.len : q.len + min(w0 / group, q.n - 1) + 1;
-    const int some = w0 >= rows ? 0 : a.parent ? all : q.len + min((w0 + 31) / group, q.n - 1) + 1;
-    if (a.parent && !q.bad && end * KT > q.len) walk_tree<Threads>(a, q, tok0, tok1, par, seen);
+    const int clear = a.parent ? q.len : q.len + min((rt * M + rw * 32) / group, q.n - 1) + 1;  // seen by all its rows
+    if (a.parent && !q.bad && end * KT > q.len)
+      walk_tree<Threads>(a, q, tok0, tok1, reinterpret_cast<int32_t*>(tiles), seen, words);
 
-    f32x16 o[DB];
+    const f32x16 zero = {};
+    f32x16 o[DB], sc[NB];
     float mx = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
-    const int32_t* table = c.table + int64_t(s) * c.max_pages;
+    const int32_t* table = c.table + int64_t(uniform(s)) * c.max_pages;
     const int64_t head_stride = int64_t(c.page_tokens) * CH;  // 16-byte words
     const u32x4* kv = static_cast<const u32x4*>(c.kv) + (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
     const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
-    const int my_row = tid / CH, my_ch = tid % CH;
-    u32x4 kr[P], vr[P];
-    int32_t pg[P];
-    // keys past the end are read from the last row: in bounds, and masked
-#define TMS_PAGES(kt)                                                                                  \
-  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
-    const int32_t p_ = table[min((kt) * KT + i * RPP + my_row, all - 1) >> c.page_shift];              \
-    pg[i] = max(0, min(p_, c.pages - 1));                                                              \
-  }
-#define TMS_LOAD(kt)                                                                                   \
-  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
-    const int r_ = min((kt) * KT + i * RPP + my_row, all - 1);                                         \
-    const u32x4* p_ = kv + pg[i] * page_stride + int64_t(r_ & (c.page_tokens - 1)) * CH + my_ch;       \
-    kr[i] = p_[0];                                                                                     \
-    vr[i] = p_[v_off];                                                                                 \
-  }
-#define TMS_STAGE(b)                                                                                   \
-  _Pragma("unroll") for (int i = 0; i < P; ++i) {                                                      \
-    kt_lds[b][k_at(i * RPP + my_row, my_ch)] = kr[i];                                                  \
-    vt_lds[b][v_at(i * RPP + my_row, my_ch)] = vr[i];                                                  \
-  }
+    // Copies from the cache straight into LDS, 1 KB an instruction: rows r0 ..
+    // r0 + RPI - 1 of a tile, in one page (a page has at least 8 rows).  LDS
+    // fills in the lanes' order, so the lanes take the words in the order that
+    // k_at and v_at have them.  Rows past the last one to be used are filled
+    // with that one: in bounds, and masked or never used.
+    const int final_row = uniform(max(min(all, end * KT) - 1, 0));
+    const int my_row = lane / CH, k_ch = lane % CH ^ ((wave * RPI + my_row) & (CH - 1)),
+              v_ch = lane % CH ^ ((wave * RPI + my_row) << 1 & (CH - 1));
+    // Step x copies K of tile x + 1 + Ahead and V of tile x + Ahead; a tile's
+    // page numbers are asked for one step before its K, its addresses are kept
+    // for its V.
+    const const_i32 pages = (const_i32)(table);
+    const uint32_t page_words = 2 * c.kv_heads * c.page_tokens * CH;
+    int next_page[P], row_at[P];
+    int64_t from[P];  // addresses
+    auto look = [&](int kt, int i) __attribute__((always_inline)) {
+      next_page[i] = pages[uint32_t(min(kt * KT + (i * W + wave) * RPI, final_row)) >> c.page_shift];
+    };
+    auto find = [&](int kt, int i) __attribute__((always_inline)) {
+      const int r0 = kt * KT + (i * W + wave) * RPI, first = min(r0, final_row & ~(RPI - 1));
+      const uint32_t page = uniform(max(0, min(next_page[i], c.pages - 1)));
+      from[i] = uniform(reinterpret_cast<int64_t>(kv) +
+                        (int64_t(uint64_t(page) * page_words) + uint32_t(first & (c.page_tokens - 1)) * CH) * 16);
+      row_at[i] = (min(r0 + my_row, final_row) - first) * (CH * 16);
+    };
+    auto copy = [&](int64_t off, int ch, int step, int to, int i) __attribute__((always_inline)) {
+      copy_to_lds(from[i] + off, row_at[i] + (ch ^ (i * W * RPI * step & (CH - 1))) * 16,
+                  tiles_at + to * (TileWords * 16) + (i * W + wave) * (kWave * 16));
+    };
+    // buffers of the V tile and of the K tile of the next step
+    int to_v = 0, to_k = 1;
+    auto ask = [&](int x, int piece) __attribute__((always_inline)) {
+      const int i = piece % P;
+      if (piece < P) {
+        copy(v_off * 16, v_ch, 2, Bufs + to_v, i);
+      } else {
+        find(x + 1 + Ahead, i);
+        copy(0, k_ch, 1, to_k, i);
+        look(x + 2 + Ahead, i);
+      }
+      if (piece == 2 * P - 1) {
+        to_v = to_v + 1 == Bufs ? 0 : to_v + 1;
+        to_k = to_k + 1 == Bufs ? 0 : to_k + 1;
+      }
+    };
+    // words of LDS that the products read.  V^T: lane (d = lane % 32 of the
+    // block, keys 4 hi2 .. +3 of two groups of 8) as the weights have them
+    const int vrow = 4 * hi2 + lane % 16 / 4, vch = 2 * (lane % 32 / 16) + lane % 4 / 2, vb = lane % 2 * 8;
+    int k_at_lds[KK], v_at_lds[DB];
+#pragma unroll
+    for (int j = 0; j < KK; ++j) k_at_lds[j] = tiles_at + k_at(ks * NB * 32 + col, 2 * j + hi2) * 16;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      v_at_lds[d] = tiles_at + (Bufs * TileWords + v_at(ks * NB * 32 + vrow, 4 * d + vch)) * 16 + vb;
+    // operands of the products: K of 32 rows from byte `from` of the K tiles on,
+    // V of 16 keys from byte `from` of the V tiles on
+    auto k_words = [&](int j, int from) __attribute__((always_inline)) {
+      return __builtin_bit_cast(bf16x8, *(lds_u32x4)(k_at_lds[j] + from));
+    };
+    auto v_words = [&](int d, int from) __attribute__((always_inline)) {
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(v_at_lds[d] + from));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(v_at_lds[d] + from + 8 * CH * 16));
+      return __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)));
+    };
     if (kt0 < end) {
-      TMS_PAGES(kt0);
-      TMS_LOAD(kt0);
-      TMS_PAGES(min(kt0 + 1, end - 1));
-      TMS_STAGE(0);
-    }
-    lds_barrier();
-    for (int kt = kt0; kt < end; ++kt) {
-      const int b = (kt - kt0) & 1;
-      if (kt + 1 < end) {
-        TMS_LOAD(kt + 1);
-        TMS_PAGES(min(kt + 2, end - 1));
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        look(kt0, i);
+        find(kt0, i);
+        copy(0, k_ch, 1, 0, i);
+        look(kt0 + 1, i);
       }
-      if (kt * KT < some) {
-        f32x16 sc[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int x = -Ahead; x < 0; ++x)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
+        for (int i = 0; i < 2 * P; ++i) ask(kt0 + x, i);
+      wait_copies<2 * P * Ahead>();
+      lds_barrier();
+      if (behind) lds_barrier();
 #pragma unroll
-          for (int j = 0; j < KK; ++j)
-            sc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, kt_lds[b][k_at(i * 32 + col, 2 * j + hi2)]), qr[j], sc[i], 0, 0, 0);
-        }
-        if ((kt + 1) * KT > clear) {
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int first = kt * KT + 32 * i;
-            uint32_t word = 0;
-            if (a.parent ? first + 32 > q.len && first < all : true) word = sees(a, q, tok, tok0, first, seen);
-            else word = first < q.len ? ~0u : 0u;
-            word >>= 4 * hi2;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sc[i][e] = word >> (8 * (e / 4) + e % 4) & 1 ? sc[i][e] : -INFINITY;
-          }
-        }
-        float top = fmaxf(sc[0][0], sc[1][0]);
-#pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(sc[0][e], sc[1][e]));
-        {
-          auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-          top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * scale;
-        }
-        // the maximum is moved only when a row has outgrown it by 2^8: weights
-        // stay below 256, and most tiles need no rescaling
-        if (__any(top > mx + 8.f)) {
-          const float next = fmaxf(mx, top), turn = next == -INFINITY ? 1.f : exp2_fast(mx - next);
-          mx = next;
-          sum *= turn;
-#pragma unroll
-          for (int d = 0; d < DB; ++d) o[d] *= turn;
-        }
-        const float at = mx == -INFINITY ? 0.f : mx;
-        u32x4 pw[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            sc[i][e] = exp2_fast(fmaf(sc[i][e], scale, -at));
-            sum += sc[i][e];
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            pw[2 * i + j] = u32x4{pack_bf16(sc[i][8 * j], sc[i][8 * j + 1]), pack_bf16(sc[i][8 * j + 2], sc[i][8 * j + 3]),
-                                  pack_bf16(sc[i][8 * j + 4], sc[i][8 * j + 5]), pack_bf16(sc[i][8 * j + 6], sc[i][8 * j + 7])};
-        }
-        // V^T: lane (d = lane % 32 of the block, keys 4 hi2 .. +3 of two
-        // groups of 8) as the weights have them
-        const int vrow = 4 * hi2 + lane % 16 / 4, vch = 2 * (lane % 32 / 16) + lane % 4 / 2, vb = lane % 2 * 8;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const char* p0 = reinterpret_cast<const char*>(&vt_lds[b][v_at(16 * j + vrow, 4 * d + vch)]) + vb;
-            const char* p1 = reinterpret_cast<const char*>(&vt_lds[b][v_at(16 * j + 8 + vrow, 4 * d + vch)]) + vb;
-            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
-            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
-            const s16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                           __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
-          }
-      }
-      if (kt + 1 < end) TMS_STAGE(b ^ 1);
+        for (int j = 0; j < KK; ++j)
+          sc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_words(j, i * 32 * CH * 16), qr[j], j ? sc[i] : zero, 0, 0, 0);
+      if (behind) wait_copies<2 * P * (Ahead - 1)>();  // K of tile kt0 + 1, V of tile kt0
       lds_barrier();
     }
-#undef TMS_PAGES
-#undef TMS_LOAD
-#undef TMS_STAGE
+    // a tile: softmax, output, the scores of the next tile (past the last one:
+    // not used)
+    int v_buf = 0, k_buf = 1;
+    for (int kt = kt0; kt < end; ++kt) {
+      if ((kt + 1) * KT > clear) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int first = kt * KT + 32 * (ks * NB + i);
+          uint32_t word = first < q.len ? ~0u : 0u;
+          if (!a.parent || (first + 32 > q.len && first < all)) word = sees(a, q, tok, tok0, first, seen, words);
+          word >>= 4 * hi2;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[i][e] = word >> (8 * (e / 4) + e % 4) & 1 ? sc[i][e] : -INFINITY;
+        }
+      }
+      float top = sc[0][0];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[i][e]);
+      {
+        auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * scale;
+      }
+      // the maximum is moved only when a row has outgrown it by 2^8: weights
+      // stay below 256, and most tiles need no rescaling
+      if (__any(top > mx + 8.f)) {
+        const float next = fmaxf(mx, top), turn = next == -INFINITY ? 1.f : exp2_fast(mx - next);
+        mx = next;
+        sum *= turn;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] *= turn;
+      }
+      const float at = mx == -INFINITY ? 0.f : mx;
+      // the weights, and between them the copies of a step: all at once they
+      // would wait for each other's way to LDS
+      u32x4 pw[2 * NB];
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) {
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] = exp2_fast(fmaf(sc[j / 2][j % 2 * 8 + e], scale, -at));
+          sum += w[e];
+        }
+        pw[j] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+#pragma unroll
+        for (int i = j * P / NB; i < (j + 1) * P / NB; ++i) ask(kt, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // the weights are finished before the barrier: behind it the other
+      // wavefront of the SIMD has the vector units
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) asm volatile("" : "+v"(pw[j]));
+      asm volatile("" : "+v"(sum));
+      // K of tile kt + 1 and V of tile kt are there, of all wavefronts behind the barrier
+      if (!behind) wait_copies<2 * P * Ahead>();
+      lds_barrier();
+      // O^T += V^T P^T, then the scores of the next tile.  The operands come
+      // from LDS kAhead products before their use; the order is fixed here
+      // because the compiler's own puts every read next to its product
+      constexpr int PV = DB * 2 * NB, QK = NB * KK;
+      const int v_from = v_buf * (TileWords * 16), k_from = k_buf * (TileWords * 16);
+      v_buf = k_buf, k_buf = k_buf + 1 == Bufs ? 0 : k_buf + 1;
+      auto fetch = [&](int i) __attribute__((always_inline)) {
+        if (i < PV) return v_words(i % DB, v_from + i / DB * (16 * CH * 16));
+        return k_words((i - PV) / NB, k_from + (i - PV) % NB * (32 * CH * 16));
+      };
+      bf16x8 f[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = fetch(i);
+#pragma unroll
+      for (int i = 0; i < PV + QK; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (i < PV) {
+          const int j = i / DB, d = i % DB;
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
+        } else {
+          const int j = (i - PV) / NB, k = (i - PV) % NB;
+          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], qr[j], j ? sc[k] : zero, 0, 0, 0);
+        }
+        if (i + kAhead < PV + QK) f[i % kAhead] = fetch(i + kAhead);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (behind) wait_copies<2 * P * (Ahead - 1)>();  // K of tile kt + 2, V of tile kt + 1
+      lds_barrier();
+    }
+    if (kt0 < end) {  // the copies asked for past the end, before LDS is used for anything else
+      wait_copies<0>();
+      if (Behind && !behind) lds_barrier();
+      lds_barrier();
+    }
     {
       auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
       sum = __uint_as_float(x[0]) + __uint_as_float(x[1]);
     }
+    if constexpr (KS == 2) {  // the two halves of the keys joined
+      static_assert(KS == 1 || RW * DB * 4 * kWave <= 2 * Bufs * TileWords, "the outputs of one half fit the tiles");
+      f32x4* buf = reinterpret_cast<f32x4*>(tiles);
+      if (ks == 1) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            buf[((rw * DB + d) * 4 + j) * kWave + lane] =
+                f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+        if (hi2 == 0) stat[rw * 64 + col] = mx, stat[rw * 64 + 32 + col] = sum;
+      }
+      lds_barrier();
+      if (ks == 0) {
+        const float m1 = stat[rw * 64 + col], top = fmaxf(mx, m1), at = top == -INFINITY ? 0.f : top;
+        const float mine = exp2_fast(mx - at), other = exp2_fast(m1 - at);
+        mx = top;
+        sum = sum * mine + stat[rw * 64 + 32 + col] * other;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 y = buf[((rw * DB + d) * 4 + j) * kWave + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][4 * j + e] = o[d][4 * j + e] * mine + y[e] * other;
+          }
+      }
+      lds_barrier();
+    }
+    if (ks != 0) continue;
     if (kt0 == 0 && kt1 == q.key_tiles) {
       if (r < rows) {
         const float inv = 1.f / sum;
@@ -684,16 +849,15 @@ __global__ __launch_bounds__(W * kWave, 2) void many_rows_kernel(KvCache c, KvAt
       }
     } else {
       float* to = part(c, blockIdx.x, kt0 == 0, part_floats(M, D));
-      if (hi2 == 0) to[wave * 32 + col] = mx, to[M + wave * 32 + col] = sum;
+      if (hi2 == 0) to[rw * 32 + col] = mx, to[M + rw * 32 + col] = sum;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          reinterpret_cast<f32x4*>(to + 2 * M)[((wave * DB + d) * 4 + j) * kWave + lane] =
+          reinterpret_cast<f32x4*>(to + 2 * M)[((rw * DB + d) * 4 + j) * kWave + lane] =
               f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, lo + q.key_tiles - 1)};
+      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, last)};
     }
-    lo += split ? kt1 - kt0 : 1;
   }
 }
 
@@ -748,16 +912,18 @@ hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D, int W>
+template <int D, int RW, int KS>
 hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
-  constexpr int M = 32 * W;
+  constexpr int M = 32 * RW, Threads = RW * KS * kWave;
   // row tiles of all sequences, at most
   const int64_t segments = (int64_t(a.T) * (a.q_heads / c.kv_heads) / M + c.seqs) * c.kv_heads;
-  if (segments >= (int64_t(1) << 31) / (W * kWave)) return hipErrorInvalidValue;
-  const int split = segments < 2 * kManyShares;
-  many_rows_kernel<D, W><<<split ? kManyShares : int(segments), W * kWave, 0, s>>>(c, a, kManyShares, split);
+  if (segments >= (int64_t(1) << 32) / Threads) return hipErrorInvalidValue;
+  // workgroups that the chip holds at once
+  constexpr int kFit = Threads == 512 ? kManyShares : 2 * kManyShares;
+  const int split = KS > 1 || segments < 2 * kFit;
+  many_rows_kernel<D, RW, KS><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW>(a.q_heads / c.kv_heads));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
-  combine_kernel<1, D><<<dim3(kManyShares, M * D / 4 / 256), 256, 0, s>>>(c, a, M, 1);
+  combine_kernel<1, D><<<dim3(kFit, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, M, 1);
   return hipGetLastError();
 }
 
@@ -765,7 +931,11 @@ template <int DT, int D>
 hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
   const int64_t rows = int64_t(a.max_new) * (a.q_heads / c.kv_heads);
   if constexpr (DT == 1 && D <= 128) {
-    if (rows > 64) return many_rows<D, 8>(c, a, s);
+    const bool fits = !a.parent || a.max_new <= 512 || a.q_heads > c.kv_heads;
+    if (fits && rows > 128) return many_rows<D, 8, 1>(c, a, s);
+    if (fits && rows > 64) return many_rows<D, 4, 1>(c, a, s);
+    if (fits && rows > 32) return many_rows<D, 2, 2>(c, a, s);
+    if (fits && rows > 16) return many_rows<D, 1, 2>(c, a, s);
   }
   constexpr int kMost = DT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);
   if constexpr (kMost >= 4)
@@ -785,9 +955,8 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
 }  // namespace
 
 int64_t kv_attention_work_bytes(const KvCache& c) {
-  // two parts of a share: 64 rows for each of the few-row shares, 256 for each of the many-row shares
-  const int64_t few = kShares * part_floats(64, c.head_dim), many = kManyShares * part_floats(256, c.head_dim);
-  return round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * (many > few ? many : few);
+  // two parts of a share: at most 128 rows in each of kShares, or 256 in each of half as many
+  return round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * kShares * part_floats(128, c.head_dim);
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, hipStream_t s) {
