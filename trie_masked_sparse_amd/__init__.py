@@ -461,28 +461,32 @@ def debug_set_live(st, s: int, edge: int, value: int, stream=None):
 # --------------------------------------------------------------------------- paged key/value cache
 
 def _sized(t, dtype, numel: int, name: str):
-    """Data pointer of a contiguous GPU tensor of at least numel values."""
-    p = _dev(t, dtype, name)
+    """Address of a contiguous GPU tensor of at least numel values."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _dev(t, dtype, name)  # says what is wrong, or takes a subclass of Tensor
     if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} values, {numel} are needed")
-    return p
+    return t.data_ptr()
 
 
 def _token_rows(t, dtype, dim: int, name: str):
-    """(pointer, row stride in elements) of a GPU tensor [T][heads][dim] whose
-    tokens are contiguous (a slice of a wider projection may hold them)."""
+    """(address, tokens, heads, row stride in elements) of a GPU tensor
+    [T][heads][dim] whose tokens are contiguous (a slice of a wider projection
+    may hold them)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3 or t.shape[2] != dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"{name} must be [T][heads][{dim}]")
-    if t.shape[0] == 0:  # no tokens: strides say nothing
-        return None, t.shape[1] * dim
-    s = t.stride()
-    if s[2] != 1 or (s[1] != dim and t.shape[1] > 1):
+    T, heads, _ = shape
+    if T == 0:  # no tokens: strides say nothing
+        return None, 0, heads, heads * dim
+    row, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * dim)
+    return t.data_ptr(), T, heads, row if T > 1 else max(row, heads * dim)
 
 
 class PagedCache:
@@ -504,6 +508,7 @@ class PagedCache:
             raise ValueError("table must be [seqs][max_pages]")
         self.layers, self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = kv.shape
         self.seqs, self.max_pages = table.shape
+        self.dtype = kv.dtype
         for name, t, n in (("length", length, self.seqs), ("held", held, self.seqs), ("status", status, self.seqs),
                            ("refs", refs, self.pages)):
             if t.numel() != n:
@@ -520,7 +525,8 @@ class PagedCache:
         need = C.c_int64()
         _check(lib().tms_kv_work_bytes(C.byref(d), C.byref(need)), "PagedCache")
         self.work = torch.empty(need.value, dtype=torch.uint8, device=kv.device)
-        self._made_on = torch.cuda.current_stream(kv.device).cuda_stream
+        self._index = kv.device.index
+        self._made_on = torch._C._cuda_getCurrentRawStream(self._index)
         d.work, d.work_bytes = self.work.data_ptr(), need.value
         self.d = d
         self.ref = C.byref(d)
@@ -544,12 +550,13 @@ class PagedCache:
 def _kv_stream(cache: PagedCache, stream):
     """The stream of a call; the work memory is told of streams other than the
     one it was allocated on, so that it is not handed on while they use it."""
-    s = torch.cuda.current_stream(cache.kv.device) if stream is None else stream
-    if not isinstance(s, torch.cuda.Stream):
-        s = torch.cuda.ExternalStream(int(s), device=cache.kv.device)
-    if s.cuda_stream != cache._made_on:
-        cache.work.record_stream(s)
-    return s.cuda_stream
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(cache._index)
+    else:
+        s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if s != cache._made_on:
+        cache.work.record_stream(torch.cuda.ExternalStream(s, device=cache.kv.device))
+    return s
 
 
 def _raise_kv_errors(cache: PagedCache, stream, where: str):
@@ -585,16 +592,15 @@ def kv_write(cache: PagedCache, layer: int, k, v, start, q=None, q_out=None, q_w
     """Norm, rotation and cache rows of the packed new tokens (tms_kv_write).
     k, v, q: [T][heads][head_dim], the tokens' rows any multiple of 16 bytes
     apart; start: int32 [seqs+1].  Asynchronous: PagedCache.status() reports."""
-    dt, D, T = cache.kv.dtype, cache.head_dim, k.shape[0]
-    kp, ldk = _token_rows(k, dt, D, "k")
-    vp, ldv = _token_rows(v, dt, D, "v")
-    if k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads or v.shape[0] != T:
+    dt, D, hkv = cache.dtype, cache.head_dim, cache.kv_heads
+    kp, T, hk, ldk = _token_rows(k, dt, D, "k")
+    vp, Tv, hv, ldv = _token_rows(v, dt, D, "v")
+    if hk != hkv or hv != hkv or Tv != T:
         raise ValueError("k and v must be [T][kv_heads][head_dim]")
     qp, ldq, hq, qo = None, 0, 0, None
     if q is not None:
-        qp, ldq = _token_rows(q, dt, D, "q")
-        hq = q.shape[1]
-        if q.shape[0] != T:
+        qp, Tq, hq, ldq = _token_rows(q, dt, D, "q")
+        if Tq != T:
             raise ValueError("q must have the tokens of k")
         if q_out is None:
             raise ValueError("q needs q_out")
@@ -606,7 +612,7 @@ def kv_write(cache: PagedCache, layer: int, k, v, start, q=None, q_out=None, q_w
                               kp, ldk, vp, ldv, None if q_weight is None else _sized(q_weight, dt, D, "q_weight"),
                               None if k_weight is None else _sized(k_weight, dt, D, "k_weight"), eps,
                               _sized(pos, torch.int32, T, "pos") if n_freq else None,
-                              _dev(inv_freq, torch.float32, "inv_freq") if n_freq else None, n_freq, int(interleaved),
+                              _sized(inv_freq, torch.float32, n_freq, "inv_freq") if n_freq else None, n_freq, int(interleaved),
                               _kv_stream(cache, stream)), "kv_write")
 
 
@@ -616,9 +622,8 @@ def kv_attention(cache: PagedCache, layer: int, q, start, out, scale: float | No
     parent (int32 [T]) makes them a tree of drafts, without it they are causal.
     q, out: [T][q_heads][head_dim]; scale: head_dim ** -0.5 by default;
     max_new: the most tokens of a sequence (T if not given).  Asynchronous."""
-    dt, D = cache.kv.dtype, cache.head_dim
-    qp, ldq = _token_rows(q, dt, D, "q")
-    T, hq = q.shape[0], q.shape[1]
+    dt, D = cache.dtype, cache.head_dim
+    qp, T, hq, ldq = _token_rows(q, dt, D, "q")
     _check(lib().tms_kv_attention(cache.ref, layer, qp, ldq, hq, _sized(start, torch.int32, cache.seqs + 1, "start"), T,
                                   T if max_new is None else max_new,
                                   None if parent is None else _sized(parent, torch.int32, T, "parent"),
@@ -637,7 +642,7 @@ def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = T
             raise ValueError("keep must be [seqs][stride]")
         stride = keep.shape[1]
     _check(lib().tms_kv_commit(cache.ref, _sized(n_keep, torch.int32, cache.seqs, "n_keep"),
-                               _dev(keep, torch.int32, "keep"), stride, _kv_stream(cache, stream)), "kv_commit")
+                               None if keep is None else _sized(keep, torch.int32, 1, "keep"), stride, _kv_stream(cache, stream)), "kv_commit")
     if check:
         _raise_kv_errors(cache, stream, "kv_commit")
 

@@ -10,6 +10,8 @@
 // contiguous piece is up to page_tokens * head_dim elements.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv_cache.h"
 #include "tms.h"
 
@@ -17,6 +19,7 @@ namespace tms {
 namespace {
 
 constexpr int kWave = 64;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct ForkRec {
   int32_t length, pages, status, changed;
@@ -42,12 +45,10 @@ __device__ inline CopyRec* copy_recs(const KvCache& c) {
 
 __device__ inline bool page_ok(const KvCache& c, int32_t p) { return p >= 0 && p < c.pages; }
 
-// Fork, first half: what every changed sequence becomes, read from the state
-// before the call and staged in work (a reordering may replace a sequence
-// that others are forked from); the references of the new rows are counted.
-__global__ __launch_bounds__(256) void fork_stage_kernel(KvCache c, const int32_t* __restrict__ src) {
-  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  if (s >= c.seqs) return;
+// Fork, first half, by one wavefront: what sequence s becomes, read from the
+// state before the call and staged in work (a reordering may replace a sequence
+// that others are forked from); the references of the new row are counted.
+__device__ inline void fork_stage(const KvCache& c, const int32_t* src, int s, int lane) {
   const int from = src[s];
   ForkRec r{0, 0, TMS_OK, from != s};
   if (from < -1 || from >= c.seqs) r = ForkRec{0, 0, TMS_ERR_INVALID_ARG, -1};
@@ -64,10 +65,8 @@ __global__ __launch_bounds__(256) void fork_stage_kernel(KvCache c, const int32_
   if (lane == 0) fork_recs(c)[s] = r;
 }
 
-// Fork, second half: the old rows' references go, the staged rows come in.
-__global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
-  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  if (s >= c.seqs) return;
+// Fork, second half: the old row's references go, the staged row comes in.
+__device__ inline void fork_apply(const KvCache& c, int s, int lane) {
   const ForkRec r = fork_recs(c)[s];
   if (r.changed < 0 && lane == 0) c.status[s] = r.status;
   if (r.changed != 1) return;
@@ -85,6 +84,25 @@ __global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
     c.held[s] = r.pages;
     c.status[s] = r.status;
   }
+}
+
+__global__ __launch_bounds__(256) void fork_stage_kernel(KvCache c, const int32_t* __restrict__ src) {
+  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+  if (s < c.seqs) fork_stage(c, src, s, threadIdx.x % kWave);
+}
+__global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
+  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+  if (s < c.seqs) fork_apply(c, s, threadIdx.x % kWave);
+}
+// Both halves in one workgroup: a wavefront for each of at most kSmall
+// sequences saves the second launch.
+constexpr int kSmall = 16;
+__global__ __launch_bounds__(kSmall * kWave) void fork_small_kernel(KvCache c, const int32_t* __restrict__ src) {
+  const int s = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  if (s < c.seqs) fork_stage(c, src, s, lane);
+  __threadfence_block();
+  __syncthreads();
+  if (s < c.seqs) fork_apply(c, s, lane);
 }
 
 constexpr int kPlan = 1024;  // threads of the one workgroup that hands out pages
@@ -113,15 +131,40 @@ __device__ inline int block_before(int v, int* total) {
   return before + incl - v;
 }
 
+// 16-byte words that a thread has in flight.
+constexpr int kFlight = 8;
+
+// The committed rows of a page that reserve replaced by a copy: one piece, the
+// keys or values of a head in a layer (contiguous), by `threads` threads.
+__device__ inline void copy_piece(const KvCache& c, const CopyRec& r, int piece, int elem_bytes, int tid, int threads) {
+  const int parts = 2 * c.kv_heads, words = c.page_tokens * c.head_dim * elem_bytes / 16;
+  const int64_t page0 = int64_t(piece / parts) * c.pages;
+  const u32x4* __restrict__ from = static_cast<const u32x4*>(c.kv) + ((page0 + r.from) * parts + piece % parts) * words;
+  u32x4* __restrict__ to = static_cast<u32x4*>(c.kv) + ((page0 + r.to) * parts + piece % parts) * words;
+  const int n = r.rows * c.head_dim * elem_bytes / 16;
+  for (int base = tid; base < n; base += threads * (kFlight / 2)) {
+    u32x4 v[kFlight / 2];
+#pragma unroll
+    for (int u = 0; u < kFlight / 2; ++u)
+      if (base + u * threads < n) v[u] = from[base + u * threads];
+#pragma unroll
+    for (int u = 0; u < kFlight / 2; ++u)
+      if (base + u * threads < n) to[base + u * threads] = v[u];
+  }
+}
+
 // Reserve: demands of all sequences, their prefix sums, the lowest free pages,
 // and who gets which.  The order is fixed (sequences ascending, pages
-// ascending), so the tables do not depend on timing.
-__global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const int32_t* __restrict__ n_new) {
-  __shared__ int begin[4096];   // first page of the sequence's share of the free list
-  __shared__ int want[4096];    // pages it holds afterwards; -1: left as it is
+// ascending), so the tables do not depend on timing.  pieces: where the copies
+// are few, this workgroup makes them too (the pieces of a page; 0: it does not).
+__global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const int32_t* __restrict__ n_new, int elem_bytes,
+                                                             int pieces) {
+  constexpr int kSplit = 1 << 30;  // of want: the last page is copied (pages of a sequence stay below 2^28)
+  __shared__ int begin[4096 + 1];  // first page of the sequence's share of the free list
+  __shared__ int want[4096];       // pages it holds afterwards; -1: left as it is
   const int tid = threadIdx.x;
   CopyRec* recs = copy_recs(c);
-  int64_t need = 0;  // all demands (at most pages + 1 counts: more never fits)
+  int64_t need = 0;
   for (int base = 0; base < c.seqs; base += kPlan) {
     const int s = base + tid;
     int more = 0, w = -1;
@@ -139,28 +182,26 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
           const int32_t p = c.table[int64_t(s) * c.max_pages + last];
           if (page_ok(c, p) && c.refs[p] > 1) {
             rec = CopyRec{p, -1, fill, 0};
+            w |= kSplit;
             ++more;
           }
         }
       }
     }
-    // a demand above the whole pool never fits; cutting it there keeps the
-    // sums below 2^31 (4096 * (pages + 1) could pass it: sum in 64 bits)
-    int total;
+    // a demand above the whole pool never fits: cut there, 4096 of them are
+    // summed in two 16-bit halves without passing 2^31
     more = min(more, c.pages + 1);
-    const int hi = more >> 16, lo = more & 0xffff;
-    int total_hi;
-    const int before_lo = block_before(lo, &total), before_hi = block_before(hi, &total_hi);
+    int total_lo, total_hi;
+    const int before_lo = block_before(more & 0xffff, &total_lo), before_hi = block_before(more >> 16, &total_hi);
     const int64_t at = need + (int64_t(before_hi) << 16) + before_lo;
     if (s < c.seqs) {
       begin[s] = static_cast<int>(min(at, int64_t(c.pages) + 1));
       want[s] = w;
-      // the demand itself rides in rec.pad until the pages are known
-      rec.pad = more;
       recs[s] = rec;
     }
-    need += (int64_t(total_hi) << 16) + total;
+    need += (int64_t(total_hi) << 16) + total_lo;
   }
+  if (tid == 0) begin[c.seqs] = static_cast<int>(min(need, int64_t(c.pages) + 1));
   // the lowest free pages, as many as are asked for at most
   const int most = static_cast<int>(min(need, int64_t(c.pages)));
   int32_t* list = free_list(c);
@@ -184,53 +225,53 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
     found += total;
   }
   found = min(found, most);
+  __threadfence_block();
   __syncthreads();
-  const int lane = tid % kWave;
-  for (int s = tid / kWave; s < c.seqs; s += kPlan / kWave) {
-    if (want[s] < 0) continue;
-    CopyRec rec = recs[s];
-    const int at = begin[s], more = rec.pad;
-    rec.pad = 0;
-    if (more > 0 && int64_t(at) + more > found) {
-      if (lane == 0) {
-        c.status[s] = TMS_ERR_OOM;
-        recs[s] = CopyRec{-1, -1, 0, 0};
-      }
-      continue;
-    }
+  // every page to its sequence: the last one that begins at or before it (a
+  // demand that does not fit ends past the pages found)
+  for (int k = tid; k < found; k += kPlan) {
+    int s = 0;
+    for (int step = 2048; step > 0; step /= 2)
+      if (s + step < c.seqs && begin[s + step] <= k) s += step;
+    const int i = k - begin[s], split = want[s] >= kSplit;
+    if (begin[s + 1] > found) continue;
+    const int32_t p = list[k];
     int32_t* row = c.table + int64_t(s) * c.max_pages;
-    const int held = min(c.held[s], c.max_pages), split = rec.rows > 0;
-    for (int j = held + lane; j < want[s]; j += kWave) {
-      const int32_t p = list[at + split + j - held];
-      row[j] = p;
-      c.refs[p] = 1;
+    c.refs[p] = 1;
+    if (split && i == 0) {
+      const int32_t old = recs[s].from;
+      recs[s].to = p;
+      row[c.length[s] >> c.page_shift] = p;
+      atomicSub(&c.refs[old], 1);
+    } else {
+      row[min(c.held[s], c.max_pages) + i - split] = p;
     }
-    if (lane == 0) {
-      if (split) {
-        rec.to = list[at];
-        row[c.length[s] >> c.page_shift] = rec.to;
-        c.refs[rec.to] = 1;
-        atomicSub(&c.refs[rec.from], 1);
-      }
-      recs[s] = rec;
-      c.held[s] = want[s];
+  }
+  __threadfence_block();
+  __syncthreads();
+  for (int s = tid; s < c.seqs; s += kPlan) {
+    if (want[s] < 0) continue;
+    if (begin[s + 1] > found && begin[s + 1] > begin[s]) {
+      c.status[s] = TMS_ERR_OOM;
+      recs[s].rows = 0;
+    } else {
+      c.held[s] = want[s] & (kSplit - 1);
+    }
+  }
+  if (pieces) {
+    __threadfence_block();
+    __syncthreads();
+    for (int i = tid / kWave; i < c.seqs * pieces; i += kPlan / kWave) {
+      const CopyRec r = recs[i / pieces];
+      if (r.rows > 0) copy_piece(c, r, i % pieces, elem_bytes, tid % kWave, kWave);
     }
   }
 }
 
-// The committed rows of every page that reserve replaced by a copy.  One
-// workgroup for the keys or values of one head in one layer.
 __global__ __launch_bounds__(256) void copy_pages_kernel(KvCache c, int elem_bytes) {
   const int parts = 2 * c.kv_heads;
-  const int s = blockIdx.x / parts, part = blockIdx.x % parts, layer = blockIdx.y;
-  const CopyRec r = copy_recs(c)[s];
-  if (r.rows <= 0) return;
-  const int64_t piece = int64_t(c.page_tokens) * c.head_dim * elem_bytes / 16;  // 16-byte words
-  const int64_t page0 = (int64_t(layer) * c.pages) * parts;
-  const uint4* from = static_cast<const uint4*>(c.kv) + (page0 + int64_t(r.from) * parts + part) * piece;
-  uint4* to = static_cast<uint4*>(c.kv) + (page0 + int64_t(r.to) * parts + part) * piece;
-  const int n = r.rows * c.head_dim * elem_bytes / 16;
-  for (int i = threadIdx.x; i < n; i += 256) to[i] = from[i];
+  const CopyRec r = copy_recs(c)[blockIdx.x / parts];
+  if (r.rows > 0) copy_piece(c, r, blockIdx.y * parts + blockIdx.x % parts, elem_bytes, threadIdx.x, 256);
 }
 
 // Whether entry i of a sequence's keep list is out of order or past the rows
@@ -240,16 +281,17 @@ __device__ inline bool keep_bad(const KvCache& c, int s, const int32_t* keep, in
   return k <= prev || int64_t(c.length[s]) + k >= int64_t(min(c.held[s], c.max_pages)) << c.page_shift;
 }
 
-// Accepted rows moved together, in place.  An ascending list never moves a row
-// upwards, so a chunk of rows may be written once every row of the chunk has
-// been read: later chunks read only rows at or past their own targets.
-constexpr int kMove = 8;  // 16-byte words in flight for each thread
+// Accepted rows of sequence s moved together, in place, in `pieces` of its
+// (layer, keys or values of a head) pieces from p0 on, by one workgroup.  An
+// ascending list never moves a row upwards, so the rows of a chunk may be
+// written once all of them have been read: later chunks read only rows at or
+// past their own targets.
+constexpr int kRows = 512;  // rows of a chunk at most
 
-__global__ __launch_bounds__(256) void move_rows_kernel(KvCache c, const int32_t* __restrict__ n_keep,
-                                                        const int32_t* __restrict__ keep_all, int keep_stride,
-                                                        int elem_bytes) {
-  const int parts = 2 * c.kv_heads;
-  const int s = blockIdx.x / parts, part = blockIdx.x % parts, layer = blockIdx.y;
+__device__ inline void move_rows(const KvCache& c, const int32_t* n_keep, const int32_t* keep_all, int keep_stride,
+                                 int elem_bytes, int s, int p0, int pieces) {
+  __shared__ int32_t from_page[kRows], from_slot[kRows], to_page[kRows], to_slot[kRows];
+  __shared__ int count;
   const int n = n_keep[s];
   if (n <= 0 || n > keep_stride || c.status[s] != TMS_OK) return;
   const int32_t* keep = keep_all + int64_t(s) * keep_stride;
@@ -261,43 +303,64 @@ __global__ __launch_bounds__(256) void move_rows_kernel(KvCache c, const int32_t
   bad = __syncthreads_or(bad);
   moves = __syncthreads_or(moves);
   if (bad || !moves) return;
+  const int parts = 2 * c.kv_heads, p1 = min(p0 + pieces, c.layers * parts);
   const int words = c.head_dim * elem_bytes / 16, shift = __builtin_ctz(words), len = c.length[s];  // words: 8 .. 64
   const int32_t* row = c.table + int64_t(s) * c.max_pages;
-  uint4* kv = static_cast<uint4*>(c.kv);
-  auto at = [&](int r, int w) -> int64_t {
-    const int32_t p = row[r >> c.page_shift];
-    if (!page_ok(c, p)) return -1;
-    return (((int64_t(layer) * c.pages + p) * parts + part) * c.page_tokens + (r & (c.page_tokens - 1))) * words + w;
+  u32x4* kv = static_cast<u32x4*>(c.kv);
+  auto place = [&](int piece, int page, int slot, int w) {
+    return (((int64_t(piece / parts) * c.pages + page) * parts + piece % parts) * c.page_tokens + slot) * words + w;
   };
-  for (int64_t base = 0; base < int64_t(n) << shift; base += 256 * kMove) {
-    uint4 v[kMove];
-    int64_t to[kMove];
-#pragma unroll
-    for (int u = 0; u < kMove; ++u) {
-      const int64_t i = base + u * 256 + threadIdx.x;
-      const int j = static_cast<int>(i >> shift), w = static_cast<int>(i) & (words - 1);
-      to[u] = -1;
-      if (j < n && keep[j] != j) {
-        const int64_t from = at(len + keep[j], w);
-        to[u] = at(len + j, w);
-        if (from < 0) to[u] = -1;
-        if (to[u] >= 0) v[u] = kv[from];
+  const int most = min(kRows, (256 * kFlight) >> shift);  // a chunk of one piece is in flight at once
+  for (int j0 = 0; j0 < n; j0 += most) {
+    // the chunk's rows that move, packed in their order
+    __syncthreads();
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const int in = min(most, n - j0);
+    for (int base = 0; base < in; base += 256) {  // `in` is at most 512: two turns
+      const int j = j0 + base + threadIdx.x, k = base + static_cast<int>(threadIdx.x) < in ? keep[j] : 0;
+      int32_t fp = -1, tp = -1;
+      if (base + static_cast<int>(threadIdx.x) < in && k != j) {
+        fp = row[(len + k) >> c.page_shift], tp = row[(len + j) >> c.page_shift];
+        if (!page_ok(c, fp) || !page_ok(c, tp)) fp = -1;
+      }
+      if (fp >= 0) {
+        const int at = atomicAdd(&count, 1);  // any order: a chunk is read whole before it is written
+        from_page[at] = fp, to_page[at] = tp;
+        from_slot[at] = (len + k) & (c.page_tokens - 1), to_slot[at] = (len + j) & (c.page_tokens - 1);
       }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // every row of the chunk is in registers
     __syncthreads();
+    const int rows = count;
+    if (rows == 0) continue;
+    const int per = rows << shift, group = max(1, 256 * kFlight / per);  // words of a piece, pieces in flight
+    for (int p = p0; p < p1; p += group) {
+      const int total = min(group, p1 - p) * per;  // at most 256 * kFlight
+      u32x4 v[kFlight];
+      int64_t to[kFlight];
 #pragma unroll
-    for (int u = 0; u < kMove; ++u)
-      if (to[u] >= 0) kv[to[u]] = v[u];
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = u * 256 + threadIdx.x;
+        to[u] = -1;
+        if (i < total) {
+          const int piece = p + i / per, at = i % per >> shift, w = i & (words - 1);
+          v[u] = kv[place(piece, from_page[at], from_slot[at], w)];
+          to[u] = place(piece, to_page[at], to_slot[at], w);
+        }
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // every row in flight is in registers
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u)
+        if (to[u] >= 0) kv[to[u]] = v[u];
+    }
   }
 }
 
-// Lengths after a commit, and the pages past them given back.  One wavefront
-// for each sequence.
-__global__ __launch_bounds__(256) void commit_kernel(KvCache c, const int32_t* __restrict__ n_keep,
-                                                     const int32_t* __restrict__ keep_all, int keep_stride) {
-  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  if (s >= c.seqs) return;
+// Length of sequence s after a commit, and the pages past it given back, by one
+// wavefront.
+__device__ inline void commit_sequence(const KvCache& c, const int32_t* n_keep, const int32_t* keep_all, int keep_stride,
+                                       int s, int lane) {
   const int n = n_keep[s];
   if (n < 0 || c.status[s] != TMS_OK) return;
   const int len = c.length[s], held = min(c.held[s], c.max_pages);
@@ -324,6 +387,26 @@ __global__ __launch_bounds__(256) void commit_kernel(KvCache c, const int32_t* _
   }
 }
 
+__global__ __launch_bounds__(256) void commit_kernel(KvCache c, const int32_t* __restrict__ n_keep,
+                                                     const int32_t* __restrict__ keep_all, int keep_stride) {
+  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+  if (s < c.seqs) commit_sequence(c, n_keep, keep_all, keep_stride, s, threadIdx.x % kWave);
+}
+
+__global__ __launch_bounds__(256) void move_rows_kernel(KvCache c, const int32_t* __restrict__ n_keep,
+                                                        const int32_t* __restrict__ keep, int keep_stride, int elem_bytes,
+                                                        int pieces) {
+  move_rows(c, n_keep, keep, keep_stride, elem_bytes, blockIdx.x, blockIdx.y * pieces, pieces);
+}
+// Where one workgroup moves all pieces of a sequence it does the rest too.
+__global__ __launch_bounds__(256) void move_commit_kernel(KvCache c, const int32_t* __restrict__ n_keep,
+                                                          const int32_t* __restrict__ keep, int keep_stride,
+                                                          int elem_bytes) {
+  move_rows(c, n_keep, keep, keep_stride, elem_bytes, blockIdx.x, 0, c.layers * 2 * c.kv_heads);
+  __syncthreads();
+  if (threadIdx.x < kWave) commit_sequence(c, n_keep, keep, keep_stride, blockIdx.x, threadIdx.x);
+}
+
 int waves_grid(int seqs) { return (seqs + 3) / 4; }
 int elem_bytes(const KvCache& c) { return c.dtype == TMS_F32 ? 4 : 2; }
 
@@ -336,6 +419,10 @@ int64_t kv_page_work_bytes(const KvCache& c) {
 }
 
 hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
+  if (c.seqs <= kSmall) {
+    fork_small_kernel<<<1, kSmall * kWave, 0, s>>>(c, src);
+    return hipGetLastError();
+  }
   fork_stage_kernel<<<waves_grid(c.seqs), 256, 0, s>>>(c, src);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   fork_apply_kernel<<<waves_grid(c.seqs), 256, 0, s>>>(c);
@@ -343,8 +430,11 @@ hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
 }
 
 hipError_t launch_kv_reserve(const KvCache& c, const int32_t* n_new, hipStream_t s) {
-  reserve_plan_kernel<<<1, kPlan, 0, s>>>(c, n_new);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  // up to 64 pieces to copy: four for each wavefront of the plan's workgroup
+  const int64_t pieces = int64_t(c.layers) * 2 * c.kv_heads;
+  const bool here = c.seqs * pieces <= 64;
+  reserve_plan_kernel<<<1, kPlan, 0, s>>>(c, n_new, elem_bytes(c), here ? static_cast<int>(pieces) : 0);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || here) return e;
   copy_pages_kernel<<<dim3(c.seqs * 2 * c.kv_heads, c.layers), 256, 0, s>>>(c, elem_bytes(c));
   return hipGetLastError();
 }
@@ -352,8 +442,15 @@ hipError_t launch_kv_reserve(const KvCache& c, const int32_t* n_new, hipStream_t
 hipError_t launch_kv_commit(const KvCache& c, const int32_t* n_keep, const int32_t* keep, int32_t keep_stride,
                             hipStream_t s) {
   if (keep) {
-    move_rows_kernel<<<dim3(c.seqs * 2 * c.kv_heads, c.layers), 256, 0, s>>>(c, n_keep, keep, keep_stride,
-                                                                             elem_bytes(c));
+    // about 2048 workgroups in all; one for a sequence where it has few pieces
+    const int64_t pieces = int64_t(c.layers) * 2 * c.kv_heads, wgs = std::max<int64_t>(1, 2048 / c.seqs);
+    if (pieces <= 16 || wgs == 1) {
+      move_commit_kernel<<<c.seqs, 256, 0, s>>>(c, n_keep, keep, keep_stride, elem_bytes(c));
+      return hipGetLastError();
+    }
+    const int each = static_cast<int>(std::max((pieces + wgs - 1) / wgs, (pieces + 65534) / 65535));
+    move_rows_kernel<<<dim3(c.seqs, (pieces + each - 1) / each), 256, 0, s>>>(c, n_keep, keep, keep_stride,
+                                                                             elem_bytes(c), each);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   commit_kernel<<<waves_grid(c.seqs), 256, 0, s>>>(c, n_keep, keep, keep_stride);

@@ -10,6 +10,8 @@
 // pos * inv_freq passes 10^5 and its fp32 product would be off by 10^-2.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv_cache.h"
 #include "tms.h"
 
@@ -62,6 +64,10 @@ __device__ inline int sequence_of(const int32_t* __restrict__ start, int seqs, i
   return block * kWave + __popcll(__ballot(fine <= seqs && start[min(fine, seqs)] <= t));
 }
 
+// Heads that a wavefront has in flight: 64 / LPR of them to a load, kBatch
+// loads before the first is used.
+constexpr int kBatch = 4;
+
 // DT: 0 fp32, 1 bf16.  LPR: lanes of a head.  One wavefront: token t, the
 // groups of 64 / LPR heads g0, g0 + step, ...; heads are the queries', then
 // the keys', then the values'.
@@ -71,59 +77,73 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
   const int lane = threadIdx.x % kWave, wave = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
   const int t = __builtin_amdgcn_readfirstlane(wave / waves_per_token);
   if (t >= a.T) return;
+  const int g0 = __builtin_amdgcn_readfirstlane(wave % waves_per_token) * RPW, step = waves_per_token * RPW;
   const int col = lane % LPR, sub = lane / LPR;  // chunk of the head, head of the group
-  const int heads = a.q_heads + 2 * c.kv_heads;
-  const uint4* q = static_cast<const uint4*>(a.q) + int64_t(t) * (a.ldq / N);
-  const uint4* k = static_cast<const uint4*>(a.k) + int64_t(t) * (a.ldk / N);
-  const uint4* v = static_cast<const uint4*>(a.v) + int64_t(t) * (a.ldv / N);
-  // the angles of the lane's values
-  const int first = col * N, turned = 2 * a.n_freq;
-  const bool rotate = first < turned;
+  const int heads = a.q_heads + 2 * c.kv_heads, k_end = a.q_heads + c.kv_heads;
+  const uint4* q = static_cast<const uint4*>(a.q) + int64_t(t) * (a.ldq / N) + col;
+  const uint4* k = static_cast<const uint4*>(a.k) + int64_t(t) * (a.ldk / N) + col;
+  const uint4* v = static_cast<const uint4*>(a.v) + int64_t(t) * (a.ldv / N) + col;
+  auto load = [&](int h) {
+    return h < a.q_heads ? q[h * LPR] : h < k_end ? k[(h - a.q_heads) * LPR] : v[(min(h, heads - 1) - k_end) * LPR];
+  };
+  uint4 raw[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u)
+    if (g0 + u * step < heads) raw[u] = load(g0 + u * step + sub);
+  // the angles of the lane's values: bf16 results leave no trace of the
+  // hardware's sine (about 2^-20 off); fp32 ones take the library's
+  const int first = col * N;
+  const bool rotate = first < 2 * a.n_freq;
   float cs[N], sn[N];
-  if (rotate) {
+  if (rotate && g0 < k_end) {
     const double pos = a.pos[t] * 0.15915494309189533577;  // in turns for a frequency of 1
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = first + i, f = a.interleaved ? e / 2 : (e < a.n_freq ? e : e - a.n_freq);
       double turn = pos * static_cast<double>(a.inv_freq[f]);
       turn -= rint(turn);
-      const float r = 2.f * static_cast<float>(turn);
-      sincospif(r, &sn[i], &cs[i]);
+      if constexpr (DT == 1) {
+        sn[i] = __builtin_amdgcn_sinf(static_cast<float>(turn));
+        cs[i] = __builtin_amdgcn_cosf(static_cast<float>(turn));
+      } else {
+        sincospif(2.f * static_cast<float>(turn), &sn[i], &cs[i]);
+      }
     }
   }
-  const int s = sequence_of(a.start, c.seqs, t, lane);
   // where the token's keys and values go; null where they may not
   uint4* kv_row = nullptr;
-  if (s < c.seqs && c.status[s] == TMS_OK) {
-    const int64_t row = int64_t(c.length[s]) + (t - a.start[s]);
-    if (t >= a.start[s] && row < int64_t(min(c.held[s], c.max_pages)) << c.page_shift) {
-      const int32_t p = c.table[int64_t(s) * c.max_pages + (row >> c.page_shift)];
-      if (p >= 0 && p < c.pages)
-        kv_row = static_cast<uint4*>(c.kv) +
-                 ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR;
+  const int groups = (heads - g0 + step - 1) / step, last = g0 + (groups - 1) * step + RPW - 1;
+  if (last >= a.q_heads) {
+    const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.start, c.seqs, t, lane));
+    if (s < c.seqs && c.status[s] == TMS_OK) {
+      const int64_t row = int64_t(c.length[s]) + (t - a.start[s]);
+      if (t >= a.start[s] && row < int64_t(min(c.held[s], c.max_pages)) << c.page_shift) {
+        const int32_t p = c.table[int64_t(s) * c.max_pages + (row >> c.page_shift)];
+        if (p >= 0 && p < c.pages)
+          kv_row = static_cast<uint4*>(c.kv) +
+                   ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR +
+                   col;
+      }
+      if (!kv_row && lane == 0) c.status[s] = TMS_ERR_INVALID_ARG;
     }
-    if (!kv_row && lane == 0) c.status[s] = TMS_ERR_INVALID_ARG;
   }
-  for (int g = (wave % waves_per_token) * RPW; g < heads; g += waves_per_token * RPW) {
-    const int h = g + sub;
-    const bool is_q = h < a.q_heads, is_k = !is_q && h < a.q_heads + c.kv_heads;
-    if (h >= heads) continue;  // whole heads: the lanes that exchange values leave together
-    const int kh = h - a.q_heads, vh = kh - c.kv_heads;
-    uint4 raw = is_q ? q[h * LPR + col] : is_k ? k[kh * LPR + col] : v[vh * LPR + col];
-    const void* weight = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
-    if (is_q || is_k) {
+  auto finish = [&](int h, uint4 r) {
+    if (h >= heads) return;  // whole heads: the lanes that exchange values leave together
+    const bool is_q = h < a.q_heads;
+    if (h < k_end) {
+      const void* weight = is_q ? a.q_weight : a.k_weight;
       float x[N];
-      Chunk<DT>::unpack(raw, x);
+      Chunk<DT>::unpack(r, x);
       if (weight) {
         float ss = 0.f, w[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int d = 1; d < LPR; d *= 2) ss += __shfl_xor(ss, d);
-        const float r = 1.f / sqrtf(ss / D + a.eps);
+        const float inv = 1.f / sqrtf(ss / D + a.eps);
         Chunk<DT>::unpack(static_cast<const uint4*>(weight)[col], w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = x[i] * r * w[i];
+        for (int i = 0; i < N; ++i) x[i] = x[i] * inv * w[i];
       }
       if (a.n_freq) {
         if (a.interleaved) {
@@ -145,14 +165,19 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
           }
         }
       }
-      raw = Chunk<DT>::pack(x);
+      r = Chunk<DT>::pack(x);
     }
-    if (is_q) {
-      static_cast<uint4*>(a.q_out)[(int64_t(t) * a.q_heads + h) * LPR + col] = raw;
-    } else if (kv_row) {
-      const int part = is_k ? kh : c.kv_heads + vh;
-      kv_row[int64_t(part) * c.page_tokens * LPR + col] = raw;
-    }
+    if (is_q) static_cast<uint4*>(a.q_out)[(int64_t(t) * a.q_heads + h) * LPR + col] = r;
+    else if (kv_row) kv_row[int64_t(h - a.q_heads) * c.page_tokens * LPR] = r;  // keys, then values of a page
+  };
+  for (int g = g0; g < heads; g += kBatch * step) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (g + u * step < heads) finish(g + u * step + sub, raw[u]);
+    if (g + kBatch * step >= heads) break;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (g + (kBatch + u) * step < heads) raw[u] = load(g + (kBatch + u) * step + sub);
   }
 }
 
@@ -160,12 +185,14 @@ template <int DT>
 hipError_t launch(const KvCache& c, const KvWrite& a, hipStream_t s) {
   const int lpr = c.head_dim / Chunk<DT>::N, rpw = kWave / lpr;
   const int groups = (a.q_heads + 2 * c.kv_heads + rpw - 1) / rpw;
-  int per = 1;
-  while (per < groups && int64_t(a.T) * per < 4096) per *= 2;
+  // all loads of a wavefront at once; more wavefronts while they do not fill
+  // the chip (4096: four on a SIMD)
+  int64_t per = (groups + kBatch - 1) / kBatch;
+  if (per * a.T < 4096) per = std::min<int64_t>(groups, (4096 + a.T - 1) / a.T);
   const int64_t grid = (int64_t(a.T) * per + 3) / 4;
   if (grid > (int64_t(1) << 24) - 1) return hipErrorInvalidValue;
   auto run = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(c, a, per);
+    kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(c, a, static_cast<int>(per));
     return hipGetLastError();
   };
   switch (lpr) {
