@@ -414,7 +414,7 @@ typedef struct {
   int32_t* held;    /* dev [seqs]: pages held (reserved ones included) */
   int32_t* refs;    /* dev [pages]: reference counts */
   int32_t* status;  /* dev [seqs]: tms_status */
-  void* work;       /* dev, 256-byte aligned: at least tms_kv_work_bytes */
+  void* work;       /* dev, 256-byte aligned: at least tms_kv_work_bytes, zeroed before the first call */
   int64_t work_bytes;
   int32_t dtype;    /* tms_dtype of kv, queries, outputs and norm weights */
   int32_t layers, pages, kv_heads, page_tokens, head_dim, seqs, max_pages;

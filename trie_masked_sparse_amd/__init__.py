@@ -524,7 +524,7 @@ class PagedCache:
                          self.max_pages)
         need = C.c_int64()
         _check(lib().tms_kv_work_bytes(C.byref(d), C.byref(need)), "PagedCache")
-        self.work = torch.empty(need.value, dtype=torch.uint8, device=kv.device)
+        self.work = torch.zeros(need.value, dtype=torch.uint8, device=kv.device)
         self._index = kv.device.index
         self._made_on = torch._C._cuda_getCurrentRawStream(self._index)
         d.work, d.work_bytes = self.work.data_ptr(), need.value

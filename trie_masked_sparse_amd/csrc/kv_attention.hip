@@ -103,8 +103,9 @@ __device__ inline void store4(void* out, int64_t i, f32x4 x) {
 // sequence; its keys are cut into tiles.  All tiles in the order (sequence,
 // key head, row tile, key tile) are dealt to the workgroups in equal
 // contiguous shares, so ragged batches and long contexts balance by
-// themselves; a segment that does not lie in one share is joined by
-// combine_kernel.
+// themselves; the parts of a segment that does not lie in one share are joined
+// by the last of its workgroups (few rows) or by combine_kernel (many rows,
+// whose parts are too large for one workgroup).
 struct Seq {
   int begin, n, len, rows_tiles, key_tiles;  // tokens, committed rows; key_tiles 1 where bad
   bool bad;                                  // the outputs are NaN
@@ -145,7 +146,9 @@ struct Join {
   int32_t s, h, rt, last;  // last: the last workgroup that holds a part (-1: nothing to join)
 };
 
-// Work memory: Join [shares], then for every share two parts (its first and
+// Work memory: a count of the parts that have arrived for every share in which
+// a segment starts (zero between calls), Join [shares], then for every share
+// two parts (its first and
 // its last segment) of kRows rows: maximum and sum of every row, then the
 // unnormalised outputs in the lanes' order.
 __host__ __device__ inline int64_t round256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -153,10 +156,14 @@ __host__ __device__ inline int64_t part_floats(int rows, int dim) { return int64
 
 constexpr int kShares = 512;  // few rows: two workgroups for each compute unit
 constexpr int kManyShares = 256;
+static_assert(kShares * 4 <= kWorkCounts, "a counter for each share");
 
-__device__ inline Join* joins(const KvCache& c) { return static_cast<Join*>(c.work); }
+__device__ inline uint32_t* arrived(const KvCache& c) { return static_cast<uint32_t*>(c.work); }
+__device__ inline Join* joins(const KvCache& c) {
+  return reinterpret_cast<Join*>(static_cast<char*>(c.work) + kWorkCounts);
+}
 __device__ inline float* part(const KvCache& c, int share, int which, int64_t floats) {
-  return reinterpret_cast<float*>(static_cast<char*>(c.work) + round256(kShares * int64_t(sizeof(Join)))) +
+  return reinterpret_cast<float*>(static_cast<char*>(c.work) + kWorkCounts + round256(kShares * int64_t(sizeof(Join)))) +
          (2 * int64_t(share) + which) * floats;
 }
 
@@ -169,21 +176,25 @@ __device__ inline int share_of(int64_t total, int shares, int64_t tile) {
 }
 
 // The share [*lo, *hi) of this workgroup among all units, the sequence *s that
-// it starts in and that sequence's first unit *base: a prefix sum over the
-// sequences (*shares is cut so that a share has at least `least` units).
+// it starts in (*q) and that sequence's first unit *base: a prefix sum over the
+// sequences (shares is cut so that a share has at least `least` units).
 // Returns whether there is work.
 template <int M, int KW, int W>
-__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, int& shares, int least, int64_t* lo,
-                                int64_t* hi, int* s_out, int64_t* base_out, int64_t* total_out) {
+__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, bool mark, int& shares, int least, int64_t* lo,
+                                int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
   __shared__ int64_t scan[W];
   __shared__ int found_s;
   __shared__ int64_t found_base;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
   const int each = (c.seqs + W * kWave - 1) / (W * kWave);
+  Seq q{};  // the thread's last sequence; its only one for up to 256 of them
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
-    if (s < c.seqs) mine += units_of(c, sequence(c, a, s, M, KW), split);
+    if (s < c.seqs) {
+      q = sequence(c, a, s, M, KW);
+      mine += units_of(c, q, split);
+    }
   }
   int64_t incl = mine;
 #pragma unroll
@@ -201,23 +212,24 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   total = uniform(total);
   if (split) shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / least)));
   const int me = blockIdx.x;
-  if (split && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
+  if (mark && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
   *lo = split ? share_begin(total, shares, me) : me;
   *hi = split ? share_begin(total, shares, me + 1) : me + 1;
   if (total == 0 || (split ? me >= shares : me >= total)) return false;
   if (*lo >= before && *lo < before + mine) {
     int64_t base = before;
-    for (int s = tid * each;; ++s) {
-      const int64_t t = units_of(c, sequence(c, a, s, M, KW), split);
-      if (*lo < base + t) {
-        found_s = s;
-        found_base = base;
-        break;
-      }
+    int s = tid * each;
+    for (; each > 1; ++s) {
+      q = sequence(c, a, s, M, KW);
+      const int64_t t = units_of(c, q, split);
+      if (*lo < base + t) break;
       base += t;
     }
+    found_s = s;
+    found_base = base;
   }
   __syncthreads();
+  *q_out = uniform(sequence(c, a, __builtin_amdgcn_readfirstlane(found_s), M, KW));
   *s_out = __builtin_amdgcn_readfirstlane(found_s);
   *base_out = uniform(found_base);
   *total_out = total;
@@ -251,6 +263,89 @@ __device__ inline uint32_t sees(const KvAttention& a, const Seq& q, int tok, int
   if (a.parent) return seen[max(tok - tok0, 0) * words + ((first - (q.len & ~31)) >> 5)];
   const int count = q.len + tok + 1 - first;
   return count >= 32 ? ~0u : (1u << max(count, 0)) - 1;
+}
+
+// Row and column of value 4 i of a part's outputs: the lanes' order of the
+// 16-row (few rows) and of the 32-row products (many rows).
+template <int D>
+__device__ inline void part_place(int i, int wide, int* row, int* column) {
+  const int lane = i % kWave, block = i / kWave;
+  if (wide) {
+    *row = block / (D / 8) * 32 + lane % 32;
+    *column = block % (D / 8) * 8 + lane / 32 * 4;
+  } else {
+    *row = block / (D / 16) * 16 + lane % 16;
+    *column = block % (D / 16) * 16 + lane / 16 * 4;
+  }
+}
+
+// Parts that another workgroup of the same launch reads go past the XCD's L2,
+// by device-scope accesses: a fence would write back and drop all of it
+// (measured: 64 ragged sequences 53 -> 188 us).
+template <bool Shared, typename T>
+__device__ inline T part_load(const T* p) {
+  if constexpr (!Shared) {
+    return *p;
+  } else if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __hip_atomic_load(reinterpret_cast<const uint32_t*>(p), __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT));
+  } else {
+    uint64_t w[2];
+    for (int i = 0; i < 2; ++i)
+      w[i] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    T x;
+    __builtin_memcpy(&x, w, 16);
+    return x;
+  }
+}
+__device__ inline void part_store(float* p, float x) {
+  __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void part_store(f32x4* p, f32x4 x) {
+  uint64_t w[2];
+  __builtin_memcpy(w, &x, 16);
+  for (int i = 0; i < 2; ++i)
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Values 4 i .. 4 i + 3 of the output of a segment of M rows, joined from its
+// parts in the shares first .. j.last, in that order.
+template <int DT, int D, bool Shared>
+__device__ inline void join_parts(const KvCache& c, const KvAttention& a, const Join& j, int first, int M, int wide, int i) {
+  const int group = a.q_heads / c.kv_heads, begin = a.start[j.s], rows = (a.start[j.s + 1] - begin) * group;
+  int row, column;
+  part_place<D>(i, wide, &row, &column);
+  const int r = j.rt * M + row;
+  if (row >= M || r >= rows) return;
+  const int64_t floats = part_floats(M, D);
+  f32x4 x{0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, l = 0.f;
+  constexpr int kParts = 8;  // in flight
+  for (int w = first; w <= j.last; w += kParts) {
+    float t[kParts], k[kParts];
+    f32x4 y[kParts];
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {  // past the last one: the last one again, with no weight
+      const float* p = part(c, min(w + u, j.last), w + u == first, floats);
+      t[u] = part_load<Shared>(p + row), k[u] = part_load<Shared>(p + M + row);
+      y[u] = part_load<Shared>(reinterpret_cast<const f32x4*>(p + 2 * M) + i);
+      if (w + u > j.last) t[u] = -INFINITY;
+    }
+    float next = top;
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) next = fmaxf(next, t[u]);
+    const float at = next == -INFINITY ? 0.f : next, old = exp2_fast(top - at);
+    top = next;
+    l *= old, x *= old;
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+      const float now = exp2_fast(t[u] - at);
+      l += k[u] * now;
+      x += y[u] * now;
+    }
+  }
+  const int64_t at = (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + column;
+  store4<DT>(a.out, at, x * (1.f / l));
 }
 
 // ------------------------------------------------- few rows: token, drafts --
@@ -290,6 +385,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   constexpr int kLds = kWaves * kVWords > kWaves * M * D / 4 ? kWaves * kVWords : kWaves * M * D / 4;
   __shared__ u32x4 lds[kLds];
   __shared__ float stat[kWaves][2][M];
+  __shared__ uint32_t arrivals;
   __shared__ uint32_t seen[M * kTreeWords];
   __shared__ int32_t par[kTree];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
@@ -301,9 +397,9 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
 
   int64_t lo, hi, base, total;
   int s;
-  if (!my_share<M, KW, kWaves>(c, a, true, shares, kWaves, &lo, &hi, &s, &base, &total)) return;
+  Seq q;
+  if (!my_share<M, KW, kWaves>(c, a, true, false, shares, kWaves, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
-  Seq q = uniform(sequence(c, a, s, M, KW));
 
   while (lo < hi) {
     while (lo >= base + units_of(c, q, true)) {
@@ -501,7 +597,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         weight[w] = exp2_fast(stat[w][0][m * 16 + col] - at);
         l += weight[w] * stat[w][1][m * 16 + col];
       }
-      if (!whole && wave == 0 && g == 0) to[m * 16 + col] = top, to[M + m * 16 + col] = l;
+      if (!whole && wave == 0 && g == 0) part_store(to + m * 16 + col, top), part_store(to + M + m * 16 + col, l);
       const int r = rt * M + m * 16 + col;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
@@ -510,7 +606,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) x += buf[((w * MT + m) * DB + d) * kWave + lane] * weight[w];
         if (!whole) {
-          reinterpret_cast<f32x4*>(to + 2 * M)[(m * DB + d) * kWave + lane] = x;
+          part_store(reinterpret_cast<f32x4*>(to + 2 * M) + (m * DB + d) * kWave + lane, x);
         } else if (r < rows) {
           if (q.bad) x = f32x4{NAN, NAN, NAN, NAN}, l = 1.f;
           const int64_t at_out = (int64_t(q.begin + r / group) * a.q_heads + h * group + r % group) * D + 16 * d + 4 * g;
@@ -518,8 +614,23 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         }
       }
     }
-    if (kt0 == 0 && !whole && tid == 0)
-      joins(c)[me] = Join{s, h, rt, share_of(total, shares, last)};
+    if (!whole) {
+      // the last share to arrive joins the parts, in their order: every share
+      // from the one with the segment's first tile to the one with its last
+      // has a part
+      const int first = share_of(total, shares, last - q.key_tiles + 1), end_share = share_of(total, shares, last);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the part is written
+      __syncthreads();
+      if (tid == 0) {
+        arrivals = atomicAdd(&arrived(c)[first], 1u);
+        if (arrivals == uint32_t(end_share - first)) arrived(c)[first] = 0;
+      }
+      __syncthreads();
+      if (arrivals == uint32_t(end_share - first)) {
+        for (int i = tid; i < M * D / 4; i += kBlock)
+          join_parts<DT, D, true>(c, a, Join{s, h, rt, end_share}, first, M, 0, i);
+      }
+    }
     __syncthreads();
   }
 }
@@ -572,8 +683,8 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
 
   int64_t lo, hi, base, total;
   int s;
-  if (!my_share<M, KT, W>(c, a, split, shares, 1, &lo, &hi, &s, &base, &total)) return;
-  Seq q = uniform(sequence(c, a, s, M, KT));
+  Seq q;
+  if (!my_share<M, KT, W>(c, a, split, split, shares, 1, &lo, &hi, &s, &q, &base, &total)) return;
   while (lo < hi) {
     while (lo >= base + units_of(c, q, split)) {
       base += units_of(c, q, split);
@@ -861,54 +972,17 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
   }
 }
 
-// Row and column of value 4 i of a part's outputs: the lanes' order of the
-// 16-row (few rows) and of the 32-row products (many rows).
-template <int D>
-__device__ inline void part_place(int i, int wide, int* row, int* column) {
-  const int lane = i % kWave, block = i / kWave;
-  if (wide) {
-    *row = block / (D / 8) * 32 + lane % 32;
-    *column = block % (D / 8) * 8 + lane / 32 * 4;
-  } else {
-    *row = block / (D / 16) * 16 + lane % 16;
-    *column = block % (D / 16) * 16 + lane / 16 * 4;
-  }
-}
-
 // Joins the parts of a segment that starts in share blockIdx.x and ends in a
 // later one; a thread takes 4 values of a row.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, int M, int wide) {
+template <int D>
+__global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, int M) {
   const Join j = joins(c)[blockIdx.x];
-  if (j.last < 0) return;
-  const int group = a.q_heads / c.kv_heads, begin = a.start[j.s], rows = (a.start[j.s + 1] - begin) * group;
-  const int i = blockIdx.y * 256 + threadIdx.x;
-  int row, column;
-  part_place<D>(i, wide, &row, &column);
-  const int r = j.rt * M + row;
-  if (row >= M || r >= rows) return;
-  const int64_t floats = part_floats(M, D);
-  f32x4 x{0.f, 0.f, 0.f, 0.f};
-  float top = -INFINITY, l = 0.f;
-  for (int w = blockIdx.x; w <= j.last; ++w) {
-    const float* p = part(c, w, w == static_cast<int>(blockIdx.x), floats);
-    const float t = p[row], k = p[M + row];
-    const f32x4 y = reinterpret_cast<const f32x4*>(p + 2 * M)[i];
-    const float next = fmaxf(top, t), at = next == -INFINITY ? 0.f : next;
-    const float old = exp2_fast(top - at), now = exp2_fast(t - at);
-    top = next;
-    l = l * old + k * now;
-    x = x * old + y * now;
-  }
-  const int64_t at = (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + column;
-  store4<DT>(a.out, at, x * (1.f / l));
+  if (j.last >= 0) join_parts<1, D, false>(c, a, j, blockIdx.x, M, 1, blockIdx.y * 256 + threadIdx.x);
 }
 
 template <int DT, int D, int MT>
 hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   few_rows_kernel<DT, D, MT><<<kShares, kBlock, 0, s>>>(c, a, kShares);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  combine_kernel<DT, D><<<dim3(kShares, (16 * MT * D / 4 + 255) / 256), 256, 0, s>>>(c, a, 16 * MT, 0);
   return hipGetLastError();
 }
 
@@ -923,7 +997,7 @@ hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   const int split = KS > 1 || segments < 2 * kFit;
   many_rows_kernel<D, RW, KS><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW>(a.q_heads / c.kv_heads));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
-  combine_kernel<1, D><<<dim3(kFit, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, M, 1);
+  combine_kernel<D><<<dim3(kFit, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, M);
   return hipGetLastError();
 }
 
@@ -956,7 +1030,7 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
 
 int64_t kv_attention_work_bytes(const KvCache& c) {
   // two parts of a share: at most 128 rows in each of kShares, or 256 in each of half as many
-  return round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * kShares * part_floats(128, c.head_dim);
+  return kWorkCounts + round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * kShares * part_floats(128, c.head_dim);
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, hipStream_t s) {

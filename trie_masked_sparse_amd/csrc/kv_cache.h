@@ -14,12 +14,14 @@ struct KvCache {
   int32_t dtype, layers, pages, kv_heads, page_tokens, page_shift, head_dim, seqs, max_pages;
 };
 
-// Layout of KvCache::work.  The page operations' scratch and the attention's
-// partial results are never live at once (every call leaves nothing behind),
-// so they share the same bytes.
+// Layout of KvCache::work.  Its first kWorkCounts bytes are counters, zero
+// between calls.  The page operations' scratch and the attention's partial
+// results behind them are never live at once (every call leaves nothing
+// behind), so they share the same bytes.
 //   fork:    int32 table rows [seqs][max_pages], then {length, pages, status, changed} [seqs]
 //   reserve: int32 free pages [pages], then {from, to, rows, 0} [seqs]
 //   attention: see kv_attention.hip
+constexpr int64_t kWorkCounts = 2048;
 int64_t kv_page_work_bytes(const KvCache& c);
 int64_t kv_attention_work_bytes(const KvCache& c);
 

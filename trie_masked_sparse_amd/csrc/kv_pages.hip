@@ -34,13 +34,14 @@ __device__ inline int pages_of(const KvCache& c, int64_t rows) {
   return static_cast<int>((rows + c.page_tokens - 1) >> c.page_shift);
 }
 
-__device__ inline int32_t* fork_rows(const KvCache& c) { return static_cast<int32_t*>(c.work); }
+__device__ inline char* scratch(const KvCache& c) { return static_cast<char*>(c.work) + kWorkCounts; }
+__device__ inline int32_t* fork_rows(const KvCache& c) { return reinterpret_cast<int32_t*>(scratch(c)); }
 __device__ inline ForkRec* fork_recs(const KvCache& c) {
-  return reinterpret_cast<ForkRec*>(static_cast<char*>(c.work) + round256(4ll * c.seqs * c.max_pages));
+  return reinterpret_cast<ForkRec*>(scratch(c) + round256(4ll * c.seqs * c.max_pages));
 }
-__device__ inline int32_t* free_list(const KvCache& c) { return static_cast<int32_t*>(c.work); }
+__device__ inline int32_t* free_list(const KvCache& c) { return reinterpret_cast<int32_t*>(scratch(c)); }
 __device__ inline CopyRec* copy_recs(const KvCache& c) {
-  return reinterpret_cast<CopyRec*>(static_cast<char*>(c.work) + round256(4ll * c.pages));
+  return reinterpret_cast<CopyRec*>(scratch(c) + round256(4ll * c.pages));
 }
 
 __device__ inline bool page_ok(const KvCache& c, int32_t p) { return p >= 0 && p < c.pages; }
@@ -415,7 +416,7 @@ int elem_bytes(const KvCache& c) { return c.dtype == TMS_F32 ? 4 : 2; }
 int64_t kv_page_work_bytes(const KvCache& c) {
   const int64_t fork = round256(4ll * c.seqs * c.max_pages) + int64_t(sizeof(ForkRec)) * c.seqs;
   const int64_t reserve = round256(4ll * c.pages) + int64_t(sizeof(CopyRec)) * c.seqs;
-  return round256(fork > reserve ? fork : reserve);
+  return kWorkCounts + round256(fork > reserve ? fork : reserve);
 }
 
 hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
