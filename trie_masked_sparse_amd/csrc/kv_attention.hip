@@ -183,7 +183,7 @@ template <int M, int KW, int W>
 __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, bool mark, int& shares, int least, int64_t* lo,
                                 int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
   __shared__ int64_t scan[W];
-  __shared__ int found_s;
+  __shared__ int found[7];
   __shared__ int64_t found_base;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
@@ -225,12 +225,15 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
       if (*lo < base + t) break;
       base += t;
     }
-    found_s = s;
+    const int words[7] = {s, q.begin, q.n, q.len, q.rows_tiles, q.key_tiles, q.bad};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) found[i] = words[i];
     found_base = base;
   }
   __syncthreads();
-  *q_out = uniform(sequence(c, a, __builtin_amdgcn_readfirstlane(found_s), M, KW));
-  *s_out = __builtin_amdgcn_readfirstlane(found_s);
+  *s_out = uniform(found[0]);
+  *q_out = Seq{uniform(found[1]), uniform(found[2]), uniform(found[3]), uniform(found[4]), uniform(found[5]),
+               uniform(found[6]) != 0};
   *base_out = uniform(found_base);
   *total_out = total;
   return true;
@@ -325,11 +328,13 @@ __device__ inline void join_parts(const KvCache& c, const KvAttention& a, const 
     float t[kParts], k[kParts];
     f32x4 y[kParts];
 #pragma unroll
-    for (int u = 0; u < kParts; ++u) {  // past the last one: the last one again, with no weight
-      const float* p = part(c, min(w + u, j.last), w + u == first, floats);
-      t[u] = part_load<Shared>(p + row), k[u] = part_load<Shared>(p + M + row);
-      y[u] = part_load<Shared>(reinterpret_cast<const f32x4*>(p + 2 * M) + i);
-      if (w + u > j.last) t[u] = -INFINITY;
+    for (int u = 0; u < kParts; ++u) {
+      t[u] = -INFINITY, k[u] = 0.f, y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (w + u <= j.last) {
+        const float* p = part(c, w + u, w + u == first, floats);
+        t[u] = part_load<Shared>(p + row), k[u] = part_load<Shared>(p + M + row);
+        y[u] = part_load<Shared>(reinterpret_cast<const f32x4*>(p + 2 * M) + i);
+      }
     }
     float next = top;
 #pragma unroll
@@ -415,7 +420,26 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     const int h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
     const int rows = q.n * group;  // of the sequence and key head
     const int all = q.len + q.n;
-    // the queries: B operand, row = lane % 16
+    const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // tokens of the tile
+    const int limit = a.parent ? all : q.len + tok1 + 1;                             // keys that any row sees
+    const int end = q.bad ? 0 : min(kt1, (limit + KW - 1) / KW);
+    const int32_t* table = c.table + int64_t(s) * c.max_pages;
+    const int64_t head_stride = int64_t(c.page_tokens) * T::Chunks;  // 16-byte words
+    const u32x4* kv = static_cast<const u32x4*>(c.kv) +
+                      (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
+    const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
+    // keys past the end are read from the last row: in bounds, and masked
+    auto page_at = [&](int kt, int i) {
+      const int32_t p = table[min(kt * KW + i * 16 + col, all - 1) >> c.page_shift];
+      return max(0, min(p, c.pages - 1));
+    };
+    int kt = kt0 + wave;
+    int32_t pg[T::Sub];
+    if (kt < end)
+#pragma unroll
+      for (int i = 0; i < T::Sub; ++i) pg[i] = page_at(kt, i);
+    // the queries: B operand, row = lane % 16; asked for before the first keys,
+    // used after them
     u32x4 qr[MT][L];
     int tok[MT];
 #pragma unroll
@@ -425,36 +449,10 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       const int64_t at = int64_t(q.begin + max(tok[m], 0)) * a.ldq + int64_t(h * group + (r < rows ? r % group : 0)) * D;
       const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + at * (DT == 0 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        qr[m][i] = (p[i * 4 + g] ^ flip) & on;
-      }
+      for (int i = 0; i < L; ++i) qr[m][i] = p[i * 4 + g];
     }
-    const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // tokens of the tile
-    const int limit = a.parent ? all : q.len + tok1 + 1;                             // keys that any row sees
-    const int end = min(kt1, (limit + KW - 1) / KW);
-    if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen, kTreeWords);
-
-    f32x4 o[MT][DB];
-    float mx[MT], sum[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mx[m] = -INFINITY, sum[m] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    const int32_t* table = c.table + int64_t(s) * c.max_pages;
-    const int64_t head_stride = int64_t(c.page_tokens) * T::Chunks;  // 16-byte words
-    const u32x4* kv = static_cast<const u32x4*>(c.kv) +
-                      (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
-    const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
     u32x4* vt = lds + wave * kVWords;
     u32x4 kr[T::Sub][L], vr[T::Sub][L];
-    // keys past the end are read from the last row: in bounds, and masked
-    auto page_at = [&](int kt, int i) {
-      const int32_t p = table[min(kt * KW + i * 16 + col, all - 1) >> c.page_shift];
-      return max(0, min(p, c.pages - 1));
-    };
-    int32_t pg[T::Sub];
     auto load = [&](int kt) {
 #pragma unroll
       for (int i = 0; i < T::Sub; ++i) {
@@ -466,15 +464,23 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         for (int j = 0; j < L; ++j) vr[i][j] = p[v_off + j * 4];
       }
     };
-    int kt = kt0 + wave;
-    if (!q.bad && kt < end) {
-#pragma unroll
-      for (int i = 0; i < T::Sub; ++i) pg[i] = page_at(kt, i);
+    if (kt < end) {
       load(kt);
 #pragma unroll
       for (int i = 0; i < T::Sub; ++i) pg[i] = page_at(min(kt + kWaves, end - 1), i);
     }
-    for (; !q.bad && kt < end; kt += kWaves) {
+    if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen, kTreeWords);
+    f32x4 o[MT][DB];
+    float mx[MT], sum[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m] = -INFINITY, sum[m] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < L; ++i) qr[m][i] = (qr[m][i] ^ flip) & on;
+    }
+    for (; kt < end; kt += kWaves) {
       // V to LDS, S^T from the registers
 #pragma unroll
       for (int i = 0; i < T::Sub; ++i)
@@ -670,6 +676,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
   __shared__ u32x4 tiles[2 * Bufs * TileWords];
   __shared__ float stat[KS == 2 ? 2 * M : 1];
   __shared__ uint32_t seen[kSeen<RW>];
+  __shared__ int32_t par[RW == 8 ? kTree : M];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int rw = wave % RW, ks = wave / RW, col = lane % 32, hi2 = lane / 32;
   const bool behind = Behind && wave >= 4;
@@ -708,23 +715,25 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
     h = uniform(h), rt = uniform(rt), kt0 = uniform(kt0), kt1 = uniform(kt1);
     const int rows = q.n * group, all = q.len + q.n;
     const int r = rt * M + rw * 32 + col, tok = r < rows ? r / group : -1;
-    bf16x8 qr[KK];
+    u32x4 qr[KK];  // asked for here, used after the first copies are
     {
       const int64_t at = int64_t(q.begin + max(tok, 0)) * a.ldq + int64_t(h * group + (r < rows ? r % group : 0)) * D;
       const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + at * 2);
 #pragma unroll
-      for (int i = 0; i < KK; ++i) qr[i] = __builtin_bit_cast(bf16x8, (p[2 * i + hi2] ^ flip) & on);
+      for (int i = 0; i < KK; ++i) qr[i] = p[2 * i + hi2];
     }
     const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // of the workgroup
     const int limit = a.parent ? all : q.len + tok1 + 1;
     const int end = q.bad ? kt0 : min(kt1, (limit + KT - 1) / KT);
-    const int clear = a.parent ? q.len : q.len + min((rt * M + rw * 32) / group, q.n - 1) + 1;  // seen by all its rows
-    if (a.parent && !q.bad && end * KT > q.len)
-      walk_tree<Threads>(a, q, tok0, tok1, reinterpret_cast<int32_t*>(tiles), seen, words);
+    // keys that all rows of the wavefront see
+    const int clear = uniform(a.parent ? q.len : q.len + min((rt * M + rw * 32) / group, q.n - 1) + 1);
 
     const f32x16 zero = {};
-    f32x16 o[DB], sc[NB];
-    float mx = -INFINITY, sum = 0.f;
+    f32x16 o[DB], sc[NB], total_w;  // total_w: a row's sum of weights, in every register
+    float mx = -INFINITY;
+    const bf16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) total_w[e] = 0.f;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -787,14 +796,11 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
 #pragma unroll
     for (int d = 0; d < DB; ++d)
       v_at_lds[d] = tiles_at + (Bufs * TileWords + v_at(ks * NB * 32 + vrow, 4 * d + vch)) * 16 + vb;
-    // operands of the products: K of 32 rows from byte `from` of the K tiles on,
-    // V of 16 keys from byte `from` of the V tiles on
-    auto k_words = [&](int j, int from) __attribute__((always_inline)) {
-      return __builtin_bit_cast(bf16x8, *(lds_u32x4)(k_at_lds[j] + from));
-    };
-    auto v_words = [&](int d, int from) __attribute__((always_inline)) {
-      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(v_at_lds[d] + from));
-      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(v_at_lds[d] + from + 8 * CH * 16));
+    // operands of the products: K of 32 rows, V of 16 keys, from LDS byte `at` on
+    auto k_words = [&](int at) __attribute__((always_inline)) { return __builtin_bit_cast(bf16x8, *(lds_u32x4)(at)); };
+    auto v_words = [&](int at) __attribute__((always_inline)) {
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 8 * CH * 16));
       return __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)));
     };
     if (kt0 < end) {
@@ -809,6 +815,10 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       for (int x = -Ahead; x < 0; ++x)
 #pragma unroll
         for (int i = 0; i < 2 * P; ++i) ask(kt0 + x, i);
+      // the tree is walked while the first copies are on their way
+      if (a.parent && end * KT > q.len) walk_tree<Threads>(a, q, tok0, tok1, par, seen, words);
+#pragma unroll
+      for (int i = 0; i < KK; ++i) qr[i] = (qr[i] ^ flip) & on;
       wait_copies<2 * P * Ahead>();
       lds_barrier();
       if (behind) lds_barrier();
@@ -816,7 +826,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < KK; ++j)
-          sc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_words(j, i * 32 * CH * 16), qr[j], j ? sc[i] : zero, 0, 0, 0);
+          sc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_words(k_at_lds[j] + i * 32 * CH * 16), __builtin_bit_cast(bf16x8, qr[j]), j ? sc[i] : zero, 0, 0, 0);
       if (behind) wait_copies<2 * P * (Ahead - 1)>();  // K of tile kt0 + 1, V of tile kt0
       lds_barrier();
     }
@@ -849,7 +859,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       if (__any(top > mx + 8.f)) {
         const float next = fmaxf(mx, top), turn = next == -INFINITY ? 1.f : exp2_fast(mx - next);
         mx = next;
-        sum *= turn;
+        total_w *= turn;
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[d] *= turn;
       }
@@ -863,7 +873,6 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           w[e] = exp2_fast(fmaf(sc[j / 2][j % 2 * 8 + e], scale, -at));
-          sum += w[e];
         }
         pw[j] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
 #pragma unroll
@@ -874,7 +883,6 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       // wavefront of the SIMD has the vector units
 #pragma unroll
       for (int j = 0; j < 2 * NB; ++j) asm volatile("" : "+v"(pw[j]));
-      asm volatile("" : "+v"(sum));
       // K of tile kt + 1 and V of tile kt are there, of all wavefronts behind the barrier
       if (!behind) wait_copies<2 * P * Ahead>();
       lds_barrier();
@@ -882,11 +890,19 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       // from LDS kAhead products before their use; the order is fixed here
       // because the compiler's own puts every read next to its product
       constexpr int PV = DB * 2 * NB, QK = NB * KK;
-      const int v_from = v_buf * (TileWords * 16), k_from = k_buf * (TileWords * 16);
+      int k_now[KK], v_now[DB];
+#pragma unroll
+      for (int j = 0; j < KK; ++j) k_now[j] = k_at_lds[j] + k_buf * (TileWords * 16);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) v_now[d] = v_at_lds[d] + v_buf * (TileWords * 16);
+#pragma unroll
+      for (int j = 0; j < KK; ++j) asm volatile("" : "+v"(k_now[j]));
+#pragma unroll
+      for (int d = 0; d < DB; ++d) asm volatile("" : "+v"(v_now[d]));
       v_buf = k_buf, k_buf = k_buf + 1 == Bufs ? 0 : k_buf + 1;
       auto fetch = [&](int i) __attribute__((always_inline)) {
-        if (i < PV) return v_words(i % DB, v_from + i / DB * (16 * CH * 16));
-        return k_words((i - PV) / NB, k_from + (i - PV) % NB * (32 * CH * 16));
+        if (i < PV) return v_words(v_now[i % DB] + i / DB * (16 * CH * 16));
+        return k_words(k_now[(i - PV) / NB] + (i - PV) % NB * (32 * CH * 16));
       };
       bf16x8 f[kAhead];
 #pragma unroll
@@ -896,10 +912,11 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
         __builtin_amdgcn_sched_barrier(0);
         if (i < PV) {
           const int j = i / DB, d = i % DB;
+          if (d == 0) total_w = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, __builtin_bit_cast(bf16x8, pw[j]), total_w, 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
         } else {
           const int j = (i - PV) / NB, k = (i - PV) % NB;
-          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], qr[j], j ? sc[k] : zero, 0, 0, 0);
+          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], __builtin_bit_cast(bf16x8, qr[j]), j ? sc[k] : zero, 0, 0, 0);
         }
         if (i + kAhead < PV + QK) f[i % kAhead] = fetch(i + kAhead);
       }
@@ -912,10 +929,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       if (Behind && !behind) lds_barrier();
       lds_barrier();
     }
-    {
-      auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
-      sum = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-    }
+    float sum = total_w[0];
     if constexpr (KS == 2) {  // the two halves of the keys joined
       static_assert(KS == 1 || RW * DB * 4 * kWave <= 2 * Bufs * TileWords, "the outputs of one half fit the tiles");
       f32x4* buf = reinterpret_cast<f32x4*>(tiles);
