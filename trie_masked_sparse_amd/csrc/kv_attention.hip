@@ -105,10 +105,11 @@ __device__ inline void store4(void* out, int64_t i, f32x4 x) {
 // contiguous shares, so ragged batches and long contexts balance by
 // themselves; the parts of a segment that does not lie in one share are joined
 // by the last of its workgroups (few rows) or by combine_kernel (many rows,
-// whose parts are too large for one workgroup).
+// whose parts are too large for one workgroup).  Where there are row tiles
+// enough, a workgroup takes a whole segment instead.
 struct Seq {
   int begin, n, len, rows_tiles, key_tiles;  // tokens, committed rows; key_tiles 1 where bad
-  bool bad;                                  // the outputs are NaN
+  int bad;                                   // the outputs are NaN
 };
 
 __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, int rows, int keys) {
@@ -128,17 +129,91 @@ __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, in
 }
 
 __device__ inline Seq uniform(const Seq& q) {
-  return Seq{uniform(q.begin), uniform(q.n), uniform(q.len), uniform(q.rows_tiles), uniform(q.key_tiles), uniform(int(q.bad)) != 0};
+  return Seq{uniform(q.begin), uniform(q.n), uniform(q.len), uniform(q.rows_tiles), uniform(q.key_tiles), uniform(q.bad)};
 }
 
-// Units of work of a sequence: its key tiles and kOpen more for every segment,
-// or whole segments.  A segment's start (queries, page numbers, the first keys,
-// the join of the wavefronts) is a chain of memory latencies that a share pays
-// for each of its segments: without kOpen a share of many short contexts takes
-// several times as long as one of a long context.
+// Key tiles that row tile rt works on: all, or the ones up to its last token
+// (causal; at most one more at the end of the sequence).
+template <int M, int KT>
+__device__ inline int tiles_of(const KvAttention& a, const Seq& q, int rt, int group) {
+  if (a.parent || q.bad) return q.key_tiles;
+  return (q.len + (rt * M + M - 1) / group + KT) / KT;
+}
+
+// Units of work.  Of a segment: its key tiles and kOpen more.  A segment's start
+// (queries, page numbers, the first keys, the join of the wavefronts) is a
+// chain of memory latencies that a share pays for each of its segments:
+// without kOpen a share of many short contexts takes several times as long as
+// one of a long context.  Causal row tiles are taken in pairs, a long one and a
+// short one, whose sum is the same for all up to the rounding of two tiles.
 constexpr int kOpen = 4;
-__device__ inline int64_t units_of(const KvCache& c, const Seq& q, bool split) {
-  return int64_t(q.rows_tiles) * (split ? q.key_tiles + kOpen : 1) * c.kv_heads;
+
+template <int M, int KT>
+__device__ inline int units_each(const KvAttention& a, const Seq& q, int group, bool* pairs) {
+  *pairs = !a.parent && !q.bad && q.rows_tiles > 1;
+  if (!*pairs) return q.key_tiles + kOpen;
+  return tiles_of<M, KT>(a, q, 0, group) + tiles_of<M, KT>(a, q, q.rows_tiles - 1, group) + 2 + 2 * kOpen;
+}
+
+// Of a sequence; whole segments where they are not split.
+template <int M, int KT>
+__device__ inline int64_t units_of(const KvCache& c, const KvAttention& a, const Seq& q, bool split) {
+  if (!split) return int64_t(q.rows_tiles) * c.kv_heads;
+  bool pairs;
+  const int each = units_each<M, KT>(a, q, a.q_heads / c.kv_heads, &pairs);
+  return int64_t(pairs ? (q.rows_tiles + 1) / 2 : q.rows_tiles) * each * c.kv_heads;
+}
+
+// The segment at unit lo of sequence q (whose first unit is base), as far as
+// the share goes: key tiles kt0 .. kt1 - 1 of `tiles`; first and last are the
+// units of the segment's first and last tile.  lo moves past it.
+struct Segment {
+  int h, rt, kt0, kt1, tiles;
+  int64_t first, last;
+};
+
+template <int M, int KT>
+__device__ inline bool next_segment(const KvCache& c, const KvAttention& a, const Seq& q, bool split, int64_t base,
+                                    int64_t hi, int64_t& lo, Segment* g) {
+  if (!split) {  // heads of a row tile next to each other (each on its own XCD's cache), long rows first
+    const int off = static_cast<int>(lo - base);
+    g->h = off % c.kv_heads, g->rt = q.rows_tiles - 1 - off / c.kv_heads;
+    g->tiles = q.key_tiles, g->kt0 = 0, g->kt1 = q.key_tiles;
+    g->first = g->last = 0;
+    ++lo;
+    return true;
+  }
+  const int group = a.q_heads / c.kv_heads;
+  bool pairs;
+  const int each = units_each<M, KT>(a, q, group, &pairs);
+  const int count = pairs ? (q.rows_tiles + 1) / 2 : q.rows_tiles;  // of a head
+  const int at = static_cast<int>((lo - base) / each);
+  int u = static_cast<int>((lo - base) % each);
+  const int64_t next = lo - u + each;
+  g->h = at / count, g->rt = at % count;
+  int units = each;
+  if (pairs) {
+    const int other = g->rt;
+    g->rt = q.rows_tiles - 1 - other;
+    units = kOpen + tiles_of<M, KT>(a, q, g->rt, group);
+    if (u >= units) {  // past the long one
+      u -= units;
+      units = other < g->rt ? kOpen + tiles_of<M, KT>(a, q, other, group) : 0;
+      g->rt = other;
+      if (u >= units) {
+        lo = next;
+        return false;
+      }
+    }
+  }
+  const int end = static_cast<int>(min(int64_t(units), u + hi - lo));
+  g->tiles = units - kOpen;
+  g->last = lo + units - u - 1;
+  g->first = g->last - g->tiles + 1;
+  lo += end - u;
+  if (end <= kOpen) return false;  // the share ends before the segment's first tile
+  g->kt0 = max(u - kOpen, 0), g->kt1 = end - kOpen;
+  return true;
 }
 
 // A segment that several workgroups share, written by the one it starts in.
@@ -188,12 +263,12 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
   const int each = (c.seqs + W * kWave - 1) / (W * kWave);
-  Seq q{};  // the thread's last sequence; its only one for up to 256 of them
+  Seq q{};  // the thread's last sequence; its only one where each is 1
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
     if (s < c.seqs) {
       q = sequence(c, a, s, M, KW);
-      mine += units_of(c, q, split);
+      mine += units_of<M, KW>(c, a, q, split);
     }
   }
   int64_t incl = mine;
@@ -221,7 +296,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
     int s = tid * each;
     for (; each > 1; ++s) {
       q = sequence(c, a, s, M, KW);
-      const int64_t t = units_of(c, q, split);
+      const int64_t t = units_of<M, KW>(c, a, q, split);
       if (*lo < base + t) break;
       base += t;
     }
@@ -233,7 +308,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   __syncthreads();
   *s_out = uniform(found[0]);
   *q_out = Seq{uniform(found[1]), uniform(found[2]), uniform(found[3]), uniform(found[4]), uniform(found[5]),
-               uniform(found[6]) != 0};
+               uniform(found[6])};
   *base_out = uniform(found_base);
   *total_out = total;
   return true;
@@ -383,7 +458,7 @@ struct Tile<0, D> {                      // fp32
 // registers, V through its own part of LDS, no barrier among them; the next
 // tile's loads are in flight during the softmax and the second product.
 template <int DT, int D, int MT>
-__global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention a, int shares) {
+__global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention a, int shares, int split) {
   using T = Tile<DT, D>;
   constexpr int M = 16 * MT, KW = T::Keys, DB = D / 16, L = T::Loads;
   constexpr int kVWords = KW * T::Chunks;                  // 16-byte words of a V tile
@@ -403,21 +478,17 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KW, kWaves>(c, a, true, false, shares, kWaves, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kWaves, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
 
   while (lo < hi) {
-    while (lo >= base + units_of(c, q, true)) {
-      base += units_of(c, q, true);
+    while (lo >= base + units_of<M, KW>(c, a, q, split)) {
+      base += units_of<M, KW>(c, a, q, split);
       q = uniform(sequence(c, a, ++s, M, KW));
     }
-    const int units = q.key_tiles + kOpen, seg = static_cast<int>((lo - base) / units);
-    const int u0 = static_cast<int>((lo - base) % units), u1 = static_cast<int>(min(int64_t(units), u0 + hi - lo));
-    const int64_t last = lo + units - u0 - 1;  // unit of the segment's last tile
-    lo += u1 - u0;
-    if (u1 <= kOpen) break;  // the share ends before the segment's first tile
-    const int kt0 = max(u0 - kOpen, 0), kt1 = u1 - kOpen;
-    const int h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
+    Segment sg;
+    if (!next_segment<M, KW>(c, a, q, split, base, hi, lo, &sg)) continue;
+    const int h = sg.h, rt = sg.rt, kt0 = sg.kt0, kt1 = sg.kt1;
     const int rows = q.n * group;  // of the sequence and key head
     const int all = q.len + q.n;
     const int tok0 = rt * M / group, tok1 = min(q.n - 1, (rt * M + M - 1) / group);  // tokens of the tile
@@ -590,7 +661,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     }
     __syncthreads();
     constexpr int Q = DB / kWaves;
-    const bool whole = kt0 == 0 && kt1 == q.key_tiles;
+    const bool whole = kt0 == 0 && kt1 == sg.tiles;
     float* to = part(c, me, kt0 == 0, part_floats(M, D));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -624,7 +695,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       // the last share to arrive joins the parts, in their order: every share
       // from the one with the segment's first tile to the one with its last
       // has a part
-      const int first = share_of(total, shares, last - q.key_tiles + 1), end_share = share_of(total, shares, last);
+      const int first = share_of(total, shares, sg.first), end_share = share_of(total, shares, sg.last);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the part is written
       __syncthreads();
       if (tid == 0) {
@@ -664,7 +735,7 @@ int tree_words(int group) {
 // wavefronts, two on a SIMD, the second four run one phase behind: while one
 // wavefront of a SIMD feeds the matrix cores the other has the vector units.
 template <int D, int RW, int KS>
-__global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
+__global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
   constexpr bool Behind = W == 8;
   constexpr int KT = 64, TileWords = KT * CH;       // keys of a tile, its 16-byte words
@@ -685,34 +756,22 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, on = a.scale == 0.f ? 0u : ~0u;
   const int tiles_at = static_cast<int>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)tiles));
   // places in LDS: K is read 16 bytes of 32 rows at a time, V 32 bytes of 8
-  auto k_at = [](int r, int ch) { return r * CH + (ch ^ (r & (CH - 1))); };
-  auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << 1 & (CH - 1))); };
+  constexpr int Mask = (CH < 16 ? CH : 16) - 1;
+  auto k_at = [](int r, int ch) { return r * CH + (ch ^ (r & Mask)); };
+  auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << 1 & Mask)); };
 
   int64_t lo, hi, base, total;
   int s;
   Seq q;
   if (!my_share<M, KT, W>(c, a, split, split, shares, 1, &lo, &hi, &s, &q, &base, &total)) return;
   while (lo < hi) {
-    while (lo >= base + units_of(c, q, split)) {
-      base += units_of(c, q, split);
+    while (lo >= base + units_of<M, KT>(c, a, q, split)) {
+      base += units_of<M, KT>(c, a, q, split);
       q = uniform(sequence(c, a, ++s, M, KT));
     }
-    int h, rt, kt0 = 0, kt1 = q.key_tiles;
-    int64_t last = 0;  // unit of the segment's last tile
-    if (split) {
-      const int units = q.key_tiles + kOpen, seg = static_cast<int>((lo - base) / units);
-      const int u0 = static_cast<int>((lo - base) % units), u1 = static_cast<int>(min(int64_t(units), u0 + hi - lo));
-      last = lo + units - u0 - 1;
-      lo += u1 - u0;
-      if (u1 <= kOpen) break;  // the share ends before the segment's first tile
-      kt0 = max(u0 - kOpen, 0), kt1 = u1 - kOpen;
-      h = seg / q.rows_tiles, rt = seg % q.rows_tiles;
-    } else {  // heads of a row tile next to each other (each on its own XCD's cache), long rows first
-      const int off = static_cast<int>(lo - base);
-      h = off % c.kv_heads, rt = q.rows_tiles - 1 - off / c.kv_heads;
-      ++lo;
-    }
-    h = uniform(h), rt = uniform(rt), kt0 = uniform(kt0), kt1 = uniform(kt1);
+    Segment sg;
+    if (!next_segment<M, KT>(c, a, q, split, base, hi, lo, &sg)) continue;
+    const int h = uniform(sg.h), rt = uniform(sg.rt), kt0 = uniform(sg.kt0), kt1 = uniform(sg.kt1);
     const int rows = q.n * group, all = q.len + q.n;
     const int r = rt * M + rw * 32 + col, tok = r < rows ? r / group : -1;
     u32x4 qr[KK];  // asked for here, used after the first copies are
@@ -748,8 +807,8 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
     // k_at and v_at have them.  Rows past the last one to be used are filled
     // with that one: in bounds, and masked or never used.
     const int final_row = uniform(max(min(all, end * KT) - 1, 0));
-    const int my_row = lane / CH, k_ch = lane % CH ^ ((wave * RPI + my_row) & (CH - 1)),
-              v_ch = lane % CH ^ ((wave * RPI + my_row) << 1 & (CH - 1));
+    const int my_row = lane / CH, k_ch = lane % CH ^ ((wave * RPI + my_row) & Mask),
+              v_ch = lane % CH ^ ((wave * RPI + my_row) << 1 & Mask);
     // Step x copies K of tile x + 1 + Ahead and V of tile x + Ahead; a tile's
     // page numbers are asked for one step before its K, its addresses are kept
     // for its V.
@@ -768,7 +827,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       row_at[i] = (min(r0 + my_row, final_row) - first) * (CH * 16);
     };
     auto copy = [&](int64_t off, int ch, int step, int to, int i) __attribute__((always_inline)) {
-      copy_to_lds(from[i] + off, row_at[i] + (ch ^ (i * W * RPI * step & (CH - 1))) * 16,
+      copy_to_lds(from[i] + off, row_at[i] + (ch ^ (i * W * RPI * step & Mask)) * 16,
                   tiles_at + to * (TileWords * 16) + (i * W + wave) * (kWave * 16));
     };
     // buffers of the V tile and of the K tile of the next step
@@ -960,7 +1019,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
       lds_barrier();
     }
     if (ks != 0) continue;
-    if (kt0 == 0 && kt1 == q.key_tiles) {
+    if (kt0 == 0 && kt1 == sg.tiles) {
       if (r < rows) {
         const float inv = 1.f / sum;
         const int64_t at = (int64_t(q.begin + tok) * a.q_heads + h * group + r % group) * D + 4 * hi2;
@@ -981,7 +1040,7 @@ __global__ __launch_bounds__(RW * KS * kWave, 2) void many_rows_kernel(KvCache c
         for (int j = 0; j < 4; ++j)
           reinterpret_cast<f32x4*>(to + 2 * M)[((rw * DB + d) * 4 + j) * kWave + lane] =
               f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, last)};
+      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, sg.last)};
     }
   }
 }
@@ -994,20 +1053,29 @@ __global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, 
   if (j.last >= 0) join_parts<1, D, false>(c, a, j, blockIdx.x, M, 1, blockIdx.y * 256 + threadIdx.x);
 }
 
+// Row tiles of all sequences and key heads, at most.
+int64_t segments_of(const KvCache& c, const KvAttention& a, int rows) {
+  return (int64_t(a.T) * (a.q_heads / c.kv_heads) / rows + c.seqs) * c.kv_heads;
+}
+
 template <int DT, int D, int MT>
 hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
-  few_rows_kernel<DT, D, MT><<<kShares, kBlock, 0, s>>>(c, a, kShares);
+  const int64_t group = a.q_heads / c.kv_heads, segments = segments_of(c, a, 16 * MT);
+  if (segments >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
+  // one row tile a sequence, and drafts, are split always (contexts differ);
+  // prompts while their row tiles would not fill the chip twice
+  const int split = a.parent || a.max_new * group <= 16 * MT || segments < 2 * kShares;
+  few_rows_kernel<DT, D, MT><<<split ? kShares : int(segments), kBlock, 0, s>>>(c, a, kShares, split);
   return hipGetLastError();
 }
 
 template <int D, int RW, int KS>
 hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   constexpr int M = 32 * RW, Threads = RW * KS * kWave;
-  // row tiles of all sequences, at most
-  const int64_t segments = (int64_t(a.T) * (a.q_heads / c.kv_heads) / M + c.seqs) * c.kv_heads;
+  const int64_t segments = segments_of(c, a, M);
   if (segments >= (int64_t(1) << 32) / Threads) return hipErrorInvalidValue;
   // workgroups that the chip holds at once
-  constexpr int kFit = Threads == 512 ? kManyShares : 2 * kManyShares;
+  constexpr int kFit = Threads == 512 || D == 256 ? kManyShares : 2 * kManyShares;
   const int split = KS > 1 || segments < 2 * kFit;
   many_rows_kernel<D, RW, KS><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW>(a.q_heads / c.kv_heads));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
@@ -1017,20 +1085,26 @@ hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
 
 template <int DT, int D>
 hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
-  const int64_t rows = int64_t(a.max_new) * (a.q_heads / c.kv_heads);
-  if constexpr (DT == 1 && D <= 128) {
-    const bool fits = !a.parent || a.max_new <= 512 || a.q_heads > c.kv_heads;
-    if (fits && rows > 128) return many_rows<D, 8, 1>(c, a, s);
-    if (fits && rows > 64) return many_rows<D, 4, 1>(c, a, s);
-    if (fits && rows > 32) return many_rows<D, 2, 2>(c, a, s);
-    if (fits && rows > 16) return many_rows<D, 1, 2>(c, a, s);
+  const int64_t group = a.q_heads / c.kv_heads, rows = a.max_new * group;
+  if (rows <= 16) return few_rows<DT, D, 1>(c, a, s);
+  if constexpr (DT == 0) {
+    if constexpr (D == 256) return few_rows<DT, D, 1>(c, a, s);
+    else return few_rows<DT, D, 2>(c, a, s);
+  } else if constexpr (D == 256) {
+    if (a.parent && rows > 128) return few_rows<DT, D, 2>(c, a, s);
+    return rows > 64 ? many_rows<D, 4, 1>(c, a, s) : many_rows<D, 2, 2>(c, a, s);
+  } else {
+    if (a.parent && a.max_new > 512 && group == 1) return few_rows<DT, D, 4>(c, a, s);  // the table of drafts is too small
+    // 256 rows a workgroup have the faster loop (16 x 1000 tokens of 32 query
+    // heads 249 against 256 us, one of 512 tokens behind 30000 255 against 285),
+    // two workgroups of 128 rows overlap their starts and ends, which are most
+    // of a short prompt (64 x 300 tokens of 16 query heads 98 against 120 us,
+    // 32 x 600 117 against 137)
+    const bool short_prompts = !a.parent && a.T * group < 4096ll * c.seqs && segments_of(c, a, 256) >= 2 * kManyShares;
+    if (rows > 128 && !short_prompts) return many_rows<D, 8, 1>(c, a, s);
+    if (rows > 64) return many_rows<D, 4, 1>(c, a, s);
+    return rows > 32 ? many_rows<D, 2, 2>(c, a, s) : many_rows<D, 1, 2>(c, a, s);
   }
-  constexpr int kMost = DT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);
-  if constexpr (kMost >= 4)
-    if (rows > 32) return few_rows<DT, D, 4>(c, a, s);
-  if constexpr (kMost >= 2)
-    if (rows > 16) return few_rows<DT, D, 2>(c, a, s);
-  return few_rows<DT, D, 1>(c, a, s);
 }
 
 template <int DT>
@@ -1044,7 +1118,8 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
 
 int64_t kv_attention_work_bytes(const KvCache& c) {
   // two parts of a share: at most 128 rows in each of kShares, or 256 in each of half as many
-  return kWorkCounts + round256(kShares * int64_t(sizeof(Join))) + 2 * 4 * kShares * part_floats(128, c.head_dim);
+  return kWorkCounts + round256(kShares * int64_t(sizeof(Join))) +
+         2 * 4 * (c.head_dim == 256 ? kManyShares : kShares) * part_floats(128, c.head_dim);
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, hipStream_t s) {
