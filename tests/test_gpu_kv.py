@@ -126,6 +126,81 @@ def test_attention_scores_far_apart(dtype):
             check_attention(q, out, ks, vs, lens, new, scale, p, dtype == BF, scale)
 
 
+BATCHES = [
+    # heads of queries, of keys, head_dim, committed rows, new rows, trees; what is taken by it
+    (8, 2, 64, [100, 0, 7], [700, 333, 1], False),        # causal row tiles in pairs, an odd count of them
+    (4, 1, 128, [1000, 0], [257, 600], False),
+    (4, 2, 256, [64, 9], [400, 130], False),
+    (2, 2, 256, [0], [40], False),
+    (8, 8, 64, [3] * 20, [210] * 20, False),              # whole segments: fp32
+    (128, 16, 64, [10], [1100], False),                   # whole segments of 256 rows
+    (32, 8, 64, [0, 5] * 32, [70, 64] * 32, False),       # short prompts
+    (8, 4, 256, [0, 5] * 32, [70, 64] * 32, False),
+    (5, 5, 128, [50, 0], [20, 32], False),                # 17 .. 32 rows
+    (6, 2, 128, [50, 900], [20, 1], False),               # 33 .. 64 rows, of three heads
+    (6, 2, 64, [50, 0], [30, 42], False),                 # 65 .. 128 rows
+    (5, 5, 128, [50, 0], [20, 32], True),
+    (6, 2, 128, [50, 900], [20, 1], True),
+    (6, 2, 64, [31, 0], [30, 42], True),
+    (2, 2, 64, [33, 500], [600, 513], True),              # more drafts than one row of the table
+    (2, 2, 128, [95], [1024], True),
+    (2, 2, 128, [95], [512], True),
+    (4, 2, 64, [31, 0], [1024, 700], True),
+    (4, 2, 256, [31, 200], [80, 300], True),
+    (2, 1, 64, [9, 0, 40] * 200, [1, 2, 0] * 200, False),  # several sequences to a thread of the plan
+    (2, 1, 64, [9, 0, 40] * 400, [20, 3, 0] * 400, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(BATCHES)))
+def test_attention_of_every_kind_of_batch(dtype, case):
+    hq, hkv, D, lens, new, trees = BATCHES[case]
+    print(f"attention {dtype} {BATCHES[case][:3]} {len(new)} sequences, new <= {max(new)}, trees {trees}", flush=True)
+    rng = np.random.default_rng(300 + case)
+    cache, ks, vs = filled(rng, dtype, hkv, D, 32, lens, new)
+    q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+    parents = [tree(rng, b) for b in new] if trees else None
+    for _ in range(2):  # the counters in the work memory are zero again after a call
+        out = run_attention(cache, q, new, parents)
+        check_attention(q, out, ks, vs, lens, new, D ** -0.5, parents, dtype == BF, case)
+        assert not cache.work[:2048].any()
+
+
+def set_row(cache, s, row, which, column, value):
+    page = cache.kv.shape[4]
+    cache.kv[0, int(cache.table[s, row // page]), which, :, row % page, column] = value
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (4, 2, 128), (8, 2, 256)], ids=lambda h: "x".join(map(str, h)))
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_attention_rows_not_seen_may_hold_anything(dtype, heads, kind):
+    """Infinities and NaN in a draft's or a later token's key and value reach the
+    rows that see it, in its columns, and no others."""
+    hq, hkv, D = heads
+    for n, (lens, new) in enumerate((([50], [7]), ([3000], [8]), ([33, 40], [25, 3]), ([1000, 64], [70, 33]), ([31], [150]),
+                                     ([700, 20], [300, 5]))):
+        print(f"attention not finite {dtype} {heads} {kind} lens {lens} new {new}", flush=True)
+        rng = np.random.default_rng(400 + n)
+        cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)
+        parents = [tree(rng, b) for b in new] if kind == "tree" else None
+        for s, (a, b) in enumerate(zip(lens, new)):
+            for row, which, column, value in ((a + b // 2, 1, 3, np.inf), (a + b // 2 + 1, 1, 21, -np.inf),
+                                              (a + b - 1, 1, 5, np.nan), (a + b - 2, 0, 7, np.nan)):
+                set_row(cache, s, row, which, column, value)
+                (vs if which else ks)[s][row, :, column] = value
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+        out = run_attention(cache, q, new, parents).double().cpu().numpy()
+        qd, at = q.double().cpu().numpy(), offsets(new)
+        for s, (a, b) in enumerate(zip(lens, new)):
+            want, bound = attention(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, parents and parents[s], dtype == BF)
+            got, fine = out[at[s]:at[s + 1]], np.isfinite(want)
+            assert fine.any() and not fine.all()
+            assert (np.abs(got[fine] - want[fine]) <= bound[fine]).all(), (n, s)
+            assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (n, s)
+
+
 def test_attention_parents_that_are_not_earlier_tokens_count_as_none():
     rng = np.random.default_rng(12)
     lens, new = [20], [6]

@@ -26,6 +26,7 @@ namespace {
 constexpr int kWave = 64, kWaves = 4, kBlock = kWave * kWaves;
 constexpr int kAhead = 4;  // products of 32 rows that the reads of LDS run ahead
 constexpr int kTree = 1024, kTreeWords = kTree / 32 + 1;  // drafts of a tree; words of 32 keys they may touch
+constexpr int kMixedWords = kTreeWords + 2;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -334,6 +335,91 @@ __device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, i
   __syncthreads();
 }
 
+// New rows of a segment that some of its query rows see and others do not: keys
+// first .. first + count - 1.  A value there that is not finite would reach all
+// rows of a product, as 0 x inf or 0 x NaN.  So a segment whose outputs are not
+// all finite is worked through once more: such values are looked for, taken out
+// of the tiles in LDS, and added to the rows that see them at the end (looking
+// for them in every segment before its first tile took 4 % of a prompt's time).
+// bits: one bit a key from key (first & ~31) on, set where a row has such a
+// value (also for the copies of the last row that fill up its tile).
+struct Mixed {
+  int first, count;
+  uint32_t* bits;
+
+  __device__ uint32_t word(int at) const {  // of the keys at .. at + 31, at a multiple of 32
+    const int i = (at - (first & ~31)) >> 5;
+    return i >= 0 && i < kMixedWords ? bits[i] : 0u;
+  }
+};
+__device__ inline Mixed mixed_rows(const KvAttention& a, const Seq& q, int tok0, int tok1, uint32_t* bits) {
+  return a.parent ? Mixed{q.len, q.n, bits} : Mixed{q.len + tok0, tok1 - tok0 + 1, bits};
+}
+
+// 0, or NaN where a value is not finite.
+template <typename V, int N>
+__device__ inline float zero_or_nan(const V (&x)[N], float z = 0.f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < int(sizeof(V) / 4); ++e) z = fmaf(x[i][e], 0.f, z);
+  return z;
+}
+
+// The values of a 16-byte word that are not finite, or the ones that are; 0 in
+// the others' places.
+template <int DT>
+__device__ inline uint32_t keep_finite(uint32_t w, bool finite) {
+  if constexpr (DT == 0) return ((w & 0x7f800000u) != 0x7f800000u) == finite ? w : 0u;
+  const uint32_t low = ((w & 0x7f80u) != 0x7f80u) == finite ? 0xffffu : 0u;
+  return w & (low | (((w & 0x7f800000u) != 0x7f800000u) == finite ? 0xffff0000u : 0u));
+}
+template <int DT>
+__device__ inline u32x4 keep_finite(u32x4 w, bool finite) {
+  return u32x4{keep_finite<DT>(w[0], finite), keep_finite<DT>(w[1], finite), keep_finite<DT>(w[2], finite),
+               keep_finite<DT>(w[3], finite)};
+}
+
+// The values from column `at` (a multiple of 4) on of a V row that are not finite.
+template <int DT>
+__device__ inline f32x4 odd_values(const u32x4* row, int at) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (DT == 0 ? at : at / 2);
+  f32x4 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (DT == 0) x[e] = __uint_as_float(keep_finite<DT>(w[e], false));
+    else x[e] = __uint_as_float(e % 2 ? keep_finite<DT>(w[e / 2], false) & 0xffff0000u : keep_finite<DT>(w[e / 2], false) << 16);
+  }
+  return x;
+}
+
+// Address of the V row of a key.
+__device__ inline const u32x4* value_row(const KvCache& c, const int32_t* table, const u32x4* values, int64_t page_stride,
+                                         int ch, int row) {
+  const int page = max(0, min(table[row >> c.page_shift], c.pages - 1));
+  return values + page * page_stride + int64_t(row & (c.page_tokens - 1)) * ch;
+}
+
+// Sets m.bits; whether any is set.  Ends with a barrier.
+template <int Threads, int DT, int D>
+__device__ inline bool find_nonfinite(const KvCache& c, const int32_t* table, const u32x4* values, int64_t page_stride,
+                                      const Mixed& m) {
+  constexpr int CH = D * (DT == 0 ? 4 : 2) / 16, kFill = 63;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  for (int i = tid; i < kMixedWords; i += Threads) m.bits[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < m.count * CH; i += Threads) {
+    const int row = m.first + i / CH;
+    const u32x4 w = value_row(c, table, values, page_stride, CH, row)[i % CH], odd = keep_finite<DT>(w, false);
+    if (odd[0] | odd[1] | odd[2] | odd[3]) {
+      const int last = i / CH + 1 == m.count ? row + kFill : row;
+      for (int r = row; r <= last; ++r) atomicOr(&m.bits[(r - (m.first & ~31)) >> 5], 1u << (r & 31));
+    }
+  }
+  __syncthreads();
+  return __any(lane < kMixedWords && m.bits[min(lane, kMixedWords - 1)] != 0);
+}
+
 // Keys first .. first+31 (first a multiple of 32 in the tree's region) that
 // token tok sees, one bit each.
 __device__ inline uint32_t sees(const KvAttention& a, const Seq& q, int tok, int tok0, int first, const uint32_t* seen,
@@ -436,6 +522,7 @@ struct Tile;
 template <int D>
 struct Tile<1, D> {                      // bf16
   static constexpr int Keys = 32, Sub = 2;  // two 16-key halves
+  static constexpr uint32_t Mask = ~0u;     // of a word of 32 keys
   static constexpr int Loads = D / 32;      // 16-byte words of a key for each lane
   static constexpr int Chunks = D / 8;      // 16-byte words of a row
   // place of word c of key r in the LDS tile: the transposing read takes 2
@@ -448,6 +535,7 @@ struct Tile<1, D> {                      // bf16
 template <int D>
 struct Tile<0, D> {                      // fp32
   static constexpr int Keys = 16, Sub = 1;
+  static constexpr uint32_t Mask = 0xffffu;
   static constexpr int Loads = D / 16;
   static constexpr int Chunks = D / 4;
   static __device__ inline int at(int r, int c) { return r * Chunks + (c ^ (r & 15)); }
@@ -468,6 +556,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   __shared__ uint32_t arrivals;
   __shared__ uint32_t seen[M * kTreeWords];
   __shared__ int32_t par[kTree];
+  __shared__ uint32_t nonfinite[kMixedWords];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int col = lane % 16, g = lane / 16;
   const int group = a.q_heads / c.kv_heads;
@@ -481,7 +570,9 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kWaves, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
 
+  int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
+    const int64_t lo_here = lo;
     while (lo >= base + units_of<M, KW>(c, a, q, split)) {
       base += units_of<M, KW>(c, a, q, split);
       q = uniform(sequence(c, a, ++s, M, KW));
@@ -499,9 +590,9 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     const u32x4* kv = static_cast<const u32x4*>(c.kv) +
                       (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
     const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
-    // keys past the end are read from the last row: in bounds, and masked
+    // keys past the last one to be used are read from that one: in bounds, and masked
     auto page_at = [&](int kt, int i) {
-      const int32_t p = table[min(kt * KW + i * 16 + col, all - 1) >> c.page_shift];
+      const int32_t p = table[min(kt * KW + i * 16 + col, limit - 1) >> c.page_shift];
       return max(0, min(p, c.pages - 1));
     };
     int kt = kt0 + wave;
@@ -527,7 +618,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
     auto load = [&](int kt) {
 #pragma unroll
       for (int i = 0; i < T::Sub; ++i) {
-        const int r = min(kt * KW + i * 16 + col, all - 1);
+        const int r = min(kt * KW + i * 16 + col, limit - 1);
         const u32x4* p = kv + pg[i] * page_stride + int64_t(r & (c.page_tokens - 1)) * T::Chunks + g;
 #pragma unroll
         for (int j = 0; j < L; ++j) kr[i][j] = p[j * 4];
@@ -541,6 +632,10 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       for (int i = 0; i < T::Sub; ++i) pg[i] = page_at(min(kt + kWaves, end - 1), i);
     }
     if (a.parent && !q.bad && end * KW > q.len) walk_tree<kBlock>(a, q, tok0, tok1, par, seen, kTreeWords);
+    const Mixed mixed = mixed_rows(a, q, tok0, tok1, nonfinite);
+    bool odd = false;
+    if (again)
+      odd = find_nonfinite<kBlock, DT, D>(c, table, kv + v_off, page_stride, mixed);
     f32x4 o[MT][DB];
     float mx[MT], sum[MT];
 #pragma unroll
@@ -585,8 +680,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         const int first = kt * KW, at = first & 31;  // key and bit of the tile's first key
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          uint32_t word = sees(a, q, tok[m], tok0, first & ~31, seen, kTreeWords);
-          word >>= at + 4 * g;
+          const uint32_t word = sees(a, q, tok[m], tok0, first & ~31, seen, kTreeWords) >> (at + 4 * g);
 #pragma unroll
           for (int i = 0; i < T::Sub; ++i)
 #pragma unroll
@@ -622,6 +716,13 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
                         pack_bf16(sc[m][1][0], sc[m][1][1]), pack_bf16(sc[m][1][2], sc[m][1][3])};
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (odd) {
+        for (uint32_t word = mixed.word(kt * KW & ~31) >> (kt * KW & 31) & T::Mask; word; word &= word - 1) {
+          const int r = __builtin_ctz(word);
+          for (int i = lane; i < T::Chunks; i += kWave) vt[r * T::Chunks + i] = keep_finite<DT>(vt[r * T::Chunks + i], true);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         if constexpr (DT == 1) {
@@ -648,6 +749,16 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 
+    if (!again && mixed.count > 1 && !q.bad && end * KW > mixed.first) {
+      float z = 0.f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) z = zero_or_nan(o[m], z);
+      if (__syncthreads_or(z != z)) {
+        again = 1, lo = lo_here;
+        continue;
+      }
+    }
+    again = 0;
     // the four wavefronts' parts joined; wavefront w ends with a quarter of
     // the columns
     __syncthreads();
@@ -659,6 +770,19 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
 #pragma unroll
       for (int d = 0; d < DB; ++d) buf[((wave * MT + m) * DB + d) * kWave + lane] = o[m][d];
     }
+    if (odd)  // every wavefront for the tiles that it had
+      for (kt = kt0 + wave; kt < end; kt += kWaves)
+        for (uint32_t word = mixed.word(kt * KW & ~31) >> (kt * KW & 31) & T::Mask; word; word &= word - 1) {
+          const int row = kt * KW + __builtin_ctz(word);
+          if (row >= limit) break;
+          const u32x4* p = value_row(c, table, kv + v_off, page_stride, T::Chunks, row);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            if (sees(a, q, tok[m], tok0, row & ~31, seen, kTreeWords) >> (row & 31) & 1)
+#pragma unroll 1
+              for (int d = 0; d < DB; ++d)
+                buf[((wave * MT + m) * DB + d) * kWave + lane] += odd_values<DT>(p, 16 * d + 4 * g);
+        }
     __syncthreads();
     constexpr int Q = DB / kWaves;
     const bool whole = kt0 == 0 && kt1 == sg.tiles;
@@ -748,6 +872,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   __shared__ float stat[KS == 2 ? 2 * M : 1];
   __shared__ uint32_t seen[kSeen<RW>];
   __shared__ int32_t par[RW == 8 ? kTree : M];
+  __shared__ uint32_t nonfinite[kMixedWords];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int rw = wave % RW, ks = wave / RW, col = lane % 32, hi2 = lane / 32;
   const bool behind = Behind && wave >= 4;
@@ -764,7 +889,9 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   int s;
   Seq q;
   if (!my_share<M, KT, W>(c, a, split, split, shares, 1, &lo, &hi, &s, &q, &base, &total)) return;
+  int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
+    const int64_t lo_here = lo;
     while (lo >= base + units_of<M, KT>(c, a, q, split)) {
       base += units_of<M, KT>(c, a, q, split);
       q = uniform(sequence(c, a, ++s, M, KT));
@@ -806,7 +933,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
     // fills in the lanes' order, so the lanes take the words in the order that
     // k_at and v_at have them.  Rows past the last one to be used are filled
     // with that one: in bounds, and masked or never used.
-    const int final_row = uniform(max(min(all, end * KT) - 1, 0));
+    const int final_row = uniform(max(min(limit, end * KT) - 1, 0));
     const int my_row = lane / CH, k_ch = lane % CH ^ ((wave * RPI + my_row) & Mask),
               v_ch = lane % CH ^ ((wave * RPI + my_row) << 1 & Mask);
     // Step x copies K of tile x + 1 + Ahead and V of tile x + Ahead; a tile's
@@ -862,6 +989,8 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 8 * CH * 16));
       return __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)));
     };
+    const Mixed mixed = mixed_rows(a, q, tok0, tok1, nonfinite);
+    int odd = 0;
     if (kt0 < end) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -876,6 +1005,8 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
         for (int i = 0; i < 2 * P; ++i) ask(kt0 + x, i);
       // the tree is walked while the first copies are on their way
       if (a.parent && end * KT > q.len) walk_tree<Threads>(a, q, tok0, tok1, par, seen, words);
+      if (again)
+        odd = uniform(find_nonfinite<Threads, 1, D>(c, table, kv + v_off, page_stride, mixed));
 #pragma unroll
       for (int i = 0; i < KK; ++i) qr[i] = (qr[i] ^ flip) & on;
       wait_copies<2 * P * Ahead>();
@@ -949,6 +1080,16 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       // from LDS kAhead products before their use; the order is fixed here
       // because the compiler's own puts every read next to its product
       constexpr int PV = DB * 2 * NB, QK = NB * KK;
+      if (odd) {  // the wavefronts write the same
+        for (int i = 0; i < NB; ++i) {
+          const int block = ks * NB + i;
+          for (uint32_t word = mixed.word(kt * KT + 32 * block); word; word &= word - 1) {
+            u32x4* p = tiles + (Bufs + v_buf) * TileWords + (32 * block + __builtin_ctz(word)) * CH;
+            if (lane < CH) p[lane] = keep_finite<1>(p[lane], true);
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
       int k_now[KK], v_now[DB];
 #pragma unroll
       for (int j = 0; j < KK; ++j) k_now[j] = k_at_lds[j] + k_buf * (TileWords * 16);
@@ -988,6 +1129,14 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       if (Behind && !behind) lds_barrier();
       lds_barrier();
     }
+    if (!again && kt0 < end && mixed.count > 1 && end * KT > mixed.first) {
+      const float z = zero_or_nan(o);
+      if (__syncthreads_or(z != z)) {
+        again = 1, lo = uniform(lo_here);
+        continue;
+      }
+    }
+    again = 0;
     float sum = total_w[0];
     if constexpr (KS == 2) {  // the two halves of the keys joined
       static_assert(KS == 1 || RW * DB * 4 * kWave <= 2 * Bufs * TileWords, "the outputs of one half fit the tiles");
@@ -1019,7 +1168,8 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       lds_barrier();
     }
     if (ks != 0) continue;
-    if (kt0 == 0 && kt1 == sg.tiles) {
+    const bool whole = kt0 == 0 && kt1 == sg.tiles;
+    if (whole) {
       if (r < rows) {
         const float inv = 1.f / sum;
         const int64_t at = (int64_t(q.begin + tok) * a.q_heads + h * group + r % group) * D + 4 * hi2;
@@ -1042,6 +1192,26 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
               f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
       if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, sg.last)};
     }
+    if (odd && r < rows)  // to the values that this lane has just stored
+      for (int at = kt0 * KT; at < end * KT; at += 32)
+        for (uint32_t word = mixed.word(at); word; word &= word - 1) {
+          const int row = at + __builtin_ctz(word);
+          if (row >= limit) break;
+          if (!(sees(a, q, tok, tok0, at, seen, words) >> (row & 31) & 1)) continue;
+          const u32x4* p = value_row(c, table, kv + v_off, page_stride, CH, row);
+#pragma unroll 1
+          for (int d = 0; d < 4 * DB; ++d) {
+            const f32x4 x = odd_values<1>(p, 8 * d + 4 * hi2);
+            if (whole) {
+              const int64_t out = (int64_t(q.begin + tok) * a.q_heads + h * group + r % group) * D + 8 * d + 4 * hi2;
+              const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const char*>(a.out) + out * 2);
+              store4<1>(a.out, out, x + f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u),
+                                              __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xffff0000u)});
+            } else {
+              reinterpret_cast<f32x4*>(part(c, blockIdx.x, kt0 == 0, part_floats(M, D)) + 2 * M)[(rw * DB * 4 + d) * kWave + lane] += x;
+            }
+          }
+        }
   }
 }
 
