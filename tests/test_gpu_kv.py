@@ -525,3 +525,32 @@ def test_binding_refusals():
     tms.kv_attention(cache, 0, none, dev32([0, 0, 0, 0]), none, max_new=1)
     tms.kv_write(cache, 0, none[:, :2], none[:, :2], dev32([0, 0, 0, 0]))
     assert (cache.status() == tms.OK).all()
+
+
+def test_the_example_decodes_the_same_with_and_without_drafts():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples", "tree_decode.py")
+    spec = importlib.util.spec_from_file_location("tree_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    c = ex.CONFIGS["tiny"]
+    rng = np.random.default_rng(8)
+    trie = tms.Trie(ex.catalog("tiny"), c.vocab, c.sep, c.stop)
+    model = ex.Model(torch.from_numpy(ex.embedding("tiny").copy()).cuda(), seed=1)
+    prompt, questions = rng.integers(0, c.sep, 50).tolist(), [rng.integers(0, c.sep, n).tolist() for n in (1, 7, 3)]
+    plain, many = ex.decode(trie, model, prompt, questions, c.k, 0)
+    answers, passes = ex.decode(trie, model, prompt, questions, c.k, 40)
+    assert answers == plain and passes < many
+    entries = {tuple(e) for e in ex.catalog("tiny")}
+    for a in answers:  # k different entries, separated, and stop
+        parts, part = [], []
+        for t in a[:-1]:
+            if t == c.sep:
+                parts.append(tuple(part))
+                part = []
+            else:
+                part.append(t)
+        parts.append(tuple(part))
+        assert a[-1] == c.stop and len(parts) == c.k and len(set(parts)) == c.k and set(parts) <= entries
+    trie.close()
