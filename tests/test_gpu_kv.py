@@ -149,6 +149,11 @@ BATCHES = [
     (4, 2, 256, [31, 200], [80, 300], True),
     (2, 1, 64, [9, 0, 40] * 200, [1, 2, 0] * 200, False),  # several sequences to a thread of the plan
     (2, 1, 64, [9, 0, 40] * 400, [20, 3, 0] * 400, True),
+    (4, 2, 64, [20000], [18], True),                      # many parts of few segments
+    (8, 1, 128, [15000, 300], [30, 2], True),
+    (4, 2, 64, [30000, 17], [2, 1], True),
+    (8, 2, 256, [9000], [1], False),
+    (2, 1, 256, [9000, 0], [60, 3], False),
 ]
 
 

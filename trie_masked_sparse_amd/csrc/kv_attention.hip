@@ -17,6 +17,8 @@
 // one column to a lane), fp32 through one word per key.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv_cache.h"
 #include "tms.h"
 
@@ -149,6 +151,17 @@ __device__ inline int tiles_of(const KvAttention& a, const Seq& q, int rt, int g
 // short one, whose sum is the same for all up to the rounding of two tiles.
 constexpr int kOpen = 4;
 
+// The least units of a share, and the tiles that take as long as the join of a
+// part.  Few rows: one tile for each wavefront (8 units: one sequence of 517
+// tokens of 8 key heads 12 -> 15 us), and 0.4 of a tile to a part, which one
+// workgroup joins (without that rule 36000 keys of 2 heads took 45 us, with it
+// 22; 8000 keys of 8 heads 35 and 23).  Many rows: parts are joined by
+// many workgroups, so only the start of a segment counts (1, 2 and 5 units:
+// 1000 keys of 8 heads and 30 drafts 16.8, 16.6 and 20.4 us; 10000 of 2 heads
+// and 18 drafts 17.9, 15.6 and 17.9).
+constexpr int kLeastFew = kWaves, kLeastMany = 2;
+constexpr float kJoinFew = 0.4f, kJoinMany = 0.f;
+
 template <int M, int KT>
 __device__ inline int units_each(const KvAttention& a, const Seq& q, int group, bool* pairs) {
   *pairs = !a.parent && !q.bad && q.rows_tiles > 1;
@@ -253,16 +266,20 @@ __device__ inline int share_of(int64_t total, int shares, int64_t tile) {
 
 // The share [*lo, *hi) of this workgroup among all units, the sequence *s that
 // it starts in (*q) and that sequence's first unit *base: a prefix sum over the
-// sequences (shares is cut so that a share has at least `least` units).
-// Returns whether there is work.
+// sequences.  shares is cut so that a share has at least `least` units, and
+// sqrt(`join` n) for the n tiles of the longest segment: the time of a
+// share's tiles and the time to join a segment's parts are the same then,
+// if a part takes as long to join as `join` tiles.  Returns whether there is
+// work.
 template <int M, int KW, int W>
-__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, bool mark, int& shares, int least, int64_t* lo,
+__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, bool mark, int& shares, int least, float join, int64_t* lo,
                                 int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
   __shared__ int64_t scan[W];
-  __shared__ int found[7];
+  __shared__ int longest[W], found[7];
   __shared__ int64_t found_base;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
+  int tiles = 0;
   const int each = (c.seqs + W * kWave - 1) / (W * kWave);
   Seq q{};  // the thread's last sequence; its only one where each is 1
   for (int i = 0; i < each; ++i) {
@@ -270,6 +287,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
     if (s < c.seqs) {
       q = sequence(c, a, s, M, KW);
       mine += units_of<M, KW>(c, a, q, split);
+      if (q.n) tiles = max(tiles, q.key_tiles);
     }
   }
   int64_t incl = mine;
@@ -277,15 +295,18 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool spl
   for (int d = 1; d < kWave; d *= 2) {
     const int64_t o = __shfl_up(incl, d);
     if (lane >= d) incl += o;
+    tiles = max(tiles, __shfl_up(tiles, d));
   }
-  if (lane == kWave - 1) scan[wave] = incl;
+  if (lane == kWave - 1) scan[wave] = incl, longest[wave] = tiles;
   __syncthreads();
   for (int i = 0; i < W; ++i) {
     if (i < wave) before += scan[i];
     total += scan[i];
+    tiles = max(tiles, longest[i]);
   }
   before += incl - mine;
   total = uniform(total);
+  least = uniform(max(least, static_cast<int>(sqrtf(join * tiles))));
   if (split) shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / least)));
   const int me = blockIdx.x;
   if (mark && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
@@ -472,46 +493,62 @@ __device__ inline void part_store(f32x4* p, f32x4 x) {
     __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Values 4 i .. 4 i + 3 of the output of a segment of M rows, joined from its
-// parts in the shares first .. j.last, in that order.
-template <int DT, int D, bool Shared>
-__device__ inline void join_parts(const KvCache& c, const KvAttention& a, const Join& j, int first, int M, int wide, int i) {
-  const int group = a.q_heads / c.kv_heads, begin = a.start[j.s], rows = (a.start[j.s + 1] - begin) * group;
-  int row, column;
-  part_place<D>(i, wide, &row, &column);
-  const int r = j.rt * M + row;
-  if (row >= M || r >= rows) return;
-  const int64_t floats = part_floats(M, D);
-  f32x4 x{0.f, 0.f, 0.f, 0.f};
+struct Sum {
   float top = -INFINITY, l = 0.f;
-  constexpr int kParts = 8;  // in flight
-  for (int w = first; w <= j.last; w += kParts) {
+  f32x4 x{0.f, 0.f, 0.f, 0.f};
+};
+
+// Values 4 i .. 4 i + 3, of row `row`, of a segment of M rows that starts in
+// share `first`: the parts in the shares w .. last joined, in that order.
+template <int D, bool Shared>
+__device__ inline Sum sum_parts(const KvCache& c, int first, int w, int last, int M, int row, int i) {
+  const int64_t floats = part_floats(M, D);
+  Sum s;
+  constexpr int kParts = Shared ? 12 : 8;  // in flight
+  for (; w <= last; w += kParts) {
     float t[kParts], k[kParts];
     f32x4 y[kParts];
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
       t[u] = -INFINITY, k[u] = 0.f, y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (w + u <= j.last) {
+      if (w + u <= last) {
         const float* p = part(c, w + u, w + u == first, floats);
         t[u] = part_load<Shared>(p + row), k[u] = part_load<Shared>(p + M + row);
         y[u] = part_load<Shared>(reinterpret_cast<const f32x4*>(p + 2 * M) + i);
       }
     }
-    float next = top;
+    float next = s.top;
 #pragma unroll
     for (int u = 0; u < kParts; ++u) next = fmaxf(next, t[u]);
-    const float at = next == -INFINITY ? 0.f : next, old = exp2_fast(top - at);
-    top = next;
-    l *= old, x *= old;
+    const float at = next == -INFINITY ? 0.f : next, old = exp2_fast(s.top - at);
+    s.top = next;
+    s.l *= old, s.x *= old;
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
       const float now = exp2_fast(t[u] - at);
-      l += k[u] * now;
-      x += y[u] * now;
+      s.l += k[u] * now;
+      s.x += y[u] * now;
     }
   }
-  const int64_t at = (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + column;
-  store4<DT>(a.out, at, x * (1.f / l));
+  return s;
+}
+
+template <int DT, int D>
+__device__ inline void store_joined(const KvAttention& a, const KvCache& c, const Join& j, int M, int row, int column,
+                                    const Sum& s) {
+  const int group = a.q_heads / c.kv_heads, begin = a.start[j.s], rows = (a.start[j.s + 1] - begin) * group;
+  const int r = j.rt * M + row;
+  if (row < M && r < rows)
+    store4<DT>(a.out, (int64_t(begin + r / group) * a.q_heads + j.h * group + r % group) * D + column, s.x * (1.f / s.l));
+}
+
+// Values 4 i .. 4 i + 3 of the output of a segment whose parts are in the
+// shares first .. j.last.
+template <int DT, int D, bool Shared>
+__device__ inline void join_parts(const KvCache& c, const KvAttention& a, const Join& j, int first, int M, int wide, int i) {
+  int row, column;
+  part_place<D>(i, wide, &row, &column);
+  if (row < M) store_joined<DT, D>(a, c, j, M, row, column, sum_parts<D, Shared>(c, first, first, j.last, M, row, i));
 }
 
 // ------------------------------------------------- few rows: token, drafts --
@@ -567,7 +604,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kWaves, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kLeastFew, kJoinFew, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
 
   int again = 0;  // the segment is worked on for the second time
@@ -888,7 +925,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KT, W>(c, a, split, split, shares, 1, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KT, W>(c, a, split, split, shares, kLeastMany, kJoinMany, &lo, &hi, &s, &q, &base, &total)) return;
   int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
     const int64_t lo_here = lo;
@@ -1215,12 +1252,65 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   }
 }
 
-// Joins the parts of a segment that starts in share blockIdx.x and ends in a
-// later one; a thread takes 4 values of a row.
-template <int D>
-__global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, int M) {
-  const Join j = joins(c)[blockIdx.x];
-  if (j.last >= 0) join_parts<1, D, false>(c, a, j, blockIdx.x, M, 1, blockIdx.y * 256 + threadIdx.x);
+// Joins the parts of the segment blockIdx.x of those that several shares have;
+// they are found by the shares in which one starts.  A thread takes 4 values of
+// a row; with few segments (long contexts of few heads: many parts each), G
+// threads take them, each a run of the parts: the join is bound by the loads'
+// latency (calls of 18 drafts over 10000 keys of 2 heads 47 -> 16 us, of 30
+// over 30000 of one head 123 -> 31).
+template <int D, int G>
+__global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, int shares, int M) {
+  const int tid = threadIdx.x;
+  int first = blockIdx.x;
+  if (int(gridDim.x) < shares) {
+    __shared__ int count[4], start;
+    int before = blockIdx.x;  // segments to go
+    if (tid == 0) start = -1;
+    __syncthreads();
+    for (int base = 0; base < shares; base += 256) {
+      const bool here = base + tid < shares && joins(c)[min(base + tid, shares - 1)].last >= 0;
+      const uint64_t all = __ballot(here);
+      if (tid % kWave == 0) count[tid / kWave] = __popcll(all);
+      __syncthreads();
+      int rank = __popcll(all & ((uint64_t(1) << tid % kWave) - 1)), sum = 0;
+      for (int i = 0; i < 4; ++i) {
+        if (i < tid / kWave) rank += count[i];
+        sum += count[i];
+      }
+      if (here && rank == before) start = base + tid;
+      before -= sum;
+      __syncthreads();
+    }
+    first = start;
+    if (first < 0) return;
+  }
+  const Join j = joins(c)[first];
+  if (j.last < 0) return;
+  if constexpr (G == 1) {
+    join_parts<1, D, false>(c, a, j, first, M, 1, blockIdx.y * 256 + tid);
+  } else {
+    __shared__ float stat[2][256];
+    __shared__ f32x4 values[256];
+    const int parts = j.last - first + 1, each = (parts + G - 1) / G, g = tid / (256 / G);
+    const int i = blockIdx.y * (256 / G) + tid % (256 / G);
+    int row, column;
+    part_place<D>(i, 1, &row, &column);
+    Sum sum;
+    if (row < M) sum = sum_parts<D, false>(c, first, first + g * each, min(j.last, first + (g + 1) * each - 1), M, row, i);
+    stat[0][tid] = sum.top, stat[1][tid] = sum.l, values[tid] = sum.x;
+    __syncthreads();
+    if (g == 0 && row < M) {
+      float top = sum.top;
+      for (int o = 1; o < G; ++o) top = fmaxf(top, stat[0][tid + o * (256 / G)]);
+      const float at = top == -INFINITY ? 0.f : top;
+      Sum all{top, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+      for (int o = 0; o < G; ++o) {
+        const float now = exp2_fast(stat[0][tid + o * (256 / G)] - at);
+        all.l += stat[1][tid + o * (256 / G)] * now, all.x += values[tid + o * (256 / G)] * now;
+      }
+      store_joined<1, D>(a, c, j, M, row, column, all);
+    }
+  }
 }
 
 // Row tiles of all sequences and key heads, at most.
@@ -1249,7 +1339,9 @@ hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   const int split = KS > 1 || segments < 2 * kFit;
   many_rows_kernel<D, RW, KS><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW>(a.q_heads / c.kv_heads));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
-  combine_kernel<D><<<dim3(kFit, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, M);
+  const int joined = static_cast<int>(std::min<int64_t>(segments, kFit));  // at most: one starts in a share
+  if (8 * joined <= kFit) combine_kernel<D, 8><<<dim3(joined, M * D / 4 / 32), 256, 0, s>>>(c, a, kFit, M);
+  else combine_kernel<D, 1><<<dim3(joined, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, kFit, M);
   return hipGetLastError();
 }
 
