@@ -878,12 +878,13 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
 // Words of the table of drafts that a workgroup of 32 RW rows has, and of a
 // token's row in it: a tree fits in one row tile below 8 x 32 rows; there, the
 // rows are of at most 128 tokens with two query heads or more to a key head
-// (any tree), and of 256 with one (trees of up to 512 drafts).
-template <int RW>
-constexpr int kSeen = RW == 8 ? 256 * 17 : 32 * RW * (RW + 1);
-template <int RW>
+// (any tree), and of 256 with one (trees of up to 512 drafts).  Trees that do
+// not fit these take 128 rows with the whole table (AnyTree).
+template <int RW, bool AnyTree>
+constexpr int kSeen = AnyTree ? 32 * RW * kTreeWords : RW == 8 ? 256 * 17 : 32 * RW * (RW + 1);
+template <int RW, bool AnyTree>
 int tree_words(int group) {
-  return RW < 8 ? RW + 1 : group > 1 ? kTreeWords : 17;
+  return AnyTree ? kTreeWords : RW < 8 ? RW + 1 : group > 1 ? kTreeWords : 17;
 }
 
 // Workgroup of RW x KS wavefronts over a segment (whole prompts: the heaviest
@@ -895,7 +896,7 @@ int tree_words(int group) {
 // before) and the softmax with the copies of later tiles into LDS.  With 8
 // wavefronts, two on a SIMD, the second four run one phase behind: while one
 // wavefront of a SIMD feeds the matrix cores the other has the vector units.
-template <int D, int RW, int KS>
+template <int D, int RW, int KS, bool AnyTree>
 __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
   constexpr bool Behind = W == 8;
@@ -907,8 +908,8 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   // K tiles, then V tiles; the outputs of the second half of the keys at the end
   __shared__ u32x4 tiles[2 * Bufs * TileWords];
   __shared__ float stat[KS == 2 ? 2 * M : 1];
-  __shared__ uint32_t seen[kSeen<RW>];
-  __shared__ int32_t par[RW == 8 ? kTree : M];
+  __shared__ uint32_t seen[kSeen<RW, AnyTree>];
+  __shared__ int32_t par[AnyTree || RW == 8 ? kTree : M];
   __shared__ uint32_t nonfinite[kMixedWords];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int rw = wave % RW, ks = wave / RW, col = lane % 32, hi2 = lane / 32;
@@ -1329,15 +1330,15 @@ hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D, int RW, int KS>
+template <int D, int RW, int KS, bool AnyTree = false>
 hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   constexpr int M = 32 * RW, Threads = RW * KS * kWave;
   const int64_t segments = segments_of(c, a, M);
   if (segments >= (int64_t(1) << 32) / Threads) return hipErrorInvalidValue;
   // workgroups that the chip holds at once
-  constexpr int kFit = Threads == 512 || D == 256 ? kManyShares : 2 * kManyShares;
+  constexpr int kFit = Threads == 512 || D == 256 || AnyTree ? kManyShares : 2 * kManyShares;
   const int split = KS > 1 || segments < 2 * kFit;
-  many_rows_kernel<D, RW, KS><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW>(a.q_heads / c.kv_heads));
+  many_rows_kernel<D, RW, KS, AnyTree><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW, AnyTree>(a.q_heads / c.kv_heads));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
   const int joined = static_cast<int>(std::min<int64_t>(segments, kFit));  // at most: one starts in a share
   if (8 * joined <= kFit) combine_kernel<D, 8><<<dim3(joined, M * D / 4 / 32), 256, 0, s>>>(c, a, kFit, M);
@@ -1353,10 +1354,9 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
     if constexpr (D == 256) return few_rows<DT, D, 1>(c, a, s);
     else return few_rows<DT, D, 2>(c, a, s);
   } else if constexpr (D == 256) {
-    if (a.parent && rows > 128) return few_rows<DT, D, 2>(c, a, s);
-    return rows > 64 ? many_rows<D, 4, 1>(c, a, s) : many_rows<D, 2, 2>(c, a, s);
+    return rows > 64 ? many_rows<D, 4, 1, true>(c, a, s) : many_rows<D, 2, 2>(c, a, s);
   } else {
-    if (a.parent && a.max_new > 512 && group == 1) return few_rows<DT, D, 4>(c, a, s);  // the table of drafts is too small
+    if (a.parent && a.max_new > 512 && group == 1) return many_rows<D, 4, 1, true>(c, a, s);  // the table of drafts
     // 256 rows a workgroup have the faster loop (16 x 1000 tokens of 32 query
     // heads 249 against 256 us, one of 512 tokens behind 30000 255 against 285),
     // two workgroups of 128 rows overlap their starts and ends, which are most
