@@ -154,6 +154,9 @@ BATCHES = [
     (4, 2, 64, [30000, 17], [2, 1], True),
     (8, 2, 256, [9000], [1], False),
     (2, 1, 256, [9000, 0], [60, 3], False),
+    (16, 8, 64, [20000] + [0] * 40, [100] * 41, False),   # one context much longer than the others
+    (8, 4, 128, [0, 9000, 3], [900, 30, 700], False),
+    (4, 4, 64, [0] * 7 + [12000], [300] * 8, False),
 ]
 
 

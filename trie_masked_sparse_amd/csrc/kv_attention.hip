@@ -162,6 +162,15 @@ constexpr int kOpen = 4;
 constexpr int kLeastFew = kWaves, kLeastMany = 2;
 constexpr float kJoinFew = 0.4f, kJoinMany = 0.f;
 
+// Whole segments instead of shares, chosen by the kernel: where the longest
+// takes no more than a share and the writing and joining of its parts,
+// kApart units for each row of a workgroup and part (three prompts of 610 to
+// 1125 tokens of 16 query heads 49 -> 44 us, two of 1000 of 32 59 -> 45, 64 trees of
+// 50 to 64 drafts behind 1000 tokens 97 -> 75; four times that 45 -> 54, 59
+// -> 64).
+constexpr float kApart = 9.f / 256;
+enum { kWhole = 0, kSplit, kEither };
+
 template <int M, int KT>
 __device__ inline int units_each(const KvAttention& a, const Seq& q, int group, bool* pairs) {
   *pairs = !a.parent && !q.bad && q.rows_tiles > 1;
@@ -264,55 +273,85 @@ __device__ inline int share_of(int64_t total, int shares, int64_t tile) {
   return w;
 }
 
+// The value of a lane before this one (DPP control), 0 where there is none.
+template <int Control, int Rows>
+__device__ inline int from_lane(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, Control, Rows, 0xf, false);
+}
+
 // The share [*lo, *hi) of this workgroup among all units, the sequence *s that
 // it starts in (*q) and that sequence's first unit *base: a prefix sum over the
 // sequences.  shares is cut so that a share has at least `least` units, and
 // sqrt(`join` n) for the n tiles of the longest segment: the time of a
 // share's tiles and the time to join a segment's parts are the same then,
-// if a part takes as long to join as `join` tiles.  Returns whether there is
-// work.
+// if a part takes as long to join as `join` tiles.  With split = kEither it
+// becomes kWhole, and a
+// workgroup takes a whole segment, where the longest one, or all of them
+// with the last ones to be started, end within a share and `more` units
+// (writing and joining parts is saved), or no segment is longer than three
+// quarters of a share.
+// Returns whether there is work.
 template <int M, int KW, int W>
-__device__ inline bool my_share(const KvCache& c, const KvAttention& a, bool split, bool mark, int& shares, int least, float join, int64_t* lo,
-                                int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
+__device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& split, bool mark, int& shares, int least, float join,
+                                float more, int64_t* lo, int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
   __shared__ int64_t scan[W];
-  __shared__ int longest[W], found[7];
+  __shared__ int segments[W], longest[W], latest[W], found[7];
   __shared__ int64_t found_base;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
-  int tiles = 0;
+  int tiles = 0, tail = 0, my_count = 0, count = 0, count_before = 0;
   const int each = (c.seqs + W * kWave - 1) / (W * kWave);
   Seq q{};  // the thread's last sequence; its only one where each is 1
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
     if (s < c.seqs) {
       q = sequence(c, a, s, M, KW);
-      mine += units_of<M, KW>(c, a, q, split);
-      if (q.n) tiles = max(tiles, q.key_tiles);
+      mine += units_of<M, KW>(c, a, q, kSplit);
+      my_count += static_cast<int>(units_of<M, KW>(c, a, q, kWhole));
+      if (q.n) {
+        tiles = max(tiles, q.key_tiles);
+        if (split == kEither) tail = max(tail, tiles_of<M, KW>(a, q, 0, a.q_heads / c.kv_heads));
+      }
     }
   }
   int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int64_t o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-    tiles = max(tiles, __shfl_up(tiles, d));
-  }
-  if (lane == kWave - 1) scan[wave] = incl, longest[wave] = tiles;
+  int incl_count = my_count;
+  auto step = [&](auto from) __attribute__((always_inline)) {
+    const uint64_t low = uint32_t(from(int(incl))), high = uint32_t(from(int(incl >> 32)));
+    incl += int64_t(high << 32 | low), incl_count += from(incl_count);
+    tiles = max(tiles, from(tiles)), tail = max(tail, from(tail));
+  };
+  step([](int x) { return from_lane<0x111, 0xf>(x); });  // 1, 2, 4 and 8 lanes down in rows of 16
+  step([](int x) { return from_lane<0x112, 0xf>(x); });
+  step([](int x) { return from_lane<0x114, 0xf>(x); });
+  step([](int x) { return from_lane<0x118, 0xf>(x); });
+  step([](int x) { return from_lane<0x142, 0xa>(x); });  // row 0 to row 1, row 2 to row 3
+  step([](int x) { return from_lane<0x143, 0xc>(x); });  // lane 31 to rows 2 and 3
+  if (lane == kWave - 1) scan[wave] = incl, segments[wave] = incl_count, longest[wave] = tiles, latest[wave] = tail;
   __syncthreads();
   for (int i = 0; i < W; ++i) {
-    if (i < wave) before += scan[i];
-    total += scan[i];
-    tiles = max(tiles, longest[i]);
+    if (i < wave) before += scan[i], count_before += segments[i];
+    total += scan[i], count += segments[i];
+    tiles = max(tiles, longest[i]), tail = max(tail, latest[i]);
   }
   before += incl - mine;
-  total = uniform(total);
+  total = uniform(total), count = uniform(count), tiles = uniform(tiles), tail = uniform(tail);
+  if (split == kEither) {
+    const float share = static_cast<float>(total) / shares;
+    const float whole = fmaxf(tiles + kOpen, count <= shares ? 0.f : share + tail + kOpen);
+    if (count <= int(gridDim.x) && (whole <= share + more * (shares + min(count, shares)) / shares || 1.33f * tiles <= share))
+      split = kWhole;
+  }
+  if (split == kWhole) {
+    before = count_before + incl_count - my_count, mine = my_count, total = count;
+  }
   least = uniform(max(least, static_cast<int>(sqrtf(join * tiles))));
   if (split) shares = static_cast<int>(max(int64_t(1), min(int64_t(shares), total / least)));
   const int me = blockIdx.x;
   if (mark && tid == 0) joins(c)[me] = Join{0, 0, 0, -1};
   *lo = split ? share_begin(total, shares, me) : me;
   *hi = split ? share_begin(total, shares, me + 1) : me + 1;
-  if (total == 0 || (split ? me >= shares : me >= total)) return false;
+  if (me >= (split ? shares : total) || total == 0) return false;
   if (*lo >= before && *lo < before + mine) {
     int64_t base = before;
     int s = tid * each;
@@ -604,7 +643,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kLeastFew, kJoinFew, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kLeastFew, kJoinFew, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
 
   int again = 0;  // the segment is worked on for the second time
@@ -926,7 +965,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KT, W>(c, a, split, split, shares, kLeastMany, kJoinMany, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KT, W>(c, a, split, int(blockIdx.x) < shares, shares, kLeastMany, kJoinMany, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
   int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
     const int64_t lo_here = lo;
@@ -1288,7 +1327,7 @@ __global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, 
   const Join j = joins(c)[first];
   if (j.last < 0) return;
   if constexpr (G == 1) {
-    join_parts<1, D, false>(c, a, j, first, M, 1, blockIdx.y * 256 + tid);
+    for (int i = blockIdx.y * 256 + tid; i < M * D / 4; i += gridDim.y * 256) join_parts<1, D, false>(c, a, j, first, M, 1, i);
   } else {
     __shared__ float stat[2][256];
     __shared__ f32x4 values[256];
@@ -1321,12 +1360,11 @@ int64_t segments_of(const KvCache& c, const KvAttention& a, int rows) {
 
 template <int DT, int D, int MT>
 hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
-  const int64_t group = a.q_heads / c.kv_heads, segments = segments_of(c, a, 16 * MT);
+  const int64_t segments = segments_of(c, a, 16 * MT);
   if (segments >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  // one row tile a sequence, and drafts, are split always (contexts differ);
-  // prompts while their row tiles would not fill the chip twice
-  const int split = a.parent || a.max_new * group <= 16 * MT || segments < 2 * kShares;
-  few_rows_kernel<DT, D, MT><<<split ? kShares : int(segments), kBlock, 0, s>>>(c, a, kShares, split);
+  // drafts and single tokens are split always: their contexts differ
+  const int split = a.parent || a.max_new * (a.q_heads / c.kv_heads) <= 16 * MT ? kSplit : kEither;
+  few_rows_kernel<DT, D, MT><<<split == kEither ? int(std::max<int64_t>(segments, kShares)) : kShares, kBlock, 0, s>>>(c, a, kShares, split);
   return hipGetLastError();
 }
 
@@ -1337,12 +1375,19 @@ hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   if (segments >= (int64_t(1) << 32) / Threads) return hipErrorInvalidValue;
   // workgroups that the chip holds at once
   constexpr int kFit = Threads == 512 || D == 256 || AnyTree ? kManyShares : 2 * kManyShares;
-  const int split = KS > 1 || segments < 2 * kFit;
-  many_rows_kernel<D, RW, KS, AnyTree><<<split ? kFit : int(segments), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW, AnyTree>(a.q_heads / c.kv_heads));
-  if (hipError_t e = hipGetLastError(); e != hipSuccess || !split) return e;
+  const int64_t group = a.q_heads / c.kv_heads, longest = ((int64_t(c.max_pages) << c.page_shift) + 63) / 64;
+  // prompts that are whole segments by my_share's last rule, however long their
+  // contexts are: T tokens of `seqs` sequences have at least these units (the
+  // launch that would join parts is saved, 3 to 5 us)
+  const double units = (double(a.T) * a.T * group / (2.0 * 64 * c.seqs) + double(kOpen) * a.T * group) / M * c.kv_heads;
+  const int split = a.parent || 1.34 * longest * kFit > units ? kEither : kWhole;
+  many_rows_kernel<D, RW, KS, AnyTree><<<int(std::max<int64_t>(segments, kFit)), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW, AnyTree>(group));
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || split == kWhole) return e;
   const int joined = static_cast<int>(std::min<int64_t>(segments, kFit));  // at most: one starts in a share
+  // few segments have many parts; else as many workgroups as are quickly gone
+  // where there is nothing to join
   if (8 * joined <= kFit) combine_kernel<D, 8><<<dim3(joined, M * D / 4 / 32), 256, 0, s>>>(c, a, kFit, M);
-  else combine_kernel<D, 1><<<dim3(joined, (M * D / 4 + 255) / 256), 256, 0, s>>>(c, a, kFit, M);
+  else combine_kernel<D, 1><<<dim3(joined, std::max(1, std::min(4096 / joined, M * D / 4 / 256))), 256, 0, s>>>(c, a, kFit, M);
   return hipGetLastError();
 }
 
