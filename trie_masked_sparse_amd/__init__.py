@@ -460,10 +460,15 @@ def debug_set_live(st, s: int, edge: int, value: int, stream=None):
 
 # --------------------------------------------------------------------------- paged key/value cache
 
+# The calls of a decode step are short: what they look up is bound here.
+_Tensor, _int32, _raw_stream = torch.Tensor, torch.int32, torch._C._cuda_getCurrentRawStream
+
+
 def _sized(t, dtype, numel: int, name: str):
     """Address of a contiguous GPU tensor of at least numel values."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _dev(t, dtype, name)  # says what is wrong, or takes a subclass of Tensor
+    if type(t) is _Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    _dev(t, dtype, name)  # says what is wrong, or takes a subclass of Tensor
     if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} values, {numel} are needed")
     return t.data_ptr()
@@ -473,7 +478,7 @@ def _token_rows(t, dtype, dim: int, name: str):
     """(address, tokens, heads, row stride in elements) of a GPU tensor
     [T][heads][dim] whose tokens are contiguous (a slice of a wider projection
     may hold them)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -530,6 +535,8 @@ class PagedCache:
         d.work, d.work_bytes = self.work.data_ptr(), need.value
         self.d = d
         self.ref = C.byref(d)
+        c = lib()
+        self._c = c.tms_kv_fork, c.tms_kv_reserve, c.tms_kv_write, c.tms_kv_attention, c.tms_kv_commit
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int, seqs: int, max_pages: int,
@@ -551,7 +558,7 @@ def _kv_stream(cache: PagedCache, stream):
     """The stream of a call; the work memory is told of streams other than the
     one it was allocated on, so that it is not handed on while they use it."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(cache._index)
+        s = _raw_stream(cache._index)
     else:
         s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     if s != cache._made_on:
@@ -571,18 +578,22 @@ def _raise_kv_errors(cache: PagedCache, stream, where: str):
 def kv_fork(cache: PagedCache, src, stream=None, check: bool = True):
     """Sequence s becomes what src[s] was (int32 [seqs]; itself: unchanged,
     -1: emptied).  check: synchronise and raise on device errors."""
-    _refuse_check_while_recording(check, stream, "kv_fork")
-    _check(lib().tms_kv_fork(cache.ref, _sized(src, torch.int32, cache.seqs, "src"), _kv_stream(cache, stream)),
-           "kv_fork")
+    if check:
+        _refuse_check_while_recording(check, stream, "kv_fork")
+    rc = cache._c[0](cache.ref, _sized(src, _int32, cache.seqs, "src"), _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_fork")
     if check:
         _raise_kv_errors(cache, stream, "kv_fork")
 
 
 def kv_reserve(cache: PagedCache, n_new, stream=None, check: bool = True):
     """Pages for n_new[s] more rows of every sequence (int32 [seqs])."""
-    _refuse_check_while_recording(check, stream, "kv_reserve")
-    _check(lib().tms_kv_reserve(cache.ref, _sized(n_new, torch.int32, cache.seqs, "n_new"), _kv_stream(cache, stream)),
-           "kv_reserve")
+    if check:
+        _refuse_check_while_recording(check, stream, "kv_reserve")
+    rc = cache._c[1](cache.ref, _sized(n_new, _int32, cache.seqs, "n_new"), _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_reserve")
     if check:
         _raise_kv_errors(cache, stream, "kv_reserve")
 
@@ -608,12 +619,14 @@ def kv_write(cache: PagedCache, layer: int, k, v, start, q=None, q_out=None, q_w
     n_freq = 0 if inv_freq is None else inv_freq.numel()
     if n_freq and pos is None:
         raise ValueError("inv_freq needs pos")
-    _check(lib().tms_kv_write(cache.ref, layer, _sized(start, torch.int32, cache.seqs + 1, "start"), T, qp, ldq, hq, qo,
-                              kp, ldk, vp, ldv, None if q_weight is None else _sized(q_weight, dt, D, "q_weight"),
-                              None if k_weight is None else _sized(k_weight, dt, D, "k_weight"), eps,
-                              _sized(pos, torch.int32, T, "pos") if n_freq else None,
-                              _sized(inv_freq, torch.float32, n_freq, "inv_freq") if n_freq else None, n_freq, int(interleaved),
-                              _kv_stream(cache, stream)), "kv_write")
+    rc = cache._c[2](cache.ref, layer, _sized(start, _int32, cache.seqs + 1, "start"), T, qp, ldq, hq, qo, kp, ldk, vp, ldv,
+                     None if q_weight is None else _sized(q_weight, dt, D, "q_weight"),
+                     None if k_weight is None else _sized(k_weight, dt, D, "k_weight"), eps,
+                     _sized(pos, _int32, T, "pos") if n_freq else None,
+                     _sized(inv_freq, torch.float32, n_freq, "inv_freq") if n_freq else None, n_freq, int(interleaved),
+                     _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_write")
 
 
 def kv_attention(cache: PagedCache, layer: int, q, start, out, scale: float | None = None, parent=None,
@@ -624,25 +637,27 @@ def kv_attention(cache: PagedCache, layer: int, q, start, out, scale: float | No
     max_new: the most tokens of a sequence (T if not given).  Asynchronous."""
     dt, D = cache.dtype, cache.head_dim
     qp, T, hq, ldq = _token_rows(q, dt, D, "q")
-    _check(lib().tms_kv_attention(cache.ref, layer, qp, ldq, hq, _sized(start, torch.int32, cache.seqs + 1, "start"), T,
-                                  T if max_new is None else max_new,
-                                  None if parent is None else _sized(parent, torch.int32, T, "parent"),
-                                  D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"),
-                                  _kv_stream(cache, stream)), "kv_attention")
+    rc = cache._c[3](cache.ref, layer, qp, ldq, hq, _sized(start, _int32, cache.seqs + 1, "start"), T,
+                     T if max_new is None else max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
+                     D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"), _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_attention")
 
 
 def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = True):
     """Keep the accepted new rows: n_keep int32 [seqs], keep int32
     [seqs][stride] ascending indices (None: the first n_keep), and give the
     pages past them back."""
-    _refuse_check_while_recording(check, stream, "kv_commit")
-    stride = 0
+    if check:
+        _refuse_check_while_recording(check, stream, "kv_commit")
+    stride, at = 0, None
     if keep is not None:
         if keep.dim() != 2 or keep.shape[0] != cache.seqs:
             raise ValueError("keep must be [seqs][stride]")
-        stride = keep.shape[1]
-    _check(lib().tms_kv_commit(cache.ref, _sized(n_keep, torch.int32, cache.seqs, "n_keep"),
-                               None if keep is None else _sized(keep, torch.int32, 1, "keep"), stride, _kv_stream(cache, stream)), "kv_commit")
+        stride, at = keep.shape[1], _sized(keep, _int32, 1, "keep")
+    rc = cache._c[4](cache.ref, _sized(n_keep, _int32, cache.seqs, "n_keep"), at, stride, _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_commit")
     if check:
         _raise_kv_errors(cache, stream, "kv_commit")
 

@@ -46,9 +46,10 @@ __device__ inline CopyRec* copy_recs(const KvCache& c) {
 
 __device__ inline bool page_ok(const KvCache& c, int32_t p) { return p >= 0 && p < c.pages; }
 
-// Fork, first half, by one wavefront: what sequence s becomes, read from the
+// Fork, first half, by Lanes lanes: what sequence s becomes, read from the
 // state before the call and staged in work (a reordering may replace a sequence
 // that others are forked from); the references of the new row are counted.
+template <int Lanes>
 __device__ inline void fork_stage(const KvCache& c, const int32_t* src, int s, int lane) {
   const int from = src[s];
   ForkRec r{0, 0, TMS_OK, from != s};
@@ -57,7 +58,7 @@ __device__ inline void fork_stage(const KvCache& c, const int32_t* src, int s, i
     r.length = c.length[from];
     r.status = c.status[from];
     r.pages = min(pages_of(c, r.length), min(c.held[from], c.max_pages));
-    for (int j = lane; j < r.pages; j += kWave) {
+    for (int j = lane; j < r.pages; j += Lanes) {
       const int32_t p = c.table[int64_t(from) * c.max_pages + j];
       fork_rows(c)[int64_t(s) * c.max_pages + j] = p;
       if (page_ok(c, p)) atomicAdd(&c.refs[p], 1);
@@ -67,13 +68,14 @@ __device__ inline void fork_stage(const KvCache& c, const int32_t* src, int s, i
 }
 
 // Fork, second half: the old row's references go, the staged row comes in.
+template <int Lanes>
 __device__ inline void fork_apply(const KvCache& c, int s, int lane) {
   const ForkRec r = fork_recs(c)[s];
   if (r.changed < 0 && lane == 0) c.status[s] = r.status;
   if (r.changed != 1) return;
   int32_t* row = c.table + int64_t(s) * c.max_pages;
   const int old = min(c.held[s], c.max_pages);
-  for (int j = lane; j < max(old, r.pages); j += kWave) {
+  for (int j = lane; j < max(old, r.pages); j += Lanes) {
     if (j < old) {
       const int32_t p = row[j];
       if (page_ok(c, p)) atomicSub(&c.refs[p], 1);
@@ -89,46 +91,51 @@ __device__ inline void fork_apply(const KvCache& c, int s, int lane) {
 
 __global__ __launch_bounds__(256) void fork_stage_kernel(KvCache c, const int32_t* __restrict__ src) {
   const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
-  if (s < c.seqs) fork_stage(c, src, s, threadIdx.x % kWave);
+  if (s < c.seqs) fork_stage<kWave>(c, src, s, threadIdx.x % kWave);
 }
 __global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
   const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
-  if (s < c.seqs) fork_apply(c, s, threadIdx.x % kWave);
+  if (s < c.seqs) fork_apply<kWave>(c, s, threadIdx.x % kWave);
 }
-// Both halves in one workgroup: a wavefront for each of at most kSmall
-// sequences saves the second launch.
-constexpr int kSmall = 16;
-__global__ __launch_bounds__(kSmall * kWave) void fork_small_kernel(KvCache c, const int32_t* __restrict__ src) {
-  const int s = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  if (s < c.seqs) fork_stage(c, src, s, lane);
+// Both halves in one workgroup, Lanes lanes for each of at most 1024 / Lanes
+// sequences: saves the second launch.
+template <int Lanes>
+__global__ __launch_bounds__(1024) void fork_small_kernel(KvCache c, const int32_t* __restrict__ src) {
+  const int s = threadIdx.x / Lanes, lane = threadIdx.x % Lanes;
+  if (s < c.seqs) fork_stage<Lanes>(c, src, s, lane);
   __threadfence_block();
   __syncthreads();
-  if (s < c.seqs) fork_apply(c, s, lane);
+  if (s < c.seqs) fork_apply<Lanes>(c, s, lane);
 }
 
 constexpr int kPlan = 1024;  // threads of the one workgroup that hands out pages
 
+// The value of a lane before this one (DPP control), 0 where there is none.
+template <int Control, int Rows>
+__device__ inline int from_lane(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, Control, Rows, 0xf, false);
+}
+// Sum of v over the lanes up to this one.
+__device__ inline int wave_sum_to(int v) {
+  v += from_lane<0x111, 0xf>(v);  // 1, 2, 4 and 8 lanes down in rows of 16
+  v += from_lane<0x112, 0xf>(v);
+  v += from_lane<0x114, 0xf>(v);
+  v += from_lane<0x118, 0xf>(v);
+  v += from_lane<0x142, 0xa>(v);  // row 0 to row 1, row 2 to row 3
+  return v + from_lane<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
+}
+
 // Sum of v over the threads before this one, and over all of them.  Every
-// thread of the workgroup calls it.
-__device__ inline int block_before(int v, int* total) {
-  __shared__ int wave_total[kPlan / kWave];
+// thread of the workgroup calls it, with another `buffer` than the call before.
+__device__ inline int block_before(int v, int* total, int buffer) {
+  __shared__ int wave_total[2][kPlan / kWave];
   const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
-  int incl = v;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == kWave - 1) wave_total[w] = incl;
+  const int incl = wave_sum_to(v);
+  if (lane == kWave - 1) wave_total[buffer][w] = incl;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < kPlan / kWave; ++i) {
-    const int t = wave_total[i];
-    if (i < w) before += t;
-    all += t;
-  }
-  __syncthreads();
-  *total = all;
+  const int sums = wave_sum_to(lane < kPlan / kWave ? wave_total[buffer][lane] : 0);
+  const int before = w ? __builtin_amdgcn_readlane(sums, w - 1) : 0;
+  *total = __builtin_amdgcn_readlane(sums, kPlan / kWave - 1);
   return before + incl - v;
 }
 
@@ -189,11 +196,16 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
         }
       }
     }
-    // a demand above the whole pool never fits: cut there, 4096 of them are
-    // summed in two 16-bit halves without passing 2^31
+    // a demand above the whole pool never fits: cut there, up to 1024 of them
+    // are summed in two 16-bit halves where they could pass 2^31 together
     more = min(more, c.pages + 1);
-    int total_lo, total_hi;
-    const int before_lo = block_before(more & 0xffff, &total_lo), before_hi = block_before(more >> 16, &total_hi);
+    int total_lo, total_hi = 0, before_lo, before_hi = 0;
+    if (c.pages < 1 << 20) {
+      before_lo = block_before(more, &total_lo, 0);
+    } else {
+      before_lo = block_before(more & 0xffff, &total_lo, 0), before_hi = block_before(more >> 16, &total_hi, 1);
+    }
+    __syncthreads();
     const int64_t at = need + (int64_t(before_hi) << 16) + before_lo;
     if (s < c.seqs) {
       begin[s] = static_cast<int>(min(at, int64_t(c.pages) + 1));
@@ -216,7 +228,7 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
       n += is_free[i];
     }
     int total;
-    int rank = found + block_before(n, &total);
+    int rank = found + block_before(n, &total, base / (4 * kPlan) & 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (is_free[i]) {
@@ -420,8 +432,9 @@ int64_t kv_page_work_bytes(const KvCache& c) {
 }
 
 hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
-  if (c.seqs <= kSmall) {
-    fork_small_kernel<<<1, kSmall * kWave, 0, s>>>(c, src);
+  if (c.seqs <= 64) {
+    if (c.seqs <= 16) fork_small_kernel<64><<<1, 1024, 0, s>>>(c, src);
+    else fork_small_kernel<16><<<1, 1024, 0, s>>>(c, src);
     return hipGetLastError();
   }
   fork_stage_kernel<<<waves_grid(c.seqs), 256, 0, s>>>(c, src);

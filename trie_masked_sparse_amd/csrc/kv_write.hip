@@ -54,14 +54,27 @@ struct Chunk<1> {
   }
 };
 
-// Sequence of token t: the number of offsets start[1..seqs] at or below t, in
-// two reads of the wavefront (blocks of 64, then within the block; seqs is at
-// most 4096).
-__device__ inline int sequence_of(const int32_t* __restrict__ start, int seqs, int t, int lane) {
-  const int coarse = (lane + 1) * kWave;  // last offset of block `lane`
-  const int block = __popcll(__ballot(coarse <= seqs && start[min(coarse, seqs)] <= t));
-  const int fine = block * kWave + lane + 1;
-  return block * kWave + __popcll(__ballot(fine <= seqs && start[min(fine, seqs)] <= t));
+// What a token's row depends on: its sequence s, the number of offsets
+// start[1..seqs] at or below t (seqs where there is none), and that sequence's
+// first token, committed and held rows and status.  A small write is a chain of
+// memory latencies, so every lane reads all of that of one sequence at once
+// (only with more than 64 sequences, at most 4096, after a read of the
+// blocks of 64).  Forks, drafts written into 8 layers and commits of 256
+// sequences: 204 -> 200 us.
+struct Place {
+  int s, begin, length, held, status;
+};
+__device__ inline Place place_of(const KvCache& c, const int32_t* __restrict__ start, int t, int lane) {
+  int block = 0;
+  if (c.seqs > kWave) {
+    const int coarse = (lane + 1) * kWave;  // last offset of block `lane`
+    block = __popcll(__ballot(coarse <= c.seqs && start[min(coarse, c.seqs)] <= t));
+  }
+  const int mine = min(block * kWave + lane, c.seqs - 1);
+  const int end = start[mine + 1], begin = start[mine], length = c.length[mine], held = c.held[mine], status = c.status[mine];
+  const int n = __popcll(__ballot(block * kWave + lane < c.seqs && end <= t)), at = min(n, kWave - 1);
+  return Place{block * kWave + n, __builtin_amdgcn_readlane(begin, at), __builtin_amdgcn_readlane(length, at),
+               __builtin_amdgcn_readlane(held, at), __builtin_amdgcn_readlane(status, at)};
 }
 
 // Heads that a wavefront has in flight: 64 / LPR of them to a load, kBatch
@@ -86,6 +99,10 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
   auto load = [&](int h) {
     return h < a.q_heads ? q[h * LPR] : h < k_end ? k[(h - a.q_heads) * LPR] : v[(min(h, heads - 1) - k_end) * LPR];
   };
+  const int groups = (heads - g0 + step - 1) / step;
+  const bool rows = g0 + (groups - 1) * step + RPW - 1 >= a.q_heads;  // keys or values among them
+  Place at{};
+  if (rows) at = place_of(c, a.start, t, lane);
   uint4 raw[kBatch];
 #pragma unroll
   for (int u = 0; u < kBatch; ++u)
@@ -112,20 +129,16 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
   }
   // where the token's keys and values go; null where they may not
   uint4* kv_row = nullptr;
-  const int groups = (heads - g0 + step - 1) / step, last = g0 + (groups - 1) * step + RPW - 1;
-  if (last >= a.q_heads) {
-    const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.start, c.seqs, t, lane));
-    if (s < c.seqs && c.status[s] == TMS_OK) {
-      const int64_t row = int64_t(c.length[s]) + (t - a.start[s]);
-      if (t >= a.start[s] && row < int64_t(min(c.held[s], c.max_pages)) << c.page_shift) {
-        const int32_t p = c.table[int64_t(s) * c.max_pages + (row >> c.page_shift)];
-        if (p >= 0 && p < c.pages)
-          kv_row = static_cast<uint4*>(c.kv) +
-                   ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR +
-                   col;
-      }
-      if (!kv_row && lane == 0) c.status[s] = TMS_ERR_INVALID_ARG;
+  if (rows && at.s < c.seqs && at.status == TMS_OK) {
+    const int64_t row = int64_t(at.length) + (t - at.begin);
+    if (t >= at.begin && row < int64_t(min(at.held, c.max_pages)) << c.page_shift) {
+      const int32_t p = c.table[int64_t(at.s) * c.max_pages + (row >> c.page_shift)];
+      if (p >= 0 && p < c.pages)
+        kv_row = static_cast<uint4*>(c.kv) +
+                 ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR +
+                 col;
     }
+    if (!kv_row && lane == 0) c.status[at.s] = TMS_ERR_INVALID_ARG;
   }
   auto finish = [&](int h, uint4 r) {
     if (h >= heads) return;  // whole heads: the lanes that exchange values leave together
