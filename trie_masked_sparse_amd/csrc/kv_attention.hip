@@ -621,6 +621,16 @@ struct Tile<0, D> {                      // fp32
 // holds all rows of the segment and takes every 4th key tile: K straight into
 // registers, V through its own part of LDS, no barrier among them; the next
 // tile's loads are in flight during the softmax and the second product.
+//
+// Up to 16 rows fill half of a matrix product and read K and V once, so memory
+// bounds them: 8 sequences of 40000 to 60000 tokens (32 query, 8 key heads of
+// 128, bf16) 298 us, 5.6 TB/s of 6.1 that a plain read reaches; 64 of 0 to 8191
+// tokens 50 us, 3.7 TB/s, the rest being the start of a workgroup (about 8 us
+// of dependent reads: offsets, page numbers, first keys).  One sequence of 517
+// tokens 12 us, nothing but that chain and the join.  fp32 takes 32
+// rows to a workgroup where there are more than 16, which halves the reads of K
+// and V: two prompts of 2000 to 3000 tokens 809 us, 44 % of the rate of a plain
+// product (the reads of V by single words bound it).
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention a, int shares, int split) {
   using T = Tile<DT, D>;
@@ -935,6 +945,15 @@ int tree_words(int group) {
 // before) and the softmax with the copies of later tiles into LDS.  With 8
 // wavefronts, two on a SIMD, the second four run one phase behind: while one
 // wavefront of a SIMD feeds the matrix cores the other has the vector units.
+//
+// Bound by the matrix cores and by the exponentials beside them (a 64-key tile
+// of 256 rows: 2048 cycles of products, about 4000 in all).  32 query, 8 key
+// heads of 128: three prompts of 2300 to 4097 tokens 336 us (884 TFLOP/s; the
+// matrix cores busy 49 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
+// product of 16384^3: 1340), 63 drafts over two contexts of 90000 to 120000
+// 263 us (824 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
+// contexts of 1201 to 2500 tokens 114 us, 4.0 TB/s.  K and V go straight into LDS:
+// through registers 463 us for the prompts.
 template <int D, int RW, int KS, bool AnyTree>
 __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
@@ -1424,7 +1443,8 @@ hipError_t launch(const KvCache& c, const KvAttention& a, hipStream_t s) {
 }  // namespace
 
 int64_t kv_attention_work_bytes(const KvCache& c) {
-  // two parts of a share: at most 128 rows in each of kShares, or 256 in each of half as many
+  // two parts of a share: at most 128 rows in each of kShares, or 256 in each of
+  // half as many; heads of 256: 128 in each of kManyShares
   return kWorkCounts + round256(kShares * int64_t(sizeof(Join))) +
          2 * 4 * (c.head_dim == 256 ? kManyShares : kShares) * part_floats(128, c.head_dim);
 }
