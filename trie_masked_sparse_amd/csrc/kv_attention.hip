@@ -166,9 +166,12 @@ constexpr float kJoinFew = 0.4f, kJoinMany = 0.f;
 // takes no more than a share and the writing and joining of its parts,
 // kApart units for each row of a workgroup and part (three prompts of 610 to
 // 1125 tokens of 16 query heads 49 -> 44 us, two of 1000 of 32 59 -> 45, 64 trees of
-// 50 to 64 drafts behind 1000 tokens 97 -> 75; four times that 45 -> 54, 59
-// -> 64).
-constexpr float kApart = 9.f / 256;
+// 50 to 64 drafts behind 1000 tokens 97 -> 78; four times that 36 -> 45 us for
+// two prompts of 374 to 618 with heads of 256).  Kernels that memory bounds (up
+// to 64 rows) lose less by a long segment, as the others' bandwidth goes to it:
+// 1.5 shares (5 to 31 drafts behind 64 contexts of 1201 to 2500 tokens 114 -> 99
+// us, tokens of 16 rows behind 64 of 3000 to 5000 196 -> 188).
+constexpr float kScaleMemory = 1.5f, kApart = 9.f / 256;
 enum { kWhole = 0, kSplit, kEither };
 
 template <int M, int KT>
@@ -287,13 +290,13 @@ __device__ inline int from_lane(int x) {
 // if a part takes as long to join as `join` tiles.  With split = kEither it
 // becomes kWhole, and a
 // workgroup takes a whole segment, where the longest one, or all of them
-// with the last ones to be started, end within a share and `more` units
+// with the last ones to be started, end within `scale` shares and `more` units
 // (writing and joining parts is saved), or no segment is longer than three
 // quarters of a share.
 // Returns whether there is work.
 template <int M, int KW, int W>
 __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& split, bool mark, int& shares, int least, float join,
-                                float more, int64_t* lo, int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
+                                float scale, float more, int64_t* lo, int64_t* hi, int* s_out, Seq* q_out, int64_t* base_out, int64_t* total_out) {
   __shared__ int64_t scan[W];
   __shared__ int segments[W], longest[W], latest[W], found[7];
   __shared__ int64_t found_base;
@@ -310,7 +313,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
       my_count += static_cast<int>(units_of<M, KW>(c, a, q, kWhole));
       if (q.n) {
         tiles = max(tiles, q.key_tiles);
-        if (split == kEither) tail = max(tail, tiles_of<M, KW>(a, q, 0, a.q_heads / c.kv_heads));
+        if (split == kEither && int(gridDim.x) > shares) tail = max(tail, tiles_of<M, KW>(a, q, 0, a.q_heads / c.kv_heads));
       }
     }
   }
@@ -339,7 +342,7 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
   if (split == kEither) {
     const float share = static_cast<float>(total) / shares;
     const float whole = fmaxf(tiles + kOpen, count <= shares ? 0.f : share + tail + kOpen);
-    if (count <= int(gridDim.x) && (whole <= share + more * (shares + min(count, shares)) / shares || 1.33f * tiles <= share))
+    if (count <= int(gridDim.x) && (whole <= scale * share + more * (shares + min(count, shares)) / shares || 1.33f * tiles <= share))
       split = kWhole;
   }
   if (split == kWhole) {
@@ -653,7 +656,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kLeastFew, kJoinFew, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KW, kWaves>(c, a, split, false, shares, kLeastFew, kJoinFew, kScaleMemory, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
   const int me = blockIdx.x;
 
   int again = 0;  // the segment is worked on for the second time
@@ -952,7 +955,7 @@ int tree_words(int group) {
 // matrix cores busy 49 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
 // product of 16384^3: 1340), 63 drafts over two contexts of 90000 to 120000
 // 263 us (824 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
-// contexts of 1201 to 2500 tokens 114 us, 4.0 TB/s.  K and V go straight into LDS:
+// contexts of 1201 to 2500 tokens 99 us, 4.6 TB/s.  K and V go straight into LDS:
 // through registers 463 us for the prompts.
 template <int D, int RW, int KS, bool AnyTree>
 __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
@@ -984,7 +987,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KT, W>(c, a, split, int(blockIdx.x) < shares, shares, kLeastMany, kJoinMany, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KT, W>(c, a, split, int(blockIdx.x) < shares, shares, kLeastMany, kJoinMany, KS == 2 ? kScaleMemory : 1.f, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
   int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
     const int64_t lo_here = lo;
@@ -1381,9 +1384,10 @@ template <int DT, int D, int MT>
 hipError_t few_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   const int64_t segments = segments_of(c, a, 16 * MT);
   if (segments >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  // drafts and single tokens are split always: their contexts differ
-  const int split = a.parent || a.max_new * (a.q_heads / c.kv_heads) <= 16 * MT ? kSplit : kEither;
-  few_rows_kernel<DT, D, MT><<<split == kEither ? int(std::max<int64_t>(segments, kShares)) : kShares, kBlock, 0, s>>>(c, a, kShares, split);
+  // more segments than shares: whole ones of prompts only (the contexts of
+  // tokens and drafts differ)
+  const bool prompts = !a.parent && a.max_new * (a.q_heads / c.kv_heads) > 16 * MT;
+  few_rows_kernel<DT, D, MT><<<prompts ? int(std::max<int64_t>(segments, kShares)) : kShares, kBlock, 0, s>>>(c, a, kShares, kEither);
   return hipGetLastError();
 }
 
