@@ -102,6 +102,12 @@ __device__ inline void store4(void* out, int64_t i, f32x4 x) {
 
 // ------------------------------------------------------------------ plan --
 
+// a / b of values that are not negative: the division of 64-bit integers is some 150
+// instructions, and stands several times in the start of a workgroup.
+__device__ inline int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // What a launch works on.  A segment is the row tile of one key head of one
 // sequence; its keys are cut into tiles.  All tiles in the order (sequence,
 // key head, row tile, key tile) are dealt to the workgroups in equal
@@ -213,8 +219,9 @@ __device__ inline bool next_segment(const KvCache& c, const KvAttention& a, cons
   bool pairs;
   const int each = units_each<M, KT>(a, q, group, &pairs);
   const int count = pairs ? (q.rows_tiles + 1) / 2 : q.rows_tiles;  // of a head
-  const int at = static_cast<int>((lo - base) / each);
-  int u = static_cast<int>((lo - base) % each);
+  const int64_t past = quotient(lo - base, each);
+  const int at = static_cast<int>(past);
+  int u = static_cast<int>(lo - base - past * each);
   const int64_t next = lo - u + each;
   g->h = at / count, g->rt = at % count;
   int units = each;
@@ -268,18 +275,26 @@ __device__ inline float* part(const KvCache& c, int share, int which, int64_t fl
          (2 * int64_t(share) + which) * floats;
 }
 
-// First tile of a share of the `total` tiles, and the share that a tile is in.
-__device__ inline int64_t share_begin(int64_t total, int shares, int w) { return total * w / shares; }
-__device__ inline int share_of(int64_t total, int shares, int64_t tile) {
-  int w = static_cast<int>(tile * shares / total);
-  while (w + 1 < shares && share_begin(total, shares, w + 1) <= tile) ++w;
-  return w;
+// First unit of a share of the `total` units, and the share that a unit is in:
+// the first total % shares of them have one unit more.
+__device__ inline int64_t share_begin(int64_t total, int shares, int w) {
+  const int64_t each = quotient(total, shares);
+  return w * each + min(int64_t(w), total - each * shares);
+}
+__device__ inline int share_of(int64_t total, int shares, int64_t unit) {
+  const int64_t each = quotient(total, shares), longer = total - each * shares, past = unit - longer * (each + 1);
+  return static_cast<int>(past < 0 ? quotient(unit, each + 1) : longer + quotient(past, each));
 }
 
 // The value of a lane before this one (DPP control), 0 where there is none.
 template <int Control, int Rows>
 __device__ inline int from_lane(int x) {
   return __builtin_amdgcn_update_dpp(0, x, Control, Rows, 0xf, false);
+}
+
+__device__ inline int64_t read_lane(int64_t x, int lane) {
+  const uint64_t low = uint32_t(__builtin_amdgcn_readlane(int(x), lane)), high = uint32_t(__builtin_amdgcn_readlane(int(x >> 32), lane));
+  return int64_t(high << 32 | low);
 }
 
 // The share [*lo, *hi) of this workgroup among all units, the sequence *s that
@@ -303,10 +318,12 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
   int64_t mine = 0, total = 0, before = 0;
   int tiles = 0, tail = 0, my_count = 0, count = 0, count_before = 0;
-  const int each = (c.seqs + W * kWave - 1) / (W * kWave);
+  // up to 64 sequences: every wavefront has them all, and none waits for another
+  const bool alone = c.seqs <= kWave;
+  const int each = alone ? 1 : (c.seqs + W * kWave - 1) / (W * kWave), place = alone ? lane : tid * each;
   Seq q{};  // the thread's last sequence; its only one where each is 1
   for (int i = 0; i < each; ++i) {
-    const int s = tid * each + i;
+    const int s = place + i;
     if (s < c.seqs) {
       q = sequence(c, a, s, M, KW);
       mine += units_of<M, KW>(c, a, q, kSplit);
@@ -330,12 +347,18 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
   step([](int x) { return from_lane<0x118, 0xf>(x); });
   step([](int x) { return from_lane<0x142, 0xa>(x); });  // row 0 to row 1, row 2 to row 3
   step([](int x) { return from_lane<0x143, 0xc>(x); });  // lane 31 to rows 2 and 3
-  if (lane == kWave - 1) scan[wave] = incl, segments[wave] = incl_count, longest[wave] = tiles, latest[wave] = tail;
-  __syncthreads();
-  for (int i = 0; i < W; ++i) {
-    if (i < wave) before += scan[i], count_before += segments[i];
-    total += scan[i], count += segments[i];
-    tiles = max(tiles, longest[i]), tail = max(tail, latest[i]);
+  constexpr int kLast = kWave - 1;
+  if (alone) {
+    total = read_lane(incl, kLast), count = __builtin_amdgcn_readlane(incl_count, kLast);
+    tiles = __builtin_amdgcn_readlane(tiles, kLast), tail = __builtin_amdgcn_readlane(tail, kLast);
+  } else {
+    if (lane == kLast) scan[wave] = incl, segments[wave] = incl_count, longest[wave] = tiles, latest[wave] = tail;
+    __syncthreads();
+    for (int i = 0; i < W; ++i) {
+      if (i < wave) before += scan[i], count_before += segments[i];
+      total += scan[i], count += segments[i];
+      tiles = max(tiles, longest[i]), tail = max(tail, latest[i]);
+    }
   }
   before += incl - mine;
   total = uniform(total), count = uniform(count), tiles = uniform(tiles), tail = uniform(tail);
@@ -355,9 +378,19 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
   *lo = split ? share_begin(total, shares, me) : me;
   *hi = split ? share_begin(total, shares, me + 1) : me + 1;
   if (me >= (split ? shares : total) || total == 0) return false;
-  if (*lo >= before && *lo < before + mine) {
+  *total_out = total;
+  const bool here = *lo >= before && *lo < before + mine;
+  if (alone) {
+    const int from = __builtin_ctzll(__ballot(here));
+    auto word = [&](int x) { return __builtin_amdgcn_readlane(x, from); };
+    *s_out = from;
+    *q_out = Seq{word(q.begin), word(q.n), word(q.len), word(q.rows_tiles), word(q.key_tiles), word(q.bad)};
+    *base_out = read_lane(before, from);
+    return true;
+  }
+  if (here) {
     int64_t base = before;
-    int s = tid * each;
+    int s = place;
     for (; each > 1; ++s) {
       q = sequence(c, a, s, M, KW);
       const int64_t t = units_of<M, KW>(c, a, q, split);
@@ -374,7 +407,6 @@ __device__ inline bool my_share(const KvCache& c, const KvAttention& a, int& spl
   *q_out = Seq{uniform(found[1]), uniform(found[2]), uniform(found[3]), uniform(found[4]), uniform(found[5]),
                uniform(found[6])};
   *base_out = uniform(found_base);
-  *total_out = total;
   return true;
 }
 
