@@ -26,7 +26,7 @@ namespace tms {
 namespace {
 
 constexpr int kWave = 64, kWaves = 4, kBlock = kWave * kWaves;
-constexpr int kAhead = 4;  // products of 32 rows that the reads of LDS run ahead
+constexpr int kAhead = 3;  // products of 32 rows that the reads of LDS run ahead
 constexpr int kTree = 1024, kTreeWords = kTree / 32 + 1;  // drafts of a tree; words of 32 keys they may touch
 constexpr int kMixedWords = kTreeWords + 2;
 
@@ -1011,10 +1011,12 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, on = a.scale == 0.f ? 0u : ~0u;
   const int tiles_at = static_cast<int>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)tiles));
-  // places in LDS: K is read 16 bytes of 32 rows at a time, V 32 bytes of 8
-  constexpr int Mask = (CH < 16 ? CH : 16) - 1;
+  // places in LDS: K is read 16 bytes of 16 rows at a time, V 64 bytes of 4, each
+  // from 64 different banks (but K of 64-value heads, where pairs of rows meet: an
+  // order without that was 3 % slower)
+  constexpr int Mask = (CH < 16 ? CH : 16) - 1, VShift = D == 64 ? 1 : 2;
   auto k_at = [](int r, int ch) { return r * CH + (ch ^ (r & Mask)); };
-  auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << 1 & Mask)); };
+  auto v_at = [](int r, int ch) { return r * CH + (ch ^ (r << VShift & Mask)); };
 
   int64_t lo, hi, base, total;
   int s;
@@ -1066,7 +1068,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
     // with that one: in bounds, and masked or never used.
     const int final_row = uniform(max(min(limit, end * KT) - 1, 0));
     const int my_row = lane / CH, k_ch = lane % CH ^ ((wave * RPI + my_row) & Mask),
-              v_ch = lane % CH ^ ((wave * RPI + my_row) << 1 & Mask);
+              v_ch = lane % CH ^ ((wave * RPI + my_row) << VShift & Mask);
     // Step x copies K of tile x + 1 + Ahead and V of tile x + Ahead; a tile's
     // page numbers are asked for one step before its K, its addresses are kept
     // for its V.
@@ -1093,7 +1095,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
     auto ask = [&](int x, int piece) __attribute__((always_inline)) {
       const int i = piece % P;
       if (piece < P) {
-        copy(v_off * 16, v_ch, 2, Bufs + to_v, i);
+        copy(v_off * 16, v_ch, 1 << VShift, Bufs + to_v, i);
       } else {
         find(x + 1 + Ahead, i);
         copy(0, k_ch, 1, to_k, i);
