@@ -983,10 +983,10 @@ int tree_words(int group) {
 //
 // Bound by the matrix cores and by the exponentials beside them (a 64-key tile
 // of 256 rows: 2048 cycles of products, about 4000 in all).  32 query, 8 key
-// heads of 128: three prompts of 2300 to 4097 tokens 336 us (884 TFLOP/s; the
-// matrix cores busy 49 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
+// heads of 128: three prompts of 2300 to 4097 tokens 322 us (924 TFLOP/s; the
+// matrix cores busy 51 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
 // product of 16384^3: 1340), 63 drafts over two contexts of 90000 to 120000
-// 263 us (824 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
+// 255 us (851 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
 // contexts of 1201 to 2500 tokens 99 us, 4.6 TB/s.  K and V go straight into LDS:
 // through registers 463 us for the prompts.
 template <int D, int RW, int KS, bool AnyTree>
