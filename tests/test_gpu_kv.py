@@ -157,6 +157,9 @@ BATCHES = [
     (16, 8, 64, [20000] + [0] * 40, [100] * 41, False),   # one context much longer than the others
     (8, 4, 128, [0, 9000, 3], [900, 30, 700], False),
     (4, 4, 64, [0] * 7 + [12000], [300] * 8, False),
+    (16, 8, 128, [0, 700, 3000, 40] * 12, [10, 20, 9, 32] * 12, True),  # parts joined by the last workgroup
+    (8, 8, 64, [0, 700, 3000, 40] * 12, [10, 20, 9, 32] * 12, False),
+    (8, 4, 256, [0, 700, 3000, 40] * 20, [10, 20, 9, 32] * 20, True),
 ]
 
 
@@ -188,7 +191,7 @@ def test_attention_rows_not_seen_may_hold_anything(dtype, heads, kind):
     rows that see it, in its columns, and no others."""
     hq, hkv, D = heads
     for n, (lens, new) in enumerate((([50], [7]), ([3000], [8]), ([33, 40], [25, 3]), ([1000, 64], [70, 33]), ([31], [150]),
-                                     ([700, 20], [300, 5]))):
+                                     ([700, 20], [300, 5]), ([0, 700, 2500, 40] * 30, [10, 20, 9, 32] * 30))):
         print(f"attention not finite {dtype} {heads} {kind} lens {lens} new {new}", flush=True)
         rng = np.random.default_rng(400 + n)
         cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)

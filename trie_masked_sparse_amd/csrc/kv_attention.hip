@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_cache.h"
 #include "tms.h"
@@ -557,14 +558,37 @@ __device__ inline T part_load(const T* p) {
     return x;
   }
 }
+template <bool Shared>
 __device__ inline void part_store(float* p, float x) {
-  __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if constexpr (Shared)
+    __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  else
+    *p = x;
 }
+template <bool Shared>
 __device__ inline void part_store(f32x4* p, f32x4 x) {
-  uint64_t w[2];
-  __builtin_memcpy(w, &x, 16);
-  for (int i = 0; i < 2; ++i)
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if constexpr (Shared) {
+    uint64_t w[2];
+    __builtin_memcpy(w, &x, 16);
+    for (int i = 0; i < 2; ++i)
+      __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  } else {
+    *p = x;
+  }
+}
+
+// Whether this workgroup is the last of the shares first .. last of a segment to
+// have written its part.
+__device__ inline bool last_to_arrive(const KvCache& c, int first, int last) {
+  __shared__ uint32_t arrivals;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the part is written
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    arrivals = atomicAdd(&arrived(c)[first], 1u);
+    if (arrivals == uint32_t(last - first)) arrived(c)[first] = 0;
+  }
+  __syncthreads();
+  return arrivals == uint32_t(last - first);
 }
 
 struct Sum {
@@ -674,7 +698,6 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
   constexpr int kLds = kWaves * kVWords > kWaves * M * D / 4 ? kWaves * kVWords : kWaves * M * D / 4;
   __shared__ u32x4 lds[kLds];
   __shared__ float stat[kWaves][2][M];
-  __shared__ uint32_t arrivals;
   __shared__ uint32_t seen[M * kTreeWords];
   __shared__ int32_t par[kTree];
   __shared__ uint32_t nonfinite[kMixedWords];
@@ -919,7 +942,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
         weight[w] = exp2_fast(stat[w][0][m * 16 + col] - at);
         l += weight[w] * stat[w][1][m * 16 + col];
       }
-      if (!whole && wave == 0 && g == 0) part_store(to + m * 16 + col, top), part_store(to + M + m * 16 + col, l);
+      if (!whole && wave == 0 && g == 0) part_store<true>(to + m * 16 + col, top), part_store<true>(to + M + m * 16 + col, l);
       const int r = rt * M + m * 16 + col;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
@@ -928,7 +951,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) x += buf[((w * MT + m) * DB + d) * kWave + lane] * weight[w];
         if (!whole) {
-          part_store(reinterpret_cast<f32x4*>(to + 2 * M) + (m * DB + d) * kWave + lane, x);
+          part_store<true>(reinterpret_cast<f32x4*>(to + 2 * M) + (m * DB + d) * kWave + lane, x);
         } else if (r < rows) {
           if (q.bad) x = f32x4{NAN, NAN, NAN, NAN}, l = 1.f;
           const int64_t at_out = (int64_t(q.begin + r / group) * a.q_heads + h * group + r % group) * D + 16 * d + 4 * g;
@@ -941,14 +964,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       // from the one with the segment's first tile to the one with its last
       // has a part
       const int first = share_of(total, shares, sg.first), end_share = share_of(total, shares, sg.last);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the part is written
-      __syncthreads();
-      if (tid == 0) {
-        arrivals = atomicAdd(&arrived(c)[first], 1u);
-        if (arrivals == uint32_t(end_share - first)) arrived(c)[first] = 0;
-      }
-      __syncthreads();
-      if (arrivals == uint32_t(end_share - first)) {
+      if (last_to_arrive(c, first, end_share)) {
         for (int i = tid; i < M * D / 4; i += kBlock)
           join_parts<DT, D, true>(c, a, Join{s, h, rt, end_share}, first, M, 0, i);
       }
@@ -987,10 +1003,10 @@ int tree_words(int group) {
 // matrix cores busy 51 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
 // product of 16384^3: 1340), 63 drafts over two contexts of 90000 to 120000
 // 255 us (851 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
-// contexts of 1201 to 2500 tokens 99 us, 4.6 TB/s.  K and V go straight into LDS:
+// contexts of 1201 to 2500 tokens 96 us, 4.8 TB/s.  K and V go straight into LDS:
 // through registers 463 us for the prompts.
 template <int D, int RW, int KS, bool AnyTree>
-__global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words) {
+__global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words, int join) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
   constexpr bool Behind = W == 8;
   constexpr int KT = 64, TileWords = KT * CH;       // keys of a tile, its 16-byte words
@@ -1021,7 +1037,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
   int64_t lo, hi, base, total;
   int s;
   Seq q;
-  if (!my_share<M, KT, W>(c, a, split, int(blockIdx.x) < shares, shares, kLeastMany, kJoinMany, KS == 2 ? kScaleMemory : 1.f, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
+  if (!my_share<M, KT, W>(c, a, split, !join && int(blockIdx.x) < shares, shares, kLeastMany, kJoinMany, KS == 2 ? kScaleMemory : 1.f, M * kApart, &lo, &hi, &s, &q, &base, &total)) return;
   int again = 0;  // the segment is worked on for the second time
   while (lo < hi) {
     const int64_t lo_here = lo;
@@ -1300,9 +1316,10 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       }
       lds_barrier();
     }
-    if (ks != 0) continue;
     const bool whole = kt0 == 0 && kt1 == sg.tiles;
-    if (whole) {
+    if (ks != 0) {
+      // the other half has its outputs
+    } else if (whole) {
       if (r < rows) {
         const float inv = 1.f / sum;
         const int64_t at = (int64_t(q.begin + tok) * a.q_heads + h * group + r % group) * D + 4 * hi2;
@@ -1316,16 +1333,21 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       }
     } else {
       float* to = part(c, blockIdx.x, kt0 == 0, part_floats(M, D));
-      if (hi2 == 0) to[rw * 32 + col] = mx, to[M + rw * 32 + col] = sum;
+      auto write = [&](auto shared) __attribute__((always_inline)) {
+        constexpr bool Shared = decltype(shared)::value;
+        if (hi2 == 0) part_store<Shared>(to + rw * 32 + col, mx), part_store<Shared>(to + M + rw * 32 + col, sum);
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          reinterpret_cast<f32x4*>(to + 2 * M)[((rw * DB + d) * 4 + j) * kWave + lane] =
-              f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-      if (kt0 == 0 && tid == 0) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, sg.last)};
+          for (int j = 0; j < 4; ++j)
+            part_store<Shared>(reinterpret_cast<f32x4*>(to + 2 * M) + ((rw * DB + d) * 4 + j) * kWave + lane,
+                               f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]});
+      };
+      if (KS == 2 && join) write(std::true_type());
+      else write(std::false_type());
+      if (kt0 == 0 && tid == 0 && !join) joins(c)[blockIdx.x] = Join{s, h, rt, share_of(total, shares, sg.last)};
     }
-    if (odd && r < rows)  // to the values that this lane has just stored
+    if (odd && ks == 0 && r < rows)  // to the values that this lane has just stored
       for (int at = kt0 * KT; at < end * KT; at += 32)
         for (uint32_t word = mixed.word(at); word; word &= word - 1) {
           const int row = at + __builtin_ctz(word);
@@ -1341,10 +1363,21 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
               store4<1>(a.out, out, x + f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u),
                                               __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xffff0000u)});
             } else {
-              reinterpret_cast<f32x4*>(part(c, blockIdx.x, kt0 == 0, part_floats(M, D)) + 2 * M)[(rw * DB * 4 + d) * kWave + lane] += x;
+              f32x4* to = reinterpret_cast<f32x4*>(part(c, blockIdx.x, kt0 == 0, part_floats(M, D)) + 2 * M) + (rw * DB * 4 + d) * kWave + lane;
+              if (KS == 2 && join) part_store<true>(to, part_load<true>(to) + x);
+              else *to += x;
             }
           }
         }
+    if (odd) lds_barrier();  // the next segment's tree comes after the last use of this one's
+    if constexpr (KS == 2)
+      if (join && !whole) {
+        const int first = share_of(total, shares, sg.first), last = share_of(total, shares, sg.last);
+        if (last_to_arrive(c, first, last)) {
+          for (int i = tid; i < M * D / 4; i += Threads) join_parts<1, D, true>(c, a, Join{s, h, rt, last}, first, M, 1, i);
+        }
+        lds_barrier();
+      }
   }
 }
 
@@ -1438,9 +1471,13 @@ hipError_t many_rows(const KvCache& c, const KvAttention& a, hipStream_t s) {
   // launch that would join parts is saved, 3 to 5 us)
   const double units = (double(a.T) * a.T * group / (2.0 * 64 * c.seqs) + double(kOpen) * a.T * group) / M * c.kv_heads;
   const int split = a.parent || 1.34 * longest * kFit > units ? kEither : kWhole;
-  many_rows_kernel<D, RW, KS, AnyTree><<<int(std::max<int64_t>(segments, kFit)), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW, AnyTree>(group));
-  if (hipError_t e = hipGetLastError(); e != hipSuccess || split == kWhole) return e;
   const int joined = static_cast<int>(std::min<int64_t>(segments, kFit));  // at most: one starts in a share
+  // small parts, and few of a segment: joined by the last of its workgroups (5 to
+  // 31 drafts behind 64 contexts of 1201 to 2500 tokens 98 -> 96 us; 8 drafts behind 8
+  // of 20000 to 30000, with 8 parts of a segment, 162 -> 165)
+  const int join = KS == 2 && 2 * joined > kFit;
+  many_rows_kernel<D, RW, KS, AnyTree><<<int(std::max<int64_t>(segments, kFit)), Threads, 0, s>>>(c, a, kFit, split, tree_words<RW, AnyTree>(group), join);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || split == kWhole || join) return e;
   // few segments have many parts; else as many workgroups as are quickly gone
   // where there is nothing to join
   if (8 * joined <= kFit) combine_kernel<D, 8><<<dim3(joined, M * D / 4 / 32), 256, 0, s>>>(c, a, kFit, M);
