@@ -114,9 +114,10 @@ __device__ inline int64_t quotient(int64_t a, int64_t b) {
 // key head, row tile, key tile) are dealt to the workgroups in equal
 // contiguous shares, so ragged batches and long contexts balance by
 // themselves; the parts of a segment that does not lie in one share are joined
-// by the last of its workgroups (few rows) or by combine_kernel (many rows,
-// whose parts are too large for one workgroup).  Where there are row tiles
-// enough, a workgroup takes a whole segment instead.
+// by the last of its workgroups (few rows; up to 64 with few parts) or by
+// combine_kernel (more rows, whose parts are too large for one workgroup).
+// Where no segment is much longer than a share, a workgroup takes a whole one
+// instead.
 struct Seq {
   int begin, n, len, rows_tiles, key_tiles;  // tokens, committed rows; key_tiles 1 where bad
   int bad;                                   // the outputs are NaN
