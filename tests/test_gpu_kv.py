@@ -414,6 +414,92 @@ def test_page_operations_follow_the_model(seqs, pages, page, max_pages, seed):
             model.fork(clear)
 
 
+def check_reserve(cache, model, n_new):
+    """Reserves on the device and on the model; tables, counts, statuses and
+    every page: a page that was given as a copy has its rows, the others are
+    bit for bit what they were."""
+    before, tables = cache.kv.clone(), [list(t) for t in model.table]
+    tms.kv_reserve(cache, dev32(n_new), check=False)
+    model.reserve(n_new)
+    table = np.full((cache.seqs, cache.max_pages), -1)
+    for s, t in enumerate(model.table):
+        table[s, :len(t)] = t
+    assert cache.status().tolist() == model.status
+    assert np.array_equal(cache.table.cpu().numpy(), table)
+    assert np.array_equal(cache.refs.cpu().numpy(), model.refs())
+    assert cache.held.tolist() == [len(t) for t in model.table]
+    assert cache.length.tolist() == [len(r) for r in model.rows]
+    for s, (old, now) in enumerate(zip(tables, model.table)):
+        last, fill = len(model.rows[s]) // cache.page_tokens, len(model.rows[s]) % cache.page_tokens
+        if last < len(old) and old[last] != now[last]:
+            before[:, now[last], :, :, :fill] = before[:, old[last], :, :, :fill]
+    assert torch.equal(before, cache.kv)
+
+
+@pytest.mark.parametrize("layers,kv_heads", [(1, 1), (3, 4)], ids=["in_the_plan", "by_a_launch"])
+def test_reserve_past_the_pool_refuses_everyone_after(layers, kv_heads):
+    """Demands that pass the whole pool: every later demand gets OOM too, with or
+    without a copy of its last page, and holds what it held; who asks for
+    nothing stays."""
+    for seqs, n_new in ((4, [60, 60, 3, 3]), (6, [200, 0, 3, 20, 1, 2]), (6, [9, 200, 0, 3, 3, -1]), (5, [3, 3, 400, 400, 3])):
+        print(f"reserve past the pool {layers} layers n_new {n_new}", flush=True)
+        cache = tms.PagedCache.empty(layers, 10, kv_heads, 8, 64, seqs, 60, dtype=F)
+        cache.kv.copy_(torch.arange(cache.kv.numel(), device="cuda").view(cache.kv.shape) % 1000003)
+        model = Pages(seqs, 10, 8, 60)
+        check_reserve(cache, model, [5] + [0] * (seqs - 1))
+        tms.kv_commit(cache, dev32([5] + [0] * (seqs - 1)))
+        model.commit([5] + [0] * (seqs - 1), None, [[1] * 5] + [[]] * (seqs - 1))
+        tms.kv_fork(cache, dev32([0] * seqs))
+        model.fork([0] * seqs)
+        check_reserve(cache, model, n_new)
+        assert model.status.count(Pages.OOM) >= 2
+        clear = [-1 if x else s for s, x in enumerate(model.status)]
+        tms.kv_fork(cache, dev32(clear))
+        model.fork(clear)
+        check_reserve(cache, model, [4] * seqs)
+
+
+@pytest.mark.parametrize("seqs,pages,max_pages,most", [(8, 12, 40, 100), (70, 90, 200, 400), (1500, 4000, 40, 60),
+                                                       (2500, 900, 40, 60), (4096, 9000, 30, 40)])
+def test_reserve_follows_the_model_in_pools_too_small(seqs, pages, max_pages, most):
+    """Also more sequences than the plan takes in one turn."""
+    rng = np.random.default_rng(seqs)
+    cache = tms.PagedCache.empty(2, pages, 1, 8, 64, seqs, max_pages)
+    cache.kv.copy_(torch.arange(cache.kv.numel(), device="cuda").view(cache.kv.shape) % 251)
+    model = Pages(seqs, pages, 8, max_pages)
+    for step in range(6):
+        print(f"reserve {seqs} sequences, {pages} pages, step {step}", flush=True)
+        check_reserve(cache, model, [int(x) for x in rng.integers(-2, most if step % 2 else 12, seqs)])
+        grown = [min(int(rng.integers(0, 20)), len(t) * 8 - len(r)) for t, r in zip(model.table, model.rows)]
+        tms.kv_commit(cache, dev32(grown), check=False)
+        model.commit(grown, None, [[1] * n for n in grown])
+        src = np.where(rng.random(seqs) < 0.4, rng.integers(-1, seqs, seqs), np.arange(seqs))
+        src = [-1 if model.status[s] and x == s else int(x) for s, x in enumerate(src)]
+        tms.kv_fork(cache, dev32(src), check=False)
+        model.fork(src)
+
+
+def test_reserve_from_a_pool_of_a_million_pages():
+    """2^20 pages and more: demands above 2^16 pages, summed in two halves."""
+    pages, max_pages = (1 << 20) + 77, 700000
+    cache = tms.PagedCache.empty(1, pages, 1, 8, 64, 5, max_pages)
+    for n_new, status in (([8 * 70000 - 3, 5, 8 * 650000, 8 * 400000, 9], [0, 0, 0, 9, 9]),
+                          ([8 * 65536, 8 * 65535, 0, 5, 5], [0, 0, 0, 0, 0])):
+        print(f"reserve {n_new} of {pages} pages", flush=True)
+        tms.kv_reserve(cache, dev32(n_new), check=False)
+        assert cache.status().tolist() == status
+        held = cache.held.tolist()
+        assert held == [-(-n // 8) if n > 0 and not x else 0 for n, x in zip(n_new, status)]
+        at = 0
+        for s, h in enumerate(held):  # ascending pages, sequence after sequence
+            assert torch.equal(cache.table[s, :h], torch.arange(at, at + h, dtype=torch.int32, device="cuda"))
+            assert (cache.table[s, h:] == -1).all()
+            at += h
+        assert (cache.refs[:at] == 1).all() and not cache.refs[at:].any()
+        tms.kv_fork(cache, dev32([-1] * 5))
+        assert not cache.refs.any() and (cache.table == -1).all() and not cache.held.any()
+
+
 def test_commit_moves_long_keep_lists_in_place():
     """Several hundred rows that overlap their targets, in every layer and head."""
     rng = np.random.default_rng(21)

@@ -25,7 +25,7 @@ struct ForkRec {
   int32_t length, pages, status, changed;
 };
 struct CopyRec {
-  int32_t from, to, rows, pad;
+  int32_t from, to, rows, pad;  // to: -1 where no page was given, and nothing is copied
 };
 
 __host__ __device__ inline int64_t round256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -171,7 +171,10 @@ __device__ inline void copy_piece(const KvCache& c, const CopyRec& r, int piece,
 // sums through LDS exchanges), 256 7.1.
 __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const int32_t* __restrict__ n_new, int elem_bytes,
                                                              int pieces) {
-  constexpr int kSplit = 1 << 30;  // of want: the last page is copied (pages of a sequence stay below 2^28)
+  // of want: the last page is copied; pages are asked for (pages of a sequence
+  // stay below 2^28).  begin cannot say the latter: it ends at pages + 1, and
+  // all sequences past that point begin and end there.
+  constexpr int kSplit = 1 << 30, kMore = 1 << 29;
   __shared__ int begin[4096 + 1];  // first page of the sequence's share of the free list
   __shared__ int want[4096];       // pages it holds afterwards; -1: left as it is
   const int tid = threadIdx.x;
@@ -198,6 +201,7 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
             ++more;
           }
         }
+        if (more) w |= kMore;
       }
     }
     // a demand above the whole pool never fits: cut there, up to 1024 of them
@@ -268,19 +272,15 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
   __syncthreads();
   for (int s = tid; s < c.seqs; s += kPlan) {
     if (want[s] < 0) continue;
-    if (begin[s + 1] > found && begin[s + 1] > begin[s]) {
-      c.status[s] = TMS_ERR_OOM;
-      recs[s].rows = 0;
-    } else {
-      c.held[s] = want[s] & (kSplit - 1);
-    }
+    if (want[s] & kMore && begin[s + 1] > found) c.status[s] = TMS_ERR_OOM;
+    else c.held[s] = want[s] & (kMore - 1);
   }
   if (pieces) {
     __threadfence_block();
     __syncthreads();
     for (int i = tid / kWave; i < c.seqs * pieces; i += kPlan / kWave) {
       const CopyRec r = recs[i / pieces];
-      if (r.rows > 0) copy_piece(c, r, i % pieces, elem_bytes, tid % kWave, kWave);
+      if (r.to >= 0) copy_piece(c, r, i % pieces, elem_bytes, tid % kWave, kWave);
     }
   }
 }
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
 __global__ __launch_bounds__(256) void copy_pages_kernel(KvCache c, int elem_bytes) {
   const int parts = 2 * c.kv_heads;
   const CopyRec r = copy_recs(c)[blockIdx.x / parts];
-  if (r.rows > 0) copy_piece(c, r, blockIdx.y * parts + blockIdx.x % parts, elem_bytes, threadIdx.x, 256);
+  if (r.to >= 0) copy_piece(c, r, blockIdx.y * parts + blockIdx.x % parts, elem_bytes, threadIdx.x, 256);
 }
 
 // Whether entry i of a sequence's keep list is out of order or past the rows
