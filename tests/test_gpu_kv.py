@@ -286,6 +286,25 @@ def test_caches_past_32_bits():
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 30, 300])
+def test_attention_row_numbers_at_the_end_of_32_bits_give_nan(dtype, new):
+    """A table that holds one page 2^25 - 1 times: rows that cannot be counted on
+    from are refused, and a short sequence beside them is not."""
+    print(f"attention {dtype} {new} tokens behind 2^31 - 64 rows", flush=True)
+    rng = np.random.default_rng(16)
+    small, ks, vs = filled(rng, dtype, 2, 64, 64, [70], [new])
+    most = 2 ** 25 - 1
+    table = torch.zeros((2, most), dtype=torch.int32, device="cuda")
+    table[1, :small.table.shape[1]] = small.table[0]
+    cache = tms.PagedCache(small.kv, table, dev32([64 * most - new, 70]), dev32([most, int(small.held[0])]), small.refs,
+                           dev32([0, 0]))
+    q = torch.from_numpy(rng.standard_normal((2 * new, 4, 64)).astype(np.float32)).to(dtype).cuda()
+    out = run_attention(cache, q, [new, new])
+    assert torch.isnan(out[:new].float()).all()
+    check_attention(q[new:], out[new:], ks, vs, [70], [new], 64 ** -0.5, None, dtype == BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("dim,n_freq,interleaved", [(64, 32, False), (64, 32, True), (128, 64, False), (128, 16, False),
                                                     (128, 16, True), (256, 128, False), (64, 0, False), (256, 8, True)])
 def test_write_matches_the_64_bit_form(dtype, dim, n_freq, interleaved):

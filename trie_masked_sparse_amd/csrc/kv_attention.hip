@@ -123,6 +123,11 @@ struct Seq {
   int bad;                                   // the outputs are NaN
 };
 
+// Rows of a sequence at most: row numbers are 32 bits, and the kernels count on
+// from the last one to the end of its row tile (256) and of the key tiles that
+// copies are planned for (four of 64).
+constexpr int64_t kMostRows = (int64_t(1) << 31) - 1024;
+
 __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, int rows, int keys) {
   Seq q{};
   q.begin = a.start[s];
@@ -132,7 +137,7 @@ __device__ inline Seq sequence(const KvCache& c, const KvAttention& a, int s, in
   q.len = c.length[s];
   const int64_t all = int64_t(q.len) + q.n;
   q.bad = c.status[s] != TMS_OK || q.n > a.max_new || q.len < 0 ||
-          all > int64_t(min(c.held[s], c.max_pages)) << c.page_shift;
+          all > min(int64_t(min(c.held[s], c.max_pages)) << c.page_shift, kMostRows);
   const int64_t r = int64_t(q.n) * (a.q_heads / c.kv_heads);
   q.rows_tiles = static_cast<int>((r + rows - 1) / rows);
   q.key_tiles = q.bad ? 1 : static_cast<int>((all + keys - 1) / keys);
