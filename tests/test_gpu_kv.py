@@ -212,6 +212,38 @@ def test_attention_rows_not_seen_may_hold_anything(dtype, heads, kind):
             assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (n, s)
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (4, 2, 128), (8, 2, 256), (32, 1, 128)], ids=lambda h: "x".join(map(str, h)))
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_attention_a_last_token_whose_value_is_not_finite(dtype, heads, kind):
+    """The last row of a sequence fills its key tile up: infinities of its own
+    value stay infinities in its columns, also where it is the only new token
+    or alone in its row tile."""
+    hq, hkv, D = heads
+    group = hq // hkv
+    for n, (lens, new) in enumerate((([0], [1]), ([40], [1]), ([63], [1]), ([5, 700, 31, 2000], [1, 1, 1, 1]), ([9000], [1]),
+                                     ([33, 3], [256 // group + 1, 1]), ([100], [2]), ([17], [64 // group + 1]))):
+        for most in (None, 200):  # also by the kernels for more rows
+            print(f"attention last value not finite {dtype} {heads} {kind} lens {lens} new {new} max_new {most}", flush=True)
+            rng = np.random.default_rng(500 + n)
+            cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)
+            # every draft follows the context itself: nobody else sees the last one
+            parents = [[-1] * b for b in new] if kind == "tree" else None
+            for s, (a, b) in enumerate(zip(lens, new)):
+                for column, value in ((3, np.inf), (21, -np.inf), (5, np.nan), (D - 1, np.inf)):
+                    set_row(cache, s, a + b - 1, 1, column, value)
+                    vs[s][a + b - 1, :, column] = value
+            q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+            out = run_attention(cache, q, new, parents, max_new=most and max(most, max(new))).double().cpu().numpy()
+            qd, at = q.double().cpu().numpy(), offsets(new)
+            for s, (a, b) in enumerate(zip(lens, new)):
+                want, bound = attention(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, parents and parents[s], dtype == BF)
+                got, fine = out[at[s]:at[s + 1]], np.isfinite(want)
+                assert np.isposinf(want).any() and np.isneginf(want).any() and np.isnan(want).any()
+                assert (np.abs(got[fine] - want[fine]) <= bound[fine]).all(), (n, s)
+                assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (n, s)
+
+
 def test_attention_parents_that_are_not_earlier_tokens_count_as_none():
     rng = np.random.default_rng(12)
     lens, new = [20], [6]

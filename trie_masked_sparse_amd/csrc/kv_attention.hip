@@ -438,7 +438,8 @@ __device__ inline void walk_tree(const KvAttention& a, const Seq& q, int tok0, i
 }
 
 // New rows of a segment that some of its query rows see and others do not: keys
-// first .. first + count - 1.  A value there that is not finite would reach all
+// first .. first + count - 1, the last of them also because its copies fill up
+// its tile, which no row sees.  A value there that is not finite would reach all
 // rows of a product, as 0 x inf or 0 x NaN.  So a segment whose outputs are not
 // all finite is worked through once more: such values are looked for, taken out
 // of the tiles in LDS, and added to the rows that see them at the end (looking
@@ -899,19 +900,18 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 
-    if (!again && mixed.count > 1 && !q.bad && end * KW > mixed.first) {
-      float z = 0.f;
+    float z = 0.f;
+    if (!again && !q.bad && end * KW > mixed.first)
 #pragma unroll
       for (int m = 0; m < MT; ++m) z = zero_or_nan(o[m], z);
-      if (__syncthreads_or(z != z)) {
-        again = 1, lo = lo_here;
-        continue;
-      }
+    // every wavefront is done with its tiles
+    if (__syncthreads_or(z != z)) {
+      again = 1, lo = lo_here;
+      continue;
     }
     again = 0;
     // the four wavefronts' parts joined; wavefront w ends with a quarter of
     // the columns
-    __syncthreads();
     f32x4* buf = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -1284,7 +1284,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       if (Behind && !behind) lds_barrier();
       lds_barrier();
     }
-    if (!again && kt0 < end && mixed.count > 1 && end * KT > mixed.first) {
+    if (!again && kt0 < end && end * KT > mixed.first) {
       const float z = zero_or_nan(o);
       if (__syncthreads_or(z != z)) {
         again = 1, lo = uniform(lo_here);
