@@ -481,7 +481,9 @@ tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, in
  * are fp32; bf16 weights of the second product are rounded to bf16
  * unnormalised, relative to their running maximum.  Keys and values that a
  * token does not see (other drafts' rows, later tokens', rows past the end)
- * may hold infinities and NaN.  The outputs of a sequence in error, with rows
+ * may hold infinities and NaN.  An infinite value of a new row stays infinite
+ * for the tokens that see it; of a committed row it becomes NaN where its
+ * weight is below what fp32 holds (0 x inf).  The outputs of a sequence in error, with rows
  * not reserved, with more than max_new tokens or with more than 2^31 - 1024
  * rows are NaN. */
 tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,

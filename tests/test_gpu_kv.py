@@ -244,6 +244,34 @@ def test_attention_a_last_token_whose_value_is_not_finite(dtype, heads, kind):
                 assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (n, s)
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (4, 2, 128), (8, 2, 256), (8, 1, 64)], ids=lambda h: "x".join(map(str, h)))
+def test_attention_an_infinite_value_behind_a_part_of_little_weight(dtype, heads):
+    """A draft's infinite value whose weight, and that of every key worked on
+    with it, is below what fp32 holds: the sum is infinite all the same."""
+    hq, hkv, D = heads
+    for n, (lens, new) in enumerate((([40], [1]), ([500], [3]), ([9000], [2]), ([3000, 70], [20, 9]), ([2000], [70]))):
+        print(f"attention infinite value of little weight {dtype} {heads} lens {lens} new {new}", flush=True)
+        rng = np.random.default_rng(600 + n)
+        cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype)
+        q[:, :, 0] = 64.0
+        for s, (a, b) in enumerate(zip(lens, new)):
+            for row in range(a + b):  # scores of the first row lead those of all later ones by hundreds
+                set_row(cache, s, row, 0, 0, 0.0 if row == 0 else -64.0)
+                ks[s][row, :, 0] = 0.0 if row == 0 else -64.0
+            set_row(cache, s, a + b - 1, 1, 7, np.inf)
+            vs[s][a + b - 1, :, 7] = np.inf
+        out = run_attention(cache, q.cuda(), new).double().cpu().numpy()
+        at = offsets(new)
+        for s, (a, b) in enumerate(zip(lens, new)):
+            last = out[at[s + 1] - 1]
+            assert np.isposinf(last[:, 7]).all(), (n, s, last[:, 7])
+            others = np.delete(out[at[s]:at[s + 1]], 7, 2)
+            want = np.repeat(np.delete(vs[s][0], 7, 1), hq // hkv, 0)[None]  # the first row has all the weight
+            assert (np.abs(others - want) <= (2.0 ** -8 if dtype == BF else 2.0 ** -18) * np.abs(want) + 2.0 ** -100).all(), (n, s)
+
+
 def test_attention_parents_that_are_not_earlier_tokens_count_as_none():
     rng = np.random.default_rng(12)
     lens, new = [20], [6]

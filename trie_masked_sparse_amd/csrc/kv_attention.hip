@@ -598,6 +598,11 @@ __device__ inline bool last_to_arrive(const KvCache& c, int first, int last) {
   return arrivals == uint32_t(last - first);
 }
 
+// Weight 2^x of a part (or half) of a row's keys beside the others.  Never 0: a
+// draft's infinite value stays infinite however little its part weighs, and
+// finite ones do not notice 2^-126.
+__device__ inline float part_weight(float x) { return fmaxf(exp2_fast(x), 0x1p-126f); }
+
 struct Sum {
   float top = -INFINITY, l = 0.f;
   f32x4 x{0.f, 0.f, 0.f, 0.f};
@@ -625,12 +630,12 @@ __device__ inline Sum sum_parts(const KvCache& c, int first, int w, int last, in
     float next = s.top;
 #pragma unroll
     for (int u = 0; u < kParts; ++u) next = fmaxf(next, t[u]);
-    const float at = next == -INFINITY ? 0.f : next, old = exp2_fast(s.top - at);
+    const float at = next == -INFINITY ? 0.f : next, old = part_weight(s.top - at);
     s.top = next;
     s.l *= old, s.x *= old;
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
-      const float now = exp2_fast(t[u] - at);
+      const float now = part_weight(t[u] - at);
       s.l += k[u] * now;
       s.x += y[u] * now;
     }
@@ -945,7 +950,7 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
       const float at = top == -INFINITY ? 0.f : top;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        weight[w] = exp2_fast(stat[w][0][m * 16 + col] - at);
+        weight[w] = part_weight(stat[w][0][m * 16 + col] - at);
         l += weight[w] * stat[w][1][m * 16 + col];
       }
       if (!whole && wave == 0 && g == 0) part_store<true>(to + m * 16 + col, top), part_store<true>(to + M + m * 16 + col, l);
@@ -1308,7 +1313,7 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       lds_barrier();
       if (ks == 0) {
         const float m1 = stat[rw * 64 + col], top = fmaxf(mx, m1), at = top == -INFINITY ? 0.f : top;
-        const float mine = exp2_fast(mx - at), other = exp2_fast(m1 - at);
+        const float mine = part_weight(mx - at), other = part_weight(m1 - at);
         mx = top;
         sum = sum * mine + stat[rw * 64 + 32 + col] * other;
 #pragma unroll
@@ -1440,7 +1445,7 @@ __global__ __launch_bounds__(256) void combine_kernel(KvCache c, KvAttention a, 
       const float at = top == -INFINITY ? 0.f : top;
       Sum all{top, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
       for (int o = 0; o < G; ++o) {
-        const float now = exp2_fast(stat[0][tid + o * (256 / G)] - at);
+        const float now = part_weight(stat[0][tid + o * (256 / G)] - at);
         all.l += stat[1][tid + o * (256 / G)] * now, all.x += values[tid + o * (256 / G)] * now;
       }
       store_joined<1, D>(a, c, j, M, row, column, all);
