@@ -458,9 +458,9 @@ tms_status tms_kv_reserve(const tms_kv* c, const int32_t* n_new, void* stream);
  * rows ldk, ldv apart.  q_weight, k_weight dev [D] or null; pos dev int32 [T]
  * and inv_freq dev fp32 [n_freq] (null with n_freq = 0).  The row strides are
  * multiples of 16 bytes; n_freq a multiple of 8, at most D/2.  Sums, angles
- * (reduced in fp64) and rotation are fp32 or wider, rounded once.  A row past
- * the pages held sets the sequence's status to INVALID_ARG and is not written
- * (reserving is also what makes a shared last page the sequence's own: reserve
+ * (reduced in fp64) and rotation are fp32 or wider, rounded once.  A sequence
+ * whose new rows do not all fit the pages held gets INVALID_ARG and none of
+ * them are written (reserving is also what makes a shared last page the sequence's own: reserve
  * after every fork, before writing). */
 tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, int32_t T, const void* q, int64_t ldq,
                         int32_t q_heads, void* q_out, const void* k, int64_t ldk, const void* v, int64_t ldv,

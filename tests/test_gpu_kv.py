@@ -415,6 +415,35 @@ def test_write_refuses_rows_that_are_not_reserved():
     assert (cache.status() == tms.OK).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_write_refuses_all_rows_of_a_sequence_that_does_not_fit(dtype):
+    """Not the ones that happen to come before its status is set: no row of it
+    is written, every row of the others is, and queries come out of all."""
+    hkv, hq, D, page = 2, 3, 128, 16
+    for lens, new, held in (([5, 0, 9], [20, 1000, 30], [2, 62, 3]), ([0] * 70, [2] * 70, [i % 3 for i in range(70)]),
+                            ([3, 30], [30, 3], [2, 3])):
+        print(f"write that does not fit {dtype} {len(lens)} sequences", flush=True)
+        rng = np.random.default_rng(len(lens))
+        cache, _, _ = filled(rng, dtype, hkv, D, page, lens, new, layers=2, layer=1, fill=3.0)
+        cache.held.copy_(dev32(held))
+        before, T, at = cache.kv.clone(), sum(new), offsets(new)
+        fused = torch.from_numpy(rng.standard_normal((T, hq + 2 * hkv, D)).astype(np.float32)).to(dtype).cuda()
+        q, k, v = fused.split([hq, hkv, hkv], 1)
+        q_out = torch.empty((T, hq, D), dtype=dtype, device="cuda")
+        tms.kv_write(cache, 1, k, v, dev32(at), q=q, q_out=q_out)
+        fits = [a + b <= page * h for a, b, h in zip(lens, new, held)]
+        assert not all(fits) and any(fits)
+        assert cache.status().tolist() == [tms.OK if x else tms.ERR_INVALID_ARG for x in fits]
+        table = cache.table.cpu().numpy()
+        for s, (a, b) in enumerate(zip(lens, new)):
+            if fits[s]:
+                row = np.arange(a, a + b)
+                where = torch.from_numpy(table[s, row // page]).long().cuda(), torch.from_numpy(row % page).cuda()
+                before[1][where[0], 0, :, where[1]] = k[at[s]:at[s + 1]]
+                before[1][where[0], 1, :, where[1]] = v[at[s]:at[s + 1]]
+        assert torch.equal(before, cache.kv) and torch.equal(q_out, q)
+
+
 def _live_rows(cache, s):
     page = cache.page_tokens
     n = int(cache.length[s])

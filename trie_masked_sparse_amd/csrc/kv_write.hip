@@ -56,13 +56,13 @@ struct Chunk<1> {
 
 // What a token's row depends on: its sequence s, the number of offsets
 // start[1..seqs] at or below t (seqs where there is none), and that sequence's
-// first token, committed and held rows and status.  A small write is a chain of
+// first token and the one past its last, committed and held rows and status.  A small write is a chain of
 // memory latencies, so every lane reads all of that of one sequence at once
 // (only with more than 64 sequences, at most 4096, after a read of the
 // blocks of 64).  Forks, drafts written into 8 layers and commits of 256
 // sequences: 204 -> 200 us.
 struct Place {
-  int s, begin, length, held, status;
+  int s, begin, end, length, held, status;
 };
 __device__ inline Place place_of(const KvCache& c, const int32_t* __restrict__ start, int t, int lane) {
   int block = 0;
@@ -73,8 +73,9 @@ __device__ inline Place place_of(const KvCache& c, const int32_t* __restrict__ s
   const int mine = min(block * kWave + lane, c.seqs - 1);
   const int end = start[mine + 1], begin = start[mine], length = c.length[mine], held = c.held[mine], status = c.status[mine];
   const int n = __popcll(__ballot(block * kWave + lane < c.seqs && end <= t)), at = min(n, kWave - 1);
-  return Place{block * kWave + n, __builtin_amdgcn_readlane(begin, at), __builtin_amdgcn_readlane(length, at),
-               __builtin_amdgcn_readlane(held, at), __builtin_amdgcn_readlane(status, at)};
+  return Place{block * kWave + n, __builtin_amdgcn_readlane(begin, at), __builtin_amdgcn_readlane(end, at),
+               __builtin_amdgcn_readlane(length, at), __builtin_amdgcn_readlane(held, at),
+               __builtin_amdgcn_readlane(status, at)};
 }
 
 // Heads that a wavefront has in flight: 64 / LPR of them to a load, kBatch
@@ -130,11 +131,13 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
       }
     }
   }
-  // where the token's keys and values go; null where they may not
+  // Where the token's keys and values go; null where they may not.  A sequence
+  // is refused as a whole: wavefronts that read its status before and after one
+  // of them sets it all decide alike.
   uint4* kv_row = nullptr;
   if (rows && at.s < c.seqs && at.status == TMS_OK) {
-    const int64_t row = int64_t(at.length) + (t - at.begin);
-    if (t >= at.begin && row < int64_t(min(at.held, c.max_pages)) << c.page_shift) {
+    const int64_t row = int64_t(at.length) + (t - at.begin), end = int64_t(at.length) + (min(at.end, a.T) - at.begin);
+    if (t >= at.begin && end <= int64_t(min(at.held, c.max_pages)) << c.page_shift) {
       const int32_t p = c.table[int64_t(at.s) * c.max_pages + (row >> c.page_shift)];
       if (p >= 0 && p < c.pages)
         kv_row = static_cast<uint4*>(c.kv) +
