@@ -459,9 +459,10 @@ tms_status tms_kv_reserve(const tms_kv* c, const int32_t* n_new, void* stream);
  * and inv_freq dev fp32 [n_freq] (null with n_freq = 0).  The row strides are
  * multiples of 16 bytes; n_freq a multiple of 8, at most D/2.  Sums, angles
  * (reduced in fp64) and rotation are fp32 or wider, rounded once.  A sequence
- * whose new rows do not all fit the pages held gets INVALID_ARG and none of
- * them are written (reserving is also what makes a shared last page the sequence's own: reserve
- * after every fork, before writing). */
+ * whose new rows do not all fit the pages held, or begin in a page that other
+ * sequences hold too, gets INVALID_ARG and none of them are written (reserving
+ * is also what makes a shared last page the sequence's own: reserve after every
+ * fork, before writing). */
 tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, int32_t T, const void* q, int64_t ldq,
                         int32_t q_heads, void* q_out, const void* k, int64_t ldk, const void* v, int64_t ldv,
                         const void* q_weight, const void* k_weight, float eps, const int32_t* pos,
@@ -496,7 +497,9 @@ tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64
  * keep null: the first n_keep[s].  length grows by n_keep[s] (dev int32
  * [seqs]; 0: all drafts dropped; negative: sequence left as it is) and the
  * pages past it are given back.  Indices that are not ascending or not
- * reserved set INVALID_ARG and leave the sequence unchanged. */
+ * reserved set INVALID_ARG and leave the sequence unchanged.  The rows have to
+ * be ones that the sequence wrote itself: those behind length in a page that a
+ * fork has brought are not looked for here. */
 tms_status tms_kv_commit(const tms_kv* c, const int32_t* n_keep, const int32_t* keep, int32_t keep_stride,
                          void* stream);
 

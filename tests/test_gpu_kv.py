@@ -444,6 +444,47 @@ def test_write_refuses_all_rows_of_a_sequence_that_does_not_fit(dtype):
         assert torch.equal(before, cache.kv) and torch.equal(q_out, q)
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_write_refuses_a_page_that_others_hold(dtype):
+    """After a fork and without a reserve the next rows would land in a page of
+    the other sequences too; with it, or from a page's edge on, they do not."""
+    rng = np.random.default_rng(31)
+    for rows in (40, 48, 5, 70):
+        cache = tms.PagedCache.empty(2, 40, 2, 16, 64, 4, 8, dtype=dtype)
+        cache.kv.fill_(2.0)
+        k = torch.from_numpy(rng.standard_normal((2, 100, 2, 64)).astype(np.float32)).to(dtype).cuda()
+        tms.kv_reserve(cache, dev32([rows + 20, 9, 0, 0]))
+        tms.kv_write(cache, 0, k[0, :rows + 9], k[1, :rows + 9], dev32([0, rows, rows + 9, rows + 9, rows + 9]))
+        tms.kv_commit(cache, dev32([rows, 9, 0, 0]))
+        tms.kv_fork(cache, dev32([0, 1, 0, 0]))
+        before = cache.kv.clone()
+        start = dev32([0, 0, 3, 33, 34])  # the sequence of 9 rows is its own, the others share
+        tms.kv_write(cache, 0, k[0, :34], k[1, :34], start)
+        # the copies' rows past the edge have no page yet either
+        assert cache.status().tolist() == [tms.OK, tms.OK, tms.ERR_INVALID_ARG, tms.ERR_INVALID_ARG], rows
+        page = int(cache.table[1, 0])
+        before[0, page, 0, :, 9:12], before[0, page, 1, :, 9:12] = k[0, :3].transpose(0, 1), k[1, :3].transpose(0, 1)
+        assert torch.equal(before, cache.kv)
+        tms.kv_fork(cache, dev32([0, 1, 0, -1]))
+        tms.kv_write(cache, 0, k[0, :3], k[1, :3], dev32([0, 1, 1, 3, 3]))
+        want = tms.ERR_INVALID_ARG  # the source shares as well, and what lies past the edge is not reserved here
+        assert cache.status().tolist() == [want, tms.OK, want, tms.OK], rows
+        assert torch.equal(before, cache.kv)
+        # given anew and reserved: pages of their own
+        cache.status_codes.zero_()
+        tms.kv_reserve(cache, dev32([30, 1, 30, 0]))
+        tms.kv_write(cache, 0, k[0, :61], k[1, :61], dev32([0, 30, 31, 61, 61]))
+        assert (cache.status() == tms.OK).all()
+        for s, at, length, n in ((0, 0, rows, 30), (1, 30, 9, 1), (2, 31, rows, 30)):
+            r = torch.arange(length, length + n, device="cuda")
+            page = cache.table[s].long()[r // 16]
+            assert torch.equal(cache.kv[0][page, 0, :, r % 16], k[0, at:at + n]), (rows, s)
+            r = torch.arange(length, device="cuda")  # the committed ones
+            page = cache.table[s].long()[r // 16]
+            first = {0: 0, 1: rows, 2: 0}[s]
+            assert torch.equal(cache.kv[0][page, 0, :, r % 16], k[0, first:first + length]), (rows, s)
+
+
 def _live_rows(cache, s):
     page = cache.page_tokens
     n = int(cache.length[s])

@@ -138,8 +138,13 @@ __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int wa
   if (rows && at.s < c.seqs && at.status == TMS_OK) {
     const int64_t row = int64_t(at.length) + (t - at.begin), end = int64_t(at.length) + (min(at.end, a.T) - at.begin);
     if (t >= at.begin && end <= int64_t(min(at.held, c.max_pages)) << c.page_shift) {
-      const int32_t p = c.table[int64_t(at.s) * c.max_pages + (row >> c.page_shift)];
-      if (p >= 0 && p < c.pages)
+      const int32_t* pages = c.table + int64_t(at.s) * c.max_pages;
+      const int32_t p = pages[row >> c.page_shift];
+      // the page that the committed rows end in may be others' too (a fork
+      // without a reserve); the ones behind it never are
+      const int32_t first = at.length & (c.page_tokens - 1) ? pages[at.length >> c.page_shift] : -1;
+      const bool shared = first >= 0 && first < c.pages && c.refs[first] > 1;
+      if (p >= 0 && p < c.pages && !shared)
         kv_row = static_cast<uint4*>(c.kv) +
                  ((int64_t(a.layer) * c.pages + p) * 2 * c.kv_heads * c.page_tokens + (row & (c.page_tokens - 1))) * LPR +
                  col;
