@@ -476,7 +476,7 @@ tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, in
  *   parent dev int32 [T]: itself and its ancestors, parent[t] being the index
  *     among its sequence's new tokens of the token it follows, -1 where it
  *     follows the committed rows (a tree of drafts; what is not the index of
- *     an earlier token counts as -1; max_new at most 1024).
+ *     an earlier token counts as -1; max_new, or T if less, at most 1024).
  * q, out dev [T][q_heads][D], q's rows ldq elements apart.  max_new: the most
  * tokens any sequence has (host; the launch is chosen by it).  Scores and sums
  * are fp32; bf16 weights of the second product are rounded to bf16

@@ -313,6 +313,31 @@ def test_attention_sequences_in_error_give_nan(dtype):
     check_attention(q[7:], out[7:], ks[3:], vs[3:], lens[3:], new[3:], 64 ** -0.5, None, dtype == BF)
 
 
+def test_attention_max_new_of_a_batch_of_trees():
+    """The limit of 1024 drafts is a tree's, not the batch's: without max_new,
+    on another stream too, and with a max_new above all tokens there are."""
+    rng = np.random.default_rng(17)
+    lens, new = [int(x) for x in rng.integers(0, 200, 64)], [31] * 63 + [3]
+    cache, ks, vs = filled(rng, BF, 2, 64, 16, lens, new)
+    q = torch.from_numpy(rng.standard_normal((sum(new), 4, 64)).astype(np.float32)).to(BF).cuda()
+    parents = [tree(rng, b) for b in new]
+    start, parent, side = dev32(offsets(new)), dev32([p for t in parents for p in t]), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for max_new, stream in ((None, None), (None, side), (31, None)):
+        out = torch.zeros_like(q)
+        side.wait_stream(torch.cuda.current_stream())
+        tms.kv_attention(cache, 0, q, start, out, parent=parent, max_new=max_new, stream=stream)
+        side.synchronize()
+        check_attention(q, out, ks, vs, lens, new, 64 ** -0.5, parents, True)
+    few, n = dev32([0, 31, 62] + [62] * 62), 62
+    out = torch.zeros_like(q[:n])
+    tms.kv_attention(cache, 0, q[:n], few, out, parent=parent[:n], max_new=5000)
+    check_attention(q[:n], out, ks[:2], vs[:2], lens[:2], new[:2], 64 ** -0.5, parents[:2], True)
+    with pytest.raises(tms.TmsError) as ei:  # a tree of all tokens is too large
+        tms.kv_attention(cache, 0, q, dev32([0] + [sum(new)] * 64), torch.zeros_like(q), parent=parent)
+    assert "1024" in str(ei.value)
+
+
 def test_caches_past_32_bits():
     """A pool of more than 2^32 bytes and 2^31 elements, pages at its end."""
     rng = np.random.default_rng(15)

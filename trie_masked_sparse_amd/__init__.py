@@ -629,16 +629,35 @@ def kv_write(cache: PagedCache, layer: int, k, v, start, q=None, q_out=None, q_w
         _check(rc, "kv_write")
 
 
+_MAX_TREE = 1024  # drafts of a tree
+
+
+def _longest(cache: PagedCache, start, stream, T: int) -> int:
+    """The most tokens of a sequence, read back from start on the call's stream;
+    T where that is being recorded into a graph."""
+    s = torch.cuda.ExternalStream(_kv_stream(cache, stream), device=cache.kv.device)
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return T
+        at = start.flatten()[:cache.seqs + 1].cpu()
+    return int((at[1:] - at[:-1]).max().clamp(1, T))
+
+
 def kv_attention(cache: PagedCache, layer: int, q, start, out, scale: float | None = None, parent=None,
                  max_new: int | None = None, stream=None):
     """Attention of the packed new tokens over the cache (tms_kv_attention):
     parent (int32 [T]) makes them a tree of drafts, without it they are causal.
     q, out: [T][q_heads][head_dim]; scale: head_dim ** -0.5 by default;
-    max_new: the most tokens of a sequence (T if not given).  Asynchronous."""
+    max_new: the most tokens of a sequence.  Give it: the kernels are chosen by
+    it, and without it (T) a batch of single tokens runs on those for whole
+    prompts.  Asynchronous, but for trees of more than 1024 tokens in all
+    without max_new, which read it from start."""
     dt, D = cache.dtype, cache.head_dim
     qp, T, hq, ldq = _token_rows(q, dt, D, "q")
-    rc = cache._c[3](cache.ref, layer, qp, ldq, hq, _sized(start, _int32, cache.seqs + 1, "start"), T,
-                     T if max_new is None else max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
+    at = _sized(start, _int32, cache.seqs + 1, "start")
+    if max_new is None:
+        max_new = _longest(cache, start, stream, T) if parent is not None and T > _MAX_TREE else T
+    rc = cache._c[3](cache.ref, layer, qp, ldq, hq, at, T, max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
                      D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"), _kv_stream(cache, stream))
     if rc:
         _check(rc, "kv_attention")

@@ -134,10 +134,11 @@ tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64
   if (q_heads < 1 || q_heads > 4096 || q_heads % c->kv_heads) return bad("q_heads must be a multiple of kv_heads, at most 4096");
   if (T == 0) return TMS_OK;
   if (max_new < 1) return bad("max_new must be positive");
-  if (parent && max_new > 1024) return bad("a tree of drafts has at most 1024 tokens");
+  if (max_new > T) max_new = T;
+  if (parent && max_new > 1024) return bad("a tree of drafts has at most 1024 tokens (max_new)");
   if (!rows_ok(c, q, ldq, q_heads) || !out || !aligned(out, 16))
     return bad("q or out null or not aligned, or the row stride of q too small or not a multiple of 16 bytes");
-  tms::KvAttention a{start, T, layer, max_new < T ? max_new : T, q, ldq, q_heads, parent, scale, out};
+  tms::KvAttention a{start, T, layer, max_new, q, ldq, q_heads, parent, scale, out};
   TMS_KV_HIP(tms::launch_kv_attention(view(c), a, static_cast<hipStream_t>(stream)), "kv attention launch");
   return TMS_OK;
 }
