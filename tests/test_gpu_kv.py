@@ -754,6 +754,34 @@ def test_a_whole_step_replays_in_a_graph():
             assert "recorded" in str(ei.value)
 
 
+def test_a_cache_dropped_while_another_stream_works_on_it():
+    """Its memory is handed on only when that stream is done, whichever stream
+    was current when the cache was made of them."""
+    side = torch.cuda.Stream()
+    for made_on in (torch.cuda.current_stream(), side):
+        kv = torch.zeros((1, 4096, 2, 2, 16, 64), device="cuda")
+        ints = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((1, 300000), 1, 1, 4096, 1)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(made_on):
+            cache = tms.PagedCache(kv, *ints)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # some tenths of a second
+            tms.kv_reserve(cache, torch.full((1,), 64, dtype=torch.int32, device="cuda"), check=False)
+        owned = [cache.kv, cache.table, cache.length, cache.held, cache.refs, cache.status_codes, cache.work]
+        shapes, places = [(t.shape, t.dtype) for t in owned], [t.data_ptr() for t in owned]
+        stream, done = torch.cuda.current_stream() if made_on == side else made_on, torch.cuda.Event()
+        done.record(side)
+        del cache, kv, ints, owned
+        with torch.cuda.stream(stream):
+            fresh = [torch.empty(a, dtype=b, device="cuda") for a, b in shapes]
+        early = [t.data_ptr() in places for t in fresh]
+        assert not done.query()
+        torch.cuda.synchronize()
+        assert not any(early), early
+        del fresh
+
+
 def test_binding_refusals():
     cache = tms.PagedCache.empty(2, 8, 2, 16, 64, 3, 4)
     start, q = dev32([0, 1, 1, 2]), torch.zeros((2, 4, 64), dtype=BF, device="cuda")

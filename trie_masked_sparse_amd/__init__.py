@@ -531,7 +531,7 @@ class PagedCache:
         _check(lib().tms_kv_work_bytes(C.byref(d), C.byref(need)), "PagedCache")
         self.work = torch.zeros(need.value, dtype=torch.uint8, device=kv.device)
         self._index = kv.device.index
-        self._made_on = torch._C._cuda_getCurrentRawStream(self._index)
+        self._streams = set()  # that work on the cache
         d.work, d.work_bytes = self.work.data_ptr(), need.value
         self.d = d
         self.ref = C.byref(d)
@@ -555,14 +555,17 @@ class PagedCache:
 
 
 def _kv_stream(cache: PagedCache, stream):
-    """The stream of a call; the work memory is told of streams other than the
-    one it was allocated on, so that it is not handed on while they use it."""
+    """The stream of a call; the cache's tensors are told of it the first time, so
+    that a cache that is dropped is not handed on while the stream works on it."""
     if stream is None:
         s = _raw_stream(cache._index)
     else:
         s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if s != cache._made_on:
-        cache.work.record_stream(torch.cuda.ExternalStream(s, device=cache.kv.device))
+    if s not in cache._streams:
+        on = torch.cuda.ExternalStream(s, device=cache.kv.device)
+        for t in (cache.kv, cache.table, cache.length, cache.held, cache.refs, cache.status_codes, cache.work):
+            t.record_stream(on)
+        cache._streams.add(s)
     return s
 
 
