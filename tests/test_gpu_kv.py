@@ -313,6 +313,21 @@ def test_attention_sequences_in_error_give_nan(dtype):
     check_attention(q[7:], out[7:], ks[3:], vs[3:], lens[3:], new[3:], 64 ** -0.5, None, dtype == BF)
 
 
+def test_one_token_of_a_projection_whose_width_is_odd():
+    """With one token there is no next row: the distance to it says nothing."""
+    rng = np.random.default_rng(18)
+    cache, ks, vs = filled(rng, BF, 2, 64, 16, [20], [1])
+    wide = torch.from_numpy(rng.standard_normal((1, 8 * 64 + 3)).astype(np.float32)).to(BF).cuda()
+    q, k, v = (wide.as_strided((1, b - a, 64), (wide.shape[1], 64, 1), a * 64) for a, b in ((0, 4), (4, 6), (6, 8)))
+    assert q.stride(0) % 8
+    out, q_out = torch.zeros((1, 4, 64), dtype=BF, device="cuda"), torch.zeros((1, 4, 64), dtype=BF, device="cuda")
+    tms.kv_write(cache, 0, k, v, dev32([0, 1]), q=q, q_out=q_out)
+    assert (cache.status() == tms.OK).all() and torch.equal(q_out, q)
+    tms.kv_attention(cache, 0, q, dev32([0, 1]), out, max_new=1)
+    ks[0][20], vs[0][20] = k[0].double().cpu().numpy(), v[0].double().cpu().numpy()
+    check_attention(q, out, ks, vs, [20], [1], 64 ** -0.5, None, True)
+
+
 def test_attention_max_new_of_a_batch_of_trees():
     """The limit of 1024 drafts is a tree's, not the batch's: without max_new,
     on another stream too, and with a max_new above all tokens there are."""

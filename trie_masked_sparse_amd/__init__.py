@@ -491,7 +491,7 @@ def _token_rows(t, dtype, dim: int, name: str):
     row, head, one = t.stride()
     if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), T, heads, row if T > 1 else max(row, heads * dim)
+    return t.data_ptr(), T, heads, row if T > 1 else heads * dim  # one token: no next row
 
 
 class PagedCache:
