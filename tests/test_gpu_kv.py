@@ -713,6 +713,29 @@ def test_commit_moves_long_keep_lists_in_place():
         assert cache.length.tolist() == [650, 0] and cache.held.tolist() == [41, 0]
 
 
+@pytest.mark.parametrize("seqs", [1, 130])
+def test_commit_moves_chunks_of_the_narrowest_rows(seqs):
+    """Rows of 128 bytes: 256 to a chunk, with lists of one row more and less,
+    by one workgroup for all pieces of a sequence or by several."""
+    rng = np.random.default_rng(23)
+    for n, kept, layers in ((257, 256, 1), (260, 257, 1), (600, 513, 9), (256, 255, 9)):
+        print(f"commit {seqs} sequences keep {kept} of {n} rows, {layers} layers", flush=True)
+        cache = tms.PagedCache.empty(layers, seqs * 40, 1, 16, 64, seqs, 40)
+        tms.kv_reserve(cache, dev32([n] * seqs))
+        k = torch.from_numpy(rng.standard_normal((2, seqs * n, 1, 64)).astype(np.float32)).to(BF).cuda()
+        for layer in range(layers):
+            tms.kv_write(cache, layer, k[layer % 2], k[1 - layer % 2], dev32(np.arange(seqs + 1) * n))
+        keep = np.stack([np.sort(rng.permutation(n)[:kept]) for _ in range(seqs)])
+        tms.kv_commit(cache, dev32([kept] * seqs), dev32(keep))
+        assert cache.length.tolist() == [kept] * seqs
+        r = torch.arange(kept, device="cuda")
+        for s in range(seqs):
+            page, at = cache.table[s].long()[r // 16], torch.from_numpy(keep[s] + s * n).cuda()
+            for layer in range(layers):
+                assert torch.equal(cache.kv[layer][page, 0, :, r % 16], k[layer % 2][at]), (s, layer)
+                assert torch.equal(cache.kv[layer][page, 1, :, r % 16], k[1 - layer % 2][at]), (s, layer)
+
+
 def test_a_whole_step_replays_in_a_graph():
     """Fork, reserve, write, attend and commit recorded once: every replay
     gives the eager results (the branches start from the same root each time)."""

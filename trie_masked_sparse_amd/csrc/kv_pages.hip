@@ -305,7 +305,8 @@ __device__ inline bool keep_bad(const KvCache& c, int s, const int32_t* keep, in
 // ascending list never moves a row upwards, so the rows of a chunk may be
 // written once all of them have been read: later chunks read only rows at or
 // past their own targets.
-constexpr int kRows = 512;  // rows of a chunk at most
+constexpr int kRows = 256 * kFlight / 8;  // of a chunk at most: a row has at least 8 words
+static_assert(kRows <= 256, "a thread for each row of a chunk");
 
 __device__ inline void move_rows(const KvCache& c, const int32_t* n_keep, const int32_t* keep_all, int keep_stride,
                                  int elem_bytes, int s, int p0, int pieces) {
@@ -329,25 +330,24 @@ __device__ inline void move_rows(const KvCache& c, const int32_t* n_keep, const 
   auto place = [&](int piece, int page, int slot, int w) {
     return (((int64_t(piece / parts) * c.pages + page) * parts + piece % parts) * c.page_tokens + slot) * words + w;
   };
-  const int most = min(kRows, (256 * kFlight) >> shift);  // a chunk of one piece is in flight at once
+  const int most = (256 * kFlight) >> shift;  // a chunk of one piece is in flight at once
   for (int j0 = 0; j0 < n; j0 += most) {
     // the chunk's rows that move, packed in their order
     __syncthreads();
     if (threadIdx.x == 0) count = 0;
     __syncthreads();
     const int in = min(most, n - j0);
-    for (int base = 0; base < in; base += 256) {  // `in` is at most 512: two turns
-      const int j = j0 + base + threadIdx.x, k = base + static_cast<int>(threadIdx.x) < in ? keep[j] : 0;
-      int32_t fp = -1, tp = -1;
-      if (base + static_cast<int>(threadIdx.x) < in && k != j) {
-        fp = row[(len + k) >> c.page_shift], tp = row[(len + j) >> c.page_shift];
-        if (!page_ok(c, fp) || !page_ok(c, tp)) fp = -1;
-      }
-      if (fp >= 0) {
-        const int at = atomicAdd(&count, 1);  // any order: a chunk is read whole before it is written
-        from_page[at] = fp, to_page[at] = tp;
-        from_slot[at] = (len + k) & (c.page_tokens - 1), to_slot[at] = (len + j) & (c.page_tokens - 1);
-      }
+    const bool mine = static_cast<int>(threadIdx.x) < in;
+    const int j = j0 + threadIdx.x, k = mine ? keep[j] : 0;
+    int32_t fp = -1, tp = -1;
+    if (mine && k != j) {
+      fp = row[(len + k) >> c.page_shift], tp = row[(len + j) >> c.page_shift];
+      if (!page_ok(c, fp) || !page_ok(c, tp)) fp = -1;
+    }
+    if (fp >= 0) {
+      const int at = atomicAdd(&count, 1);  // any order: a chunk is read whole before it is written
+      from_page[at] = fp, to_page[at] = tp;
+      from_slot[at] = (len + k) & (c.page_tokens - 1), to_slot[at] = (len + j) & (c.page_tokens - 1);
     }
     __syncthreads();
     const int rows = count;
