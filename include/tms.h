@@ -407,6 +407,7 @@ tms_status tms_decode_k_pointers_noalloc(const tms_trie* trie, const void* emb, 
  * tms_status): the calls leave a sequence in error unchanged until tms_kv_fork
  * gives it new content.  Calls on one descriptor share its work memory and its
  * tables: on several streams the caller orders them. */
+#define TMS_KV_WORK_ZERO 2048
 typedef struct {
   void* kv;         /* dev [layers][pages][2][kv_heads][page_tokens][head_dim]: keys, then values, of a page */
   int32_t* table;   /* dev [seqs][max_pages]: pages of every sequence, -1 past held */
@@ -414,7 +415,8 @@ typedef struct {
   int32_t* held;    /* dev [seqs]: pages held (reserved ones included) */
   int32_t* refs;    /* dev [pages]: reference counts */
   int32_t* status;  /* dev [seqs]: tms_status */
-  void* work;       /* dev, 256-byte aligned: at least tms_kv_work_bytes, zeroed before the first call */
+  void* work;       /* dev, 256-byte aligned: at least tms_kv_work_bytes, the first TMS_KV_WORK_ZERO of them zeroed
+                       before the first call (every call leaves them zero) */
   int64_t work_bytes;
   int32_t dtype;    /* tms_dtype of kv, queries, outputs and norm weights */
   int32_t layers, pages, kv_heads, page_tokens, head_dim, seqs, max_pages;

@@ -178,6 +178,35 @@ def test_attention_of_every_kind_of_batch(dtype, case):
         assert not cache.work[:2048].any()
 
 
+def test_the_work_memory_behind_its_counters_may_hold_anything():
+    """Only the counters have to be zero, and are zero again after every call."""
+    cache = tms.PagedCache.empty(1, 4, 2, 16, 256, 1, 4)
+    assert not cache.work[:tms.KV_WORK_ZERO].any()
+    for case in (0, 5, 7, 12, 21, 22, 24, 26, 29, 31):
+        hq, hkv, D, lens, new, trees = BATCHES[case]
+        for dtype in (BF, F):
+            print(f"work memory {dtype} {BATCHES[case][:3]} {len(new)} sequences", flush=True)
+            rng = np.random.default_rng(700 + case)
+            cache, ks, vs = filled(rng, dtype, hkv, D, 32, lens, new)
+            q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+            parents = [tree(rng, b) for b in new] if trees else None
+            want = run_attention(cache, q, new, parents)
+            for byte in (0xff, 0x7f):
+                cache.work[tms.KV_WORK_ZERO:] = byte
+                assert torch.equal(run_attention(cache, q, new, parents), want)
+                assert not cache.work[:tms.KV_WORK_ZERO].any()
+            cache.work[tms.KV_WORK_ZERO:] = 0xff
+            src, n_keep = list(range(len(new))), [min(b, 1) for b in new]
+            src[0] = len(new) - 1
+            tms.kv_fork(cache, dev32(src), check=False)
+            cache.work[tms.KV_WORK_ZERO:] = 0xff
+            tms.kv_reserve(cache, dev32([1] * len(new)), check=False)
+            tms.kv_commit(cache, dev32(n_keep), check=False)
+            assert all(x in (tms.OK, tms.ERR_OOM) for x in cache.status().tolist())
+            held = torch.bincount(cache.table[cache.table >= 0].long(), minlength=cache.pages)
+            assert torch.equal(held.int(), cache.refs) and not cache.work[:tms.KV_WORK_ZERO].any()
+
+
 def set_row(cache, s, row, which, column, value):
     page = cache.kv.shape[4]
     cache.kv[0, int(cache.table[s, row // page]), which, :, row % page, column] = value

@@ -80,6 +80,13 @@ def test_null_arguments_and_strides():
     assert L.tms_kv_attention(r, 0, P, 256, 4, P, 0, 1, None, 1.0, P, None) == tms.OK
 
 
+def test_the_zeroed_part_of_the_work_memory_is_the_headers():
+    import os
+    import re
+    header = open(os.path.join(os.path.dirname(tms.__file__), os.pardir, "include", "tms.h")).read()
+    assert tms.KV_WORK_ZERO == int(re.search(r"#define TMS_KV_WORK_ZERO (\d+)", header).group(1))
+
+
 def test_the_plain_forms():
     """The oracles against cases worked out by hand."""
     assert ancestors([-1, 0, 0, 2, 7]).tolist() == [

@@ -52,6 +52,7 @@ EXPORTS = (
     "tms_status_str", "tms_last_error",
 )
 NOREPEAT_LIVE, NOREPEAT_BITMASK = 0, 1
+KV_WORK_ZERO = 2048  # bytes of the work memory that are zero between calls
 STEP_GROUP_AUTO, STEP_GROUP_OFF, STEP_GROUP_ROOT, STEP_GROUP_NODES = 0, 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -529,7 +530,8 @@ class PagedCache:
                          self.max_pages)
         need = C.c_int64()
         _check(lib().tms_kv_work_bytes(C.byref(d), C.byref(need)), "PagedCache")
-        self.work = torch.zeros(need.value, dtype=torch.uint8, device=kv.device)
+        self.work = torch.empty(need.value, dtype=torch.uint8, device=kv.device)
+        self.work[:KV_WORK_ZERO].zero_()
         self._index = kv.device.index
         self._streams = set()  # that work on the cache
         d.work, d.work_bytes = self.work.data_ptr(), need.value

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include "tms.h"
+
 namespace tms {
 
 // Device view of a tms_kv (same fields, sizes with their shift).
@@ -21,7 +23,7 @@ struct KvCache {
 //   fork:    int32 table rows [seqs][max_pages], then {length, pages, status, changed} [seqs]
 //   reserve: int32 free pages [pages], then {from, to, rows, 0} [seqs]
 //   attention: see kv_attention.hip
-constexpr int64_t kWorkCounts = 2048;
+constexpr int64_t kWorkCounts = TMS_KV_WORK_ZERO;
 int64_t kv_page_work_bytes(const KvCache& c);
 int64_t kv_attention_work_bytes(const KvCache& c);
 
