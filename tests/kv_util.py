@@ -74,6 +74,16 @@ def attention(q, k, v, length, scale, parent, bf16):
     return out, bound
 
 
+def marked_values(rows, kv_heads, dim, block=16):
+    """V whose rows of `block` are 1 in a column of their own, 0 elsewhere (the
+    columns in turn): an output's column is the weight of its blocks alone, so
+    a block that is left out, or counted twice, shows as a share of the column
+    that far outgrows the bound, which is relative to the column too."""
+    v = np.zeros((rows, kv_heads, dim))
+    v[np.arange(rows), :, np.arange(rows) // block % dim] = 1.0
+    return v
+
+
 def head(x, weight, eps, pos, inv_freq, interleaved, bf16):
     """(out, bound) of x [T][heads][D] in fp64."""
     D = x.shape[-1]

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import trie_masked_sparse_amd as tms
-from kv_util import Pages, attention, head
+from kv_util import Pages, attention, head, marked_values
 
 pytestmark = pytest.mark.gpu
 
@@ -176,6 +176,42 @@ def test_attention_of_every_kind_of_batch(dtype, case):
         out = run_attention(cache, q, new, parents)
         check_attention(q, out, ks, vs, lens, new, D ** -0.5, parents, dtype == BF, case)
         assert not cache.work[:2048].any()
+
+
+LONG = [
+    (8, 2, 64, [20000, 3], [1, 1], False),
+    (16, 1, 128, [20000], [1], False),
+    (8, 4, 128, [30000], [8], True),                      # 17 .. 64 rows, many parts
+    (4, 1, 256, [30000, 100], [16, 2], False),
+    (8, 1, 64, [30000], [16], True),                      # 65 .. 128
+    (8, 1, 128, [20000, 0, 500], [63, 5, 1], True),       # over 128
+    (4, 2, 256, [20000], [80], True),
+    (2, 2, 128, [20000], [600], True),
+    (16, 8, 128, [4096] * 40, [1] * 40, False),
+    (16, 8, 128, [2048, 2000, 63, 0] * 12, [9, 20, 31, 5] * 12, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(LONG) + len(BATCHES)))
+def test_attention_counts_every_key_once(dtype, case):
+    """Values that tell the blocks of 16 keys apart: no tile, share or part is
+    left out or counted twice, however small its part of the whole."""
+    hq, hkv, D, lens, new, trees = (LONG + BATCHES)[case]
+    print(f"attention marked {dtype} {hq, hkv, D} {len(new)} sequences, longest {max(lens)}, trees {trees}", flush=True)
+    rng = np.random.default_rng(800 + case)
+    cache, ks, vs = filled(rng, dtype, hkv, D, 32, lens, new)
+    for s, (a, b) in enumerate(zip(lens, new)):
+        if a + b == 0:
+            continue
+        vs[s] = marked_values(a + b, hkv, D)
+        values = torch.zeros((-(-(a + b) // 32) * 32, hkv, D))
+        values[:a + b] = torch.from_numpy(vs[s]).float()
+        pages = cache.table[s, :len(values) // 32].long()
+        cache.kv[0, pages, 1] = values.unflatten(0, (-1, 32)).transpose(1, 2).to(dtype).cuda()
+    q = torch.from_numpy(0.7 * rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+    parents = [tree(rng, b) for b in new] if trees else None
+    check_attention(q, run_attention(cache, q, new, parents), ks, vs, lens, new, D ** -0.5, parents, dtype == BF, case)
 
 
 def test_the_work_memory_behind_its_counters_may_hold_anything():

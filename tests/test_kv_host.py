@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import trie_masked_sparse_amd as tms
-from kv_util import Pages, ancestors, attention, head
+from kv_util import Pages, ancestors, attention, head, marked_values
 
 
 def descriptor(**over):
@@ -85,6 +85,24 @@ def test_the_zeroed_part_of_the_work_memory_is_the_headers():
     import re
     header = open(os.path.join(os.path.dirname(tms.__file__), os.pardir, "include", "tms.h")).read()
     assert tms.KV_WORK_ZERO == int(re.search(r"#define TMS_KV_WORK_ZERO (\d+)", header).group(1))
+
+
+@pytest.mark.parametrize("length,new,dim,bf16", [(20000, 18, 64, True), (30000, 2, 64, True), (15000, 30, 128, False),
+                                                 (9000, 60, 256, True), (700, 3, 64, False)])
+def test_marked_values_show_any_block_left_out_or_counted_twice(length, new, dim, bf16):
+    """Mistakes planted in the plain form: keys of 16 or more dropped or twice."""
+    rng = np.random.default_rng(length)
+    q, k = 0.7 * rng.standard_normal((new, 1, dim)), rng.standard_normal((length + new, 1, dim))
+    v = marked_values(length + new, 1, dim)
+    want, bound = attention(q, k, v, length, dim ** -0.5, None, bf16)
+    for size in (16, 32, 64, 128):
+        for t in rng.integers(0, length // size, 5) * size:
+            keep = np.r_[0:t, t + size:length + new]
+            out, _ = attention(q, k[keep], v[keep], length - size, dim ** -0.5, None, bf16)
+            assert (np.abs(out - want) > 2 * bound).any(axis=(1, 2)).all(), (size, t)
+            twice = np.r_[0:t + size, t:length + new]
+            out, _ = attention(q, k[twice], v[twice], length + size, dim ** -0.5, None, bf16)
+            assert (np.abs(out - want) > 2 * bound).any(axis=(1, 2)).all(), (size, t)
 
 
 def test_the_plain_forms():
