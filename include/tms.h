@@ -481,12 +481,14 @@ tms_status tms_kv_write(const tms_kv* c, int32_t layer, const int32_t* start, in
  *     an earlier token counts as -1; max_new, or T if less, at most 1024).
  * q, out dev [T][q_heads][D], q's rows ldq elements apart.  max_new: the most
  * tokens any sequence has (host; the launch is chosen by it).  Scores and sums
- * are fp32; bf16 weights of the second product are rounded to bf16
- * unnormalised, relative to their running maximum.  Keys and values that a
+ * are fp32.  In bf16, the weights of the second product, unnormalised and
+ * relative to their running maximum, keep 16 bits where max_new * q_heads /
+ * kv_heads is at most 64, and are rounded to bf16 (8 bits) above; fp32 ones stay
+ * fp32.  Keys and values that a
  * token does not see (other drafts' rows, later tokens', rows past the end)
  * may hold infinities and NaN.  An infinite value of a new row stays infinite
  * for the tokens that see it; of a committed row it becomes NaN where its
- * weight is below what fp32 holds (0 x inf).  The outputs of a sequence in error, with rows
+ * weight is below 2^-100 of the largest (0 x inf).  The outputs of a sequence in error, with rows
  * not reserved, with more than max_new tokens or with more than 2^31 - 1024
  * rows are NaN. */
 tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,

@@ -214,6 +214,28 @@ def test_attention_counts_every_key_once(dtype, case):
     check_attention(q, run_attention(cache, q, new, parents), ks, vs, lens, new, D ** -0.5, parents, dtype == BF, case)
 
 
+@pytest.mark.parametrize("heads", [(4, 4, 64), (16, 8, 128), (8, 1, 128), (10, 2, 256), (8, 2, 64)],
+                         ids=lambda h: "x".join(map(str, h)))
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_attention_weights_of_up_to_64_rows_keep_16_bits(heads, kind):
+    """Outputs near 0 beside values of 1: no more than the rounding of the output
+    and 2^-15 of each weight."""
+    hq, hkv, D = heads
+    most = 64 // (hq // hkv)
+    for n, (lens, new) in enumerate((([60], [1]), ([700, 0, 90], [1, 1, 1]), ([5, 333], [most // 4, most // 8]), ([4000], [most]),
+                                     ([100, 60, 1000], [most // 2, 1, most]), ([9000], [most // 4]))):
+        print(f"attention 16 bits {heads} {kind} lens {lens} new {new}", flush=True)
+        rng = np.random.default_rng(900 + n)
+        cache, ks, vs = filled(rng, BF, hkv, D, 16, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(BF).cuda()
+        parents = [tree(rng, b) for b in new] if kind == "tree" else None
+        out, qd, at = run_attention(cache, q, new, parents).double().cpu().numpy(), q.double().cpu().numpy(), offsets(new)
+        for s, (a, b) in enumerate(zip(lens, new)):
+            want, bound = attention(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, parents and parents[s], True, fine=True)
+            err = np.abs(out[at[s]:at[s + 1]] - want)
+            assert (err <= bound).all(), (n, s, float((err / bound).max()))
+
+
 def test_the_work_memory_behind_its_counters_may_hold_anything():
     """Only the counters have to be zero, and are zero again after every call."""
     cache = tms.PagedCache.empty(1, 4, 2, 16, 256, 1, 4)
@@ -335,6 +357,35 @@ def test_attention_an_infinite_value_behind_a_part_of_little_weight(dtype, heads
             others = np.delete(out[at[s]:at[s + 1]], 7, 2)
             want = np.repeat(np.delete(vs[s][0], 7, 1), hq // hkv, 0)[None]  # the first row has all the weight
             assert (np.abs(others - want) <= (2.0 ** -8 if dtype == BF else 2.0 ** -18) * np.abs(want) + 2.0 ** -100).all(), (n, s)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (4, 2, 128), (8, 2, 256), (8, 1, 64)], ids=lambda h: "x".join(map(str, h)))
+def test_attention_infinite_values_of_committed_rows(dtype, heads):
+    """All tokens see them: infinite in their columns, NaN where both signs are."""
+    hq, hkv, D = heads
+    for n, (lens, new) in enumerate((([40], [1]), ([70, 3, 20], [1, 1, 1]), ([3000, 70], [6, 9]), ([9000], [2]), ([500], [30]),
+                                     ([333, 2000], [90, 3]), ([700], [400]))):
+        for rows_alike in (False, True):
+            print(f"attention infinite committed {dtype} {heads} lens {lens} new {new}", flush=True)
+            rng = np.random.default_rng(1000 + n)
+            cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)
+            q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype)
+            if rows_alike:  # weights that are powers of two: nothing is left of them in fewer bits
+                q.zero_()
+            for s, a in enumerate(lens):
+                for row, column, value in ((0, 3, np.inf), (a - 1, 21, -np.inf), (a // 2, 5, np.inf), (a // 3, 5, -np.inf),
+                                           (a // 2, D - 1, np.inf), (a - 1, D - 1, np.inf), (1, 9, np.nan)):
+                    set_row(cache, s, row, 1, column, value)
+                    vs[s][row, :, column] = value
+            out = run_attention(cache, q.cuda(), new).double().cpu().numpy()
+            qd, at = q.double().numpy(), offsets(new)
+            for s, (a, b) in enumerate(zip(lens, new)):
+                want, bound = attention(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, None, dtype == BF)
+                got, fine = out[at[s]:at[s + 1]], np.isfinite(want)
+                assert np.isposinf(want[:, :, [3, D - 1]]).all() and np.isneginf(want[:, :, 21]).all()
+                assert (np.abs(got[fine] - want[fine]) <= bound[fine]).all(), (n, s)
+                assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (n, s)
 
 
 def test_attention_parents_that_are_not_earlier_tokens_count_as_none():

@@ -92,6 +92,19 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// 8 weights cut to bf16, and what that leaves of them, rounded: together within
+// 2^-15 of each.  Of a weight that is not 0 both are above 0 (2^-24 of it is
+// added for that), so an infinite value times them is infinite.
+__device__ inline void split_bf16(const float (&x)[8], u32x4* high, u32x4* low) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __float_as_uint(x[2 * i]), b = __float_as_uint(x[2 * i + 1]) & 0xffff0000u;
+    (*high)[i] = b | a >> 16;
+    (*low)[i] = pack_bf16(fmaf(x[2 * i], 0x1p-24f, x[2 * i] - __uint_as_float(a & 0xffff0000u)),
+                          fmaf(x[2 * i + 1], 0x1p-24f, x[2 * i + 1] - __uint_as_float(b)));
+  }
+}
+
 // 4 values at element i of an output.
 template <int DT>
 __device__ inline void store4(void* out, int64_t i, f32x4 x) {
@@ -843,7 +856,11 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
             for (int e = 0; e < 4; ++e) sc[m][i][e] = word >> (16 * i + e) & 1 ? sc[m][i][e] : -INFINITY;
         }
       }
-      u32x4 pw[MT];  // bf16 weights, the keys of both halves in the order of V below
+      // Weights in two parts of bf16, the keys of both halves in the order of V
+      // below: 16 bits of each take one product more, up to 1 % here (256 tokens
+      // behind 10 to 4000 keys 147.3 -> 148.2 us, 64 behind 1000 48.3 -> 48.8, 8
+      // behind 40000 to 60000 298 -> 299).
+      u32x4 pw[MT], pl[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         float top = sc[m][0][0];
@@ -868,8 +885,8 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
             sum[m] += sc[m][i][e];
           }
         if constexpr (DT == 1)
-          pw[m] = u32x4{pack_bf16(sc[m][0][0], sc[m][0][1]), pack_bf16(sc[m][0][2], sc[m][0][3]),
-                        pack_bf16(sc[m][1][0], sc[m][1][1]), pack_bf16(sc[m][1][2], sc[m][1][3])};
+          split_bf16({sc[m][0][0], sc[m][0][1], sc[m][0][2], sc[m][0][3], sc[m][1][0], sc[m][1][1], sc[m][1][2], sc[m][1][3]},
+                     &pw[m], &pl[m]);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (odd) {
@@ -890,8 +907,10 @@ __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention
           const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
           const bf16x8 va = __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)));
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int m = 0; m < MT; ++m) {
+            o[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, __builtin_bit_cast(bf16x8, pl[m]), o[m][d], 0, 0, 0);
             o[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, __builtin_bit_cast(bf16x8, pw[m]), o[m][d], 0, 0, 0);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1019,7 +1038,7 @@ int tree_words(int group) {
 template <int D, int RW, int KS, bool AnyTree>
 __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words, int join) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
-  constexpr bool Behind = W == 8;
+  constexpr bool Behind = W == 8, Fine = KS == 2;
   constexpr int KT = 64, TileWords = KT * CH;       // keys of a tile, its 16-byte words
   constexpr int NB = KT / 32 / KS;                  // 32-key blocks of a tile for each wavefront
   constexpr int Ahead = Behind ? 2 : 1;             // tiles that the copies run ahead
@@ -1215,8 +1234,13 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
       }
       const float at = mx == -INFINITY ? 0.f : mx;
       // the weights, and between them the copies of a step: all at once they
-      // would wait for each other's way to LDS
-      u32x4 pw[2 * NB];
+      // would wait for each other's way to LDS.  Up to 64 rows they keep 16 bits,
+      // in two parts (15 to 20 drafts behind 64 contexts of 1201 to 2500 tokens 98 ->
+      // 102 us, 5 to 31 95.1 -> 96.5); more rows are bound by the products, so theirs are
+      // rounded to bf16, as the values that they weigh are (in two parts three
+      // prompts of 2300 to 4097 tokens 322 -> 474 us, 63 drafts behind 90000 to
+      // 120000 keys 253 -> 358).
+      u32x4 pw[2 * NB], pl[2 * NB];
 #pragma unroll
       for (int j = 0; j < 2 * NB; ++j) {
         float w[8];
@@ -1224,7 +1248,8 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
         for (int e = 0; e < 8; ++e) {
           w[e] = exp2_fast(fmaf(sc[j / 2][j % 2 * 8 + e], scale, -at));
         }
-        pw[j] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+        if constexpr (Fine) split_bf16(w, &pw[j], &pl[j]);
+        else pw[j] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
 #pragma unroll
         for (int i = j * P / NB; i < (j + 1) * P / NB; ++i) ask(kt, i);
         __builtin_amdgcn_sched_barrier(0);
@@ -1272,6 +1297,10 @@ __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_k
         __builtin_amdgcn_sched_barrier(0);
         if (i < PV) {
           const int j = i / DB, d = i % DB;
+          if constexpr (Fine) {
+            if (d == 0) total_w = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, __builtin_bit_cast(bf16x8, pl[j]), total_w, 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], __builtin_bit_cast(bf16x8, pl[j]), o[d], 0, 0, 0);
+          }
           if (d == 0) total_w = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, __builtin_bit_cast(bf16x8, pw[j]), total_w, 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
         } else {
