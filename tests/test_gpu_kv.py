@@ -719,6 +719,12 @@ def test_page_operations_follow_the_model(seqs, pages, page, max_pages, seed):
             model.fork(clear)
 
 
+@pytest.mark.parametrize("seqs,pages,page,max_pages,seed", [(16, 200, 8, 1025, 5), (33, 400, 8, 15, 6), (33, 400, 8, 16, 7),
+                                                            (64, 700, 8, 8, 8), (64, 2000, 8, 60, 9)])
+def test_page_operations_where_the_fork_changes_its_form(seqs, pages, page, max_pages, seed):
+    test_page_operations_follow_the_model(seqs, pages, page, max_pages, seed)
+
+
 def check_reserve(cache, model, n_new):
     """Reserves on the device and on the model; tables, counts, statuses and
     every page: a page that was given as a copy has its rows, the others are

@@ -99,8 +99,13 @@ __global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
   if (s < c.seqs) fork_apply<kWave>(c, s, threadIdx.x % kWave);
 }
 // Both halves in one workgroup, Lanes lanes for each of at most 1024 / Lanes
-// sequences: saves the second launch (8 sequences 2.8 us; 64 sequences 7.9
-// against 4.1 and 3.5, the whole of their page operations 53.6 against 54.2).
+// sequences: saves the second launch.  One workgroup makes all the atomics of
+// the counts, so with a wavefront for a sequence (up to 16) it is ahead up to
+// 1024 pages each (max_pages is what the host knows; 16 sequences of 16 pages 3.8 us against 5.9 of the two
+// kernels, of 1024 pages 18.4 against 17.5, of 4096 66 against 58), with 16 lanes
+// only where the tables are short (all forked from one: 64 sequences of 4 pages
+// 4.0 against 6.4, 32 of 16 4.8 against 6.0, 64 of 16 7.0 against 6.4, 64 of 64
+// 20.7 against 6.8, 64 of 1024 210 against 21).
 template <int Lanes>
 __global__ __launch_bounds__(1024) void fork_small_kernel(KvCache c, const int32_t* __restrict__ src) {
   const int s = threadIdx.x / Lanes, lane = threadIdx.x % Lanes;
@@ -168,7 +173,10 @@ __device__ inline void copy_piece(const KvCache& c, const CopyRec& r, int piece,
 // ascending), so the tables do not depend on timing.  pieces: where the copies
 // are few, this workgroup makes them too (the pieces of a page; 0: it does not).
 // A chain of reads and of sums over the workgroup: 8 sequences 6.2 us (7.6 with
-// sums through LDS exchanges), 256 7.1.
+// sums through LDS exchanges), 256 7.1.  The search for free pages reads the
+// counts from the pool's start on, 4096 a turn, until it has enough: where the
+// only free ones are at its end, a pool of 10^5 pages takes 28 us more, of 10^6
+// 300.
 __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const int32_t* __restrict__ n_new, int elem_bytes,
                                                              int pieces) {
   // of want: the last page is copied; pages are asked for (pages of a sequence
@@ -441,9 +449,12 @@ int64_t kv_page_work_bytes(const KvCache& c) {
 }
 
 hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
-  if (c.seqs <= 64) {
-    if (c.seqs <= 16) fork_small_kernel<64><<<1, 1024, 0, s>>>(c, src);
-    else fork_small_kernel<16><<<1, 1024, 0, s>>>(c, src);
+  if (c.seqs <= 16 && c.max_pages <= 1024) {
+    fork_small_kernel<64><<<1, 1024, 0, s>>>(c, src);
+    return hipGetLastError();
+  }
+  if (c.seqs <= 64 && int64_t(c.seqs) * c.max_pages <= 512) {
+    fork_small_kernel<16><<<1, 1024, 0, s>>>(c, src);
     return hipGetLastError();
   }
   fork_stage_kernel<<<waves_grid(c.seqs), 256, 0, s>>>(c, src);
