@@ -790,6 +790,42 @@ def test_reserve_follows_the_model_in_pools_too_small(seqs, pages, max_pages, mo
         model.fork(src)
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 64, 1024])
+def test_copies_and_moves_by_the_plan_and_by_launches(dtype, page):
+    """Last pages of a few rows up to all but one, few pieces of every size, then
+    rows moved together, by short lists and long ones."""
+    rng = np.random.default_rng(page)
+    for layers, kv_heads, D, seqs in ((1, 1, 64, 4), (1, 1, 256, 3), (2, 2, 128, 4), (1, 8, 64, 2), (3, 4, 64, 3)):
+        for rows in (1, page - 1, page + page // 2):
+            print(f"copies {dtype} page {page} {layers} layers {kv_heads}x{D} {seqs} sequences {rows} rows", flush=True)
+            new = 2 * page + 5
+            cache = tms.PagedCache.empty(layers, 5 * seqs + 3, kv_heads, page, D, seqs, 5, dtype=dtype)
+            k = torch.from_numpy(rng.standard_normal((2, rows + seqs * new, kv_heads, D)).astype(np.float32)).to(dtype).cuda()
+            tms.kv_reserve(cache, dev32([rows] + [0] * (seqs - 1)))
+            for layer in range(layers):
+                tms.kv_write(cache, layer, k[layer % 2, :rows], k[1 - layer % 2, :rows], dev32([0] + [rows] * seqs))
+            tms.kv_commit(cache, dev32([rows] + [0] * (seqs - 1)))
+            tms.kv_fork(cache, dev32([0] * seqs))
+            tms.kv_reserve(cache, dev32([new] * seqs))
+            for layer in range(layers):
+                tms.kv_write(cache, layer, k[layer % 2, rows:], k[1 - layer % 2, rows:], dev32(np.arange(seqs + 1) * new))
+            for kept in (3, new - 2):
+                keep = np.stack([np.sort(rng.permutation(new - (4 if kept > 3 else 0))[:kept - (4 if kept > 3 else 0)])
+                                 for _ in range(seqs)])
+                saved = [t.clone() for t in (cache.kv, cache.table, cache.length, cache.held, cache.refs)]
+                tms.kv_commit(cache, dev32([keep.shape[1]] * seqs), dev32(keep))
+                r = torch.arange(rows + keep.shape[1], device="cuda")
+                for s in range(seqs):
+                    at = torch.from_numpy(np.r_[0:rows, rows + s * new + keep[s]]).cuda()
+                    where = cache.table[s].long()[r // page]
+                    for layer in range(layers):
+                        assert torch.equal(cache.kv[layer][where, 0, :, r % page], k[layer % 2][at]), (rows, kept, s, layer)
+                        assert torch.equal(cache.kv[layer][where, 1, :, r % page], k[1 - layer % 2][at]), (rows, kept, s, layer)
+                for t, x in zip((cache.kv, cache.table, cache.length, cache.held, cache.refs), saved):
+                    t.copy_(x)
+
+
 def test_reserve_from_a_pool_of_a_million_pages():
     """2^20 pages and more: demands above 2^16 pages, summed in two halves."""
     pages, max_pages = (1 << 20) + 77, 700000

@@ -101,11 +101,12 @@ __global__ __launch_bounds__(256) void fork_apply_kernel(KvCache c) {
 // Both halves in one workgroup, Lanes lanes for each of at most 1024 / Lanes
 // sequences: saves the second launch.  One workgroup makes all the atomics of
 // the counts, so with a wavefront for a sequence (up to 16) it is ahead up to
-// 1024 pages each (max_pages is what the host knows; 16 sequences of 16 pages 3.8 us against 5.9 of the two
-// kernels, of 1024 pages 18.4 against 17.5, of 4096 66 against 58), with 16 lanes
-// only where the tables are short (all forked from one: 64 sequences of 4 pages
-// 4.0 against 6.4, 32 of 16 4.8 against 6.0, 64 of 16 7.0 against 6.4, 64 of 64
-// 20.7 against 6.8, 64 of 1024 210 against 21).
+// 1024 pages each, by max_pages, which is what the host knows (16 sequences of 16
+// pages 3.8 us against 5.9 of the two kernels, of 1024 pages 18.4 against 17.5,
+// of 4096 66 against 58), with 16 lanes only where the tables are short (all
+// forked from one: 64 sequences of 4 pages 4.0 against 6.4, 32 of 16 4.8 against
+// 6.0, 64 of 16 7.0 against 6.4, 64 of 64 20.7 against 6.8, 64 of 1024 210
+// against 21).
 template <int Lanes>
 __global__ __launch_bounds__(1024) void fork_small_kernel(KvCache c, const int32_t* __restrict__ src) {
   const int s = threadIdx.x / Lanes, lane = threadIdx.x % Lanes;
@@ -464,9 +465,14 @@ hipError_t launch_kv_fork(const KvCache& c, const int32_t* src, hipStream_t s) {
 }
 
 hipError_t launch_kv_reserve(const KvCache& c, const int32_t* n_new, hipStream_t s) {
-  // up to 64 pieces to copy: four for each wavefront of the plan's workgroup
+  // Up to 64 pieces to copy (four for each wavefront of the plan's workgroup) of
+  // up to 128 KB in all: beyond, one workgroup copies longer than a launch takes
+  // (64 pieces of 2 KB 6.4 to 7.1 us against 6.5 to 7.0, of 4 KB 8.4 against 6.7;
+  // 4 of 16 KB 4.2 against 6.6, of 64 KB 7.9 against 6.7; 64 of 1 MB 1100
+  // against 40).
   const int64_t pieces = int64_t(c.layers) * 2 * c.kv_heads;
-  const bool here = c.seqs * pieces <= 64;
+  const int64_t bytes = c.seqs * pieces * c.page_tokens * c.head_dim * elem_bytes(c);
+  const bool here = c.seqs * pieces <= 64 && bytes <= 128 * 1024;
   reserve_plan_kernel<<<1, kPlan, 0, s>>>(c, n_new, elem_bytes(c), here ? static_cast<int>(pieces) : 0);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || here) return e;
   copy_pages_kernel<<<dim3(c.seqs * 2 * c.kv_heads, c.layers), 256, 0, s>>>(c, elem_bytes(c));
@@ -476,9 +482,13 @@ hipError_t launch_kv_reserve(const KvCache& c, const int32_t* n_new, hipStream_t
 hipError_t launch_kv_commit(const KvCache& c, const int32_t* n_keep, const int32_t* keep, int32_t keep_stride,
                             hipStream_t s) {
   if (keep) {
-    // about 2048 workgroups in all; one for a sequence where it has few pieces
+    // About 2048 workgroups in all; one for a sequence where it has few pieces and
+    // up to 128 KB to move, which saves a launch (up to 64 sequences, 64 KB each:
+    // 4.9 to 5.2 us against 7.1 to 7.8; 128 KB 6.3 against 7.8; 256 KB 13.5 to 17
+    // against 7.5; 1 MB 70 against 7).
     const int64_t pieces = int64_t(c.layers) * 2 * c.kv_heads, wgs = std::max<int64_t>(1, 2048 / c.seqs);
-    if (pieces <= 16 || wgs == 1) {
+    const int64_t bytes = pieces * keep_stride * c.head_dim * elem_bytes(c);
+    if ((pieces <= 16 && bytes <= 128 * 1024) || wgs == 1) {
       move_commit_kernel<<<c.seqs, 256, 0, s>>>(c, n_keep, keep, keep_stride, elem_bytes(c));
       return hipGetLastError();
     }
