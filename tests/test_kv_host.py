@@ -80,6 +80,16 @@ def test_null_arguments_and_strides():
     assert L.tms_kv_attention(r, 0, P, 256, 4, P, 0, 1, None, 1.0, P, None) == tms.OK
 
 
+def test_the_package_imports_with_a_torch_without_gpus():
+    """Tries are compiled on the host: importing needs nothing of a GPU build."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(tms.__file__))
+    subprocess.run([sys.executable, "-c", "import torch; del torch._C._cuda_getCurrentRawStream; "
+                    "import trie_masked_sparse_amd as tms; assert tms.OK == 0"], cwd=root, check=True)
+
+
 def test_the_zeroed_part_of_the_work_memory_is_the_headers():
     import os
     import re

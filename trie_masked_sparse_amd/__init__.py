@@ -462,7 +462,8 @@ def debug_set_live(st, s: int, edge: int, value: int, stream=None):
 # --------------------------------------------------------------------------- paged key/value cache
 
 # The calls of a decode step are short: what they look up is bound here.
-_Tensor, _int32, _raw_stream = torch.Tensor, torch.int32, torch._C._cuda_getCurrentRawStream
+_Tensor, _int32 = torch.Tensor, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not in a torch without GPUs
 
 
 def _sized(t, dtype, numel: int, name: str):
