@@ -686,7 +686,8 @@ struct Tile<1, D> {                      // bf16
   static constexpr int Loads = D / 32;      // 16-byte words of a key for each lane
   static constexpr int Chunks = D / 8;      // 16-byte words of a row
   // place of word c of key r in the LDS tile: the transposing read takes 2
-  // words of 8 keys at once and the write 1 word of 8 keys, without conflicts
+  // words of 8 keys at once, from different banks.  Of the cycles that LDS works
+  // 32 % are conflicts all the same (64 ragged tokens); it works 7 % of the time.
   static __device__ inline int at(int r, int c) {
     const int f = D == 64 ? (r & 6) | (r >> 3 & 1) : (r & 7) << 1 | (r >> 3 & 1);
     return r * Chunks + (c ^ f);
@@ -708,12 +709,14 @@ struct Tile<0, D> {                      // fp32
 //
 // Up to 16 rows fill half of a matrix product and read K and V once, so memory
 // bounds them: 8 sequences of 40000 to 60000 tokens (32 query, 8 key heads of
-// 128, bf16) 298 us, 5.6 TB/s of 6.1 that a plain read reaches; 64 of 0 to 8191
-// tokens 50 us, 3.7 TB/s, the rest being the start of a workgroup (about 8 us
-// of dependent reads: offsets, page numbers, first keys).  One sequence of 517
+// 128, bf16) 299 us, 5.5 TB/s of 6.1 that a plain read reaches.  64 of 0 to 8191
+// tokens take 50.5 us, 3.6 TB/s, where a plain read would take 30: about 8 of the
+// 20 are the start of a workgroup (dependent reads: offsets, page numbers, first
+// keys); a share has about 26 units there, six or seven tiles of a wavefront,
+// and begins that chain again for each of its segments.  One sequence of 517
 // tokens 12 us, nothing but that chain and the join.  fp32 takes 32
 // rows to a workgroup where there are more than 16, which halves the reads of K
-// and V: two prompts of 2000 to 3000 tokens 809 us, 44 % of the rate of a plain
+// and V: two prompts of 2000 to 3000 tokens 825 us, 43 % of the rate of a plain
 // product (the reads of V by single words bound it).
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kBlock) void few_rows_kernel(KvCache c, KvAttention a, int shares, int split) {
@@ -1027,14 +1030,18 @@ int tree_words(int group) {
 // wavefronts, two on a SIMD, the second four run one phase behind: while one
 // wavefront of a SIMD feeds the matrix cores the other has the vector units.
 //
-// Bound by the matrix cores and by the exponentials beside them (a 64-key tile
-// of 256 rows: 2048 cycles of products, about 4000 in all).  32 query, 8 key
-// heads of 128: three prompts of 2300 to 4097 tokens 322 us (924 TFLOP/s; the
-// matrix cores busy 51 % of the cycles), one of 16000 tokens 1100 TFLOP/s (a plain
-// product of 16384^3: 1340), 63 drafts over two contexts of 90000 to 120000
-// 255 us (851 TFLOP/s).  Fewer rows are bound by memory: 5 to 31 drafts behind 64
-// contexts of 1201 to 2500 tokens 96 us, 4.8 TB/s.  K and V go straight into LDS:
-// through registers 463 us for the prompts.
+// Bound by the matrix cores and the vector units in turns (a 64-key tile of 256
+// rows: 2304 cycles of products, 256 of them for the row sums, about 4000 in
+// all: the time of the two adds up more than it overlaps).  32 query, 8 key heads
+// of 128: three prompts of 2300 to 4097 tokens 320 us (929 TFLOP/s; the matrix
+// cores busy 51 % of the cycles, the vector units issuing other work 37 %), one
+// of 16000 tokens 1110 TFLOP/s (a plain product of 16384^3: 1340), 63 drafts over
+// two contexts of 90000 to 120000 253 us (857 TFLOP/s).  Fewer rows are bound by
+// memory: 5 to 31 drafts behind 64 contexts of 1201 to 2500 tokens 96.5 us, 4.7
+// TB/s.  Heads of 256 have one wavefront on a SIMD and nothing beside its
+// softmax: two prompts of 2000 to 3000 tokens of 8 query, 2 key heads 128 us, 417
+// TFLOP/s.  K and V go straight into LDS: through registers 463 us for the
+// prompts.
 template <int D, int RW, int KS, bool AnyTree>
 __global__ __launch_bounds__(RW * KS * kWave, D == 256 ? 1 : 2) void many_rows_kernel(KvCache c, KvAttention a, int shares, int split, int words, int join) {
   constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;

@@ -89,7 +89,7 @@ __device__ inline void fork_apply(const KvCache& c, int s, int lane) {
   }
 }
 
-// 256 sequences of up to 33 pages: 6.0 and 5.6 us.
+// 256 sequences of up to 33 pages: 6.2 and 6.0 us.
 __global__ __launch_bounds__(256) void fork_stage_kernel(KvCache c, const int32_t* __restrict__ src) {
   const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
   if (s < c.seqs) fork_stage<kWave>(c, src, s, threadIdx.x % kWave);
@@ -173,8 +173,9 @@ __device__ inline void copy_piece(const KvCache& c, const CopyRec& r, int piece,
 // and who gets which.  The order is fixed (sequences ascending, pages
 // ascending), so the tables do not depend on timing.  pieces: where the copies
 // are few, this workgroup makes them too (the pieces of a page; 0: it does not).
-// A chain of reads and of sums over the workgroup: 8 sequences 6.2 us (7.6 with
-// sums through LDS exchanges), 256 7.1.  The search for free pages reads the
+// A chain of reads and of sums over the workgroup: 8 sequences with the copies of
+// 24 pieces of 4 KB 7.0 us (sums through LDS exchanges: 1.4 more), 256 without
+// copies 7.4.  The search for free pages reads the
 // counts from the pool's start on, 4096 a turn, until it has enough: where the
 // only free ones are at its end, a pool of 10^5 pages takes 28 us more, of 10^6
 // 300.
@@ -294,8 +295,8 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(KvCache c, const in
   }
 }
 
-// 256 sequences, 8 layers of 8 heads: 176 MB written in 41.6 us, 4.2 TB/s (the
-// shared pages are read from the cache).
+// 256 sequences, 8 layers of 8 heads: 176 MB written in 38 to 42 us, 4.2 to 4.6
+// TB/s (the shared pages are read from the cache).
 __global__ __launch_bounds__(256) void copy_pages_kernel(KvCache c, int elem_bytes) {
   const int parts = 2 * c.kv_heads;
   const CopyRec r = copy_recs(c)[blockIdx.x / parts];
@@ -421,7 +422,7 @@ __global__ __launch_bounds__(256) void commit_kernel(KvCache c, const int32_t* _
   if (s < c.seqs) commit_sequence(c, n_keep, keep_all, keep_stride, s, threadIdx.x % kWave);
 }
 
-// 256 sequences, 8 layers: 48 MB read and written in 37 us, 2.6 TB/s: reads and
+// 256 sequences, 8 layers: 48 MB read and written in 38 us, 2.5 TB/s: reads and
 // writes of a chunk wait for each other, rows of 256 bytes lie apart.
 __global__ __launch_bounds__(256) void move_rows_kernel(KvCache c, const int32_t* __restrict__ n_keep,
                                                         const int32_t* __restrict__ keep, int keep_stride, int elem_bytes,
@@ -429,7 +430,7 @@ __global__ __launch_bounds__(256) void move_rows_kernel(KvCache c, const int32_t
   move_rows(c, n_keep, keep, keep_stride, elem_bytes, blockIdx.x, blockIdx.y * pieces, pieces);
 }
 // Where one workgroup moves all pieces of a sequence it does the rest too (8
-// sequences, one layer of 2 heads: 5.7 us).
+// sequences, one layer of 2 heads: 5.5 us).
 __global__ __launch_bounds__(256) void move_commit_kernel(KvCache c, const int32_t* __restrict__ n_keep,
                                                           const int32_t* __restrict__ keep, int keep_stride,
                                                           int elem_bytes) {

@@ -85,8 +85,8 @@ constexpr int kBatch = 4;
 // DT: 0 fp32, 1 bf16.  LPR: lanes of a head.  One wavefront: token t, the
 // groups of 64 / LPR heads g0, g0 + step, ...; heads are the queries', then
 // the keys', then the values'.
-// 12220 tokens of 32 query and 8 key heads of 128 in bf16: 74 us, 4.05 TB/s of
-// the 4.93 that a plain copy reaches; 64 tokens 4.5 us, the chain of reads that
+// 12220 tokens of 32 query and 8 key heads of 128 in bf16: 74.8 us, 4.02 TB/s of
+// the 4.93 that a plain copy reaches; 64 tokens 4.6 us, the chain of reads that
 // ends in the row's page.
 template <int DT, int LPR>
 __global__ __launch_bounds__(256) void write_kernel(KvCache c, KvWrite a, int waves_per_token) {
