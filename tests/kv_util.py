@@ -12,7 +12,8 @@ Bounds (u = 2^-24 and h = 2^-8, the relative errors of rounding to fp32 and bf16
       weights normalised) the output is within (2 * rel + h) * A of the exact
       one, and rounding it adds h |out|;
       Up to 64 query rows of a key head the weights are cut to bf16 (at most 2 h
-      of them is left) and what is left is rounded to bf16: within 2 h^2 (fine);
+      of them is left) and what is left is rounded to bf16: within 2 h^2
+      (attention_fine);
   write      the sum of squares gamma(D + 8), its root and the products a few u,
       the angle (a turn in fp64 rounded to fp32) 2 pi u, sine and cosine 4 u:
       32 u + gamma(D + 8) relative to |a| + |b|, and h |out| for bf16.
@@ -40,10 +41,9 @@ def ancestors(parent):
     return sees
 
 
-def attention(q, k, v, length, scale, parent, bf16, fine=False):
+def attention(q, k, v, length, scale, parent, bf16):
     """(out, bound) of one sequence: q [n][Hq][D], k, v [length+n][Hkv][D] in
     fp64; parent [n] or None."""
-    weights = 0 if not bf16 else 2 * UBF16 ** 2 if fine else UBF16
     n, hq, D = q.shape
     group = hq // k.shape[1]
     sees = np.ones((n, length + n), bool)
@@ -58,7 +58,7 @@ def attention(q, k, v, length, scale, parent, bf16, fine=False):
             w = np.exp(x - x.max(1, keepdims=True))
             w /= w.sum(1, keepdims=True)
             out[:, h] = w @ vv
-            bound[:, h] = (2 * (np.expm1(2 * e) + rel) + weights) * (w @ np.abs(vv)) + \
+            bound[:, h] = (2 * (np.expm1(2 * e) + rel) + (UBF16 if bf16 else 0)) * (w @ np.abs(vv)) + \
                 (UBF16 if bf16 else U32) * np.abs(out[:, h])
         return out, bound
     with np.errstate(invalid="ignore"):
@@ -72,9 +72,16 @@ def attention(q, k, v, length, scale, parent, bf16, fine=False):
                 w /= w.sum()
                 out[i, h] = w @ vv[on]
                 rel = math.expm1(2 * e) + 2.0 ** -20 + gamma(int(on.sum()) + 64)
-                bound[i, h] = (2 * rel + weights) * (w @ np.abs(vv[on])) + \
+                bound[i, h] = (2 * rel + (UBF16 if bf16 else 0)) * (w @ np.abs(vv[on])) + \
                     (UBF16 if bf16 else U32) * np.abs(out[i, h])
     return out, bound
+
+
+def attention_fine(q, k, v, length, scale, parent):
+    """attention in bf16 of up to 64 query rows of a key head."""
+    out, bound = attention(q, k, v, length, scale, parent, False)
+    mass, _ = attention(q, k, np.abs(v), length, scale, parent, False)
+    return out, bound + 2 * UBF16 ** 2 * mass + (UBF16 - U32) * np.abs(out)
 
 
 def marked_values(rows, kv_heads, dim, block=16):

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import trie_masked_sparse_amd as tms
-from kv_util import Pages, attention, head, marked_values
+from kv_util import Pages, attention, head
+from kv_util import attention_fine, marked_values
 
 pytestmark = pytest.mark.gpu
 
@@ -231,7 +232,7 @@ def test_attention_weights_of_up_to_64_rows_keep_16_bits(heads, kind):
         parents = [tree(rng, b) for b in new] if kind == "tree" else None
         out, qd, at = run_attention(cache, q, new, parents).double().cpu().numpy(), q.double().cpu().numpy(), offsets(new)
         for s, (a, b) in enumerate(zip(lens, new)):
-            want, bound = attention(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, parents and parents[s], True, fine=True)
+            want, bound = attention_fine(qd[at[s]:at[s + 1]], ks[s], vs[s], a, D ** -0.5, parents and parents[s])
             err = np.abs(out[at[s]:at[s + 1]] - want)
             assert (err <= bound).all(), (n, s, float((err / bound).max()))
 

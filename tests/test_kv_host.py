@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 
 import trie_masked_sparse_amd as tms
-from kv_util import Pages, ancestors, attention, head, marked_values
+from kv_util import Pages, ancestors, attention, head
+from kv_util import marked_values
 
 
 def descriptor(**over):
