@@ -435,7 +435,7 @@ def _own(s):
             s["index"] = tms.PageIndex(s["cache"], s["bounds"], tokens=s["q"].shape[0] if op == "select" else 1)
     cache = s["cache"]
     if op == "shared":
-        tms.kv_share(cache, s["plan"], s["start"], max_new=s["max_new"])
+        tms.kv_share(cache, s["plan"], s["start"])
         for layer in range(s["kv"].shape[0]):
             tms.kv_attention_shared(cache, layer, s["q"][layer], s["start"], s["out"][layer], s["plan"], s["scale"],
                                     parent=s["parent"], max_new=s["max_new"])
