@@ -495,6 +495,72 @@ tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64
                             const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
                             void* out, void* stream);
 
+/* Attention of a batch whose sequences hold the same pages: what tms_kv_attention
+ * computes, with the pages that several sequences hold at the same place (forks
+ * of one prompt, prompts with the same beginning) read once for all their
+ * tokens.  tms_kv_share finds such runs of pages in the tables and deals the
+ * work; the plan is then good for every layer, until the next tms_kv_fork,
+ * tms_kv_reserve or tms_kv_commit.  Call it after reserving, with the start and
+ * T (at least 1) of the attention calls.  Up to three runs of a sequence are
+ * shared, those that save most reads first.  plan: dev, 256-byte aligned,
+ * tms_kv_share_bytes (which needs the cache's sizes and dtype only) for this T
+ * and q_heads; it holds the plan and the parts of the rows that are joined, so
+ * calls that use one plan on several streams are ordered by the caller.  No
+ * bytes of it need to be set before. */
+tms_status tms_kv_share_bytes(const tms_kv* c, int32_t T, int32_t q_heads, int64_t* bytes);
+tms_status tms_kv_share(const tms_kv* c, const int32_t* start, int32_t T, int32_t q_heads, void* plan,
+                        int64_t plan_bytes, void* stream);
+/* Arguments, errors and what unseen rows may hold as tms_kv_attention, which it
+ * calls where max_new * q_heads / kv_heads is above 128 (many rows of one
+ * sequence share the reads as it is; the plan is not used then).  In bf16 the
+ * weights of the second product keep 16 bits.  NaN also for
+ * sequences whose length, start or status is not the plan's, and for all tokens
+ * where the plan is of another T or q_heads or was not made. */
+tms_status tms_kv_attention_shared(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                                   const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
+                                   void* out, void* plan, int64_t plan_bytes, void* stream);
+
+/* Sparse attention over long contexts: bounds of every page's keys, kept as
+ * pages become whole; a choice of pages for each token and key head by these
+ * bounds; attention over the chosen ones.
+ *
+ * tms_kv_bounds: bounds dev [layers][pages][kv_heads][2][head_dim], of the
+ * cache's dtype: the lowest and the highest key value of each column (NaN where
+ * one is NaN) of every page that the last n_new[s] committed rows of a sequence
+ * have made whole (dev int32 [seqs]; null: of all its whole pages), in all
+ * layers.  Call it after tms_kv_commit.  A page's bounds go with the page: a
+ * fork shares them, and a whole page is never written again until it is free.
+ * max_new: the most of n_new (host; the launch is sized by it).  Sequences in
+ * error are left out. */
+tms_status tms_kv_bounds(const tms_kv* c, const int32_t* n_new, int32_t max_new, void* bounds, void* stream);
+
+/* chosen dev int32 [T][kv_heads][k]: for every new token and key head, k of the
+ * whole pages of committed rows of its sequence, in ascending order: the first
+ * `first` and the last `last` ones, and those with the highest
+ *     sum over the query heads of sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d
+ * (q with the sign of the scale; 0 for a scale of 0), the most that the heads'
+ * scores of a key of the page can add up to.  Of equal scores the lower page is
+ * taken; NaN is above all, then come first and last; sums are fp64.  Where a
+ * sequence has no more than k whole pages all are chosen, and -1 fills the rest
+ * (also of a sequence in error).  k in [1, 8192]; first, last at least 0.  q as
+ * for tms_kv_attention.  work: dev, 256-byte aligned, tms_kv_select_bytes for
+ * this T or a larger one. */
+tms_status tms_kv_select_bytes(const tms_kv* c, int32_t T, int64_t* bytes);
+tms_status tms_kv_select(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                         const int32_t* start, int32_t T, int32_t max_new, float scale, const void* bounds, int32_t k,
+                         int32_t first, int32_t last, int32_t* chosen, void* work, int64_t work_bytes, void* stream);
+
+/* tms_kv_attention over chosen pages: a token's query heads see the committed
+ * rows of the pages in its list for their key head (dev int32 [T][kv_heads][k],
+ * as tms_kv_select makes it: whole pages of committed rows in ascending order,
+ * up to the first negative entry), the committed rows behind the last whole
+ * page, and of the new rows the same as in tms_kv_attention.  k in [0, 8192].  In
+ * bf16 the weights of the second product keep 16 bits.  The outputs of a token
+ * with an entry that is out of range or not in order are NaN. */
+tms_status tms_kv_attention_pages(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                                  const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent,
+                                  const int32_t* chosen, int32_t k, float scale, void* out, void* stream);
+
 /* The accepted ones of the new tokens: keep[s][0 .. n_keep[s]) (dev int32
  * [seqs][keep_stride], ascending indices among the sequence's reserved rows)
  * become the rows length, length+1, ..., moved together in every layer;

@@ -183,3 +183,23 @@ class Pages:
                 continue
             self.rows[s] += [drafts[s][i] for i in k]
             self.table[s] = self.table[s][:-(-len(self.rows[s]) // self.page)]
+
+
+def choice(q, bounds, k, scale, first, last):
+    """The pages that one token reads: q [Hq][D], bounds [pages][Hkv][2][D] in
+    fp64 -> [Hkv][k], ascending, -1 past the pages."""
+    pages, hkv = bounds.shape[:2]
+    out = np.full((hkv, k), -1, np.int32)
+    group = q.shape[0] // hkv
+    for h in range(hkv):
+        x = np.sign(scale) * q[h * group:(h + 1) * group] if scale else np.zeros((group, q.shape[1]))
+        with np.errstate(invalid="ignore"):
+            over, under = np.maximum(x, 0).sum(0), np.minimum(x, 0).sum(0)
+            score = (over * bounds[:, h, 1] + under * bounds[:, h, 0]).sum(-1)
+        always = [j for j in range(pages) if j < first or j >= pages - last]
+        score[always] = np.inf
+        # NaN above all, then by score, of equal ones the lower page
+        order = sorted(range(pages), key=lambda j: (not np.isnan(score[j]), -score[j] if not np.isnan(score[j]) else 0, j))
+        best = sorted(order[:k])
+        out[h, :len(best)] = best
+    return out

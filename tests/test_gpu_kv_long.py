@@ -1,0 +1,689 @@
+"""Long contexts of the paged cache on the GPU against plain 64-bit forms
+(kv_util.py, which also derives the bounds): attention of batches that share
+pages, bounds of pages, the choice of pages by them, and attention over chosen
+pages."""
+import numpy as np
+import pytest
+import torch
+
+import trie_masked_sparse_amd as tms
+from kv_util import attention, attention_fine, choice, marked_values
+from test_gpu_kv import BF, F, dev32, filled, offsets, tree
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(4, 2, 64), (16, 8, 128), (8, 1, 128), (3, 3, 64), (10, 2, 256)]
+ids = dict(ids=lambda h: "x".join(map(str, h)) if isinstance(h, tuple) else None)
+
+
+# ------------------------------------------------------------------ shared pages
+
+class Branches:
+    """A cache whose sequences are paths of named runs of whole pages (a run of
+    one name is the same pages for all that have it behind the same runs), and
+    rows of their own: seqs = [(((name, pages), ...), own rows, new rows)]."""
+
+    def __init__(self, rng, dtype, kv_heads, dim, page, seqs, layers=1, spare=3, marked=False):
+        self.lens = [sum(p for _, p in path) * page + own for path, own, _ in seqs]
+        self.new = [new for _, _, new in seqs]
+        need = [-(-(a + b) // page) for a, b in zip(self.lens, self.new)]
+        total, width = sum(need) + spare, max(max(need), 1)
+        pool = list(rng.permutation(total))
+        kv = torch.full((layers, total, 2, kv_heads, page, dim), float("nan"), dtype=dtype)
+        table, refs, known = np.full((len(seqs), width), -1, np.int32), np.zeros(total, np.int32), {}
+        self.ks, self.vs = [[] for _ in range(layers)], [[] for _ in range(layers)]
+        for s, (path, own, new) in enumerate(seqs):
+            at, where, rows = 0, (), self.lens[s] + new
+            for name, count in path:
+                where += ((name, count),)
+                for i in range(count):
+                    if (where, i) not in known:
+                        known[where, i] = int(pool.pop())
+                        kv[:, known[where, i]] = self.values(rng, (layers, 2, kv_heads, page, dim), dtype)
+                    table[s, at] = known[where, i]
+                    at += 1
+            for j in range(at, need[s]):
+                table[s, j] = pool.pop()
+                have = min(page, rows - j * page)
+                kv[:, table[s, j], :, :, :have] = self.values(rng, (layers, 2, kv_heads, have, dim), dtype)
+            if marked and not (table[s, :at] < 0).any():  # values of a page by its place: the same for all that share it
+                v = torch.from_numpy(marked_values(width * page, kv_heads, dim)).to(dtype)
+                for j in range(need[s]):
+                    have = min(page, rows - j * page)
+                    kv[:, table[s, j], 1, :, :have] = v[j * page:j * page + have].transpose(0, 1)
+            for p in table[s, :need[s]]:
+                refs[p] += 1
+        for layer in range(layers):
+            for s in range(len(seqs)):
+                both = kv[layer, table[s, :need[s]].tolist()].double().numpy()  # [pages][2][heads][page][dim]
+                both = both.transpose(1, 0, 3, 2, 4).reshape(2, -1, kv_heads, dim)[:, :self.lens[s] + self.new[s]]
+                self.ks[layer].append(both[0])
+                self.vs[layer].append(both[1])
+        self.page, self.table, self.need = page, table, need
+        self.cache = tms.PagedCache(kv.cuda(), dev32(table), dev32(self.lens), dev32(need), dev32(refs), dev32([0] * len(seqs)))
+
+    @staticmethod
+    def values(rng, shape, dtype):
+        return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(dtype)
+
+
+def queries(rng, b, heads, dim, dtype):
+    return torch.from_numpy(rng.standard_normal((sum(b.new), heads, dim)).astype(np.float32)).to(dtype).cuda()
+
+
+def run_shared(b, q, parents=None, scale=None, layer=0, plan=None, max_new=None, stream=None, out=None):
+    if out is None:
+        out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    start = dev32(offsets(b.new))
+    par = None if parents is None else dev32([p for t in parents for p in t])
+    if plan is None:
+        plan = tms.SharedPlan(b.cache, q.shape[0], q.shape[1])
+        tms.kv_share(b.cache, plan, start, stream=stream)
+    tms.kv_attention_shared(b.cache, layer, q, start, out, plan, scale, parent=par, max_new=max_new or max(b.new), stream=stream)
+    return out
+
+
+def check_shared(b, q, out, scale, parents, where="", layer=0, of=None):
+    bf16 = q.dtype == BF
+    q, out, at = q.double().cpu().numpy(), out.double().cpu().numpy(), offsets(b.new)
+    for s, (a, n) in enumerate(zip(b.lens, b.new)):
+        if n and (of is None or s in of):
+            want, bound = attention(q[at[s]:at[s + 1]], b.ks[layer][s], b.vs[layer][s], a, scale,
+                                    None if parents is None else parents[s], bf16)
+            err = np.abs(out[at[s]:at[s + 1]] - want)
+            assert (err <= bound).all(), (where, s, a, n, float(np.nanmax(err / bound)), int((~(err <= bound)).sum()))
+
+
+A, B_, C_ = ("a", 40), ("b", 33), ("c", 1)
+SHARED = [
+    # (page, sequences)
+    (16, [((A,), 3, 1)] * 2),
+    (64, [((A,), i, 1) for i in range(9)]),
+    (8, [((("p", 200),), i % 5, i % 3) for i in range(40)]),
+    # two prompts with one beginning, a sequence of the beginning alone, one of nothing, some without new tokens
+    (16, [((A, B_), 5, 1), ((A, ("d", 50)), 0, 2), ((A, B_), 17, 4), ((A,), 1, 3), ((), 0, 1), ((A, ("d", 50)), 100, 0),
+          ((), 700, 5), ((A, ("d", 50)), 15, 1), ((("e", 80),), 2, 2), ((("e", 80),), 0, 7)]),
+    # a chain of beginnings, longer than the runs that are shared
+    (32, [((("x", 9),) * d, 0, 2) for d in (1, 2, 3, 4, 5, 6, 6)]),
+    # runs that are too short to be shared, pages larger than a tile
+    (128, [((C_,), 0, 1), ((C_,), 5, 1), ((("y", 7),), 9, 30), ((("y", 7),), 0, 31), ((("y", 7),), 128, 16)]),
+    # sequences of many rows beside some of few
+    (16, [((A,), 0, 200), ((A,), 7, 1), ((A,), 9, 3), ((A,), 11, 150)]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS, **ids)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_shared_matches_the_64_bit_form(dtype, heads, kind):
+    hq, hkv, D = heads
+    for n, (page, seqs) in enumerate(SHARED):
+        print(f"shared {dtype} {heads} {kind} batch {n} page {page}", flush=True)
+        rng = np.random.default_rng(17 * n + D + hq)
+        b = Branches(rng, dtype, hkv, D, page, seqs, layers=2)
+        q = queries(rng, b, hq, D, dtype)
+        parents = [tree(rng, x) for x in b.new] if kind == "tree" else None
+        out = run_shared(b, q, parents, layer=1)
+        check_shared(b, q, out, D ** -0.5, parents, (n, kind), layer=1)
+        assert torch.equal(out, run_shared(b, q, parents, layer=1))  # no order depends on timing
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_shared_large_batches(dtype):
+    rng = np.random.default_rng(3)
+    few = dict(page=16, dim=64, heads=(4, 2))
+    for seqs in ([((("p", 300),), int(x), 1) for x in rng.integers(0, 40, 256)],
+                 [((("p", 20), (f"q{i % 7}", 30), (f"r{i % 14}", 11)), int(x), int(y))
+                  for i, (x, y) in enumerate(zip(rng.integers(0, 90, 300), rng.integers(0, 4, 300)))],
+                 [(((f"p{i % 500}", 20),), 0, 1) for i in range(1500)],
+                 [((("p", 4000),), 3, 2)] * 3):
+        print(f"shared {dtype} {len(seqs)} sequences", flush=True)
+        b = Branches(rng, dtype, few["heads"][1], few["dim"], few["page"], seqs)
+        q = queries(rng, b, few["heads"][0], few["dim"], dtype)
+        out = run_shared(b, q)
+        check_shared(b, q, out, few["dim"] ** -0.5, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (16, 4, 128), (8, 1, 256)], **ids)
+def test_shared_counts_every_key_once(dtype, heads):
+    hq, hkv, D = heads
+    for n, (page, seqs) in enumerate([(16, [((("p", 900),), i, 1) for i in range(5)]),
+                                      (64, [((("p", 90), (f"q{i % 2}", 40)), 30 * i, 1) for i in range(20)]),
+                                      (8, [((("p", 500),), 900 * i, 3) for i in range(4)])]):
+        print(f"marked {dtype} {heads} batch {n}", flush=True)
+        rng = np.random.default_rng(n)
+        b = Branches(rng, dtype, hkv, D, page, seqs, marked=True)
+        q = 0.7 * queries(rng, b, hq, D, dtype)
+        check_shared(b, q, run_shared(b, q), D ** -0.5, None, n)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_shared_tables_that_no_fork_makes(dtype):
+    """Pages in common behind different ones, a page twice in a sequence, tables
+    that agree, differ and agree again."""
+    rng = np.random.default_rng(8)
+    page, dim = 16, 64
+    b = Branches(rng, dtype, 2, dim, page, [((("p", 60),), 4, 1), ((("q", 60),), 4, 2), ((("r", 60),), 4, 1), ((("s", 60),), 4, 1)])
+    table = b.table.copy()
+    table[1, 20:60] = table[0, 20:60]
+    table[2, :10], table[2, 11:40] = table[0, :10], table[0, 11:40]
+    table[3, 30] = table[3, 2]
+    table[3, :2] = table[2, :2]
+    kv = b.cache.kv[0].cpu()
+    for s in range(4):
+        both = kv[table[s, :b.need[s]].tolist()].double().numpy().transpose(1, 0, 3, 2, 4).reshape(2, -1, 2, dim)
+        b.ks[0][s], b.vs[0][s] = both[0, :b.lens[s] + b.new[s]], both[1, :b.lens[s] + b.new[s]]
+    b.cache.table.copy_(dev32(table))
+    q = queries(rng, b, 4, dim, dtype)
+    check_shared(b, q, run_shared(b, q), dim ** -0.5, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_shared_scales_strides_and_another_stream(dtype):
+    rng = np.random.default_rng(4)
+    b = Branches(rng, dtype, 2, 128, 32, [((("p", 30),), i, 1 + i % 3) for i in range(6)])
+    T = sum(b.new)
+    wide = torch.from_numpy(rng.standard_normal((T, 8 + 4, 128)).astype(np.float32)).to(dtype).cuda()
+    q = wide[:, 2:10]
+    for scale in (4.0, -2.0, 0.0):
+        check_shared(b, q, run_shared(b, q, scale=scale), scale, None, scale)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    start = dev32(offsets(b.new))
+    plan = tms.SharedPlan(b.cache, T, 8)
+    torch.cuda.synchronize()
+    tms.kv_share(b.cache, plan, start, stream=s)
+    tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=3, stream=s)
+    s.synchronize()
+    check_shared(b, q, out, 128 ** -0.5, None, "stream")
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (4, 2, 128), (8, 2, 256)], **ids)
+def test_shared_rows_not_seen_may_hold_anything(dtype, kind, heads):
+    """Infinities and NaN of drafts and later tokens reach only who sees them; an
+    infinite value of a token itself stays infinite."""
+    hq, hkv, D = heads
+    rng = np.random.default_rng(21)
+    b = Branches(rng, dtype, hkv, D, 16, [((("p", 40),), 5, 6), ((("p", 40),), 0, 3), ((("p", 40),), 30, 1)])
+    for s, i, which, value in ((0, 3, 1, float("inf")), (0, 5, 0, float("nan")), (1, 2, 1, float("nan"))):
+        row = b.lens[s] + i
+        b.cache.kv[0, int(b.table[s, row // 16]), which, :, row % 16, 1] = value
+        (b.ks if which == 0 else b.vs)[0][s][row, :, 1] = value
+    parents = [[-1, 0, 0, 1, 1, 2], [-1, 0, 0], [-1]] if kind == "tree" else None
+    q = queries(rng, b, hq, D, dtype)
+    out = run_shared(b, q, parents).double().cpu().numpy()
+    at = offsets(b.new)
+    for s in range(3):
+        with np.errstate(invalid="ignore"):
+            want, bound = attention(q[at[s]:at[s + 1]].double().cpu().numpy(), b.ks[0][s], b.vs[0][s], b.lens[s], D ** -0.5,
+                                    None if parents is None else parents[s], dtype == BF)
+        got = out[at[s]:at[s + 1]]
+        for i in range(b.new[s]):
+            fine = np.isfinite(want[i])
+            assert (np.isnan(got[i]) == np.isnan(want[i])).all() and (got[i][np.isinf(want[i])] == np.inf).all(), (s, i)
+            assert (np.abs(got[i] - want[i])[fine] <= bound[i][fine]).all(), (s, i)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_shared_an_infinite_value_of_the_last_shared_row(dtype):
+    """Rows that fill up a tile behind it weigh nothing."""
+    rng = np.random.default_rng(6)
+    for page in (8, 16, 64):
+        b = Branches(rng, dtype, 2, 64, page, [((("p", 41),), i, 1) for i in range(4)])
+        b.cache.kv[0, int(b.table[0, 40]), 1, :, page - 1, 7] = float("inf")
+        q = queries(rng, b, 4, 64, dtype)
+        q[:, :, :] *= 0.1
+        out = run_shared(b, q)
+        assert torch.isinf(out[..., 7]).all(), page
+        rest = torch.cat((out[..., :7], out[..., 8:]), -1)
+        assert torch.isfinite(rest).all()
+
+
+def test_shared_sequences_in_error_stale_plans_and_tokens_of_nobody():
+    rng = np.random.default_rng(2)
+    b = Branches(rng, BF, 2, 64, 16, [((("p", 40),), i, 1) for i in range(4)])
+    q = queries(rng, b, 4, 64, BF)
+    start = dev32(offsets(b.new))
+    b.cache.status_codes[1] = tms.ERR_OOM
+    out = run_shared(b, q)
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[[0, 2, 3]]).all()
+    check_shared(b, q, out, 0.125, None, of=(0, 2, 3))
+    b.cache.status_codes[1] = 0
+    # a plan that is older than the lengths
+    plan = tms.SharedPlan(b.cache, 4, 4)
+    out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)  # never made
+    assert torch.isnan(out).all()
+    tms.kv_share(b.cache, plan, start)
+    b.cache.length[2] -= 1
+    tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    assert torch.isnan(out[2]).all() and torch.isfinite(out[[0, 1, 3]]).all()
+    b.cache.length[2] += 1
+    # of other tokens
+    tms.kv_share(b.cache, plan, dev32([0, 1, 2, 3, 3]), tokens=3)
+    tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    assert torch.isnan(out).all()
+    out.fill_(7.0)
+    few = dev32([0, 1, 1, 2, 2])
+    tms.kv_share(b.cache, plan, few, tokens=4)
+    tms.kv_attention_shared(b.cache, 0, q, few, out, plan, max_new=1)
+    assert (out[2:] == 7.0).all() and torch.isfinite(out[:2]).all()
+    # too many tokens of a sequence for max_new
+    b2 = Branches(rng, BF, 2, 64, 16, [((("p", 40),), i, 1 + i) for i in range(3)])
+    q2 = queries(rng, b2, 4, 64, BF)
+    out = run_shared(b2, q2, max_new=2)
+    assert torch.isnan(out[3:]).all()
+    check_shared(b2, q2, out, 0.125, None, of=(0, 1))
+
+
+def test_shared_starts_out_of_order_are_refused_without_harm():
+    rng = np.random.default_rng(2)
+    b = Branches(rng, BF, 2, 64, 16, [((("p", 40),), 0, 4)] * 4)
+    q = queries(rng, b, 4, 64, BF)
+    bad = dev32([0, 10, 4, 14, 16])  # tokens of two sequences
+    b.cache.held.fill_(44)
+    out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    plan = tms.SharedPlan(b.cache, 16, 4)
+    tms.kv_share(b.cache, plan, bad)
+    tms.kv_attention_shared(b.cache, 0, q, bad, out, plan, max_new=16)
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ bounds
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 64, 1024])
+def test_bounds_are_the_lowest_and_highest_keys(dtype, dim, page):
+    rng = np.random.default_rng(dim + page)
+    lens = [0, 1, page - 1, page, page + 1, 3 * page + 5, 7 * page]
+    cache, ks, _ = filled(rng, dtype, 5, dim, page, lens, [0] * len(lens), layers=2, layer=1)
+    cache.kv[0].copy_(cache.kv[1])
+    table = cache.table.cpu().numpy()
+    for n_new in (None, [0, 1, 3, 1, 1, page + 5, 2 * page], [9, -4, 0, page, 0, 5, 6 * page + 1]):
+        print(f"bounds {dtype} {dim} {page} {n_new}", flush=True)
+        index = tms.PageIndex(cache, torch.full((2, cache.pages, 5, 2, dim), 7.0, dtype=dtype, device="cuda"))
+        want = torch.full_like(index.bounds, 7.0).cpu()
+        for s, a in enumerate(lens):
+            n = a if n_new is None else min(max(n_new[s], 0), a)
+            for j in range((a - n) // page, a // page):
+                keys = torch.from_numpy(ks[s][j * page:(j + 1) * page])
+                want[:, table[s, j], :, 0], want[:, table[s, j], :, 1] = keys.amin(0).to(dtype), keys.amax(0).to(dtype)
+        for most in (None, 1):
+            index.bounds.fill_(7.0)
+            tms.kv_bounds(cache, index, None if n_new is None else dev32(n_new), max_new=most)
+            assert torch.equal(index.bounds.cpu(), want), (n_new, most)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_bounds_of_keys_that_are_not_finite(dtype):
+    rng = np.random.default_rng(1)
+    cache, _, _ = filled(rng, dtype, 2, 64, 16, [32], [0])
+    a, b = (int(x) for x in cache.table[0, :2])
+    cache.kv[0, a, 0, 0, 3, 5] = float("nan")
+    cache.kv[0, a, 0, 1, 15, 6] = float("inf")
+    cache.kv[0, b, 0, 0, 0, 7] = -float("inf")
+    cache.kv[0, b, 0, 1, :, 8] = -float("inf")
+    index = tms.PageIndex(cache)
+    tms.kv_bounds(cache, index)
+    got = index.bounds[0]
+    keys = cache.kv[0, [a, b], 0]
+    assert torch.equal(torch.nan_to_num(got[[a, b]], nan=77.0),
+                       torch.nan_to_num(torch.stack((keys.amin(2), keys.amax(2)), 2), nan=77.0))
+    assert torch.isnan(got[a, 0, :, 5]).all() and got[a, 1, 1, 6] == float("inf") and got[b, 1, 1, 8] == -float("inf")
+
+
+def test_bounds_of_sequences_in_error_are_left():
+    rng = np.random.default_rng(1)
+    cache, _, _ = filled(rng, BF, 2, 64, 16, [32, 32], [0, 0])
+    cache.status_codes[0] = tms.ERR_OOM
+    index = tms.PageIndex(cache)
+    tms.kv_bounds(cache, index)
+    table = cache.table.cpu()
+    assert (index.bounds[0, table[0, :2].tolist()] == 0).all() and (index.bounds[0, table[1, :2].tolist()] != 0).any()
+
+
+# ------------------------------------------------------------------ choice
+
+def run_select(cache, index, q, new, k, scale=None, first=1, last=1, max_new=None):
+    chosen = torch.full((q.shape[0], cache.kv_heads, k), 77, dtype=torch.int32, device="cuda")
+    tms.kv_select(cache, 0, q, dev32(offsets(new)), index, chosen, scale, first=first, last=last, max_new=max_new or max(max(new), 1))
+    return chosen.cpu().numpy()
+
+
+def check_select(cache, index, q, lens, new, k, chosen, scale=1.0, first=1, last=1):
+    table, at = cache.table.cpu().numpy(), offsets(new)
+    bounds, q = index.bounds[0].double().cpu().numpy(), q.double().cpu().numpy()
+    for s, (a, n) in enumerate(zip(lens, new)):
+        whole = a // cache.page_tokens
+        for t in range(at[s], at[s + 1]):
+            want = choice(q[t], bounds[table[s, :whole]], k, scale, first, last)
+            assert (chosen[t] == want).all(), (s, t, a, k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS, **ids)
+def test_select_matches_the_64_bit_form(dtype, heads):
+    hq, hkv, D = heads
+    for n, (page, lens, new, k, first, last) in enumerate([
+            (16, [700], [1], 8, 1, 1), (8, [9000, 3, 64, 65, 0], [1, 1, 2, 0, 1], 8, 0, 0),
+            (16, [333, 1000, 17, 2500], [5, 1, 3, 13], 20, 2, 3), (64, [1500, 640], [1, 1], 1, 0, 0),
+            (8, [40000], [2], 300, 1, 2), (32, [900, 800], [1, 2], 5, 4, 4), (16, [700, 100], [3, 2], 8192, 1, 1)]):
+        print(f"select {dtype} {heads} {n}", flush=True)
+        rng = np.random.default_rng(n + D)
+        cache, _, _ = filled(rng, dtype, hkv, D, page, lens, new)
+        index = tms.PageIndex(cache, tokens=sum(new))
+        tms.kv_bounds(cache, index)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+        for scale in (None, -0.5):
+            chosen = run_select(cache, index, q, new, k, scale, first, last)
+            check_select(cache, index, q, lens, new, k, chosen, scale or 1.0, first, last)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_select_equal_scores_and_values_that_are_not_finite(dtype):
+    rng = np.random.default_rng(5)
+    lens, new, k = [16 * 300 + 3, 16 * 40], [1, 2], 10
+    cache, _, _ = filled(rng, dtype, 2, 64, 16, lens, new)
+    index = tms.PageIndex(cache, tokens=3)
+    tms.kv_bounds(cache, index)
+    table = cache.table.cpu()
+    p = table[0, :300].long().cuda()
+    index.bounds[0, p] = index.bounds[0, p[torch.arange(300) % 7]].clone()  # seven kinds of pages
+    q = torch.from_numpy(rng.standard_normal((3, 4, 64)).astype(np.float32)).to(dtype).cuda()
+    check_select(cache, index, q, lens, new, k, run_select(cache, index, q, new, k))
+    # a scale of 0: all equal
+    assert (run_select(cache, index, q, new, k, 0.0, 0, 0)[0] == np.arange(k)).all()
+    assert (run_select(cache, index, q, new, k, 0.0, 0, 3)[0] == np.r_[np.arange(7), 297:300]).all()
+    index.bounds[0, p[123], 0, 1, 5] = float("nan")
+    index.bounds[0, p[200], :, 1] = float("inf")
+    index.bounds[0, p[210], :, 0] = float("-inf")
+    index.bounds[0, p[220], :, 1] = float("-inf")
+    chosen = run_select(cache, index, q, new, k)
+    check_select(cache, index, q, lens, new, k, chosen)
+    assert 123 in chosen[0, 0] and 123 not in chosen[0, 1] and 200 in chosen[0, 0] and 210 in chosen[0, 0]
+    q[0, 1, 3] = float("nan")  # a query: every page the same
+    chosen = run_select(cache, index, q, new, k, first=0, last=0)
+    assert (chosen[0, 0] == np.arange(k)).all()
+    cache.status_codes[1] = tms.ERR_OOM
+    assert (run_select(cache, index, q, new, k)[1:] == -1).all()
+
+
+def test_select_leaves_tokens_of_nobody():
+    rng = np.random.default_rng(5)
+    cache, _, _ = filled(rng, BF, 2, 64, 16, [100, 200], [1, 1])
+    index = tms.PageIndex(cache, tokens=4)
+    tms.kv_bounds(cache, index)
+    q = torch.zeros((4, 4, 64), dtype=BF, device="cuda")
+    chosen = torch.full((4, 2, 3), 77, dtype=torch.int32, device="cuda")
+    tms.kv_select(cache, 0, q, dev32([0, 1, 2]), index, chosen, max_new=1)
+    assert (chosen[2:] == 77).all() and (chosen[:2] >= 0).all()
+
+
+# ------------------------------------------------------------------ attention over chosen pages
+
+def lists(rng, lens, new, kv_heads, page, k):
+    out = np.full((sum(new), kv_heads, k), -1, np.int32)
+    at = offsets(new)
+    for s, a in enumerate(lens):
+        whole = a // page
+        for t in range(at[s], at[s + 1]):
+            for h in range(kv_heads):
+                m = min(int(rng.integers(0, k + 1)) if rng.random() < 0.3 else k, whole)
+                out[t, h, :m] = np.sort(rng.permutation(whole)[:m])
+    return out
+
+
+def run_pages(cache, q, new, chosen, parents=None, scale=None, max_new=None, stream=None):
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    par = None if parents is None else dev32([p for t in parents for p in t])
+    tms.kv_attention_pages(cache, 0, q, dev32(offsets(new)), dev32(chosen), out, scale, parent=par,
+                           max_new=max_new or max(max(new), 1), stream=stream)
+    return out
+
+
+def check_pages(cache, q, out, ks, vs, lens, new, chosen, scale, parents, where=""):
+    bf16, page = q.dtype == BF, cache.page_tokens
+    q, out, at = q.double().cpu().numpy(), out.double().cpu().numpy(), offsets(new)
+    group = q.shape[1] // cache.kv_heads
+    for s, (a, n) in enumerate(zip(lens, new)):
+        for i in range(n):
+            t, mine = at[s] + i, [i] if parents is None else []
+            j = i
+            while parents is not None and j >= 0:
+                mine.append(j)
+                p = parents[s][j]
+                j = p if -1 <= p < j else -1
+            mine = list(range(i + 1)) if parents is None else sorted(mine)
+            for h in range(cache.kv_heads):
+                rows = [r for p in chosen[t, h] if p >= 0 for r in range(p * page, (p + 1) * page)]
+                rows += list(range(a // page * page, a)) + [a + m for m in mine]
+                x = q[t:t + 1, h * group:(h + 1) * group]
+                k, v = ks[s][rows, h:h + 1], vs[s][rows, h:h + 1]
+                want, bound = (attention_fine(x, k, v, len(rows) - 1, scale, None) if bf16 else
+                               attention(x, k, v, len(rows) - 1, scale, None, False))
+                err = np.abs(out[t:t + 1, h * group:(h + 1) * group] - want)
+                assert (err <= bound).all(), (where, s, i, h, a, n, float(np.nanmax(err / bound)))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS + [(40, 2, 64)], **ids)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_pages_match_the_64_bit_form(dtype, heads, kind):
+    hq, hkv, D = heads
+    for n, (page, lens, new, k) in enumerate([
+            (16, [0], [1], 0), (16, [700], [1], 5), (64, [6000], [1], 30), (8, [100, 0, 9, 333], [3, 1, 9, 20], 7),
+            (32, [4000] * 5, [1] * 5, 9), (16, [250, 15], [30, 1], 12), (128, [1000, 1], [1, 2], 3), (8, [9], [70], 1)]):
+        print(f"pages {dtype} {heads} {kind} {n}", flush=True)
+        rng = np.random.default_rng(31 * n + D + hq)
+        cache, ks, vs = filled(rng, dtype, hkv, D, page, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+        parents = [tree(rng, x) for x in new] if kind == "tree" else None
+        chosen = lists(rng, lens, new, hkv, page, k)
+        out = run_pages(cache, q, new, chosen, parents)
+        check_pages(cache, q, out, ks, vs, lens, new, chosen, D ** -0.5, parents, n)
+        assert torch.equal(out, run_pages(cache, q, new, chosen, parents))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_pages_long_lists_and_many_tokens(dtype):
+    rng = np.random.default_rng(9)
+    for page, lens, new, k in ((8, [40000], [1], 4000), (16, [int(x) for x in rng.integers(0, 900, 70)], [1] * 70, 11),
+                               (16, [500, 600], [150, 90], 6)):
+        print(f"pages long {dtype} {page} {k}", flush=True)
+        cache, ks, vs = filled(rng, dtype, 2, 64, page, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), 4, 64)).astype(np.float32)).to(dtype).cuda()
+        chosen = lists(rng, lens, new, 2, page, k)
+        check_pages(cache, q, run_pages(cache, q, new, chosen), ks, vs, lens, new, chosen, 0.125, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_pages_of_all_are_the_whole_attention(dtype):
+    rng = np.random.default_rng(10)
+    lens, new = [700, 16, 5], [4, 1, 2]
+    cache, ks, vs = filled(rng, dtype, 2, 128, 16, lens, new)
+    q = torch.from_numpy(rng.standard_normal((7, 8, 128)).astype(np.float32)).to(dtype).cuda()
+    index = tms.PageIndex(cache, tokens=7)
+    tms.kv_bounds(cache, index)
+    chosen = run_select(cache, index, q, new, 64)
+    for scale in (0.3, -1.0, 0.0):
+        out = run_pages(cache, q, new, chosen, scale=scale).double().cpu().numpy()
+        at = offsets(new)
+        for s in range(3):
+            want, bound = attention(q[at[s]:at[s + 1]].double().cpu().numpy(), ks[s], vs[s], lens[s], scale, None, dtype == BF)
+            assert (np.abs(out[at[s]:at[s + 1]] - want) <= bound).all(), (s, scale)
+
+
+def test_pages_lists_that_are_wrong_give_nan():
+    rng = np.random.default_rng(12)
+    lens, new = [330, 330], [2, 1]
+    cache, ks, vs = filled(rng, BF, 2, 64, 16, lens, new)
+    q = torch.from_numpy(rng.standard_normal((3, 4, 64)).astype(np.float32)).to(BF).cuda()
+    good = np.tile(np.array([1, 5, 19, -1], np.int32), (3, 2, 1))
+    for wrong in ([1, 1, 2, 3], [5, 4, 6, 7], [1, 2, 20, -1], [0, -1, 3, -1], [2000000000, 3, 4, 5], [0, 1, 2, 21]):
+        chosen = good.copy()
+        chosen[0, 1] = wrong
+        out = run_pages(cache, q, new, chosen)
+        assert torch.isnan(out[0, 2:]).all(), wrong
+        assert torch.isfinite(out[0, :2]).all() and torch.isfinite(out[1:]).all(), wrong
+    chosen = good.copy()
+    chosen[0, 0] = [-1, -1, -1, -1]
+    chosen[0, 1] = [3, -7, -1, -2000000000]
+    check_pages(cache, q, run_pages(cache, q, new, chosen), ks, vs, lens, new, chosen, 0.125, None)
+    cache.status_codes[1] = tms.ERR_OOM
+    out = run_pages(cache, q, new, good)
+    assert torch.isnan(out[2]).all() and torch.isfinite(out[:2]).all()
+    cache.status_codes[1] = 0
+    out = run_pages(cache, q, new, good, max_new=1)
+    assert torch.isnan(out[:2]).all() and torch.isfinite(out[2]).all()
+
+
+@pytest.mark.parametrize("k", [0, 3, 400])
+def test_pages_leave_tokens_of_nobody(k):
+    rng = np.random.default_rng(12)
+    cache, _, _ = filled(rng, BF, 2, 64, 16, [8000, 20], [1, 1])
+    q = torch.from_numpy(rng.standard_normal((5, 4, 64)).astype(np.float32)).to(BF).cuda()
+    out = torch.full((5, 4, 64), 7.0, dtype=BF, device="cuda")
+    chosen = dev32(lists(rng, [8000, 20, 0], [1, 1, 3], 2, 16, k))
+    tms.kv_attention_pages(cache, 0, q, dev32([0, 1, 2]), chosen, out, max_new=1)
+    assert (out[2:] == 7.0).all() and torch.isfinite(out[:2]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_pages_rows_not_seen_may_hold_anything(dtype, kind):
+    rng = np.random.default_rng(13)
+    lens, new, page = [330], [6], 16
+    cache, ks, vs = filled(rng, dtype, 2, 64, page, lens, new)
+    for i, which, value in ((3, 1, float("inf")), (5, 0, float("nan")), (4, 1, float("nan"))):
+        row = lens[0] + i
+        cache.kv[0, int(cache.table[0, row // page]), which, :, row % page, 1] = value
+        (ks if which == 0 else vs)[0][row, :, 1] = value
+    unseen = int(cache.table[0, 7])
+    cache.kv[0, unseen] = float("nan")  # a page that no token has chosen
+    parents = [[-1, 0, 0, 1, 1, 2]] if kind == "tree" else None
+    chosen = np.tile(np.array([0, 2, 6, 8, 19], np.int32), (6, 2, 1))
+    q = torch.from_numpy(rng.standard_normal((6, 4, 64)).astype(np.float32)).to(dtype).cuda()
+    out = run_pages(cache, q, new, chosen, parents).cpu()
+    seen = {"causal": [set(range(i + 1)) for i in range(6)], "tree": [{0}, {0, 1}, {0, 2}, {0, 1, 3}, {0, 1, 4}, {0, 2, 5}]}[kind]
+    for i in range(6):
+        rest = torch.cat((out[i, :, :1], out[i, :, 2:]), -1)
+        if 5 in seen[i]:
+            assert torch.isnan(out[i]).all(), i
+        else:
+            assert torch.isfinite(rest).all(), i
+            assert torch.isnan(out[i, :, 1]).all() if 4 in seen[i] else (out[i, :, 1] == float("inf")).all() if 3 in seen[i] \
+                else torch.isfinite(out[i, :, 1]).all(), i
+
+
+# ------------------------------------------------------------------ together
+
+def test_a_step_over_long_contexts_replays_in_a_graph():
+    """What a serving step does: fork, reserve, write, plan, shared attention in
+    one layer and chosen pages in another, commit, bounds; recorded once and
+    replayed, each replay against the same calls made eagerly."""
+    def build():
+        rng = np.random.default_rng(77)
+        cache = tms.PagedCache.empty(2, 400, 2, 16, 64, 9, 60, dtype=BF)
+        index, plan = tms.PageIndex(cache, tokens=40), tms.SharedPlan(cache, 40, 4)
+        n = dev32([700] + [0] * 8)
+        tms.kv_reserve(cache, n)
+        for layer in range(2):
+            x = torch.from_numpy(rng.standard_normal((700, 4, 64)).astype(np.float32)).to(BF).cuda()
+            tms.kv_write(cache, layer, x[:, :2], x[:, 2:], dev32([0] + [700] * 9))
+        tms.kv_commit(cache, n)
+        tms.kv_bounds(cache, index)
+        tms.kv_fork(cache, dev32([0] * 9))
+        return cache, index, plan
+
+    new = [0] + [3, 1, 5, 2, 4, 1, 1, 6]
+    T = sum(new)
+    rng = np.random.default_rng(78)
+    steps = [torch.from_numpy(rng.standard_normal((2, T, 8, 64)).astype(np.float32)).to(BF).cuda() for _ in range(4)]
+    x = steps[0].clone()
+    n_new, start, n_keep = dev32(new), dev32(offsets(new)), dev32([0, 3, 1, 2, 1, 4, 1, 0, 5])
+    chosen = torch.zeros((T, 2, 6), dtype=torch.int32, device="cuda")
+    out = torch.zeros((2, T, 4, 64), dtype=BF, device="cuda")
+
+    def step(cache, index, plan):
+        tms.kv_reserve(cache, n_new, check=False)
+        tms.kv_share(cache, plan, start, tokens=T)
+        for layer in range(2):
+            q, k, v = x[layer].split([4, 2, 2], 1)
+            tms.kv_write(cache, layer, k, v, start)
+            if layer == 0:
+                tms.kv_attention_shared(cache, layer, q, start, out[layer], plan, max_new=6)
+            else:
+                tms.kv_select(cache, layer, q, start, index, chosen, max_new=6)
+                tms.kv_attention_pages(cache, layer, q, start, chosen, out[layer], max_new=6)
+        tms.kv_commit(cache, n_keep, check=False)
+        tms.kv_bounds(cache, index, n_keep, max_new=6)
+
+    eager, results = build(), []
+    for i, s in enumerate(steps):
+        x.copy_(s)
+        step(*eager)
+        results.append((out.clone(), chosen.clone()))
+    torch.cuda.synchronize()
+    assert (eager[0].status() == tms.OK).all()
+    recorded = build()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step(*recorded)
+    for i, s in enumerate(steps):
+        x.copy_(s)
+        torch.zeros(1000, device="cuda").sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, results[i][0]) and torch.equal(chosen, results[i][1]), i
+    assert torch.equal(recorded[0].length, eager[0].length) and torch.equal(recorded[1].bounds, eager[1].bounds)
+    # every whole page has its bounds
+    cache, index = recorded[0], recorded[1]
+    for s in range(9):
+        for p in cache.table[s, :int(cache.length[s]) // 16].long():
+            keys = cache.kv[:, p, 0]
+            assert torch.equal(index.bounds[:, p], torch.stack((keys.amin(2), keys.amax(2)), 2))
+
+
+def test_binding_refusals_of_the_long_context_calls():
+    rng = np.random.default_rng(1)
+    cache, _, _ = filled(rng, BF, 2, 64, 16, [100, 200], [1, 1])
+    start = dev32([0, 1, 2])
+    q = torch.zeros((2, 4, 64), dtype=BF, device="cuda")
+    out = torch.zeros_like(q)
+    plan, index = tms.SharedPlan(cache, 2, 4), tms.PageIndex(cache, tokens=2)
+    with pytest.raises(tms.TmsError):
+        tms.SharedPlan(cache, 0, 4)
+    with pytest.raises(tms.TmsError):
+        tms.SharedPlan(cache, 2, 3)
+    with pytest.raises(ValueError, match="heads"):
+        tms.kv_attention_shared(cache, 0, q[:, :2], start, out, plan)
+    with pytest.raises(tms.TmsError, match="plan_bytes"):
+        tms.kv_share(cache, plan, start, tokens=20000)
+    with pytest.raises(tms.TmsError, match="layer"):
+        tms.kv_attention_shared(cache, 1, q, start, out, plan)
+    with pytest.raises(TypeError):
+        tms.kv_share(cache, plan, start.long())
+    with pytest.raises(ValueError, match="bounds"):
+        tms.PageIndex(cache, torch.zeros((1, 3), device="cuda"))
+    with pytest.raises(TypeError):
+        tms.PageIndex(cache, index.bounds.float())
+    chosen = torch.zeros((2, 2, 4), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="chosen"):
+        tms.kv_select(cache, 0, q, start, index, chosen[:1])
+    with pytest.raises(ValueError, match="chosen"):
+        tms.kv_attention_pages(cache, 0, q, start, chosen[:, :1], out)
+    with pytest.raises(TypeError):
+        tms.kv_attention_pages(cache, 0, q, start, chosen.long(), out)
+    with pytest.raises(tms.TmsError, match="first"):
+        tms.kv_select(cache, 0, q, start, index, chosen, first=-1)
+    with pytest.raises(tms.TmsError, match="work"):
+        tms.kv_select(cache, 0, torch.zeros((40000, 4, 64), dtype=BF, device="cuda"), start, index,
+                      torch.zeros((40000, 2, 4), dtype=torch.int32, device="cuda"))
+    with pytest.raises(tms.TmsError, match="k must"):
+        tms.kv_select(cache, 0, q, start, index, torch.zeros((2, 2, 0), dtype=torch.int32, device="cuda"))

@@ -48,7 +48,8 @@ EXPORTS = (
     "tms_state_get_launch",
     "tms_decode_k_pointers_noalloc", "tms_read_reference",
     "tms_kv_work_bytes", "tms_kv_fork", "tms_kv_reserve", "tms_kv_write", "tms_kv_attention", "tms_kv_commit",
-    "tms_kv_sync_status",
+    "tms_kv_sync_status", "tms_kv_share_bytes", "tms_kv_share", "tms_kv_attention_shared", "tms_kv_bounds",
+    "tms_kv_select_bytes", "tms_kv_select", "tms_kv_attention_pages",
     "tms_status_str", "tms_last_error",
 )
 NOREPEAT_LIVE, NOREPEAT_BITMASK = 0, 1
@@ -125,6 +126,13 @@ def lib():
             "tms_kv_attention": [P, i32, P, C.c_int64, i32, P, i32, i32, P, C.c_float, P, P],
             "tms_kv_commit": [P, P, P, i32, P],
             "tms_kv_sync_status": [P, P, P],
+            "tms_kv_share_bytes": [P, i32, i32, P],
+            "tms_kv_share": [P, P, i32, i32, P, C.c_int64, P],
+            "tms_kv_attention_shared": [P, i32, P, C.c_int64, i32, P, i32, i32, P, C.c_float, P, P, C.c_int64, P],
+            "tms_kv_bounds": [P, P, i32, P, P],
+            "tms_kv_select_bytes": [P, i32, P],
+            "tms_kv_select": [P, i32, P, C.c_int64, i32, P, i32, i32, C.c_float, P, i32, i32, i32, P, P, C.c_int64, P],
+            "tms_kv_attention_pages": [P, i32, P, C.c_int64, i32, P, i32, i32, P, P, i32, C.c_float, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -539,7 +547,8 @@ class PagedCache:
         self.d = d
         self.ref = C.byref(d)
         c = lib()
-        self._c = c.tms_kv_fork, c.tms_kv_reserve, c.tms_kv_write, c.tms_kv_attention, c.tms_kv_commit
+        self._c = c.tms_kv_fork, c.tms_kv_reserve, c.tms_kv_write, c.tms_kv_attention, c.tms_kv_commit, \
+            c.tms_kv_share, c.tms_kv_attention_shared, c.tms_kv_bounds, c.tms_kv_select, c.tms_kv_attention_pages
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int, seqs: int, max_pages: int,
@@ -685,6 +694,138 @@ def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = T
         _check(rc, "kv_commit")
     if check:
         _raise_kv_errors(cache, stream, "kv_commit")
+
+
+class SharedPlan:
+    """Work memory of the shared attention over a cache, for calls of up to
+    `tokens` new tokens in all: what kv_share finds in the tables, and the parts
+    of the rows that kv_attention_shared joins.  Calls that use one plan on
+    several streams have to be ordered by the caller."""
+
+    def __init__(self, cache: PagedCache, tokens: int, q_heads: int):
+        need = C.c_int64()
+        _check(lib().tms_kv_share_bytes(cache.ref, tokens, q_heads, C.byref(need)), "SharedPlan")
+        self.tokens, self.q_heads, self.bytes = tokens, q_heads, need.value
+        self.memory = torch.empty(need.value, dtype=torch.uint8, device=cache.kv.device)
+        self.memory[:256].zero_()  # not a plan yet
+        self._at, self._streams = self.memory.data_ptr(), set()
+
+
+class PageIndex:
+    """Bounds of the keys of a cache's whole pages, kept by kv_bounds, and the
+    work memory of kv_select for calls of up to `tokens` new tokens in all.
+    bounds [layers][pages][kv_heads][2][head_dim] of the cache's dtype (lowest,
+    highest); made here if it is not given."""
+
+    def __init__(self, cache: PagedCache, bounds=None, tokens: int = 1):
+        shape = (cache.layers, cache.pages, cache.kv_heads, 2, cache.head_dim)
+        if bounds is None:
+            bounds = torch.zeros(shape, dtype=cache.dtype, device=cache.kv.device)
+        if tuple(bounds.shape) != shape:
+            raise ValueError("bounds must be [layers][pages][kv_heads][2][head_dim]")
+        if bounds.device != cache.kv.device:
+            raise ValueError("the bounds must be on the cache's device")
+        self._bounds = _dev(bounds, cache.dtype, "bounds")
+        need = C.c_int64()
+        _check(lib().tms_kv_select_bytes(cache.ref, tokens, C.byref(need)), "PageIndex")
+        self.bounds, self.tokens, self.bytes = bounds, tokens, need.value
+        self.memory = torch.empty(max(need.value, 256), dtype=torch.uint8, device=cache.kv.device)
+        self._at, self._streams = self.memory.data_ptr(), set()
+
+
+def _with_stream(cache: PagedCache, handle, stream):
+    """_kv_stream, told to the tensors of a plan or an index too."""
+    s = _kv_stream(cache, stream)
+    if s not in handle._streams:
+        on = torch.cuda.ExternalStream(s, device=cache.kv.device)
+        handle.memory.record_stream(on)
+        if isinstance(handle, PageIndex):
+            handle.bounds.record_stream(on)
+        handle._streams.add(s)
+    return s
+
+
+def kv_share(cache: PagedCache, plan: SharedPlan, start, tokens: int | None = None, stream=None):
+    """Plan of the shared attention of `tokens` (default: plan.tokens) packed new
+    tokens, from the cache's tables (tms_kv_share): after kv_reserve, once for all
+    layers.  Asynchronous."""
+    rc = cache._c[5](cache.ref, _sized(start, _int32, cache.seqs + 1, "start"), plan.tokens if tokens is None else tokens,
+                     plan.q_heads, plan._at, plan.bytes, _with_stream(cache, plan, stream))
+    if rc:
+        _check(rc, "kv_share")
+
+
+def kv_attention_shared(cache: PagedCache, layer: int, q, start, out, plan: SharedPlan, scale: float | None = None,
+                        parent=None, max_new: int | None = None, stream=None):
+    """kv_attention where sequences share pages, each read once
+    (tms_kv_attention_shared): the same arguments, and the plan that kv_share has
+    made for these tokens.  Asynchronous, but for trees of more than 1024 tokens in
+    all without max_new."""
+    dt, D = cache.dtype, cache.head_dim
+    qp, T, hq, ldq = _token_rows(q, dt, D, "q")
+    at = _sized(start, _int32, cache.seqs + 1, "start")
+    if hq != plan.q_heads:
+        raise ValueError(f"q has {hq} heads, the plan is for {plan.q_heads}")
+    if max_new is None:
+        max_new = _longest(cache, start, stream, T) if parent is not None and T > _MAX_TREE else T
+    rc = cache._c[6](cache.ref, layer, qp, ldq, hq, at, T, max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
+                     D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"), plan._at, plan.bytes,
+                     _with_stream(cache, plan, stream))
+    if rc:
+        _check(rc, "kv_attention_shared")
+
+
+def kv_bounds(cache: PagedCache, index: PageIndex, n_new=None, max_new: int | None = None, stream=None):
+    """Bounds of the pages that the last n_new[s] committed rows (int32 [seqs];
+    None: all) have made whole (tms_kv_bounds): after kv_commit, for all layers.
+    max_new: the most of n_new.  Asynchronous."""
+    if max_new is None:
+        max_new = cache.max_pages * cache.page_tokens
+    rc = cache._c[7](cache.ref, None if n_new is None else _sized(n_new, _int32, cache.seqs, "n_new"), max_new, index._bounds,
+                     _with_stream(cache, index, stream))
+    if rc:
+        _check(rc, "kv_bounds")
+
+
+def kv_select(cache: PagedCache, layer: int, q, start, index: PageIndex, chosen, scale: float | None = None,
+              first: int = 1, last: int = 1, max_new: int | None = None, stream=None):
+    """The pages that the packed new tokens read, by the bounds on q k
+    (tms_kv_select): chosen int32 [T][kv_heads][k], ascending, -1 past a sequence's
+    whole pages; the first and the last whole pages are always among them.  Of
+    scale only the sign counts.  Asynchronous."""
+    qp, T, hq, ldq = _token_rows(q, cache.dtype, cache.head_dim, "q")
+    at = _chosen(chosen, cache, T)
+    rc = cache._c[8](cache.ref, layer, qp, ldq, hq, _sized(start, _int32, cache.seqs + 1, "start"), T,
+                     T if max_new is None else max_new, 1.0 if scale is None else scale, index._bounds, chosen.shape[2], first,
+                     last, at, index._at, index.bytes, _with_stream(cache, index, stream))
+    if rc:
+        _check(rc, "kv_select")
+
+
+def kv_attention_pages(cache: PagedCache, layer: int, q, start, chosen, out, scale: float | None = None, parent=None,
+                       max_new: int | None = None, stream=None):
+    """kv_attention of every token over its chosen pages (int32 [T][kv_heads][k],
+    of kv_select or the caller's own), the committed rows behind the last whole
+    page and the new rows (tms_kv_attention_pages).  Asynchronous, but for trees of
+    more than 1024 tokens in all without max_new."""
+    dt, D = cache.dtype, cache.head_dim
+    qp, T, hq, ldq = _token_rows(q, dt, D, "q")
+    listed = _chosen(chosen, cache, T)
+    at = _sized(start, _int32, cache.seqs + 1, "start")
+    if max_new is None:
+        max_new = _longest(cache, start, stream, T) if parent is not None and T > _MAX_TREE else T
+    rc = cache._c[9](cache.ref, layer, qp, ldq, hq, at, T, max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
+                     listed, chosen.shape[2], D ** -0.5 if scale is None else scale, _sized(out, dt, T * hq * D, "out"),
+                     _kv_stream(cache, stream))
+    if rc:
+        _check(rc, "kv_attention_pages")
+
+
+def _chosen(t, cache: PagedCache, T: int):
+    """Address of lists of pages, [T][kv_heads][k]."""
+    if not isinstance(t, _Tensor) or t.dim() != 3 or t.shape[0] != T or t.shape[1] != cache.kv_heads:
+        raise ValueError("chosen must be a tensor [T][kv_heads][k]")
+    return _sized(t, _int32, t.numel(), "chosen")
 
 
 # --------------------------------------------------------------------------- handles

@@ -32,7 +32,8 @@ def build(verbose: bool = True) -> str:
     os.makedirs(objdir, exist_ok=True)
     objs = []
     for src, lang in (("kernels.hip", "hip"), ("noalloc.hip", "hip"), ("kv_pages.hip", "hip"), ("kv_write.hip", "hip"),
-                      ("kv_attention.hip", "hip"), ("api.cpp", "c++"), ("kv_api.cpp", "c++"),
+                      ("kv_attention.hip", "hip"), ("kv_shared.hip", "hip"), ("kv_select.hip", "hip"),
+                      ("kv_chosen.hip", "hip"), ("api.cpp", "c++"), ("kv_api.cpp", "c++"),
                       ("trie_build.cpp", "c++"), ("charset_build.cpp", "c++")):
         obj = os.path.join(objdir, src + ".o")
         cmd = [HIPCC, f"--offload-arch={ARCH}", *COMMON, "-c", "-x", lang, os.path.join(CSRC, src), "-o", obj]

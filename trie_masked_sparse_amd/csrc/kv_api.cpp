@@ -3,6 +3,7 @@
 // allocated here.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "handles.h"
@@ -42,8 +43,7 @@ tms::KvCache view(const tms_kv* c) {
 }
 
 int64_t work_bytes(const tms::KvCache& v) {
-  const int64_t a = tms::kv_page_work_bytes(v), b = tms::kv_attention_work_bytes(v);
-  return a > b ? a : b;
+  return std::max({tms::kv_page_work_bytes(v), tms::kv_attention_work_bytes(v), tms::kv_chosen_work_bytes(v)});
 }
 
 tms_status check_cache(const tms_kv* c) {
@@ -65,6 +65,35 @@ int elem_size(const tms_kv* c) { return c->dtype == TMS_F32 ? 4 : 2; }
 // Packed rows [T][heads][D], ld elements apart.
 bool rows_ok(const tms_kv* c, const void* p, int64_t ld, int32_t heads) {
   return p && aligned(p, 16) && ld >= int64_t(heads) * c->head_dim && ld * elem_size(c) % 16 == 0;
+}
+
+// What the attention calls have alike.
+tms_status check_attention(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                           const int32_t* start, int32_t T, int32_t* max_new, const int32_t* parent, const void* out) {
+  if (layer < 0 || layer >= c->layers) return bad("layer out of range");
+  if (T < 0 || !start) return bad("null start or negative T");
+  if (q_heads < 1 || q_heads > 4096 || q_heads % c->kv_heads) return bad("q_heads must be a multiple of kv_heads, at most 4096");
+  if (T == 0) return TMS_OK;
+  if (*max_new < 1) return bad("max_new must be positive");
+  if (*max_new > T) *max_new = T;
+  if (parent && *max_new > 1024) return bad("a tree of drafts has at most 1024 tokens (max_new)");
+  if (!rows_ok(c, q, ldq, q_heads) || !out || !aligned(out, 16))
+    return bad("q or out null or not aligned, or the row stride of q too small or not a multiple of 16 bytes");
+  return TMS_OK;
+}
+
+tms_status check_share(const tms_kv* c, int32_t T, int32_t q_heads) {
+  if (const tms_status s = check_sizes(c); s != TMS_OK) return s;
+  if (T < 1 || T > (1 << 24)) return bad("T must be in [1, 2^24]");
+  if (q_heads < 1 || q_heads > 4096 || q_heads % c->kv_heads) return bad("q_heads must be a multiple of kv_heads, at most 4096");
+  return TMS_OK;
+}
+
+tms_status check_plan(const tms_kv* c, int32_t T, int32_t q_heads, const void* plan, int64_t bytes) {
+  if (const tms_status s = check_share(c, T, q_heads); s != TMS_OK) return s;
+  if (!plan || !aligned(plan, 256)) return bad("plan null or not 256-byte aligned");
+  if (bytes < tms::kv_share_bytes(view(c), T, q_heads)) return bad("plan_bytes below tms_kv_share_bytes");
+  return TMS_OK;
 }
 
 }  // namespace
@@ -129,17 +158,85 @@ tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64
                             const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
                             void* out, void* stream) {
   TMS_KV_CHECK(c);
-  if (layer < 0 || layer >= c->layers) return bad("layer out of range");
-  if (T < 0 || !start) return bad("null start or negative T");
-  if (q_heads < 1 || q_heads > 4096 || q_heads % c->kv_heads) return bad("q_heads must be a multiple of kv_heads, at most 4096");
-  if (T == 0) return TMS_OK;
-  if (max_new < 1) return bad("max_new must be positive");
-  if (max_new > T) max_new = T;
-  if (parent && max_new > 1024) return bad("a tree of drafts has at most 1024 tokens (max_new)");
-  if (!rows_ok(c, q, ldq, q_heads) || !out || !aligned(out, 16))
-    return bad("q or out null or not aligned, or the row stride of q too small or not a multiple of 16 bytes");
+  if (const tms_status s = check_attention(c, layer, q, ldq, q_heads, start, T, &max_new, parent, out); s != TMS_OK || T == 0)
+    return s;
   tms::KvAttention a{start, T, layer, max_new, q, ldq, q_heads, parent, scale, out};
   TMS_KV_HIP(tms::launch_kv_attention(view(c), a, static_cast<hipStream_t>(stream)), "kv attention launch");
+  return TMS_OK;
+}
+
+tms_status tms_kv_share_bytes(const tms_kv* c, int32_t T, int32_t q_heads, int64_t* bytes) {
+  if (const tms_status s = check_share(c, T, q_heads); s != TMS_OK) return s;
+  if (!bytes) return bad("bytes is null");
+  *bytes = tms::kv_share_bytes(view(c), T, q_heads);
+  return TMS_OK;
+}
+
+tms_status tms_kv_share(const tms_kv* c, const int32_t* start, int32_t T, int32_t q_heads, void* plan,
+                        int64_t plan_bytes, void* stream) {
+  TMS_KV_CHECK(c);
+  if (!start) return bad("null start");
+  if (const tms_status s = check_plan(c, T, q_heads, plan, plan_bytes); s != TMS_OK) return s;
+  tms::KvShared a{{start, T, 0, T, nullptr, 0, q_heads, nullptr, 1.f, nullptr}, plan};
+  TMS_KV_HIP(tms::launch_kv_share(view(c), a, static_cast<hipStream_t>(stream)), "kv share launch");
+  return TMS_OK;
+}
+
+tms_status tms_kv_attention_shared(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                                   const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
+                                   void* out, void* plan, int64_t plan_bytes, void* stream) {
+  TMS_KV_CHECK(c);
+  if (const tms_status s = check_attention(c, layer, q, ldq, q_heads, start, T, &max_new, parent, out); s != TMS_OK || T == 0)
+    return s;
+  if (const tms_status s = check_plan(c, T, q_heads, plan, plan_bytes); s != TMS_OK) return s;
+  tms::KvShared a{{start, T, layer, max_new, q, ldq, q_heads, parent, scale, out}, plan};
+  TMS_KV_HIP(tms::launch_kv_attention_shared(view(c), a, static_cast<hipStream_t>(stream)), "kv shared attention launch");
+  return TMS_OK;
+}
+
+tms_status tms_kv_bounds(const tms_kv* c, const int32_t* n_new, int32_t max_new, void* bounds, void* stream) {
+  TMS_KV_CHECK(c);
+  if (!bounds || !aligned(bounds, 16)) return bad("bounds null or not 16-byte aligned");
+  if (max_new < 0) return bad("negative max_new");
+  tms::KvBounds b{n_new, max_new, bounds};
+  TMS_KV_HIP(tms::launch_kv_bounds(view(c), b, static_cast<hipStream_t>(stream)), "kv bounds launch");
+  return TMS_OK;
+}
+
+tms_status tms_kv_select_bytes(const tms_kv* c, int32_t T, int64_t* bytes) {
+  if (const tms_status s = check_sizes(c); s != TMS_OK) return s;
+  if (T < 0 || !bytes) return bad("negative T or null bytes");
+  *bytes = tms::kv_select_work_bytes(view(c), T);
+  return TMS_OK;
+}
+
+tms_status tms_kv_select(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                         const int32_t* start, int32_t T, int32_t max_new, float scale, const void* bounds, int32_t k,
+                         int32_t first, int32_t last, int32_t* chosen, void* work, int64_t work_bytes, void* stream) {
+  TMS_KV_CHECK(c);
+  if (k < 1 || k > tms::kMostChosen) return bad("k must be in [1, 8192]");
+  if (first < 0 || last < 0) return bad("first and last must not be negative");
+  // chosen stands for the outputs, which are whole numbers: no alignment
+  if (const tms_status s = check_attention(c, layer, q, ldq, q_heads, start, T, &max_new, nullptr, q); s != TMS_OK || T == 0)
+    return s;
+  if (!chosen || !bounds || !aligned(bounds, 16)) return bad("chosen or bounds null or bounds not 16-byte aligned");
+  if (!work || !aligned(work, 256) || work_bytes < tms::kv_select_work_bytes(view(c), T))
+    return bad("work null, not 256-byte aligned or below tms_kv_select_bytes");
+  tms::KvSelect a{{start, T, layer, max_new, q, ldq, q_heads, nullptr, scale, nullptr}, bounds, k, first, last, chosen, work};
+  TMS_KV_HIP(tms::launch_kv_select(view(c), a, static_cast<hipStream_t>(stream)), "kv select launch");
+  return TMS_OK;
+}
+
+tms_status tms_kv_attention_pages(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
+                                  const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent,
+                                  const int32_t* chosen, int32_t k, float scale, void* out, void* stream) {
+  TMS_KV_CHECK(c);
+  if (k < 0 || k > tms::kMostChosen) return bad("k must be in [0, 8192]");
+  if (const tms_status s = check_attention(c, layer, q, ldq, q_heads, start, T, &max_new, parent, out); s != TMS_OK || T == 0)
+    return s;
+  if (k && !chosen) return bad("null chosen");
+  tms::KvChosen a{{start, T, layer, max_new, q, ldq, q_heads, parent, scale, out}, chosen, k};
+  TMS_KV_HIP(tms::launch_kv_attention_pages(view(c), a, static_cast<hipStream_t>(stream)), "kv attention over pages launch");
   return TMS_OK;
 }
 

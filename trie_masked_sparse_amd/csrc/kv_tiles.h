@@ -212,16 +212,26 @@ __device__ inline f32x4 odd_values(const u32x4* row, int at) {
   return x;
 }
 
+// Page of a key: from a table of the keys' pages, or as a function says.
+__device__ inline int key_page(const KvCache& c, const int32_t* table, int key) {
+  return max(0, min(table[key >> c.page_shift], c.pages - 1));
+}
+template <class PageAt>
+__device__ inline int key_page(const KvCache&, const PageAt& page_at, int key) {
+  return page_at(key);
+}
+
 // Address of the V row of a key.
-__device__ inline const u32x4* value_row(const KvCache& c, const int32_t* table, const u32x4* values, int64_t page_stride,
+template <class Table>
+__device__ inline const u32x4* value_row(const KvCache& c, const Table& table, const u32x4* values, int64_t page_stride,
                                          int ch, int row) {
-  const int page = max(0, min(table[row >> c.page_shift], c.pages - 1));
+  const int page = key_page(c, table, row);
   return values + page * page_stride + int64_t(row & (c.page_tokens - 1)) * ch;
 }
 
 // Sets m.bits; whether any is set.  Ends with a barrier.
-template <int Threads, int DT, int D>
-__device__ inline bool find_nonfinite(const KvCache& c, const int32_t* table, const u32x4* values, int64_t page_stride,
+template <int Threads, int DT, int D, class Table>
+__device__ inline bool find_nonfinite(const KvCache& c, const Table& table, const u32x4* values, int64_t page_stride,
                                       const Mixed& m) {
   constexpr int CH = D * (DT == 0 ? 4 : 2) / 16, kFill = 63;
   const int tid = threadIdx.x, lane = tid % kWave;
