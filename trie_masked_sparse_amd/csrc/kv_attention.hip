@@ -184,12 +184,6 @@ __device__ inline int share_of(int64_t total, int shares, int64_t unit) {
   return static_cast<int>(past < 0 ? quotient(unit, each + 1) : longer + quotient(past, each));
 }
 
-// The value of a lane before this one (DPP control), 0 where there is none.
-template <int Control, int Rows>
-__device__ inline int from_lane(int x) {
-  return __builtin_amdgcn_update_dpp(0, x, Control, Rows, 0xf, false);
-}
-
 __device__ inline int64_t read_lane(int64_t x, int lane) {
   const uint64_t low = uint32_t(__builtin_amdgcn_readlane(int(x), lane)), high = uint32_t(__builtin_amdgcn_readlane(int(x >> 32), lane));
   return int64_t(high << 32 | low);

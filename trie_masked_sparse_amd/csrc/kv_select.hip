@@ -94,88 +94,14 @@ __global__ __launch_bounds__(kBlock) void bounds_kernel(KvCache c, KvBounds b, i
 
 // ---------------------------------------------------------------- choice --
 
-// Sequence of token t, and what its list is chosen from: of `whole` pages the
-// ones in [first, end) by their scores, the others always.
-struct Range {
-  int s, whole, first, end;
-};
-
-// All threads; ends with a barrier.
-__device__ inline Range range_of(const KvCache& c, const KvSelect& a, int t) {
-  __shared__ int found;
-  if (threadIdx.x == 0) found = -1;
-  __syncthreads();
-  for (int s = threadIdx.x; s < c.seqs; s += blockDim.x)
-    if (a.a.start[s] <= t && t < a.a.start[s + 1]) found = s;
-  __syncthreads();
-  Range r{uniform(found), 0, 0, 0};
-  if (r.s < 0) return r;
-  const Seq q = sequence(c, a.a, r.s, 1, 1);
-  r.whole = q.bad ? 0 : uniform(q.len) >> c.page_shift;
-  r.first = min(a.first, r.whole), r.end = max(r.whole - a.last, r.first);
-  return r;
-}
-
-// Scores of a token and key head, [T][kv_heads][max_pages] in fp64.
-__device__ inline double* scores(const KvCache& c, const KvSelect& a, int t, int h) {
-  return static_cast<double*>(a.work) + (int64_t(t) * c.kv_heads + h) * c.max_pages;
-}
-
-// A wavefront takes pages of one token and key head: the lanes share a page's
-// 2 D bounds (or several pages', where they fit).
-template <int DT, int D>
-__global__ __launch_bounds__(kBlock) void score_kernel(KvCache c, KvSelect a, int cuts) {
-  using W = Word<DT>;
-  constexpr int CH = D / W::N, Two = 2 * CH;                       // words of the bounds of a page
-  constexpr int Lanes = Two < kWave ? Two : kWave, Each = Two / Lanes, Pages = kWave / Lanes;
-  const int cut = blockIdx.x % cuts, h = blockIdx.x / cuts % c.kv_heads, t = blockIdx.x / cuts / c.kv_heads;
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const Range r = range_of(c, a, t);
-  if (r.s < 0 || r.whole <= a.k) return;
-  const int group = a.a.q_heads / c.kv_heads, word = lane % Lanes;
-  const float sign = a.a.scale < 0.f ? -1.f : a.a.scale == 0.f ? 0.f : 1.f;
-  double f[Each][W::N];
-#pragma unroll
-  for (int i = 0; i < Each; ++i)
-#pragma unroll
-    for (int e = 0; e < W::N; ++e) f[i][e] = 0.;
-  for (int g = 0; g < group; ++g) {
-    const int64_t at = int64_t(t) * a.a.ldq + int64_t(h * group + g) * D;
-    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.a.q) + at * (DT == 0 ? 4 : 2));
-#pragma unroll
-    for (int i = 0; i < Each; ++i) {
-      float x[W::N];
-      const int w = word + i * Lanes;
-      W::unpack(q[w % CH], x);
-#pragma unroll
-      for (int e = 0; e < W::N; ++e) {
-        const float y = sign == 0.f ? 0.f : x[e] * sign;
-        f[i][e] += y != y ? y : w < CH ? fminf(y, 0.f) : fmaxf(y, 0.f);
-      }
-    }
-  }
-  const u32x4* bounds = static_cast<const u32x4*>(a.bounds) + (int64_t(a.a.layer) * c.pages * c.kv_heads + h) * Two;
-  const int32_t* table = c.table + int64_t(r.s) * c.max_pages;
-  double* out = scores(c, a, t, h);
-  const int stride = cuts * kWaves * Pages;
-  for (int j0 = r.first + (cut * kWaves + wave) * Pages; j0 < r.end; j0 += stride) {
-    const int j = min(j0 + lane / Lanes, r.end - 1), page = max(0, min(table[j], c.pages - 1));
-    const u32x4* p = bounds + int64_t(page) * c.kv_heads * Two + word;
-    double sum = 0.;
-#pragma unroll
-    for (int i = 0; i < Each; ++i) {
-      float x[W::N];
-      W::unpack(p[i * Lanes], x);
-#pragma unroll
-      for (int e = 0; e < W::N; ++e) sum = fma(f[i][e], double(x[e]), sum);
-    }
-#pragma unroll
-    for (int step = 1; step < Lanes; step *= 2) sum += __shfl_xor(sum, step);
-    if (word == 0) out[j] = sum;
-  }
-}
+constexpr int kThreads = 512, kSelectWaves = kThreads / kWave;
+constexpr int kHeld = 4096;   // keys that LDS holds
+constexpr int kBins = 2048;
+constexpr int kCutPages = 64;  // pages of a workgroup at least, where a list has several
+constexpr int kLists = kWorkCounts / 4, kGroups = 512;  // lists that are cut (a counter each), workgroups then
 
 // A score as an integer that orders as the score does, NaN above all.
+constexpr uint64_t kAlways = 0xfff0000000000000ull;  // of infinity, and of the first and last pages
 __device__ inline uint64_t order(double x) {
   if (x != x) return ~uint64_t(0);
   if (x == 0.) x = 0.;  // -0 and 0 are equal
@@ -183,74 +109,302 @@ __device__ inline uint64_t order(double x) {
   return u >> 63 ? ~u : u | uint64_t(1) << 63;
 }
 
-constexpr int kPick = 256, kBins = 256;
+// Of `Count` values of each of Lanes lanes the sums over the lanes, one of them
+// in a lane: value lane % Count.  Each step halves the values that a lane has.
+template <int Count, int Lanes>
+__device__ inline double lane_sums(double (&v)[Count]) {
+  const int lane = threadIdx.x % kWave;
+  int step = 1;
+#pragma unroll
+  for (int n = Count; n > 1; n /= 2, step *= 2) {
+    const bool odd = lane & step;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const double keep = odd ? v[2 * i + 1] : v[2 * i], give = odd ? v[2 * i] : v[2 * i + 1];
+      v[i] = keep + __shfl_xor(give, step);
+    }
+  }
+  double x = v[0];
+#pragma unroll
+  for (; step < Lanes; step *= 2) x += __shfl_xor(x, step);
+  return x;
+}
 
-// Workgroup of one token and key head: its list.  The pages above a border are
-// taken, and of those at it the lowest: the border is found digit by digit.
-__global__ __launch_bounds__(kPick) void pick_kernel(KvCache c, KvSelect a) {
+// Combines each lane's value with those of the lanes before it: the last lane
+// has all of them.  from_lane gives 0 where there is none.
+template <class F>
+__device__ inline void along_lanes(F&& f) {
+  f([](int x) { return from_lane<0x111, 0xf>(x); });  // 1, 2, 4 and 8 lanes down in rows of 16
+  f([](int x) { return from_lane<0x112, 0xf>(x); });
+  f([](int x) { return from_lane<0x114, 0xf>(x); });
+  f([](int x) { return from_lane<0x118, 0xf>(x); });
+  f([](int x) { return from_lane<0x142, 0xa>(x); });  // row 0 to row 1, row 2 to row 3
+  f([](int x) { return from_lane<0x143, 0xc>(x); });  // lane 31 to rows 2 and 3
+}
+
+// Exclusive sums over the workgroup's threads; `sums` is free again behind the
+// next barrier.
+__device__ inline int thread_prefix(int mine, int* sums, int* total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  int incl = mine;
+  along_lanes([&](auto from) __attribute__((always_inline)) { incl += from(incl); });
+  if (lane == kWave - 1) sums[wave] = incl;
+  __syncthreads();
+  int before = incl - mine;
+  *total = 0;
+  for (int w = 0; w < kSelectWaves; ++w) {
+    if (w < wave) before += sums[w];
+    *total += sums[w];
+  }
+  return before;
+}
+
+// A workgroup takes the pages of one token and key head, or one of up to `most`
+// parts of them; the last of these to arrive chooses.
+//
+// Scores: the lanes share a page's 2 D bounds (or several pages', where they
+// fit), and every lane keeps its columns' factors; the loads of the next pages
+// are in flight during the sums.  Choice: the keys' range, from the lowest to the
+// highest finite one, is cut into kBins bins, and the bin with the k-th highest
+// again, until all of a bin are taken or it is one value.
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, 6) void select_kernel(KvCache c, KvSelect a, int most) {
+  using W = Word<DT>;
+  constexpr int CH = D / W::N, Two = 2 * CH;                       // words of the bounds of a page
+  constexpr int Lanes = Two < kWave ? Two : kWave, Each = Two / Lanes, Pages = kWave / Lanes;
+  constexpr int U = Each == 1 ? 4 : 2;                             // loads in flight of a lane, of pages
+  __shared__ uint64_t held[kHeld];
   __shared__ uint32_t bins[kBins];
-  __shared__ int sums[kPick / kWave];
-  __shared__ uint64_t border_s;
-  __shared__ int need_s;
-  const int h = blockIdx.x % c.kv_heads, t = blockIdx.x / c.kv_heads, tid = threadIdx.x;
-  const Range r = range_of(c, a, t);
-  if (r.s < 0) return;
+  __shared__ int sums[kSelectWaves], sums2[kSelectWaves];
+  __shared__ uint32_t range[2];
+  __shared__ int found, last_s, bin_s[3];
+  const int cut = blockIdx.x % most, h = blockIdx.x / most % c.kv_heads, t = blockIdx.x / most / c.kv_heads;
+  const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave;
+  for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+  if (tid == 0) found = -1, range[0] = range[1] = 0;
+  __syncthreads();
+  for (int s = tid; s < c.seqs; s += kThreads)
+    if (a.a.start[s] <= t && t < a.a.start[s + 1]) found = s;
+  __syncthreads();
+  const int s = uniform(found);
+  if (s < 0) return;  // a token of nobody: its list stays as it is
+  const Seq q = sequence(c, a.a, s, 1, 1);
+  const int whole = q.bad ? 0 : uniform(q.len) >> c.page_shift;
   int32_t* out = a.chosen + (int64_t(t) * c.kv_heads + h) * a.k;
-  if (r.whole <= a.k) {
-    for (int i = tid; i < a.k; i += kPick) out[i] = i < r.whole ? i : -1;
+  if (whole <= a.k) {  // all of them
+    if (cut == 0)
+      for (int i = tid; i < a.k; i += kThreads) out[i] = i < whole ? i : -1;
     return;
   }
-  const double* in = scores(c, a, t, h);
-  constexpr uint64_t kAlways = 0xfff0000000000000ull;  // order(infinity)
-  auto key = [&](int j) { return j < r.first || j >= r.end ? kAlways : order(in[j]); };
-  // border: the k-th highest key.  Keys whose digits above `shift` are prefix's
-  // are looked at
-  uint64_t prefix = 0;
-  int need = a.k;  // how many of them are taken
-  for (int shift = 56;; shift -= 8) {
-    bins[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < r.whole; j += kPick) {
-      const uint64_t x = key(j);
-      if (shift == 56 || x >> (shift + 8) == prefix) atomicAdd(&bins[x >> shift & 255], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int left = need, d = kBins - 1;
-      for (; left > int(bins[d]); --d) left -= bins[d];
-      border_s = d, need_s = left;
-    }
-    __syncthreads();
-    prefix = prefix << 8 | border_s;
-    need = need_s;
-    __syncthreads();
-    if (shift == 0) break;
-  }
-  // in ascending order: a page is taken above the border, or at it among the first `need`
-  int before = 0, equal_before = 0;  // taken, and at the border
-  for (int j0 = 0; j0 < r.whole; j0 += kPick) {
-    const int j = j0 + tid, lane = tid % kWave, wave = tid / kWave;
-    const uint64_t x = j < r.whole ? key(j) : 0;
-    const bool equal = j < r.whole && x == prefix;
-    auto rank = [&](bool on, int& total) {
-      const uint64_t all = __ballot(on);
-      __syncthreads();
-      if (lane == 0) sums[wave] = __popcll(all);
-      __syncthreads();
-      int n = __popcll(all & ((uint64_t(1) << lane) - 1));
-      total = 0;
-      for (int w = 0; w < kPick / kWave; ++w) {
-        if (w < wave) n += sums[w];
-        total += sums[w];
+  // pages [first, end) are chosen by their scores, the others always
+  const int first = min(a.first, whole), end = max(whole - a.last, first);
+  const int cuts = max(1, min(most, (end - first) / kCutPages));
+  if (cut >= cuts) return;
+  const int each = (((end - first + cuts - 1) / cuts) + 15) & ~15;
+  const int from = min(first + cut * each, end), to = min(from + each, end);
+  double* scores = static_cast<double*>(a.work) + (int64_t(t) * c.kv_heads + h) * c.max_pages;
+  const bool in_lds = cuts == 1 && end - first <= kHeld;
+  {
+    const int group = a.a.q_heads / c.kv_heads, word = lane % Lanes;
+    const float sign = a.a.scale < 0.f ? -1.f : 1.f;
+    double f[Each][W::N];
+#pragma unroll
+    for (int i = 0; i < Each; ++i)
+#pragma unroll
+      for (int e = 0; e < W::N; ++e) f[i][e] = 0.;
+    for (int g = 0; g < group; ++g) {
+      const int64_t at = int64_t(t) * a.a.ldq + int64_t(h * group + g) * D;
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.a.q) + at * (DT == 0 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < Each; ++i) {
+        float x[W::N];
+        const int w = word + i * Lanes;
+        W::unpack(p[w % CH], x);
+#pragma unroll
+        for (int e = 0; e < W::N; ++e) {
+          const float y = a.a.scale == 0.f ? 0.f : x[e] * sign;
+          f[i][e] += y != y ? y : w < CH ? fminf(y, 0.f) : fmaxf(y, 0.f);
+        }
       }
-      return n;
+    }
+    const u32x4* bounds = static_cast<const u32x4*>(a.bounds) + (int64_t(a.a.layer) * c.pages * c.kv_heads + h) * Two;
+    const int32_t* table = c.table + int64_t(s) * c.max_pages;
+    constexpr int Step = U * Pages * kSelectWaves;  // pages of an iteration of the workgroup
+    int page[U];
+    u32x4 w[U][Each];
+    auto look = [&](int j0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) page[u] = table[max(min(j0 + u * Pages + lane / Lanes, to - 1), 0)];
     };
-    int equals, takes;
-    const int at_border = equal_before + rank(equal, equals);
-    const bool take = j < r.whole && (x > prefix || (equal && at_border < need));
-    const int place = before + rank(take, takes);
-    if (take) out[place] = j;
-    before += takes, equal_before += equals;
+    auto load = [&]() {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const u32x4* p = bounds + int64_t(max(0, min(page[u], c.pages - 1))) * c.kv_heads * Two + word;
+#pragma unroll
+        for (int i = 0; i < Each; ++i) w[u][i] = p[i * Lanes];
+      }
+    };
+    int j0 = from + wave * U * Pages;
+    if (j0 < to) {
+      look(j0);
+      load();
+      look(j0 + Step);
+    }
+    for (; j0 < to; j0 += Step) {
+      double sum[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        sum[u] = 0.;
+#pragma unroll
+        for (int i = 0; i < Each; ++i) {
+          float x[W::N];
+          W::unpack(w[u][i], x);
+#pragma unroll
+          for (int e = 0; e < W::N; ++e) sum[u] = fma(f[i][e], double(x[e]), sum[u]);
+        }
+      }
+      load();
+      look(j0 + 2 * Step);
+      const double x = lane_sums<U, Lanes>(sum);
+      const int j = j0 + word * Pages + lane / Lanes;
+      if (word < U && j < to) {
+        if (in_lds) held[j - first] = order(x);
+        else if (cuts == 1) scores[j] = x;
+        else __hip_atomic_store(reinterpret_cast<uint64_t*>(scores) + j, __double_as_longlong(x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+  }
+  const uint64_t* kept = reinterpret_cast<const uint64_t*>(scores);
+  if (cuts > 1) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the scores are written
+    __syncthreads();
+    uint32_t* arrived = static_cast<uint32_t*>(c.work) + blockIdx.x / most;
+    if (tid == 0) {
+      last_s = atomicAdd(arrived, 1u) == uint32_t(cuts - 1);
+      if (last_s) *arrived = 0;
+    }
+    __syncthreads();
+    if (!last_s) return;
+  }
+  auto score = [&](int j) {
+    return __longlong_as_double(cuts == 1 ? kept[j] : __hip_atomic_load(kept + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  };
+  const int n = end - first;
+  const bool fits = n <= kHeld;
+  if (fits && !in_lds)
+    for (int i = tid; i < n; i += kThreads) held[i] = order(score(first + i));
+  __syncthreads();
+  auto key = [&](int i) { return fits ? held[i] : order(score(first + i)); };
+  // the range of the keys, of their upper 32 bits
+  {
+    uint32_t low = 0, high = 0;  // of the complements, for the lowest
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t x = key(i) >> 32;
+      low = max(low, ~x), high = max(high, x);
+    }
+    along_lanes([&](auto from) __attribute__((always_inline)) {
+      low = max(low, uint32_t(from(low))), high = max(high, uint32_t(from(high)));
+    });
+    if (lane == kWave - 1) atomicMax(&range[0], low), atomicMax(&range[1], high);
+    __syncthreads();
+  }
+  // need: how many of the n are taken; a NaN comes before the pages that are
+  // always chosen, which may be more than k
+  const int always = whole - n;
+  int need = a.k - always;
+  uint64_t low = uint64_t(~range[0]) << 32, border = 0;
+  const uint64_t high = uint64_t(range[1]) << 32 | 0xffffffffu;
+  const bool plain = need > 0 && high < kAlways;
+  int at = 0, always_taken = always;  // taken of the pages at the border, and of those always chosen
+  if (need > 0 || high >= kAlways) {
+    if (!plain) {
+      // NaN first, then the always chosen and infinite ones by their place: the
+      // number of NaN, and of infinite scores
+      int nan = 0, inf = 0, all;
+      for (int i = tid; i < n; i += kThreads) nan += key(i) > kAlways, inf += key(i) == kAlways;
+      thread_prefix(nan, sums, &all);
+      nan = all;
+      thread_prefix(inf, sums2, &all);
+      inf = all;
+      __syncthreads();
+      if (nan >= a.k) {  // of NaN only, the lowest
+        border = ~uint64_t(0), at = a.k, always_taken = 0;
+        need = 0;
+      } else if (nan + inf + always >= a.k) {  // the border is among the infinite ones, by place
+        border = kAlways, at = a.k - nan, always_taken = -1;
+        need = 0;
+      }
+    }
+    if (need > 0) {
+      int left = need, span = 64 - __clzll((long long)((high - low) | 1));
+      // keys in [low, low + 2^span) are looked at, `left` of them are taken
+      for (;;) {
+        const int shift = max(span - 11, 0);
+        for (int i = tid; i < n; i += kThreads) {
+          const uint64_t x = key(i) - low;  // below low: a large number
+          if (key(i) >= low && (span >= 64 || x >> span == 0)) atomicAdd(&bins[x >> shift], 1u);
+        }
+        __syncthreads();
+        // the bin with the `left`-th highest key: thread t has the bins from the
+        // (4 t)-th highest on
+        constexpr int Own = kBins / kThreads;
+        int mine = 0, total;
+        uint32_t b[Own];
+#pragma unroll
+        for (int i = 0; i < Own; ++i) b[i] = bins[kBins - 1 - (tid * Own + i)], mine += b[i];
+        int before = thread_prefix(mine, sums, &total);
+        if (before < left && before + mine >= left) {
+#pragma unroll
+          for (int i = 0; i < Own; ++i) {
+            if (before < left && before + int(b[i]) >= left) bin_s[0] = kBins - 1 - (tid * Own + i), bin_s[1] = left - before, bin_s[2] = b[i];
+            before += b[i];
+          }
+        }
+        __syncthreads();
+        low += uint64_t(bin_s[0]) << shift;
+        left = bin_s[1];
+        const bool done = shift == 0 || bin_s[2] == left;
+        __syncthreads();
+        if (done) {
+          // all keys of the bin are taken, or `left` of equal ones
+          if (shift == 0) border = low, at = left;
+          else border = low - 1, at = 0;
+          break;
+        }
+        span = shift;
+        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+        __syncthreads();
+      }
+    }
+  } else {  // only of those that are always chosen: the lowest k
+    border = ~uint64_t(0), at = 0, always_taken = a.k;
+  }
+  // ascending: a thread takes a run of pages; the ones at the border by place
+  const bool by_place = always_taken < 0;  // the always chosen are at the border too
+  const int run = (whole + kThreads - 1) / kThreads, r0 = min(tid * run, whole), r1 = min(r0 + run, whole);
+  auto kind = [&](int j) {  // 2 taken, 1 at the border
+    if (j < first || j >= end) return by_place ? 1 : 3;
+    const uint64_t x = key(j - first);
+    return x > border ? 2 : x == border && at > 0 ? 1 : 0;
+  };
+  int taken = 0, equal = 0, always_here = 0, all;
+  for (int j = r0; j < r1; ++j) {
+    const int x = kind(j);
+    taken += x == 2, equal += x == 1, always_here += x == 3;
+  }
+  int e = 0, w = always_here;
+  __syncthreads();
+  if (at > 0 || always_taken != always) {  // by place
+    const int before = thread_prefix(equal, sums, &all);
+    e = min(max(at - before, 0), equal);
+    const int always_before = thread_prefix(always_here, sums2, &all);
+    w = min(max(always_taken - always_before, 0), always_here);
+    __syncthreads();
+  }
+  int place = thread_prefix(taken + e + w, sums, &all);
+  for (int j = r0; j < r1; ++j) {
+    const int x = kind(j);
+    if (x == 2 || (x == 1 && e-- > 0) || (x == 3 && w-- > 0)) out[place++] = j;
   }
 }
 
@@ -265,12 +419,11 @@ hipError_t bounds(const KvCache& c, const KvBounds& b, hipStream_t s) {
 
 template <int DT, int D>
 hipError_t select(const KvCache& c, const KvSelect& a, hipStream_t s) {
+  // long contexts of few tokens: a list by several workgroups
   const int64_t lists = int64_t(a.a.T) * c.kv_heads;
-  const int cuts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c.max_pages / 32, 1024 / lists)));
-  if (lists * cuts >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  score_kernel<DT, D><<<unsigned(lists * cuts), kBlock, 0, s>>>(c, a, cuts);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  pick_kernel<<<unsigned(lists), kPick, 0, s>>>(c, a);
+  const int most = lists > kLists ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c.max_pages / kCutPages, kGroups / lists)));
+  if (lists * most >= (int64_t(1) << 32) / kThreads) return hipErrorInvalidValue;
+  select_kernel<DT, D><<<unsigned(lists * most), kThreads, 0, s>>>(c, a, most);
   return hipGetLastError();
 }
 

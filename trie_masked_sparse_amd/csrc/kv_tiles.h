@@ -55,6 +55,12 @@ __device__ inline void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// The value of a lane before this one (DPP control), 0 where there is none.
+template <int Control, int Rows>
+__device__ inline int from_lane(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, Control, Rows, 0xf, false);
+}
+
 // Maximum and sum over the 4 lanes of a query row (lane % 16).
 __device__ inline float row_max(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
