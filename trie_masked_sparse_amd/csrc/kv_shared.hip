@@ -13,15 +13,17 @@
 #include <algorithm>
 #include <climits>
 
-#include "kv_few.h"
+#include "kv_many.h"
 
 namespace tms {
 namespace {
 
 constexpr int kLevels = 3;      // nodes of a sequence beside its own
 constexpr int kSeqs = 4096;     // sequences of a cache, at most
-constexpr int kPlan = 1024;     // threads of plan_kernel
+constexpr int kPlan = 1024, kPlanWaves = kPlan / kWave;
 constexpr int kSlots = 512;     // workgroups that a launch should have
+constexpr int kTile = 64;       // keys that the plan counts in
+constexpr int kSmall = 16;      // rows of a small node
 constexpr int kMagic = 0x73686172;
 
 // Sequences of more rows of a key head than this read their pages for
@@ -32,24 +34,27 @@ constexpr int kMostRowsShared = 128;
 // one) have to be at least this for a node.
 constexpr int kLeastSaved = 256;
 
+// Key tiles of a chunk, at least.
+constexpr int kLeastTiles = 4;
+
 struct Head {
-  int32_t magic, T, q_heads, units, nodes, rows, keys, pad;
+  int32_t magic, T, q_heads, units, nodes, rows, pad[2];
 };
 
 struct PlanSeq {
-  int32_t begin, n, len, levels;      // tokens, committed rows; nodes (-1: its outputs are NaN)
+  int32_t begin, n, len, levels;               // tokens, committed rows; nodes (-1: its outputs are NaN)
   int32_t node[kLevels + 1], at[kLevels + 1];  // nodes, and where its tokens are among a node's
 };
 
 struct Node {
-  int32_t seq, key0, keys;            // the sequence whose table has the pages; first row, rows
-  int32_t tokens, list;               // query tokens; their place in the list, -1: begin ..
-  int32_t begin, n, len;              // of one sequence's own: its new tokens, committed rows from key0 on
-  int32_t unit, chunks, tiles, pad;   // first unit, chunks of `tiles` key tiles
-  int64_t part;                       // first row of its parts
+  int32_t seq, key0, keys;   // the sequence whose table has the pages; first row, rows
+  int32_t tokens, list;      // query tokens; their place in the list, -1: begin ..
+  int32_t begin, n, len;     // of one sequence's own: its new tokens, committed rows from key0 on
+  int32_t unit, chunks, tiles, rows;  // first unit, chunks of `tiles` key tiles, rows of a row tile
+  int64_t part;              // first row of its parts
 };
 
-// Places in the plan.  M: rows of a tile.
+// Places in the plan.  M: rows of a tile of nodes that are not small.
 struct Layout {
   int64_t seqs, nodes, units, tokens, owner, stats, values, bytes;
   int32_t most_nodes, most_units;
@@ -63,7 +68,7 @@ Layout layout(const KvCache& c, int32_t T, int32_t q_heads, int M) {
   const int64_t group = q_heads / c.kv_heads, n = std::min<int64_t>(c.seqs, T);
   y.most_nodes = static_cast<int32_t>(n + kLevels * (n / 2));
   // a node's row tiles, each cut at most as often as fills the chip
-  const int64_t tiles = (kLevels + 1) * (int64_t(T) * group / M) + y.most_nodes;
+  const int64_t tiles = (kLevels + 1) * (int64_t(T) * group / std::max(M, kSmall)) + y.most_nodes;
   y.most_units = static_cast<int32_t>(tiles + kSlots / c.kv_heads + 1);
   y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + (kSlots + c.kv_heads) * int64_t(M);
   y.seqs = up(sizeof(Head));
@@ -91,26 +96,80 @@ struct Plan {
   }
 };
 
-// Pages that sequences s and t have in common from page p on, of the first
-// `most`, by one wavefront.
-__device__ inline int common(const KvCache& c, int s, int t, int p, int most) {
+// Pages that the sequences first, first + step, ... (kTogether of them) have in
+// common with their leaders, from their next pages on, by one wavefront.
+constexpr int kTogether = 2;
+__device__ inline void common(const KvCache& c, int n, int first, int step, const int* lead, const int* pos, const int* whole,
+                              int* same) {
+  constexpr int kLoads = 6;
   const int lane = threadIdx.x % kWave;
-  const int32_t *x = c.table + int64_t(s) * c.max_pages, *y = c.table + int64_t(t) * c.max_pages;
-  constexpr int kLoads = 4;
-  for (int j0 = p; j0 < most; j0 += kLoads * kWave) {
-    int a[kLoads], b[kLoads];
+  int at[kTogether], most[kTogether];
+  const int32_t *x[kTogether], *y[kTogether];
+  bool left = false;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int j = min(j0 + i * kWave + lane, most - 1);
-      a[i] = x[j], b[i] = y[j];
-    }
+  for (int i = 0; i < kTogether; ++i) {
+    const int s = first + i * step, t = s < n ? lead[s] : s;
+    at[i] = most[i] = 0;
+    if (s >= n) continue;
+    if (lane == 0) same[s] = 0;
+    if (t == s) continue;
+    at[i] = pos[s], most[i] = min(whole[s], whole[t]);
+    x[i] = c.table + int64_t(s) * c.max_pages, y[i] = c.table + int64_t(t) * c.max_pages;
+    left = true;
+  }
+  while (left) {
+    int a[kTogether][kLoads], b[kTogether][kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint64_t differ = __ballot(a[i] != b[i] || j0 + i * kWave + lane >= most);
-      if (differ) return min(j0 + i * kWave + __builtin_ctzll(differ), most) - p;
+    for (int i = 0; i < kTogether; ++i)
+      if (at[i] < most[i])
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int j = min(at[i] + u * kWave + lane, most[i] - 1);
+          a[i][u] = x[i][j], b[i][u] = y[i][j];
+        }
+    left = false;
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      if (at[i] >= most[i]) continue;
+      const int s = first + i * step;
+      int end = -1;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const uint64_t differ = __ballot(a[i][u] != b[i][u] || at[i] + u * kWave + lane >= most[i]);
+        if (differ && end < 0) end = min(at[i] + u * kWave + __builtin_ctzll(differ), most[i]);
+      }
+      at[i] += kLoads * kWave;
+      if (end < 0 && at[i] >= most[i]) end = most[i];
+      if (end >= 0) {
+        if (lane == 0) same[s] = end - pos[s];
+        at[i] = most[i];
+      } else {
+        left = true;
+      }
     }
   }
-  return most - p;
+}
+
+// Sums over the workgroup's threads before this one, and of all; `sums` is free
+// again behind the next barrier.
+template <typename T>
+__device__ inline T threads_before(T mine, T* sums, T* total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  T incl = mine;
+#pragma unroll
+  for (int step = 1; step < kWave; step *= 2) {
+    const T x = __shfl_up(incl, step);
+    if (lane >= step) incl += x;
+  }
+  if (lane == kWave - 1) sums[wave] = incl;
+  __syncthreads();
+  T before = incl - mine;
+  *total = 0;
+  for (int w = 0; w < kPlanWaves; ++w) {
+    if (w < wave) before += sums[w];
+    *total += sums[w];
+  }
+  return before;
 }
 
 // One workgroup.  In every round, sequences that have the same next page form a
@@ -118,65 +177,81 @@ __device__ inline int common(const KvCache& c, int s, int t, int p, int most) {
 // (pages in common with the leader, times the sequences that have them but one)
 // makes a node.  Its sequences go on behind it in the next round.  Pages are
 // compared one by one, so a table that no fork has made is planned rightly too.
-__global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M, int KT) {
-  __shared__ int next[kSeqs];    // next page's number; then the leader of the node that it is in
-  __shared__ int lead[kSeqs], pos[kSeqs], same[kSeqs], count[kSeqs], whole[kSeqs], cut[kSeqs];
+// Bound by latency: a dozen reads of global memory one after the other and the
+// walks of every sequence over all (4 of them at a time, from LDS).
+__global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M) {
+  // of every sequence: its next page's number, then the leader of the node that
+  // it is in; its group's leader; pages that it is past; pages in common with
+  // the leader; tokens (0: none to plan); whole pages of committed rows; of a
+  // leader: pages of its node
+  __shared__ int next[kSeqs], lead[kSeqs], pos[kSeqs], same[kSeqs], count[kSeqs], whole[kSeqs], cut[kSeqs];
   __shared__ unsigned long long best[kSeqs];
   __shared__ int nodes_s;
-  __shared__ int64_t scan[3][kPlan / kWave];
+  __shared__ int64_t sums[3][kPlanWaves];
+  __shared__ int sums32[kPlanWaves];
   constexpr int kEach = kSeqs / kPlan;
   const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = c.seqs, group = a.q_heads / c.kv_heads;
+  const int n4 = (n + 3) / 4;
   a.max_new = INT_MAX;
   if (tid == 0) nodes_s = 0;
   for (int i = tid; i < a.T; i += kPlan) plan.owner()[i] = -1;
-  __syncthreads();
-  for (int s = tid; s < n; s += kPlan) {
+  PlanSeq mine[kEach];
+  int64_t tokens = 0, all_tokens;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int s = tid + i * kPlan;
+    if (s >= n4 * 4) continue;
+    if (s >= n) {  // so that sequences are taken 4 at a time
+      next[s] = count[s] = 0, lead[s] = pos[s] = same[s] = -1;
+      continue;
+    }
     const Seq q = sequence(c, a, s, 1, 1);
     const bool on = q.n && !q.bad;
     count[s] = on ? q.n : 0, pos[s] = 0;
     whole[s] = on && int64_t(q.n) * group <= kMostRowsShared ? q.len >> c.page_shift : 0;
-    PlanSeq p{};
-    p.begin = q.begin, p.n = q.n, p.len = q.len, p.levels = on ? 0 : -1;
-    plan.seqs()[s] = p;
+    mine[i].begin = q.begin, mine[i].n = q.n, mine[i].len = q.len, mine[i].levels = on ? 0 : -1;
+    same[s] = q.begin, lead[s] = q.n;
+    tokens += count[s];
   }
-  __syncthreads();
   // tokens that two sequences claim (start not ascending) would not fit the lists
-  int64_t tokens_of = 0, all_tokens;
-  for (int s = tid; s < n; s += kPlan) tokens_of += count[s];
-  for (int step = 1; step < kWave; step *= 2) tokens_of += __shfl_xor(tokens_of, step);
-  if (lane == 0) scan[0][wave] = tokens_of;
-  __syncthreads();
-  all_tokens = 0;
-  for (int w = 0; w < kPlan / kWave; ++w) all_tokens += scan[0][w];
+  threads_before(tokens, sums[0], &all_tokens);
   if (all_tokens > a.T) {
     if (tid == 0) *plan.head() = Head{};
     return;
   }
-  __syncthreads();
-  for (int s = wave; s < n; s += kPlan / kWave) {
-    const int begin = a.start[s], end = a.start[s + 1];
-    if (begin >= 0 && end <= a.T)
-      for (int i = begin + lane; i < end; i += kWave) plan.owner()[i] = s;
-  }
+  for (int s = wave; s < n; s += kPlanWaves)
+    for (int i = lane; i < lead[s]; i += kWave) plan.owner()[same[s] + i] = s;
   for (int round = 0; round < kLevels; ++round) {
-    for (int s = tid; s < n; s += kPlan) {
-      int x = -1;
-      if (pos[s] < whole[s]) x = c.table[int64_t(s) * c.max_pages + pos[s]];
-      next[s] = x, best[s] = 0, cut[s] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int s = tid + i * kPlan;
+      if (s >= n) continue;
+      next[s] = pos[s] < whole[s] ? c.table[int64_t(s) * c.max_pages + pos[s]] : -1;
+      best[s] = 0, cut[s] = 0;
     }
     __syncthreads();
-    for (int s = tid; s < n; s += kPlan) {
+    bool groups = false;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int s = tid + i * kPlan;
+      if (s >= n) continue;
       const int x = next[s], p = pos[s];
-      int t = 0;
-      if (x >= 0) while (t < s && (next[t] != x || pos[t] != p)) ++t;
-      lead[s] = x >= 0 ? t : s;
+      int t = s;
+      if (x >= 0)
+        for (int j = 0; j * 4 < s; ++j) {
+          const int4 y = reinterpret_cast<const int4*>(next)[j], z = reinterpret_cast<const int4*>(pos)[j];
+          const int hit = y.x == x && z.x == p ? 0 : y.y == x && z.y == p ? 1 : y.z == x && z.z == p ? 2 : y.w == x && z.w == p ? 3 : 4;
+          if (hit < 4) {
+            t = min(4 * j + hit, s);
+            break;
+          }
+        }
+      lead[s] = t;
+      groups |= t != s;
     }
-    __syncthreads();
-    for (int s = wave; s < n; s += kPlan / kWave) {
-      const int t = lead[s];
-      const int d = t == s ? 0 : common(c, s, t, pos[s], min(whole[s], whole[t]));
-      if (lane == 0) same[s] = d;
-    }
+    if (!__syncthreads_or(groups)) break;
+    for (int s = wave; s < n; s += kTogether * kPlanWaves) common(c, n, s, kPlanWaves, lead, pos, whole, same);
     __syncthreads();
     unsigned long long saved[kEach];
 #pragma unroll
@@ -184,10 +259,14 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       const int s = tid + i * kPlan;
       saved[i] = 0;
       if (s >= n || lead[s] == s) continue;
-      int m = 0;
-      for (int t = lead[s] + 1; t < n; ++t) m += lead[t] == lead[s] && same[t] >= same[s];
-      saved[i] = static_cast<unsigned long long>(same[s]) * m;
-      atomicMax(&best[lead[s]], saved[i]);
+      const int l = lead[s], d = same[s];
+      int m = 0;  // sequences that have them, without the leader
+      for (int j = l / 4; j < n4; ++j) {
+        const int4 y = reinterpret_cast<const int4*>(lead)[j], z = reinterpret_cast<const int4*>(same)[j];
+        m += (y.x == l && z.x >= d) + (y.y == l && z.y >= d) + (y.z == l && z.z >= d) + (y.w == l && z.w >= d);
+      }
+      saved[i] = d > 0 ? static_cast<unsigned long long>(d) * m : 0;
+      atomicMax(&best[l], saved[i]);
     }
     __syncthreads();
 #pragma unroll
@@ -197,109 +276,119 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     }
     __syncthreads();
     bool any = false;
-    for (int s = tid; s < n; s += kPlan) {
-      const int d = cut[lead[s]];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int s = tid + i * kPlan;
+      if (s >= n4 * 4) continue;
+      const int d = s < n ? cut[lead[s]] : 0;
       any |= d > 0;
       next[s] = d > 0 && (lead[s] == s || same[s] >= d) ? lead[s] : INT_MAX;
     }
     if (!__syncthreads_or(any)) break;
     const int first_node = nodes_s;
     __syncthreads();
-    for (int s = tid; s < n; s += kPlan) {
-      const int mine = next[s];
-      if (mine == INT_MAX) continue;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int s = tid + i * kPlan;
+      const int l = s < n ? next[s] : INT_MAX;
+      if (l == INT_MAX) continue;
       // the round's list: nodes in the order of their leaders, tokens in the
       // order of their sequences
-      int node = first_node, list = 0, at = 0, tokens = 0;
-      for (int t = 0; t < n; ++t) {
-        const int x = next[t];
-        node += x == t && t < mine;
-        list += x < mine ? count[t] : 0;
-        tokens += x == mine ? count[t] : 0;
-        at += x == mine && t < s ? count[t] : 0;
+      int node = first_node, list = round * a.T, at = 0, of_node = 0;
+      for (int j = 0; j < n4; ++j) {
+        const int4 x = reinterpret_cast<const int4*>(next)[j], k = reinterpret_cast<const int4*>(count)[j];
+        auto one = [&](int t, int y, int z) {
+          node += y == t && t < l;
+          list += y < l ? z : 0;
+          of_node += y == l ? z : 0;
+          at += y == l && t < s ? z : 0;
+        };
+        one(4 * j, x.x, k.x), one(4 * j + 1, x.y, k.y), one(4 * j + 2, x.z, k.z), one(4 * j + 3, x.w, k.w);
       }
-      list += round * a.T;
-      PlanSeq& p = plan.seqs()[s];
-      for (int i = 0; i < count[s]; ++i) plan.tokens()[list + at + i] = p.begin + i;
-      p.node[p.levels] = node, p.at[p.levels] = at;
+      PlanSeq& p = mine[i];
+      for (int u = 0; u < count[s]; ++u) plan.tokens()[list + at + u] = p.begin + u;
+#pragma unroll
+      for (int v = 0; v < kLevels; ++v)
+        if (p.levels == v) p.node[v] = node, p.at[v] = at;
       ++p.levels;
-      if (s == mine) {
+      if (s == l) {
         Node x{};
         x.seq = s, x.key0 = pos[s] << c.page_shift, x.keys = cut[s] << c.page_shift;
-        x.tokens = tokens, x.list = list;
+        x.tokens = of_node, x.list = list;
         plan.nodes()[node] = x;
         atomicAdd(&nodes_s, 1);
       }
     }
     __syncthreads();
-    for (int s = tid; s < n; s += kPlan)
-      if (next[s] != INT_MAX) pos[s] += cut[next[s]];
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int s = tid + i * kPlan;
+      if (s < n && next[s] != INT_MAX) pos[s] += cut[next[s]];
+    }
   }
   __syncthreads();
-  const int shared_nodes = nodes_s;
-  __syncthreads();
   // what every sequence has for itself
-  for (int s = tid; s < n; s += kPlan) {
-    if (!count[s]) continue;
-    int node = shared_nodes;
-    for (int t = 0; t < s; ++t) node += count[t] > 0;
-    PlanSeq& p = plan.seqs()[s];
-    Node x{};
-    x.seq = s, x.key0 = pos[s] << c.page_shift;
-    x.len = p.len - x.key0, x.n = p.n, x.keys = x.len + x.n, x.begin = p.begin;
-    x.tokens = p.n, x.list = -1;
-    plan.nodes()[node] = x;
-    p.node[p.levels] = node, p.at[p.levels] = 0;
-    ++p.levels;
-    atomicAdd(&nodes_s, 1);
+  int nodes = nodes_s;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i * kPlan >= n) continue;
+    const int s = tid + i * kPlan;
+    const bool on = s < n && count[s] > 0;
+    int total;
+    const int node = nodes + threads_before(int(on), sums32, &total);
+    nodes += total;
+    __syncthreads();
+    if (s >= n) continue;
+    PlanSeq& p = mine[i];
+    if (on) {
+      Node x{};
+      x.seq = s, x.key0 = pos[s] << c.page_shift;
+      x.len = p.len - x.key0, x.n = p.n, x.keys = x.len + x.n, x.begin = p.begin;
+      x.tokens = p.n, x.list = -1;
+      plan.nodes()[node] = x;
+#pragma unroll
+      for (int v = 0; v <= kLevels; ++v)
+        if (p.levels == v) p.node[v] = node, p.at[v] = 0;
+      ++p.levels;
+    }
+    plan.seqs()[s] = p;
   }
   __syncthreads();
   // chunks of the keys, equal for all, so that there is a workgroup for each slot
-  const int nodes = nodes_s, each = (nodes + kPlan - 1) / kPlan, from = tid * each, to = min(from + each, nodes);
-  auto row_tiles = [&](const Node& x) { return (int64_t(x.tokens) * group + M - 1) / M; };
-  auto key_tiles = [&](const Node& x) { return (x.keys + KT - 1) / KT; };
-  auto prefix = [&](int64_t mine, int which, int64_t& total) {
-    int64_t incl = mine;
-    for (int step = 1; step < kWave; step *= 2) {
-      const int64_t x = __shfl_up(incl, step);
-      if (lane >= step) incl += x;
-    }
-    if (lane == kWave - 1) scan[which][wave] = incl;
-    __syncthreads();
-    int64_t before = incl - mine;
-    total = 0;
-    for (int w = 0; w < kPlan / kWave; ++w) {
-      if (w < wave) before += scan[which][w];
-      total += scan[which][w];
-    }
-    return before;
+  const int each = (nodes + kPlan - 1) / kPlan, from = min(tid * each, nodes), to = min(from + each, nodes);
+  struct Size {
+    int rows, row_tiles, key_tiles;
+  };
+  auto size = [&](const Node& x) {
+    const int64_t rows = int64_t(x.tokens) * group;
+    const int of = rows <= kSmall ? kSmall : M;
+    return Size{of, static_cast<int>((rows + of - 1) / of), (x.keys + kTile - 1) / kTile};
   };
   int64_t work = 0, total;
-  for (int i = from; i < to; ++i) work += row_tiles(plan.nodes()[i]) * key_tiles(plan.nodes()[i]);
-  prefix(work, 0, total);
-  const int64_t tiles = max(int64_t(4), (total * c.kv_heads + kSlots - 1) / kSlots);
+  for (int i = from; i < to; ++i) {
+    const Size z = size(plan.nodes()[i]);
+    work += int64_t(z.row_tiles) * z.key_tiles;
+  }
+  threads_before(work, sums[0], &total);
+  const int64_t tiles = max(int64_t(kLeastTiles), (total * c.kv_heads + kSlots - 1) / kSlots);
+  auto chunks = [&](const Size& z) { return static_cast<int>((z.key_tiles + tiles - 1) / tiles); };
   int64_t units = 0, rows = 0, all_units, all_rows;
   for (int i = from; i < to; ++i) {
-    Node& x = plan.nodes()[i];
-    x.chunks = static_cast<int>((key_tiles(x) + tiles - 1) / tiles), x.tiles = static_cast<int>(min(tiles, int64_t(key_tiles(x))));
-    units += row_tiles(x) * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
+    const Node& x = plan.nodes()[i];
+    const Size z = size(x);
+    units += int64_t(z.row_tiles) * chunks(z), rows += int64_t(x.tokens) * a.q_heads * chunks(z);
   }
-  units = prefix(units, 1, all_units), rows = prefix(rows, 2, all_rows);
-  for (int i = from; i < to; ++i) {
-    Node& x = plan.nodes()[i];
-    x.unit = static_cast<int>(units), x.part = rows;
-    units += row_tiles(x) * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
-  }
+  units = threads_before(units, sums[1], &all_units), rows = threads_before(rows, sums[2], &all_rows);
   const bool fits = all_units <= plan.y.most_units && all_rows <= plan.y.most_rows;
-  __syncthreads();
-  if (fits)
-    for (int i = wave; i < nodes; i += kPlan / kWave) {
-      const Node& x = plan.nodes()[i];
-      const int count = static_cast<int>(row_tiles(x)) * x.chunks;
-      for (int u = lane; u < count; u += kWave) plan.units()[x.unit + u] = i;
-    }
-  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all_units) : 0, nodes, M, KT, 0};
+  for (int i = from; fits && i < to; ++i) {
+    Node& x = plan.nodes()[i];
+    const Size z = size(x);
+    x.chunks = chunks(z), x.tiles = static_cast<int>(min(tiles, int64_t(z.key_tiles))), x.rows = z.rows;
+    x.unit = static_cast<int>(units), x.part = rows;
+    for (int u = 0; u < z.row_tiles * x.chunks; ++u) plan.units()[units + u] = i;
+    units += z.row_tiles * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
+  }
+  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all_units) : 0, nodes, M, {}};
 }
 
 // Whether the plan is one for this call.
@@ -310,49 +399,90 @@ __device__ inline bool planned(const Plan& plan, const KvAttention& a, int M) {
 
 // First part row of row tile rt, chunk k of a node and key head: a chunk's parts
 // are the tile's rows for head 0, then for head 1, ...
-__device__ inline int64_t part_row(const KvCache& c, const Node& x, int group, int M, int rt, int k, int h) {
-  const int64_t all = int64_t(x.tokens) * group, first = int64_t(rt) * M, rows = min(int64_t(M), all - first);
+__device__ inline int64_t part_row(const KvCache& c, const Node& x, int group, int rt, int k, int h) {
+  const int64_t all = int64_t(x.tokens) * group, first = int64_t(rt) * x.rows, rows = min(int64_t(x.rows), all - first);
   return x.part + c.kv_heads * (first * x.chunks + k * rows) + h * rows;
 }
 
-// A unit of the plan and a key head.
-template <int DT, int D, int MT>
-__global__ __launch_bounds__(kBlock) void few_nodes_kernel(KvCache c, KvAttention a, Plan plan) {
-  using Rows = FewRows<DT, D, MT>;
-  constexpr int M = Rows::M;
-  __shared__ typename Rows::Lds lds;
+// What a node that is not small is worked on by.
+enum { kFew16 = 0, kFew32, kMany64, kMany128 };
+constexpr int rows_of(int shape) { return shape == kFew16 ? 16 : shape == kFew32 ? 32 : shape == kMany64 ? 64 : 128; }
+
+template <int DT, int D, int Shape>
+struct Body {
+  using Type = FewRows<DT, D, Shape == kFew32 ? 2 : 1>;
+};
+template <int D>
+struct Body<1, D, kMany64> {
+  using Type = ManyRows<D, 2, 2>;
+};
+template <int D>
+struct Body<1, D, kMany128> {
+  using Type = ManyRows<D, 4, 1>;
+};
+
+// A unit of the plan (row tile and chunk of a node) and a key head.
+template <int DT, int D, int Shape>
+__global__ __launch_bounds__(kBlock, D == 256 ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
+  using Small = FewRows<DT, D, 1>;
+  using Large = typename Body<DT, D, Shape>::Type;
+  __shared__ union {
+    typename Small::Lds small;
+    typename Large::Lds large;
+  } lds;
   const int h = blockIdx.x % c.kv_heads, unit = blockIdx.x / c.kv_heads;
-  if (!planned(plan, a, M) || unit >= plan.head()->units) return;
-  const Node x = plan.nodes()[plan.units()[unit]];
+  if (!planned(plan, a, rows_of(Shape)) || unit >= plan.head()->units) return;
+  const Node& at = plan.nodes()[plan.units()[unit]];
+  Node x;
+  x.seq = uniform(at.seq), x.key0 = uniform(at.key0), x.keys = uniform(at.keys), x.tokens = uniform(at.tokens);
+  x.list = uniform(at.list), x.begin = uniform(at.begin), x.n = uniform(at.n), x.len = uniform(at.len);
+  x.unit = uniform(at.unit), x.chunks = uniform(at.chunks), x.tiles = uniform(at.tiles), x.rows = uniform(at.rows);
+  x.part = uniform(at.part);
   const int group = a.q_heads / c.kv_heads, all = x.tokens * group;
-  const int rt = (unit - x.unit) / x.chunks, k = (unit - x.unit) % x.chunks, row0 = rt * M, rows = min(M, all - row0);
+  const int rt = (unit - x.unit) / x.chunks, k = (unit - x.unit) % x.chunks, row0 = rt * x.rows, rows = min(x.rows, all - row0);
   const int32_t* table = c.table + int64_t(x.seq) * c.max_pages + (x.key0 >> c.page_shift);
-  const int32_t* list = x.list < 0 ? nullptr : plan.tokens() + x.list;
+  const int32_t* list = plan.tokens() + max(x.list, 0);
+  const bool own = x.list < 0;  // keys of one sequence, its new rows among them
+  if (own && x.n > a.max_new) return;
   FewTile t{};
-  t.h = h, t.kt0 = k * x.tiles, t.kt1 = min(t.kt0 + x.tiles, (x.keys + Rows::KW - 1) / Rows::KW);
-  if (list) {  // all rows see all keys
-    a.parent = nullptr;
-    t.q.len = t.limit = x.keys;
-    t.tok0 = t.tok1 = -1;
-  } else {
+  t.h = h;
+  if (own) {
     t.q.begin = x.begin, t.q.n = x.n, t.q.len = x.len;
     t.tok0 = row0 / group, t.tok1 = (row0 + rows - 1) / group;
     t.limit = a.parent ? x.keys : x.len + t.tok1 + 1;
+  } else {  // all rows see all keys
+    a.parent = nullptr;
+    t.q.len = t.limit = x.keys;
+    t.tok0 = t.tok1 = -1;
   }
-  auto page_at = [&](int key) { return max(0, min(table[key >> c.page_shift], c.pages - 1)); };
   auto query = [&](int r) {
-    const int row = row0 + min(r, rows - 1), at = row / group;
-    const int token = list ? list[at] : x.begin + at;
+    const int row = row0 + min(r, rows - 1), i = row / group;
+    const int token = own ? x.begin + i : list[i];
     return int64_t(token) * a.ldq + int64_t(h * group + row % group) * D;
   };
-  auto token = [&](int r) { return list || r >= rows ? -1 : (row0 + r) / group; };
+  auto token = [&](int r) { return own && r < rows ? (row0 + r) / group : -1; };
   const Parts parts = plan.parts();
-  const int64_t part = part_row(c, x, group, M, rt, k, h);
-  Rows::run(c, a, lds, t, page_at, query, token, [&](int r, int column, f32x4 v, float top, float l) {
+  const int64_t part = part_row(c, x, group, rt, k, h);
+  auto emit = [&](int r, int column, f32x4 v, float top, float l) {
     if (r >= rows) return;
     *reinterpret_cast<f32x4*>(parts.values + (part + r) * D + column) = v;
     if (column == 0) parts.stats[part + r] = float2{top, l};
-  });
+  };
+  auto tiles = [&](int keys) {  // key tiles of this many keys
+    t.kt0 = k * x.tiles * (kTile / keys);
+    t.kt1 = min(t.kt0 + x.tiles * (kTile / keys), (x.keys + keys - 1) / keys);
+  };
+  auto page_at = [&](int key) { return max(0, min(table[key >> c.page_shift], c.pages - 1)); };
+  if (Shape == kFew16 || x.rows == kSmall) {
+    tiles(Small::KW);
+    Small::run(c, a, lds.small, t, page_at, query, token, emit);
+  } else if constexpr (Shape == kFew32) {
+    tiles(Large::KW);
+    Large::run(c, a, lds.large, t, page_at, query, token, emit);
+  } else if constexpr (Shape >= kMany64) {
+    tiles(Large::KT);
+    Large::run(c, a, lds.large, t, table, query, token, emit);
+  }
 }
 
 // The parts of a token and query head over all its nodes: D / 4 threads to a row.
@@ -372,9 +502,9 @@ __global__ __launch_bounds__(kBlock) void join_nodes_kernel(KvCache c, KvAttenti
       PartSum sum;
       for (int i = 0; i < p.levels; ++i) {
         const Node& node = plan.nodes()[p.node[i]];
-        const int r = (p.at[i] + t - p.begin) * group + head % group, rt = r / M;
-        const int64_t first = part_row(c, node, group, M, rt, 0, h) + r % M;
-        const int64_t step = part_row(c, node, group, M, rt, 1, h) + r % M - first;
+        const int r = (p.at[i] + t - p.begin) * group + head % group, rt = r / node.rows;
+        const int64_t first = part_row(c, node, group, rt, 0, h) + r % node.rows;
+        const int64_t step = part_row(c, node, group, rt, 1, h) + r % node.rows - first;
         sum.add<D>(plan.parts(), node.chunks, column, [&](int k) { return first + k * step; });
       }
       x = sum.x * (1.f / sum.l);
@@ -383,53 +513,62 @@ __global__ __launch_bounds__(kBlock) void join_nodes_kernel(KvCache c, KvAttenti
   store4<DT>(a.out, row * D + column, x);
 }
 
-// Rows and keys of a tile.
-struct Shape {
-  int rows, keys;
-};
-Shape shape(const KvCache& c, int32_t T, int32_t q_heads) {
-  const int64_t rows = int64_t(T) * (q_heads / c.kv_heads);
-  return Shape{rows > 16 && (c.dtype == TMS_BF16 || c.head_dim < 256) ? 32 : 16, c.dtype == TMS_F32 ? 16 : 32};
+int shape(const KvCache& c, int32_t T, int32_t q_heads) {
+  const int64_t rows = int64_t(T) * (q_heads / c.kv_heads);  // of a node, at most
+  if (rows <= 16) return kFew16;
+  if (c.dtype == TMS_F32) return c.head_dim < 256 ? kFew32 : kFew16;
+  return rows <= 32 && c.head_dim < 256 ? kFew32 : rows <= 64 ? kMany64 : kMany128;
 }
 
-template <int DT, int D>
-hipError_t launch(const KvCache& c, const KvShared& sh, const Plan& plan, hipStream_t s) {
-  const KvAttention& a = sh.a;
-  const int M = shape(c, a.T, a.q_heads).rows;
+template <int DT, int D, int Shape>
+hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, hipStream_t s) {
   const int64_t blocks = int64_t(plan.y.most_units) * c.kv_heads, rows = int64_t(a.T) * a.q_heads;
   constexpr int kRows = kBlock * 4 / D;
   if (blocks >= (int64_t(1) << 32) / kBlock || rows >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  if (M == 16) few_nodes_kernel<DT, D, 1><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
-  else if constexpr (DT == 1 || D < 256) few_nodes_kernel<DT, D, 2><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  nodes_kernel<DT, D, Shape><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  join_nodes_kernel<DT, D><<<unsigned((rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, M);
+  join_nodes_kernel<DT, D><<<unsigned((rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
   return hipGetLastError();
+}
+
+template <int DT, int D>
+hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, int shape, hipStream_t s) {
+  if (shape == kFew16) return launch<DT, D, kFew16>(c, a, plan, s);
+  if constexpr (DT == 1) {
+    if (shape == kMany64) return launch<DT, D, kMany64>(c, a, plan, s);
+    if (shape == kMany128) return launch<DT, D, kMany128>(c, a, plan, s);
+  }
+  if constexpr (D < 256) return launch<DT, D, kFew32>(c, a, plan, s);
+  return hipErrorInvalidValue;
+}
+
+Plan plan_of(const KvCache& c, const KvShared& sh, int shape) {
+  return Plan{static_cast<char*>(sh.plan), layout(c, sh.a.T, sh.a.q_heads, rows_of(shape))};
 }
 
 }  // namespace
 
 int64_t kv_share_bytes(const KvCache& c, int32_t T, int32_t q_heads) {
-  return layout(c, T, q_heads, shape(c, T, q_heads).rows).bytes;
+  return layout(c, T, q_heads, rows_of(shape(c, T, q_heads))).bytes;
 }
 
 hipError_t launch_kv_share(const KvCache& c, const KvShared& sh, hipStream_t s) {
-  const Shape x = shape(c, sh.a.T, sh.a.q_heads);
-  const Plan plan{static_cast<char*>(sh.plan), layout(c, sh.a.T, sh.a.q_heads, x.rows)};
-  plan_kernel<<<1, kPlan, 0, s>>>(c, sh.a, plan, x.rows, x.keys);
+  const int x = shape(c, sh.a.T, sh.a.q_heads);
+  plan_kernel<<<1, kPlan, 0, s>>>(c, sh.a, plan_of(c, sh, x), rows_of(x));
   return hipGetLastError();
 }
 
 hipError_t launch_kv_attention_shared(const KvCache& c, const KvShared& sh, hipStream_t s) {
   // where every sequence has many rows there is nothing to share
   if (int64_t(sh.a.max_new) * (sh.a.q_heads / c.kv_heads) > kMostRowsShared) return launch_kv_attention(c, sh.a, s);
-  const Shape x = shape(c, sh.a.T, sh.a.q_heads);
-  const Plan plan{static_cast<char*>(sh.plan), layout(c, sh.a.T, sh.a.q_heads, x.rows)};
+  const int x = shape(c, sh.a.T, sh.a.q_heads);
+  const Plan plan = plan_of(c, sh, x);
   if (c.dtype == TMS_F32) {
-    if (c.head_dim == 64) return launch<0, 64>(c, sh, plan, s);
-    return c.head_dim == 128 ? launch<0, 128>(c, sh, plan, s) : launch<0, 256>(c, sh, plan, s);
+    if (c.head_dim == 64) return launch<0, 64>(c, sh.a, plan, x, s);
+    return c.head_dim == 128 ? launch<0, 128>(c, sh.a, plan, x, s) : launch<0, 256>(c, sh.a, plan, x, s);
   }
-  if (c.head_dim == 64) return launch<1, 64>(c, sh, plan, s);
-  return c.head_dim == 128 ? launch<1, 128>(c, sh, plan, s) : launch<1, 256>(c, sh, plan, s);
+  if (c.head_dim == 64) return launch<1, 64>(c, sh.a, plan, x, s);
+  return c.head_dim == 128 ? launch<1, 128>(c, sh.a, plan, x, s) : launch<1, 256>(c, sh.a, plan, x, s);
 }
 
 }  // namespace tms
