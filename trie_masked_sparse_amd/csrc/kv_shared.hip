@@ -30,9 +30,15 @@ constexpr int kMagic = 0x73686172;
 // themselves: the products bound them, and many rows share a page's read already.
 constexpr int kMostRowsShared = 128;
 
-// Rows of the prefix that are not read again (its rows times the sequences but
-// one) have to be at least this for a node.
+// A node pays where the keys that are not read again (its keys, times the
+// readers that it saves) are more than these and what its rows' parts cost: a
+// part is written and read, 8 bytes a value, a key 2 values of the cache's type.
 constexpr int kLeastSaved = 256;
+__device__ inline bool pays(int64_t keys, int64_t readers, int64_t rows, int dtype) {
+  return keys * readers >= kLeastSaved + (dtype == 0 ? 2 : 4) * rows;
+}
+
+constexpr int kRounds = 8;
 
 // Key tiles of a chunk, at least.
 constexpr int kLeastTiles = 4;
@@ -97,10 +103,12 @@ struct Plan {
 };
 
 // Pages that the sequences first, first + step, ... (kTogether of them) have in
-// common with their leaders, from their next pages on, by one wavefront.
-constexpr int kTogether = 2;
+// common with their leaders, from their next pages on, where redo says so; by one
+// wavefront.
+constexpr int kTogether = 4;
+template <class Redo>
 __device__ inline void common(const KvCache& c, int n, int first, int step, const int* lead, const int* pos, const int* whole,
-                              int* same) {
+                              int* same, Redo redo) {
   constexpr int kLoads = 6;
   const int lane = threadIdx.x % kWave;
   int at[kTogether], most[kTogether];
@@ -108,14 +116,14 @@ __device__ inline void common(const KvCache& c, int n, int first, int step, cons
   bool left = false;
 #pragma unroll
   for (int i = 0; i < kTogether; ++i) {
-    const int s = first + i * step, t = s < n ? lead[s] : s;
+    const int s = min(first + i * step, n - 1), t = uniform(lead[s]);
     at[i] = most[i] = 0;
-    if (s >= n) continue;
+    x[i] = c.table + int64_t(s) * c.max_pages, y[i] = c.table + int64_t(t) * c.max_pages;
+    if (first + i * step >= n || !redo(s)) continue;
     if (lane == 0) same[s] = 0;
     if (t == s) continue;
-    at[i] = pos[s], most[i] = min(whole[s], whole[t]);
-    x[i] = c.table + int64_t(s) * c.max_pages, y[i] = c.table + int64_t(t) * c.max_pages;
-    left = true;
+    at[i] = uniform(pos[s]), most[i] = uniform(min(whole[s], whole[t]));
+    left |= at[i] < most[i];
   }
   while (left) {
     int a[kTogether][kLoads], b[kTogether][kLoads];
@@ -173,46 +181,69 @@ __device__ inline T threads_before(T mine, T* sums, T* total) {
 }
 
 // One workgroup.  In every round, sequences that have the same next page form a
-// group; its first sequence is the leader, and the cut that saves most reads
-// (pages in common with the leader, times the sequences that have them but one)
-// makes a node.  Its sequences go on behind it in the next round.  Pages are
-// compared one by one, so a table that no fork has made is planned rightly too.
-// Bound by latency: a dozen reads of global memory one after the other and the
-// walks of every sequence over all (4 of them at a time, from LDS).
+// group; its first sequence is the leader.  The pages that the whole group has
+// make a node, if that pays: without it, every branch of the group (sequences
+// that have the same page behind them) would read them.  Else every branch is
+// a group, and the cut that saves most reads (pages in common with the leader,
+// times the sequences that have them but one) makes a node.  The sequences of a
+// node go on behind it in the next round.  Pages are compared one by one, so a
+// table that no fork has made is planned rightly too.
+//
+// Bound by latency: a dozen reads of global memory one after the other, and the
+// walks of every sequence over all, which are shared by the threads that are to
+// spare, 4 sequences a step.
 __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M) {
   // of every sequence: its next page's number, then the leader of the node that
   // it is in; its group's leader; pages that it is past; pages in common with
-  // the leader; tokens (0: none to plan); whole pages of committed rows; of a
-  // leader: pages of its node
+  // the leader; tokens (0: none to plan); whole pages of committed rows.  Of a
+  // leader: pages of its node; the fewest that one of its group has in common;
+  // branches and tokens of its group
   __shared__ int next[kSeqs], lead[kSeqs], pos[kSeqs], same[kSeqs], count[kSeqs], whole[kSeqs], cut[kSeqs];
-  __shared__ unsigned long long best[kSeqs];
-  __shared__ int nodes_s;
+  __shared__ union {
+    unsigned long long best[kSeqs];
+    struct {
+      int fewest[kSeqs], branches[kSeqs];
+    } of;
+  } lds;
+  __shared__ int nodes_s, list_s, big_s;
   __shared__ int64_t sums[3][kPlanWaves];
   __shared__ int sums32[kPlanWaves];
   constexpr int kEach = kSeqs / kPlan;
   const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = c.seqs, group = a.q_heads / c.kv_heads;
   const int n4 = (n + 3) / 4;
+  int parts = 1;  // threads of a sequence, adjacent lanes
+  while (parts < kWave && 2 * parts * n <= kPlan) parts *= 2;
+  const int first = tid / parts, share = tid % parts;
+  auto each_seq = [&](auto f) __attribute__((always_inline)) {  // f(i, s), of every sequence of this thread
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (first + i * kPlan < n) f(i, first + i * kPlan);
+  };
+  auto all_of = [&](int x, auto join) __attribute__((always_inline)) {  // over the threads of a sequence
+    for (int step = 1; step < parts; step *= 2) x = join(x, __shfl_xor(x, step));
+    return x;
+  };
+  auto plus = [](int x, int y) { return x + y; };
+  auto fours = [](const int* x, int j) { return reinterpret_cast<const int4*>(x)[j]; };
   a.max_new = INT_MAX;
-  if (tid == 0) nodes_s = 0;
+  if (tid == 0) nodes_s = list_s = big_s = 0;
   for (int i = tid; i < a.T; i += kPlan) plan.owner()[i] = -1;
+  if (tid < n4 * 4 - n) {  // so that sequences are taken 4 at a time
+    next[n + tid] = INT_MAX, count[n + tid] = 0, lead[n + tid] = pos[n + tid] = same[n + tid] = -1;
+  }
   PlanSeq mine[kEach];
   int64_t tokens = 0, all_tokens;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int s = tid + i * kPlan;
-    if (s >= n4 * 4) continue;
-    if (s >= n) {  // so that sequences are taken 4 at a time
-      next[s] = count[s] = 0, lead[s] = pos[s] = same[s] = -1;
-      continue;
-    }
+  each_seq([&](int i, int s) __attribute__((always_inline)) {
     const Seq q = sequence(c, a, s, 1, 1);
     const bool on = q.n && !q.bad;
-    count[s] = on ? q.n : 0, pos[s] = 0;
-    whole[s] = on && int64_t(q.n) * group <= kMostRowsShared ? q.len >> c.page_shift : 0;
     mine[i].begin = q.begin, mine[i].n = q.n, mine[i].len = q.len, mine[i].levels = on ? 0 : -1;
-    same[s] = q.begin, lead[s] = q.n;
-    tokens += count[s];
-  }
+    if (share == 0) {
+      count[s] = on ? q.n : 0, pos[s] = 0;
+      whole[s] = on && int64_t(q.n) * group <= kMostRowsShared ? q.len >> c.page_shift : 0;
+      same[s] = q.begin, lead[s] = q.n;
+      tokens += on ? q.n : 0;
+    }
+  });
   // tokens that two sequences claim (start not ascending) would not fit the lists
   threads_before(tokens, sums[0], &all_tokens);
   if (all_tokens > a.T) {
@@ -221,82 +252,124 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
   }
   for (int s = wave; s < n; s += kPlanWaves)
     for (int i = lane; i < lead[s]; i += kWave) plan.owner()[same[s] + i] = s;
-  for (int round = 0; round < kLevels; ++round) {
+  for (int round = 0; round < kRounds; ++round) {
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      if (s >= n) continue;
-      next[s] = pos[s] < whole[s] ? c.table[int64_t(s) * c.max_pages + pos[s]] : -1;
-      best[s] = 0, cut[s] = 0;
-    }
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      if (share) return;
+      next[s] = pos[s] < whole[s] && mine[i].levels < kLevels ? c.table[int64_t(s) * c.max_pages + pos[s]] : -1;
+      lds.of.fewest[s] = INT_MAX, lds.of.branches[s] = 0, cut[s] = 0;
+    });
     __syncthreads();
-    bool groups = false;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      if (s >= n) continue;
-      const int x = next[s], p = pos[s];
+    // the first sequence with the same x and the same y
+    auto first_like = [&](int s, const int* x, const int* y) __attribute__((always_inline)) {
+      const int u = x[s], v = y[s];
       int t = s;
-      if (x >= 0)
-        for (int j = 0; j * 4 < s; ++j) {
-          const int4 y = reinterpret_cast<const int4*>(next)[j], z = reinterpret_cast<const int4*>(pos)[j];
-          const int hit = y.x == x && z.x == p ? 0 : y.y == x && z.y == p ? 1 : y.z == x && z.z == p ? 2 : y.w == x && z.w == p ? 3 : 4;
+      if (u >= 0)
+        for (int j = share; j * 4 < s; j += parts) {
+          const int4 p = fours(x, j), q = fours(y, j);
+          const int hit = p.x == u && q.x == v ? 0 : p.y == u && q.y == v ? 1 : p.z == u && q.z == v ? 2 : p.w == u && q.w == v ? 3 : 4;
           if (hit < 4) {
             t = min(4 * j + hit, s);
             break;
           }
         }
-      lead[s] = t;
+      return all_of(t, [](int x, int y) { return min(x, y); });
+    };
+    bool groups = false;
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      const int t = first_like(s, next, pos);
+      if (share == 0) lead[s] = t;
       groups |= t != s;
-    }
+    });
     if (!__syncthreads_or(groups)) break;
-    for (int s = wave; s < n; s += kTogether * kPlanWaves) common(c, n, s, kPlanWaves, lead, pos, whole, same);
+    for (int s = wave; s < n; s += kTogether * kPlanWaves) common(c, n, s, kPlanWaves, lead, pos, whole, same, [](int) { return true; });
+    __syncthreads();
+    each_seq([&](int, int s) __attribute__((always_inline)) {
+      if (share == 0 && lead[s] != s) atomicMin(&lds.of.fewest[lead[s]], same[s]);
+    });
+    __syncthreads();
+    each_seq([&](int, int s) __attribute__((always_inline)) {  // the page behind what all have
+      if (share) return;
+      const int d = lds.of.fewest[lead[s]], p = pos[s] + d;
+      next[s] = d < INT_MAX && p < whole[s] ? c.table[int64_t(s) * c.max_pages + p] : -1;
+    });
+    __syncthreads();
+    int branch[kEach];
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      branch[i] = first_like(s, next, lead);
+      if (share == 0 && branch[i] == s) atomicAdd(&lds.of.branches[lead[s]], 1);
+    });
+    __syncthreads();
+    bool any = false, redo = false;
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      const int l = lead[s], d = lds.of.fewest[l];
+      if (d == INT_MAX) return;  // alone
+      int tokens = 0;
+      for (int j = share; j < n4; j += parts) {
+        const int4 x = fours(lead, j), k = fours(count, j);
+        tokens += (x.x == l ? k.x : 0) + (x.y == l ? k.y : 0) + (x.z == l ? k.z : 0) + (x.w == l ? k.w : 0);
+      }
+      tokens = all_of(tokens, plus);
+      const bool all = d > 0 && pays(int64_t(d) << c.page_shift, lds.of.branches[l] - 1, int64_t(tokens) * group, c.dtype);
+      if (all && share == 0 && s == l) cut[s] = d;
+      if (all) branch[i] = -1;  // in the node of the whole group
+    });
+    __syncthreads();
+    // groups that have no node: their branches
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      const bool other = branch[i] >= 0 && lds.of.fewest[lead[s]] < INT_MAX && branch[i] != lead[s];
+      if (share == 0) next[s] = other;
+      redo |= other;
+      if (share == 0 && other) lead[s] = branch[i];
+    });
+    if (__syncthreads_or(redo)) {
+      for (int s = wave; s < n; s += kTogether * kPlanWaves)
+        common(c, n, s, kPlanWaves, lead, pos, whole, same, [&](int s) { return uniform(next[s]) != 0; });
+      __syncthreads();
+    }
+    each_seq([&](int, int s) __attribute__((always_inline)) {
+      if (share == 0) lds.best[s] = 0;
+    });
     __syncthreads();
     unsigned long long saved[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
       saved[i] = 0;
-      if (s >= n || lead[s] == s) continue;
       const int l = lead[s], d = same[s];
-      int m = 0;  // sequences that have them, without the leader
-      for (int j = l / 4; j < n4; ++j) {
-        const int4 y = reinterpret_cast<const int4*>(lead)[j], z = reinterpret_cast<const int4*>(same)[j];
-        m += (y.x == l && z.x >= d) + (y.y == l && z.y >= d) + (y.z == l && z.z >= d) + (y.w == l && z.w >= d);
+      if (l == s || cut[l] > 0 || d == 0) return;
+      int m = 0, tokens = 0;  // of those that have d pages in common with the leader
+      for (int j = l / 4 + share; j < n4; j += parts) {
+        const int4 y = fours(lead, j), z = fours(same, j), k = fours(count, j);
+        auto one = [&](int y, int z, int k) {
+          const bool on = y == l && z >= d;
+          m += on, tokens += on ? k : 0;
+        };
+        one(y.x, z.x, k.x), one(y.y, z.y, k.y), one(y.z, z.z, k.z), one(y.w, z.w, k.w);
       }
-      saved[i] = d > 0 ? static_cast<unsigned long long>(d) * m : 0;
-      atomicMax(&best[l], saved[i]);
-    }
+      m = all_of(m, plus), tokens = all_of(tokens, plus) + count[l];
+      if (pays(int64_t(d) << c.page_shift, m, int64_t(tokens) * group, c.dtype)) saved[i] = static_cast<unsigned long long>(d) * m;
+      if (share == 0 && saved[i]) atomicMax(&lds.best[l], saved[i]);
+    });
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      if (saved[i] && saved[i] == best[lead[s]] && saved[i] << c.page_shift >= kLeastSaved) atomicMax(&cut[lead[s]], same[s]);
-    }
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      if (share == 0 && saved[i] && saved[i] == lds.best[lead[s]]) atomicMax(&cut[lead[s]], same[s]);
+    });
     __syncthreads();
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      if (s >= n4 * 4) continue;
-      const int d = s < n ? cut[lead[s]] : 0;
+    each_seq([&](int, int s) __attribute__((always_inline)) {
+      const int d = cut[lead[s]];
       any |= d > 0;
-      next[s] = d > 0 && (lead[s] == s || same[s] >= d) ? lead[s] : INT_MAX;
-    }
+      if (share == 0) next[s] = d > 0 && (lead[s] == s || same[s] >= d) ? lead[s] : INT_MAX;
+    });
     if (!__syncthreads_or(any)) break;
-    const int first_node = nodes_s;
+    const int first_node = nodes_s, first_token = list_s;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      const int l = s < n ? next[s] : INT_MAX;
-      if (l == INT_MAX) continue;
-      // the round's list: nodes in the order of their leaders, tokens in the
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      const int l = next[s];
+      if (l == INT_MAX) return;
+      // the lists of a round: nodes in the order of their leaders, tokens in the
       // order of their sequences
-      int node = first_node, list = round * a.T, at = 0, of_node = 0;
-      for (int j = 0; j < n4; ++j) {
-        const int4 x = reinterpret_cast<const int4*>(next)[j], k = reinterpret_cast<const int4*>(count)[j];
+      int node = 0, list = 0, at = 0, of_node = 0;
+      for (int j = share; j < n4; j += parts) {
+        const int4 x = fours(next, j), k = fours(count, j);
         auto one = [&](int t, int y, int z) {
           node += y == t && t < l;
           list += y < l ? z : 0;
@@ -305,26 +378,26 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
         };
         one(4 * j, x.x, k.x), one(4 * j + 1, x.y, k.y), one(4 * j + 2, x.z, k.z), one(4 * j + 3, x.w, k.w);
       }
+      node = first_node + all_of(node, plus), list = first_token + all_of(list, plus);
+      of_node = all_of(of_node, plus), at = all_of(at, plus);
       PlanSeq& p = mine[i];
-      for (int u = 0; u < count[s]; ++u) plan.tokens()[list + at + u] = p.begin + u;
+      for (int u = share; u < count[s]; u += parts) plan.tokens()[list + at + u] = p.begin + u;
 #pragma unroll
       for (int v = 0; v < kLevels; ++v)
         if (p.levels == v) p.node[v] = node, p.at[v] = at;
       ++p.levels;
-      if (s == l) {
+      if (s == l && share == 0) {
         Node x{};
         x.seq = s, x.key0 = pos[s] << c.page_shift, x.keys = cut[s] << c.page_shift;
         x.tokens = of_node, x.list = list;
         plan.nodes()[node] = x;
-        atomicAdd(&nodes_s, 1);
+        atomicAdd(&nodes_s, 1), atomicAdd(&list_s, of_node);
       }
-    }
+    });
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int s = tid + i * kPlan;
-      if (s < n && next[s] != INT_MAX) pos[s] += cut[next[s]];
-    }
+    each_seq([&](int, int s) __attribute__((always_inline)) {
+      if (share == 0 && next[s] != INT_MAX) pos[s] += cut[next[s]];
+    });
   }
   __syncthreads();
   // what every sequence has for itself
@@ -332,13 +405,13 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     if (i * kPlan >= n) continue;
-    const int s = tid + i * kPlan;
-    const bool on = s < n && count[s] > 0;
+    const int s = first + i * kPlan;
+    const bool on = share == 0 && s < n && count[s] > 0;
     int total;
     const int node = nodes + threads_before(int(on), sums32, &total);
     nodes += total;
     __syncthreads();
-    if (s >= n) continue;
+    if (s >= n || share) continue;
     PlanSeq& p = mine[i];
     if (on) {
       Node x{};
@@ -385,9 +458,21 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     const Size z = size(x);
     x.chunks = chunks(z), x.tiles = static_cast<int>(min(tiles, int64_t(z.key_tiles))), x.rows = z.rows;
     x.unit = static_cast<int>(units), x.part = rows;
-    for (int u = 0; u < z.row_tiles * x.chunks; ++u) plan.units()[units + u] = i;
+    const int count_here = z.row_tiles * x.chunks;
+    if (count_here <= 2) {
+      for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
+    } else {  // many: by all threads
+      const int at = atomicAdd(&big_s, 1);
+      if (at < kSeqs) next[at] = i, lead[at] = static_cast<int>(units), pos[at] = count_here;
+      else
+        for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
+    }
     units += z.row_tiles * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
   }
+  __syncthreads();
+  const int big = min(big_s, kSeqs);
+  for (int b = wave; b < big; b += kPlanWaves)
+    for (int u = lane; u < pos[b]; u += kWave) plan.units()[lead[b] + u] = next[b];
   if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all_units) : 0, nodes, M, {}};
 }
 
