@@ -38,7 +38,7 @@ __device__ inline bool pays(int64_t keys, int64_t readers, int64_t rows, int dty
   return keys * readers >= kLeastSaved + (dtype == 0 ? 2 : 4) * rows;
 }
 
-constexpr int kRounds = 8;
+constexpr int kRounds = 16;  // branchings of the trie that are looked at, one behind the other
 
 // Key tiles of a chunk, at least.
 constexpr int kLeastTiles = 4;
@@ -52,6 +52,14 @@ struct PlanSeq {
   int32_t node[kLevels + 1], at[kLevels + 1];  // nodes, and where its tokens are among a node's
 };
 
+// Of a sequence: among those before it the first that has most pages in common
+// with it, from the first page on, and how many (0: itself).  Two sequences have
+// as many pages in common as the fewest on the way from one to the other along
+// these: the trie of the tables' rows.
+struct Meet {
+  int32_t with, pages;
+};
+
 struct Node {
   int32_t seq, key0, keys;   // the sequence whose table has the pages; first row, rows
   int32_t tokens, list;      // query tokens; their place in the list, -1: begin ..
@@ -62,7 +70,7 @@ struct Node {
 
 // Places in the plan.  M: rows of a tile of nodes that are not small.
 struct Layout {
-  int64_t seqs, nodes, units, tokens, owner, stats, values, bytes;
+  int64_t seqs, meets, nodes, units, tokens, owner, stats, values, bytes;
   int32_t most_nodes, most_units;
   int64_t most_rows;
 };
@@ -78,7 +86,8 @@ Layout layout(const KvCache& c, int32_t T, int32_t q_heads, int M) {
   y.most_units = static_cast<int32_t>(tiles + kSlots / c.kv_heads + 1);
   y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + (kSlots + c.kv_heads) * int64_t(M);
   y.seqs = up(sizeof(Head));
-  y.nodes = up(y.seqs + c.seqs * int64_t(sizeof(PlanSeq)));
+  y.meets = up(y.seqs + c.seqs * int64_t(sizeof(PlanSeq)));
+  y.nodes = up(y.meets + c.seqs * int64_t(sizeof(Meet)));
   y.units = up(y.nodes + y.most_nodes * int64_t(sizeof(Node)));
   y.tokens = up(y.units + y.most_units * int64_t(4));
   y.owner = up(y.tokens + kLevels * int64_t(T) * 4);
@@ -93,6 +102,7 @@ struct Plan {
   Layout y;
   __device__ Head* head() const { return reinterpret_cast<Head*>(at); }
   __device__ PlanSeq* seqs() const { return reinterpret_cast<PlanSeq*>(at + y.seqs); }
+  __device__ Meet* meets() const { return reinterpret_cast<Meet*>(at + y.meets); }
   __device__ Node* nodes() const { return reinterpret_cast<Node*>(at + y.nodes); }
   __device__ int32_t* units() const { return reinterpret_cast<int32_t*>(at + y.units); }    // node of every unit
   __device__ int32_t* tokens() const { return reinterpret_cast<int32_t*>(at + y.tokens); }  // of the nodes, a list for each level
@@ -102,301 +112,271 @@ struct Plan {
   }
 };
 
-// Pages that the sequences first, first + step, ... (kTogether of them) have in
-// common with their leaders, from their next pages on, where redo says so; by one
-// wavefront.
-constexpr int kTogether = 4;
-template <class Redo>
-__device__ inline void common(const KvCache& c, int n, int first, int step, const int* lead, const int* pos, const int* whole,
-                              int* same, Redo redo) {
-  constexpr int kLoads = 6;
-  const int lane = threadIdx.x % kWave;
-  int at[kTogether], most[kTogether];
-  const int32_t *x[kTogether], *y[kTogether];
-  bool left = false;
-#pragma unroll
-  for (int i = 0; i < kTogether; ++i) {
-    const int s = min(first + i * step, n - 1), t = uniform(lead[s]);
-    at[i] = most[i] = 0;
-    x[i] = c.table + int64_t(s) * c.max_pages, y[i] = c.table + int64_t(t) * c.max_pages;
-    if (first + i * step >= n || !redo(s)) continue;
-    if (lane == 0) same[s] = 0;
-    if (t == s) continue;
-    at[i] = uniform(pos[s]), most[i] = uniform(min(whole[s], whole[t]));
-    left |= at[i] < most[i];
-  }
-  while (left) {
-    int a[kTogether][kLoads], b[kTogether][kLoads];
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i)
-      if (at[i] < most[i])
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const int j = min(at[i] + u * kWave + lane, most[i] - 1);
-          a[i][u] = x[i][j], b[i][u] = y[i][j];
-        }
-    left = false;
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i) {
-      if (at[i] >= most[i]) continue;
-      const int s = first + i * step;
-      int end = -1;
+// Whole pages of committed rows of a sequence that may be shared.
+__device__ inline int shared_pages(const KvCache& c, const KvAttention& a, const Seq& q) {
+  return q.n && !q.bad && int64_t(q.n) * (a.q_heads / c.kv_heads) <= kMostRowsShared ? q.len >> c.page_shift : 0;
+}
+
+// Meet of sequence s, by one wavefront; whole(t): shared_pages of a sequence.  A
+// sequence that has more pages in common than the best so far has the same page
+// behind these, which is looked for first; pages are then compared one by one,
+// so a table that no fork has made is planned rightly too.
+template <class Whole>
+__device__ inline Meet meet(const KvCache& c, int s, Whole whole) {
+  constexpr int kLoads = 4;
+  const int lane = threadIdx.x % kWave, mine = uniform(whole(s));
+  const int32_t* x = c.table + int64_t(s) * c.max_pages;
+  Meet best{s, 0};
+  for (int t0 = 0; t0 < s && best.pages < mine;) {
+    const int page = uniform(x[best.pages]);
+    // (a page that no other sequence holds is not looked for)
+    if (page < 0 || page >= c.pages || uniform(c.refs[page]) < 2) break;
+    int t = s;
+    for (; t0 < s && t == s; t0 += kWave) {
+      const int u = t0 + lane;
+      const bool hit = u < s && whole(min(u, s)) > best.pages && c.table[int64_t(min(u, s)) * c.max_pages + best.pages] == page;
+      const uint64_t hits = __ballot(hit);
+      if (hits) t = t0 + __builtin_ctzll(hits);
+    }
+    if (t == s) break;
+    t0 = t + 1;
+    const int most = min(mine, uniform(whole(t)));
+    const int32_t* y = c.table + int64_t(t) * c.max_pages;
+    int end = most;
+    for (int j0 = 0; j0 < most && end == most; j0 += kLoads * kWave) {
+      int p[kLoads], q[kLoads];
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const uint64_t differ = __ballot(a[i][u] != b[i][u] || at[i] + u * kWave + lane >= most[i]);
-        if (differ && end < 0) end = min(at[i] + u * kWave + __builtin_ctzll(differ), most[i]);
+        const int j = min(j0 + u * kWave + lane, most - 1);
+        p[u] = x[j], q[u] = y[j];
       }
-      at[i] += kLoads * kWave;
-      if (end < 0 && at[i] >= most[i]) end = most[i];
-      if (end >= 0) {
-        if (lane == 0) same[s] = end - pos[s];
-        at[i] = most[i];
-      } else {
-        left = true;
+#pragma unroll
+      for (int u = kLoads - 1; u >= 0; --u) {
+        const uint64_t differ = __ballot(p[u] != q[u]);
+        if (differ) end = min(j0 + u * kWave + __builtin_ctzll(differ), most);
       }
+    }
+    if (end > best.pages) best = Meet{t, end};
+  }
+  return best;
+}
+
+// A wavefront for each sequence.
+__global__ __launch_bounds__(kWave) void meet_kernel(KvCache c, KvAttention a, Plan plan) {
+  a.max_new = INT_MAX;
+  const Meet m = meet(c, blockIdx.x, [&](int t) { return shared_pages(c, a, sequence(c, a, t, 1, 1)); });
+  if (threadIdx.x == 0) plan.meets()[blockIdx.x] = m;
+}
+
+// Sums over the workgroup's threads before this one, and of all, of N values;
+// `sums` is free again behind the next barrier.
+template <int N, typename T>
+__device__ inline void threads_before(T (&x)[N], T (*sums)[kPlanWaves], T (&total)[N]) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  T incl[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) incl[i] = x[i];
+#pragma unroll
+  for (int step = 1; step < kWave; step *= 2) {
+    T y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = __shfl_up(incl[i], step);
+#pragma unroll
+    for (int i = 0; i < N; ++i) incl[i] += lane >= step ? y[i] : 0;
+  }
+  if (lane == kWave - 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i][wave] = incl[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = incl[i] - x[i], total[i] = 0;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      if (w < wave) x[i] += sums[i][w];
+      total[i] += sums[i][w];
     }
   }
 }
 
-// Sums over the workgroup's threads before this one, and of all; `sums` is free
-// again behind the next barrier.
-template <typename T>
-__device__ inline T threads_before(T mine, T* sums, T* total) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  T incl = mine;
-#pragma unroll
-  for (int step = 1; step < kWave; step *= 2) {
-    const T x = __shfl_up(incl, step);
-    if (lane >= step) incl += x;
-  }
-  if (lane == kWave - 1) sums[wave] = incl;
-  __syncthreads();
-  T before = incl - mine;
-  *total = 0;
-  for (int w = 0; w < kPlanWaves; ++w) {
-    if (w < wave) before += sums[w];
-    *total += sums[w];
-  }
-  return before;
+// Sum of the lanes' values up to and including this one's.
+__device__ inline int lanes_up_to(int x) {
+  x += from_lane<0x111, 0xf>(x);  // 1, 2, 4 and 8 lanes down in rows of 16
+  x += from_lane<0x112, 0xf>(x);
+  x += from_lane<0x114, 0xf>(x);
+  x += from_lane<0x118, 0xf>(x);
+  x += from_lane<0x142, 0xa>(x);  // row 0 to row 1, row 2 to row 3
+  x += from_lane<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
+  return x;
 }
 
-// One workgroup.  In every round, sequences that have the same next page form a
-// group; its first sequence is the leader.  The pages that the whole group has
-// make a node, if that pays: without it, every branch of the group (sequences
-// that have the same page behind them) would read them.  Else every branch is
-// a group, and the cut that saves most reads (pages in common with the leader,
-// times the sequences that have them but one) makes a node.  The sequences of a
-// node go on behind it in the next round.  Pages are compared one by one, so a
-// table that no fork has made is planned rightly too.
+// Calls f(value, lanes that have it), a value after the other, for the lanes
+// where `on`.
+template <class F>
+__device__ inline void each_value(bool on, int value, F f) {
+  for (uint64_t left = __ballot(on); left;) {
+    const int v = __builtin_amdgcn_readlane(value, __builtin_ctzll(left));
+    const uint64_t same = __ballot(on && value == v);
+    f(v, same);
+    left &= ~same;
+  }
+}
+
+// One workgroup.  In every round a group are the sequences that go through one
+// place of the trie; its first is the leader.  The pages that the whole group
+// has in common, from where its sequences read, make a node, if that pays:
+// without it every branch of the group (sequences that have the next page in
+// common too) would read them.  Behind them every branch is a group.
 //
-// Bound by latency: a dozen reads of global memory one after the other, and the
-// walks of every sequence over all, which are shared by the threads that are to
-// spare, 4 sequences a step.
+// Bound by latency: reads of global memory one after the other, and the code
+// itself, which is fetched for the first time in every call (kEach 4, for all
+// caches, is four times as much: 64 sequences 34 us instead of 27).
+constexpr int kMeetHere = 16;  // sequences whose meets are found here: a launch less
+template <int kEach>
 __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M) {
-  // of every sequence: its next page's number, then the leader of the node that
-  // it is in; its group's leader; pages that it is past; pages in common with
-  // the leader; tokens (0: none to plan); whole pages of committed rows.  Of a
-  // leader: pages of its node; the fewest that one of its group has in common;
-  // branches and tokens of its group
-  __shared__ int next[kSeqs], lead[kSeqs], pos[kSeqs], same[kSeqs], count[kSeqs], whole[kSeqs], cut[kSeqs];
-  __shared__ union {
-    unsigned long long best[kSeqs];
-    struct {
-      int fewest[kSeqs], branches[kSeqs];
-    } of;
-  } lds;
+  constexpr int kMost = kEach * kPlan;  // sequences
+  // of every sequence: the first of its group; tokens (0: none to share); its Meet.
+  // Of a leader: the fewest pages that one of its group has in common with it, the
+  // others' tokens, branches; its node's number and list
+  __shared__ int lead[kMost], with[kMost], pages[kMost], fewest[kMost], of_group[kMost], branches[kMost], place[kMost], whole[kMost];
+  __shared__ uint16_t count[kMost];
   __shared__ int nodes_s, list_s, big_s;
   __shared__ int64_t sums[3][kPlanWaves];
-  __shared__ int sums32[kPlanWaves];
-  constexpr int kEach = kSeqs / kPlan;
+  __shared__ int sums32[1][kPlanWaves];
   const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = c.seqs, group = a.q_heads / c.kv_heads;
-  const int n4 = (n + 3) / 4;
-  int parts = 1;  // threads of a sequence, adjacent lanes
-  while (parts < kWave && 2 * parts * n <= kPlan) parts *= 2;
-  const int first = tid / parts, share = tid % parts;
   auto each_seq = [&](auto f) __attribute__((always_inline)) {  // f(i, s), of every sequence of this thread
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if (first + i * kPlan < n) f(i, first + i * kPlan);
+      if (tid + i * kPlan < n) f(i, tid + i * kPlan);
   };
-  auto all_of = [&](int x, auto join) __attribute__((always_inline)) {  // over the threads of a sequence
-    for (int step = 1; step < parts; step *= 2) x = join(x, __shfl_xor(x, step));
-    return x;
-  };
-  auto plus = [](int x, int y) { return x + y; };
-  auto fours = [](const int* x, int j) { return reinterpret_cast<const int4*>(x)[j]; };
   a.max_new = INT_MAX;
   if (tid == 0) nodes_s = list_s = big_s = 0;
   for (int i = tid; i < a.T; i += kPlan) plan.owner()[i] = -1;
-  if (tid < n4 * 4 - n) {  // so that sequences are taken 4 at a time
-    next[n + tid] = INT_MAX, count[n + tid] = 0, lead[n + tid] = pos[n + tid] = same[n + tid] = -1;
-  }
   PlanSeq mine[kEach];
-  int64_t tokens = 0, all_tokens;
+  int64_t tokens[1] = {0}, all_tokens[1];
   each_seq([&](int i, int s) __attribute__((always_inline)) {
     const Seq q = sequence(c, a, s, 1, 1);
     const bool on = q.n && !q.bad;
     mine[i].begin = q.begin, mine[i].n = q.n, mine[i].len = q.len, mine[i].levels = on ? 0 : -1;
-    if (share == 0) {
-      count[s] = on ? q.n : 0, pos[s] = 0;
-      whole[s] = on && int64_t(q.n) * group <= kMostRowsShared ? q.len >> c.page_shift : 0;
-      same[s] = q.begin, lead[s] = q.n;
-      tokens += on ? q.n : 0;
+    whole[s] = shared_pages(c, a, q);
+    count[s] = whole[s] ? q.n : 0;
+    if (n > kMeetHere) {
+      const Meet m = plan.meets()[s];
+      with[s] = m.with, pages[s] = m.pages;
     }
+    fewest[s] = q.begin, lead[s] = q.n;
+    tokens[0] += on ? q.n : 0;
   });
   // tokens that two sequences claim (start not ascending) would not fit the lists
-  threads_before(tokens, sums[0], &all_tokens);
-  if (all_tokens > a.T) {
+  threads_before(tokens, sums, all_tokens);
+  if (all_tokens[0] > a.T) {
     if (tid == 0) *plan.head() = Head{};
     return;
   }
   for (int s = wave; s < n; s += kPlanWaves)
-    for (int i = lane; i < lead[s]; i += kWave) plan.owner()[same[s] + i] = s;
+    for (int i = lane; i < lead[s]; i += kWave) plan.owner()[fewest[s] + i] = s;
+  if (n <= kMeetHere && wave < n) {
+    const Meet m = meet(c, wave, [&](int t) { return whole[t]; });
+    if (lane == 0) with[wave] = m.with, pages[wave] = m.pages;
+  }
+  // the first sequence that goes through the place behind `depth` pages of
+  // sequence s, and the pages that s has in common with it
+  auto first_at = [&](int s, int depth, int* in_common) __attribute__((always_inline)) {
+    int m = INT_MAX, v = s;
+    for (int p = pages[v]; p > depth; p = pages[v]) m = min(m, p), v = with[v];
+    *in_common = m;
+    return v;
+  };
+  int depth[kEach], pos[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) depth[i] = pos[i] = 0;
   for (int round = 0; round < kRounds; ++round) {
     __syncthreads();
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
-      if (share) return;
-      next[s] = pos[s] < whole[s] && mine[i].levels < kLevels ? c.table[int64_t(s) * c.max_pages + pos[s]] : -1;
-      lds.of.fewest[s] = INT_MAX, lds.of.branches[s] = 0, cut[s] = 0;
-    });
-    __syncthreads();
-    // the first sequence with the same x and the same y
-    auto first_like = [&](int s, const int* x, const int* y) __attribute__((always_inline)) {
-      const int u = x[s], v = y[s];
-      int t = s;
-      if (u >= 0)
-        for (int j = share; j * 4 < s; j += parts) {
-          const int4 p = fours(x, j), q = fours(y, j);
-          const int hit = p.x == u && q.x == v ? 0 : p.y == u && q.y == v ? 1 : p.z == u && q.z == v ? 2 : p.w == u && q.w == v ? 3 : 4;
-          if (hit < 4) {
-            t = min(4 * j + hit, s);
-            break;
-          }
-        }
-      return all_of(t, [](int x, int y) { return min(x, y); });
-    };
+    int in_common[kEach];
     bool groups = false;
     each_seq([&](int i, int s) __attribute__((always_inline)) {
-      const int t = first_like(s, next, pos);
-      if (share == 0) lead[s] = t;
-      groups |= t != s;
+      lead[s] = whole[s] && mine[i].levels < kLevels ? first_at(s, depth[i], &in_common[i]) : s;
+      groups |= lead[s] != s;
+      fewest[s] = INT_MAX, of_group[s] = branches[s] = 0;
     });
     if (!__syncthreads_or(groups)) break;
-    for (int s = wave; s < n; s += kTogether * kPlanWaves) common(c, n, s, kPlanWaves, lead, pos, whole, same, [](int) { return true; });
-    __syncthreads();
-    each_seq([&](int, int s) __attribute__((always_inline)) {
-      if (share == 0 && lead[s] != s) atomicMin(&lds.of.fewest[lead[s]], same[s]);
-    });
-    __syncthreads();
-    each_seq([&](int, int s) __attribute__((always_inline)) {  // the page behind what all have
-      if (share) return;
-      const int d = lds.of.fewest[lead[s]], p = pos[s] + d;
-      next[s] = d < INT_MAX && p < whole[s] ? c.table[int64_t(s) * c.max_pages + p] : -1;
-    });
-    __syncthreads();
-    int branch[kEach];
     each_seq([&](int i, int s) __attribute__((always_inline)) {
-      branch[i] = first_like(s, next, lead);
-      if (share == 0 && branch[i] == s) atomicAdd(&lds.of.branches[lead[s]], 1);
+      const int l = lead[s];
+      each_value(l != s, l, [&](int v, uint64_t lanes) {
+        const bool on = lanes >> lane & 1;
+        int least = on ? in_common[i] : INT_MAX;
+        const int tokens = __builtin_amdgcn_readlane(lanes_up_to(on ? count[s] : 0), kWave - 1);
+        for (int step = 1; step < kWave; step *= 2) least = min(least, __shfl_xor(least, step));
+        if (lane == __builtin_ctzll(lanes)) atomicAdd(&of_group[v], tokens), atomicMin(&fewest[v], least);
+      });
     });
     __syncthreads();
-    bool any = false, redo = false;
     each_seq([&](int i, int s) __attribute__((always_inline)) {
-      const int l = lead[s], d = lds.of.fewest[l];
+      const int l = lead[s], d = fewest[l];
+      int unused;
+      each_value(d < INT_MAX && first_at(s, d, &unused) == s, l, [&](int v, uint64_t lanes) {
+        if (lane == __builtin_ctzll(lanes)) atomicAdd(&branches[v], __popcll(lanes));
+      });
+    });
+    __syncthreads();
+    bool any = false;
+    int level_pages[kEach];
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      const int l = lead[s], d = fewest[l];
+      level_pages[i] = 0;
       if (d == INT_MAX) return;  // alone
-      int tokens = 0;
-      for (int j = share; j < n4; j += parts) {
-        const int4 x = fours(lead, j), k = fours(count, j);
-        tokens += (x.x == l ? k.x : 0) + (x.y == l ? k.y : 0) + (x.z == l ? k.z : 0) + (x.w == l ? k.w : 0);
+      if (pays(int64_t(d - pos[i]) << c.page_shift, branches[l] - 1, int64_t(of_group[l] + count[l]) * group, c.dtype)) {
+        level_pages[i] = d - pos[i];
+        any = true;
       }
-      tokens = all_of(tokens, plus);
-      const bool all = d > 0 && pays(int64_t(d) << c.page_shift, lds.of.branches[l] - 1, int64_t(tokens) * group, c.dtype);
-      if (all && share == 0 && s == l) cut[s] = d;
-      if (all) branch[i] = -1;  // in the node of the whole group
+      depth[i] = d;
+    });
+    if (!__syncthreads_or(any)) continue;
+    // the lists of a round: nodes in the order of their leaders, tokens in the
+    // order of their sequences: by one wavefront, 64 sequences a step
+    each_seq([&](int i, int s) __attribute__((always_inline)) {
+      of_group[s] = 0;
+      if (level_pages[i] == 0) lead[s] = -1;  // no node
     });
     __syncthreads();
-    // groups that have no node: their branches
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
-      const bool other = branch[i] >= 0 && lds.of.fewest[lead[s]] < INT_MAX && branch[i] != lead[s];
-      if (share == 0) next[s] = other;
-      redo |= other;
-      if (share == 0 && other) lead[s] = branch[i];
-    });
-    if (__syncthreads_or(redo)) {
-      for (int s = wave; s < n; s += kTogether * kPlanWaves)
-        common(c, n, s, kPlanWaves, lead, pos, whole, same, [&](int s) { return uniform(next[s]) != 0; });
-      __syncthreads();
+    if (wave == 0) {
+      for (int s0 = 0; s0 < n; s0 += kWave) {
+        const int s = min(s0 + lane, n - 1), l = lead[s], k = count[s];
+        each_value(s0 + lane < n && l >= 0, l, [&](int v, uint64_t lanes) {
+          const bool on = lanes >> lane & 1;
+          const int up = lanes_up_to(on ? k : 0), before = of_group[v];
+          if (on) fewest[s] = before + up - k;  // place among the node's tokens
+          if (lane == 0) of_group[v] = before + __builtin_amdgcn_readlane(up, kWave - 1);
+        });
+      }
+      int node = nodes_s, list = list_s;
+      for (int s0 = 0; s0 < n; s0 += kWave) {
+        const int s = min(s0 + lane, n - 1);
+        const bool on = s0 + lane < n && lead[s] == s;
+        const uint64_t leaders = __ballot(on);
+        const int tokens = on ? of_group[s] : 0, up = lanes_up_to(tokens);
+        if (on) branches[s] = node + __popcll(leaders & ((uint64_t(1) << lane) - 1)), place[s] = list + up - tokens;  // node, its list
+        node += __popcll(leaders), list += __builtin_amdgcn_readlane(up, kWave - 1);
+      }
+      if (lane == 0) nodes_s = node, list_s = list;
     }
-    each_seq([&](int, int s) __attribute__((always_inline)) {
-      if (share == 0) lds.best[s] = 0;
-    });
-    __syncthreads();
-    unsigned long long saved[kEach];
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
-      saved[i] = 0;
-      const int l = lead[s], d = same[s];
-      if (l == s || cut[l] > 0 || d == 0) return;
-      int m = 0, tokens = 0;  // of those that have d pages in common with the leader
-      for (int j = l / 4 + share; j < n4; j += parts) {
-        const int4 y = fours(lead, j), z = fours(same, j), k = fours(count, j);
-        auto one = [&](int y, int z, int k) {
-          const bool on = y == l && z >= d;
-          m += on, tokens += on ? k : 0;
-        };
-        one(y.x, z.x, k.x), one(y.y, z.y, k.y), one(y.z, z.z, k.z), one(y.w, z.w, k.w);
-      }
-      m = all_of(m, plus), tokens = all_of(tokens, plus) + count[l];
-      if (pays(int64_t(d) << c.page_shift, m, int64_t(tokens) * group, c.dtype)) saved[i] = static_cast<unsigned long long>(d) * m;
-      if (share == 0 && saved[i]) atomicMax(&lds.best[l], saved[i]);
-    });
     __syncthreads();
     each_seq([&](int i, int s) __attribute__((always_inline)) {
-      if (share == 0 && saved[i] && saved[i] == lds.best[lead[s]]) atomicMax(&cut[lead[s]], same[s]);
-    });
-    __syncthreads();
-    each_seq([&](int, int s) __attribute__((always_inline)) {
-      const int d = cut[lead[s]];
-      any |= d > 0;
-      if (share == 0) next[s] = d > 0 && (lead[s] == s || same[s] >= d) ? lead[s] : INT_MAX;
-    });
-    if (!__syncthreads_or(any)) break;
-    const int first_node = nodes_s, first_token = list_s;
-    __syncthreads();
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
-      const int l = next[s];
-      if (l == INT_MAX) return;
-      // the lists of a round: nodes in the order of their leaders, tokens in the
-      // order of their sequences
-      int node = 0, list = 0, at = 0, of_node = 0;
-      for (int j = share; j < n4; j += parts) {
-        const int4 x = fours(next, j), k = fours(count, j);
-        auto one = [&](int t, int y, int z) {
-          node += y == t && t < l;
-          list += y < l ? z : 0;
-          of_node += y == l ? z : 0;
-          at += y == l && t < s ? z : 0;
-        };
-        one(4 * j, x.x, k.x), one(4 * j + 1, x.y, k.y), one(4 * j + 2, x.z, k.z), one(4 * j + 3, x.w, k.w);
-      }
-      node = first_node + all_of(node, plus), list = first_token + all_of(list, plus);
-      of_node = all_of(of_node, plus), at = all_of(at, plus);
+      const int l = lead[s];
+      if (l < 0) return;
+      const int node = branches[l], list = place[l], at = fewest[s];
       PlanSeq& p = mine[i];
-      for (int u = share; u < count[s]; u += parts) plan.tokens()[list + at + u] = p.begin + u;
+      for (int u = 0; u < count[s]; ++u) plan.tokens()[list + at + u] = p.begin + u;
 #pragma unroll
       for (int v = 0; v < kLevels; ++v)
         if (p.levels == v) p.node[v] = node, p.at[v] = at;
       ++p.levels;
-      if (s == l && share == 0) {
+      if (s == l) {
         Node x{};
-        x.seq = s, x.key0 = pos[s] << c.page_shift, x.keys = cut[s] << c.page_shift;
-        x.tokens = of_node, x.list = list;
+        x.seq = s, x.key0 = pos[i] << c.page_shift, x.keys = level_pages[i] << c.page_shift;
+        x.tokens = of_group[s], x.list = list;
         plan.nodes()[node] = x;
-        atomicAdd(&nodes_s, 1), atomicAdd(&list_s, of_node);
       }
-    });
-    __syncthreads();
-    each_seq([&](int, int s) __attribute__((always_inline)) {
-      if (share == 0 && next[s] != INT_MAX) pos[s] += cut[next[s]];
+      pos[i] += level_pages[i];
     });
   }
   __syncthreads();
@@ -405,17 +385,18 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     if (i * kPlan >= n) continue;
-    const int s = first + i * kPlan;
-    const bool on = share == 0 && s < n && count[s] > 0;
-    int total;
-    const int node = nodes + threads_before(int(on), sums32, &total);
-    nodes += total;
+    const int s = tid + i * kPlan;
+    const bool on = s < n && mine[i].levels >= 0;
+    int before[1] = {int(on)}, total[1];
+    threads_before(before, sums32, total);
+    const int node = nodes + before[0];
+    nodes += total[0];
     __syncthreads();
-    if (s >= n || share) continue;
+    if (s >= n) continue;
     PlanSeq& p = mine[i];
     if (on) {
       Node x{};
-      x.seq = s, x.key0 = pos[s] << c.page_shift;
+      x.seq = s, x.key0 = pos[i] << c.page_shift;
       x.len = p.len - x.key0, x.n = p.n, x.keys = x.len + x.n, x.begin = p.begin;
       x.tokens = p.n, x.list = -1;
       plan.nodes()[node] = x;
@@ -437,22 +418,23 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     const int of = rows <= kSmall ? kSmall : M;
     return Size{of, static_cast<int>((rows + of - 1) / of), (x.keys + kTile - 1) / kTile};
   };
-  int64_t work = 0, total;
+  int64_t work[1] = {0}, total[1];
   for (int i = from; i < to; ++i) {
     const Size z = size(plan.nodes()[i]);
-    work += int64_t(z.row_tiles) * z.key_tiles;
+    work[0] += int64_t(z.row_tiles) * z.key_tiles;
   }
-  threads_before(work, sums[0], &total);
-  const int64_t tiles = max(int64_t(kLeastTiles), (total * c.kv_heads + kSlots - 1) / kSlots);
+  threads_before(work, sums, total);
+  const int64_t tiles = max(int64_t(kLeastTiles), (total[0] * c.kv_heads + kSlots - 1) / kSlots);
   auto chunks = [&](const Size& z) { return static_cast<int>((z.key_tiles + tiles - 1) / tiles); };
-  int64_t units = 0, rows = 0, all_units, all_rows;
+  int64_t x_of[2] = {0, 0}, all[2];
+  int64_t &units = x_of[0], &rows = x_of[1];  // units and part rows
   for (int i = from; i < to; ++i) {
     const Node& x = plan.nodes()[i];
     const Size z = size(x);
     units += int64_t(z.row_tiles) * chunks(z), rows += int64_t(x.tokens) * a.q_heads * chunks(z);
   }
-  units = threads_before(units, sums[1], &all_units), rows = threads_before(rows, sums[2], &all_rows);
-  const bool fits = all_units <= plan.y.most_units && all_rows <= plan.y.most_rows;
+  threads_before(x_of, sums + 1, all);
+  const bool fits = all[0] <= plan.y.most_units && all[1] <= plan.y.most_rows;
   for (int i = from; fits && i < to; ++i) {
     Node& x = plan.nodes()[i];
     const Size z = size(x);
@@ -463,17 +445,17 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
     } else {  // many: by all threads
       const int at = atomicAdd(&big_s, 1);
-      if (at < kSeqs) next[at] = i, lead[at] = static_cast<int>(units), pos[at] = count_here;
+      if (at < kMost) place[at] = i, lead[at] = static_cast<int>(units), with[at] = count_here;
       else
         for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
     }
     units += z.row_tiles * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
   }
   __syncthreads();
-  const int big = min(big_s, kSeqs);
+  const int big = min(big_s, kMost);
   for (int b = wave; b < big; b += kPlanWaves)
-    for (int u = lane; u < pos[b]; u += kWave) plan.units()[lead[b] + u] = next[b];
-  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all_units) : 0, nodes, M, {}};
+    for (int u = lane; u < with[b]; u += kWave) plan.units()[lead[b] + u] = place[b];
+  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all[0]) : 0, nodes, M, {}};
 }
 
 // Whether the plan is one for this call.
@@ -639,7 +621,13 @@ int64_t kv_share_bytes(const KvCache& c, int32_t T, int32_t q_heads) {
 
 hipError_t launch_kv_share(const KvCache& c, const KvShared& sh, hipStream_t s) {
   const int x = shape(c, sh.a.T, sh.a.q_heads);
-  plan_kernel<<<1, kPlan, 0, s>>>(c, sh.a, plan_of(c, sh, x), rows_of(x));
+  const Plan plan = plan_of(c, sh, x);
+  if (c.seqs > kMeetHere) {
+    meet_kernel<<<c.seqs, kWave, 0, s>>>(c, sh.a, plan);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  if (c.seqs <= kPlan) plan_kernel<1><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x));
+  else plan_kernel<kSeqs / kPlan><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x));
   return hipGetLastError();
 }
 
