@@ -79,8 +79,8 @@ __global__ __launch_bounds__(kBlock) void chosen_kernel(KvCache c, KvChosen ch, 
     if (e < from_list) return listed[e];
     return max(0, min(table[whole + e - from_list], c.pages - 1));
   };
-  auto query = [&](int r) { return int64_t(t) * a.ldq + int64_t(h * group + row0 + min(r, rows - 1)) * D; };
-  auto emit = [&](int r, int column, f32x4 x, float top, float l) {
+  auto query = [&](int, int r) { return int64_t(t) * a.ldq + int64_t(h * group + row0 + min(r, rows - 1)) * D; };
+  auto emit = [&](int, int r, int column, f32x4 x, float top, float l) {
     if (r >= rows) return;
     if (bad) x = f32x4{NAN, NAN, NAN, NAN}, l = 1.f;
     const int64_t row = first_row + r;

@@ -20,14 +20,16 @@ struct FewTile {
   int limit;       // keys that any row sees: none is read from there on
 };
 
-// Four wavefronts: each holds all rows and takes every 4th key tile, K straight
+// Four wavefronts for Heads key heads from t.h on: each holds all rows of one head
+// and takes every Step-th key tile, K straight
 // into registers, V through its own part of LDS, the next tile's loads in
 // flight during the softmax and the second product; no barrier among them until
 // their parts are joined.  Softmax statistics and outputs are fp32; bf16
 // weights go into the second product as two bf16 parts (16 bits).
-template <int DT, int D, int MT>
+template <int DT, int D, int MT, int Heads = 1>
 struct FewRows {
   using T = Tile<DT, D>;
+  static constexpr int Step = kWaves / Heads;  // wavefronts of a head
   static constexpr int M = 16 * MT, KW = T::Keys, DB = D / 16, L = T::Loads;
   static constexpr int kVWords = KW * T::Chunks;  // 16-byte words of a V tile
   static constexpr int kLds = kWaves * kVWords > kWaves * M * D / 4 ? kWaves * kVWords : kWaves * M * D / 4;
@@ -36,31 +38,31 @@ struct FewRows {
     float stat[kWaves][2][M];
     uint32_t seen[M * kTreeWords];
     int32_t par[kTree];
-    uint32_t nonfinite[kMixedWords];
+    uint32_t nonfinite[Heads][kMixedWords];
   };
 
   // page_at(key): its page, clamped to the pool.  query(r): element of q of row r, in bounds for every r < M;
-  // token(r): its token, -1 where there is none.  emit(r, column, x, top, l): 4
+  // token(r): its token, -1 where there is none.  emit(h, r, column, x, top, l): 4
   // values of a row, not yet divided by the sum l of its weights relative to 2^top.
   template <class PageAt, class Query, class Token, class Emit>
   static __device__ inline void run(const KvCache& c, const KvAttention& a, Lds& lds, const FewTile& t, PageAt page_at,
                                     Query query, Token token, Emit emit) {
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-    const int col = lane % 16, g = lane / 16;
+    const int col = lane % 16, g = lane / 16, part = wave % Step, head = wave / Step, h = t.h + head;
     // a scale of 0 clears q instead: a masked score stays -inf
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
     const uint32_t flip = a.scale < 0.f ? (DT == 0 ? 0x80000000u : 0x80008000u) : 0u, on = a.scale == 0.f ? 0u : ~0u;
     const Seq& q = t.q;
     const int limit = t.limit, end = min(t.kt1, (limit + KW - 1) / KW);
     const int64_t head_stride = int64_t(c.page_tokens) * T::Chunks;  // 16-byte words
-    const u32x4* kv = static_cast<const u32x4*>(c.kv) + (int64_t(a.layer) * c.pages * 2 * c.kv_heads + t.h) * head_stride;
+    const u32x4* kv = static_cast<const u32x4*>(c.kv) + (int64_t(a.layer) * c.pages * 2 * c.kv_heads + h) * head_stride;
     const int64_t v_off = c.kv_heads * head_stride, page_stride = 2 * v_off;
     // keys past the last one to be used are read from that one: in bounds, and masked
     auto page_of = [&](int kt, int i) { return page_at(min(kt * KW + i * 16 + col, limit - 1)); };
     u32x4* vt = lds.tiles + wave * kVWords;
-    const Mixed mixed = mixed_rows(a, q, t.tok0, t.tok1, lds.nonfinite);
+    const Mixed mixed = mixed_rows(a, q, t.tok0, t.tok1, lds.nonfinite[head]);
     for (int again = 0;; ++again) {  // a second pass where a value is not finite
-      int kt = t.kt0 + wave;
+      int kt = t.kt0 + part;
       int32_t pg[T::Sub];
       if (kt < end)
 #pragma unroll
@@ -71,7 +73,7 @@ struct FewRows {
       int tok[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + query(m * 16 + col) * (DT == 0 ? 4 : 2));
+        const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + query(h, m * 16 + col) * (DT == 0 ? 4 : 2));
         tok[m] = token(m * 16 + col);
 #pragma unroll
         for (int i = 0; i < L; ++i) qr[m][i] = p[i * 4 + g];
@@ -91,11 +93,15 @@ struct FewRows {
       if (kt < end) {
         load(kt);
 #pragma unroll
-        for (int i = 0; i < T::Sub; ++i) pg[i] = page_of(min(kt + kWaves, end - 1), i);
+        for (int i = 0; i < T::Sub; ++i) pg[i] = page_of(min(kt + Step, end - 1), i);
       }
       if (a.parent && end * KW > q.len) walk_tree<kBlock>(a, q, t.tok0, t.tok1, lds.par, lds.seen, kTreeWords);
       bool odd = false;
-      if (again) odd = find_nonfinite<kBlock, DT, D>(c, page_at, kv + v_off, page_stride, mixed);
+      if (again)
+        for (int i = 0; i < Heads; ++i) {
+          const Mixed m = mixed_rows(a, q, t.tok0, t.tok1, lds.nonfinite[i]);
+          odd |= find_nonfinite<kBlock, DT, D>(c, page_at, kv + v_off + (i - head) * head_stride, page_stride, m);
+        }
       f32x4 o[MT][DB];
       float mx[MT], sum[MT];
 #pragma unroll
@@ -106,7 +112,7 @@ struct FewRows {
 #pragma unroll
         for (int i = 0; i < L; ++i) qr[m][i] = (qr[m][i] ^ flip) & on;
       }
-      for (; kt < end; kt += kWaves) {
+      for (; kt < end; kt += Step) {
         // V to LDS, S^T from the registers
 #pragma unroll
         for (int i = 0; i < T::Sub; ++i)
@@ -131,10 +137,10 @@ struct FewRows {
             }
             sc[m][i] = x;
           }
-        if (kt + kWaves < end) {
-          load(kt + kWaves);
+        if (kt + Step < end) {
+          load(kt + Step);
 #pragma unroll
-          for (int i = 0; i < T::Sub; ++i) pg[i] = page_of(min(kt + 2 * kWaves, end - 1), i);
+          for (int i = 0; i < T::Sub; ++i) pg[i] = page_of(min(kt + 2 * Step, end - 1), i);
         }
         if ((kt + 1) * KW > q.len) {  // new rows among the keys, or none behind them: who sees them
           const int first = kt * KW, at = first & 31;  // key and bit of the tile's first key
@@ -217,8 +223,8 @@ struct FewRows {
         for (int m = 0; m < MT; ++m) z = zero_or_nan(o[m], z);
       // every wavefront is done with its tiles
       if (__syncthreads_or(z != z)) continue;
-      // the four wavefronts' parts joined; wavefront w ends with a quarter of
-      // the columns
+      // a head's wavefronts' parts joined; each ends with as many of the
+      // columns
       f32x4* buf = reinterpret_cast<f32x4*>(lds.tiles);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -228,7 +234,7 @@ struct FewRows {
         for (int d = 0; d < DB; ++d) buf[((wave * MT + m) * DB + d) * kWave + lane] = o[m][d];
       }
       if (odd)  // every wavefront for the tiles that it had
-        for (kt = t.kt0 + wave; kt < end; kt += kWaves)
+        for (kt = t.kt0 + part; kt < end; kt += Step)
           for (uint32_t word = mixed.word(kt * KW & ~31) >> (kt * KW & 31) & T::Mask; word; word &= word - 1) {
             const int row = kt * KW + __builtin_ctz(word);
             if (row >= limit) break;
@@ -241,26 +247,27 @@ struct FewRows {
                   buf[((wave * MT + m) * DB + d) * kWave + lane] += odd_values<DT>(p, 16 * d + 4 * g);
           }
       __syncthreads();
-      constexpr int Q = DB / kWaves;
+      constexpr int Q = DB / Step;
+      const int first = head * Step;  // wavefront of the head
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int r = m * 16 + col;
-        float top = -INFINITY, weight[kWaves], l = 0.f;
+        float top = -INFINITY, weight[Step], l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds.stat[w][0][r]);
+        for (int w = 0; w < Step; ++w) top = fmaxf(top, lds.stat[first + w][0][r]);
         const float at = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          weight[w] = part_weight(lds.stat[w][0][r] - at);
-          l += weight[w] * lds.stat[w][1][r];
+        for (int w = 0; w < Step; ++w) {
+          weight[w] = part_weight(lds.stat[first + w][0][r] - at);
+          l += weight[w] * lds.stat[first + w][1][r];
         }
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-          const int d = wave * Q + i;
+          const int d = part * Q + i;
           f32x4 x{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) x += buf[((w * MT + m) * DB + d) * kWave + lane] * weight[w];
-          emit(r, 16 * d + 4 * g, x, top, l);
+          for (int w = 0; w < Step; ++w) x += buf[(((first + w) * MT + m) * DB + d) * kWave + lane] * weight[w];
+          emit(h, r, 16 * d + 4 * g, x, top, l);
         }
       }
       return;

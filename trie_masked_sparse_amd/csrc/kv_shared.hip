@@ -21,7 +21,7 @@ namespace {
 constexpr int kLevels = 3;      // nodes of a sequence beside its own
 constexpr int kSeqs = 4096;     // sequences of a cache, at most
 constexpr int kPlan = 1024, kPlanWaves = kPlan / kWave;
-constexpr int kSlots = 512;     // workgroups that a launch should have
+constexpr int kSlots = 512;     // workgroups that the chip holds at once
 constexpr int kTile = 64;       // keys that the plan counts in
 constexpr int kSmall = 16;      // rows of a small node
 constexpr int kMagic = 0x73686172;
@@ -38,10 +38,16 @@ __device__ inline bool pays(int64_t keys, int64_t readers, int64_t rows, int dty
   return keys * readers >= kLeastSaved + (dtype == 0 ? 2 : 4) * rows;
 }
 
-constexpr int kRounds = 16;  // branchings of the trie that are looked at, one behind the other
-
 // Key tiles of a chunk, at least.
 constexpr int kLeastTiles = 4;
+
+// Costs in units of 0.35 us, as measured with two workgroups on a compute unit:
+// the start of a unit and its end (queries, page numbers, first keys; joining
+// wavefronts, parts), and 64 keys of it.
+constexpr int kOpenSmall = 20, kOpenLarge = 18, kTileSmall = 4, kTileLarge = 5;
+
+constexpr int kRounds = 16;  // branchings of the trie that are looked at, one behind the other
+
 
 struct Head {
   int32_t magic, T, q_heads, units, nodes, rows, pad[2];
@@ -64,15 +70,23 @@ struct Node {
   int32_t seq, key0, keys;   // the sequence whose table has the pages; first row, rows
   int32_t tokens, list;      // query tokens; their place in the list, -1: begin ..
   int32_t begin, n, len;     // of one sequence's own: its new tokens, committed rows from key0 on
-  int32_t unit, chunks, tiles, rows;  // first unit, chunks of `tiles` key tiles, rows of a row tile
+  int32_t chunks, tiles, rows, pad;  // chunks of `tiles` key tiles, rows of a row tile
   int64_t part;              // first row of its parts
+};
+
+// What a workgroup works on: a row tile and a chunk of the keys of a node, and a
+// key head, or several of a small one.  All that it has to know, in one read.
+struct Unit {
+  int32_t seq, key0, keys, list, begin, n, len, all;  // of its node; all: rows
+  int32_t row0, rows, h, tile0, tile1, M;             // M: rows of its node's row tiles
+  int64_t part;
 };
 
 // Places in the plan.  M: rows of a tile of nodes that are not small.
 struct Layout {
   int64_t seqs, meets, nodes, units, tokens, owner, stats, values, bytes;
-  int32_t most_nodes, most_units;
-  int64_t most_rows;
+  int32_t most_nodes;
+  int64_t most_units, most_rows;
 };
 
 int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -81,15 +95,17 @@ Layout layout(const KvCache& c, int32_t T, int32_t q_heads, int M) {
   Layout y{};
   const int64_t group = q_heads / c.kv_heads, n = std::min<int64_t>(c.seqs, T);
   y.most_nodes = static_cast<int32_t>(n + kLevels * (n / 2));
-  // a node's row tiles, each cut at most as often as fills the chip
+  // A node's row tiles and heads, and what cuts add: a chunk costs a slot, less
+  // one of its tiles, of which it has kLeastTiles or more.
+  constexpr int kCuts = kSlots * (kLeastTiles + 1) / kLeastTiles;
   const int64_t tiles = (kLevels + 1) * (int64_t(T) * group / std::max(M, kSmall)) + y.most_nodes;
-  y.most_units = static_cast<int32_t>(tiles + kSlots / c.kv_heads + 1);
-  y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + (kSlots + c.kv_heads) * int64_t(M);
+  y.most_units = tiles * c.kv_heads + kCuts;
+  y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + kCuts * int64_t(M);
   y.seqs = up(sizeof(Head));
   y.meets = up(y.seqs + c.seqs * int64_t(sizeof(PlanSeq)));
   y.nodes = up(y.meets + c.seqs * int64_t(sizeof(Meet)));
   y.units = up(y.nodes + y.most_nodes * int64_t(sizeof(Node)));
-  y.tokens = up(y.units + y.most_units * int64_t(4));
+  y.tokens = up(y.units + y.most_units * int64_t(sizeof(Unit)));
   y.owner = up(y.tokens + kLevels * int64_t(T) * 4);
   y.stats = up(y.owner + int64_t(T) * 4);
   y.values = up(y.stats + y.most_rows * 8);
@@ -104,7 +120,7 @@ struct Plan {
   __device__ PlanSeq* seqs() const { return reinterpret_cast<PlanSeq*>(at + y.seqs); }
   __device__ Meet* meets() const { return reinterpret_cast<Meet*>(at + y.meets); }
   __device__ Node* nodes() const { return reinterpret_cast<Node*>(at + y.nodes); }
-  __device__ int32_t* units() const { return reinterpret_cast<int32_t*>(at + y.units); }    // node of every unit
+  __device__ Unit* units() const { return reinterpret_cast<Unit*>(at + y.units); }
   __device__ int32_t* tokens() const { return reinterpret_cast<int32_t*>(at + y.tokens); }  // of the nodes, a list for each level
   __device__ int32_t* owner() const { return reinterpret_cast<int32_t*>(at + y.owner); }    // sequence of every token, -1
   __host__ __device__ Parts parts() const {
@@ -221,6 +237,28 @@ __device__ inline void each_value(bool on, int value, F f) {
   }
 }
 
+// First part row of row tile rt, chunk k of a node and key head: a chunk's parts
+// are the tile's rows for head 0, then for head 1, ...
+__device__ inline int64_t part_row(const KvCache& c, const Node& x, int group, int rt, int k, int h) {
+  const int64_t all = int64_t(x.tokens) * group, first = int64_t(rt) * x.rows, rows = min(int64_t(x.rows), all - first);
+  return x.part + c.kv_heads * (first * x.chunks + k * rows) + h * rows;
+}
+
+// The units i, i + step, ... of a node whose first is `first`: heads next to each
+// other, then the chunks of a row tile.
+__device__ inline void write_units(const KvCache& c, const Plan& plan, const Node& x, int group, int row_tiles, int heads,
+                                   int64_t first, int i, int step) {
+  for (; i < row_tiles * x.chunks * heads; i += step) {
+    const int h = i % heads * (c.kv_heads / heads), k = i / heads % x.chunks, rt = i / heads / x.chunks;
+    Unit u{};
+    u.seq = x.seq, u.key0 = x.key0, u.keys = x.keys, u.list = x.list, u.begin = x.begin, u.n = x.n, u.len = x.len;
+    u.all = x.tokens * group, u.row0 = rt * x.rows, u.rows = min(x.rows, u.all - u.row0), u.h = h, u.M = x.rows;
+    u.tile0 = k * x.tiles, u.tile1 = u.tile0 + x.tiles;
+    u.part = part_row(c, x, group, rt, k, h);
+    plan.units()[first + i] = u;
+  }
+}
+
 // One workgroup.  In every round a group are the sequences that go through one
 // place of the trie; its first is the leader.  The pages that the whole group
 // has in common, from where its sequences read, make a node, if that pays:
@@ -232,14 +270,14 @@ __device__ inline void each_value(bool on, int value, F f) {
 // caches, is four times as much: 64 sequences 34 us instead of 27).
 constexpr int kMeetHere = 16;  // sequences whose meets are found here: a launch less
 template <int kEach>
-__global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M) {
+__global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M, int heads) {
   constexpr int kMost = kEach * kPlan;  // sequences
   // of every sequence: the first of its group; tokens (0: none to share); its Meet.
   // Of a leader: the fewest pages that one of its group has in common with it, the
   // others' tokens, branches; its node's number and list
   __shared__ int lead[kMost], with[kMost], pages[kMost], fewest[kMost], of_group[kMost], branches[kMost], place[kMost], whole[kMost];
   __shared__ uint16_t count[kMost];
-  __shared__ int nodes_s, list_s, big_s;
+  __shared__ int nodes_s, list_s;
   __shared__ int64_t sums[3][kPlanWaves];
   __shared__ int sums32[1][kPlanWaves];
   const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = c.seqs, group = a.q_heads / c.kv_heads;
@@ -249,7 +287,7 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       if (tid + i * kPlan < n) f(i, tid + i * kPlan);
   };
   a.max_new = INT_MAX;
-  if (tid == 0) nodes_s = list_s = big_s = 0;
+  if (tid == 0) nodes_s = list_s = 0;
   for (int i = tid; i < a.T; i += kPlan) plan.owner()[i] = -1;
   PlanSeq mine[kEach];
   int64_t tokens[1] = {0}, all_tokens[1];
@@ -408,67 +446,64 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     plan.seqs()[s] = p;
   }
   __syncthreads();
-  // chunks of the keys, equal for all, so that there is a workgroup for each slot
+  // Chunks of the keys: of a unit's cost as much as a slot has, or less.
   const int each = (nodes + kPlan - 1) / kPlan, from = min(tid * each, nodes), to = min(from + each, nodes);
   struct Size {
-    int rows, row_tiles, key_tiles;
+    int rows, row_tiles, key_tiles, heads;  // heads: units of a row tile and chunk
+    bool small;
+    int open, tile;  // cost of a unit and of one of its key tiles
   };
   auto size = [&](const Node& x) {
     const int64_t rows = int64_t(x.tokens) * group;
-    const int of = rows <= kSmall ? kSmall : M;
-    return Size{of, static_cast<int>((rows + of - 1) / of), (x.keys + kTile - 1) / kTile};
+    const bool small = rows <= kSmall;
+    const int of = small ? kSmall : M;
+    return Size{of, static_cast<int>((rows + of - 1) / of), (x.keys + kTile - 1) / kTile, small ? c.kv_heads / heads : c.kv_heads,
+                small, small ? kOpenSmall : kOpenLarge, small ? kTileSmall * heads : kTileLarge};
   };
   int64_t work[1] = {0}, total[1];
   for (int i = from; i < to; ++i) {
     const Size z = size(plan.nodes()[i]);
-    work[0] += int64_t(z.row_tiles) * z.key_tiles;
+    work[0] += (int64_t(z.key_tiles) * z.tile + z.open) * z.row_tiles * z.heads;
   }
   threads_before(work, sums, total);
-  const int64_t tiles = max(int64_t(kLeastTiles), (total[0] * c.kv_heads + kSlots - 1) / kSlots);
-  auto chunks = [&](const Size& z) { return static_cast<int>((z.key_tiles + tiles - 1) / tiles); };
+  const int64_t slot = total[0] / kSlots + 1;
+  auto chunks = [&](const Size& z) {
+    const int64_t most = max(slot / z.tile, int64_t(kLeastTiles));  // key tiles
+    return static_cast<int>((z.key_tiles + most - 1) / most);
+  };
   int64_t x_of[2] = {0, 0}, all[2];
   int64_t &units = x_of[0], &rows = x_of[1];  // units and part rows
   for (int i = from; i < to; ++i) {
     const Node& x = plan.nodes()[i];
     const Size z = size(x);
-    units += int64_t(z.row_tiles) * chunks(z), rows += int64_t(x.tokens) * a.q_heads * chunks(z);
+    units += int64_t(z.row_tiles) * chunks(z) * z.heads, rows += int64_t(x.tokens) * a.q_heads * chunks(z);
   }
   threads_before(x_of, sums + 1, all);
   const bool fits = all[0] <= plan.y.most_units && all[1] <= plan.y.most_rows;
+  // (places of nodes with many units in LDS, for all threads to write them)
   for (int i = from; fits && i < to; ++i) {
     Node& x = plan.nodes()[i];
     const Size z = size(x);
-    x.chunks = chunks(z), x.tiles = static_cast<int>(min(tiles, int64_t(z.key_tiles))), x.rows = z.rows;
-    x.unit = static_cast<int>(units), x.part = rows;
-    const int count_here = z.row_tiles * x.chunks;
-    if (count_here <= 2) {
-      for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
-    } else {  // many: by all threads
-      const int at = atomicAdd(&big_s, 1);
-      if (at < kMost) place[at] = i, lead[at] = static_cast<int>(units), with[at] = count_here;
-      else
-        for (int u = 0; u < count_here; ++u) plan.units()[units + u] = i;
-    }
-    units += z.row_tiles * x.chunks, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
+    x.chunks = chunks(z), x.rows = z.rows, x.part = rows;
+    x.tiles = (z.key_tiles + x.chunks - 1) / x.chunks;
+    if (i < kMost) place[i] = static_cast<int>(units);
+    else write_units(c, plan, x, group, z.row_tiles, z.heads, units, 0, 1);
+    units += int64_t(z.row_tiles) * x.chunks * z.heads, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
   }
   __syncthreads();
-  const int big = min(big_s, kMost);
-  for (int b = wave; b < big; b += kPlanWaves)
-    for (int u = lane; u < with[b]; u += kWave) plan.units()[lead[b] + u] = place[b];
-  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all[0]) : 0, nodes, M, {}};
+  if (fits)
+    for (int i = wave; i < min(nodes, kMost); i += kPlanWaves) {
+      const Node x = plan.nodes()[i];
+      const Size z = size(x);
+      write_units(c, plan, x, group, z.row_tiles, z.heads, place[i], lane, kWave);
+    }
+  if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all[0]) : 0, nodes, M, {heads, 0}};
 }
 
 // Whether the plan is one for this call.
 __device__ inline bool planned(const Plan& plan, const KvAttention& a, int M) {
   const Head* h = plan.head();
   return h->magic == kMagic && h->T == a.T && h->q_heads == a.q_heads && h->rows == M;
-}
-
-// First part row of row tile rt, chunk k of a node and key head: a chunk's parts
-// are the tile's rows for head 0, then for head 1, ...
-__device__ inline int64_t part_row(const KvCache& c, const Node& x, int group, int rt, int k, int h) {
-  const int64_t all = int64_t(x.tokens) * group, first = int64_t(rt) * x.rows, rows = min(int64_t(x.rows), all - first);
-  return x.part + c.kv_heads * (first * x.chunks + k * rows) + h * rows;
 }
 
 // What a node that is not small is worked on by.
@@ -488,31 +523,29 @@ struct Body<1, D, kMany128> {
   using Type = ManyRows<D, 4, 1>;
 };
 
-// A unit of the plan (row tile and chunk of a node) and a key head.
-template <int DT, int D, int Shape>
-__global__ __launch_bounds__(kBlock, D == 256 ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
-  using Small = FewRows<DT, D, 1>;
+// A unit of the plan.
+template <int DT, int D, int Shape, int Heads>
+__global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
+  using Small = FewRows<DT, D, 1, Heads>;
   using Large = typename Body<DT, D, Shape>::Type;
   __shared__ union {
     typename Small::Lds small;
     typename Large::Lds large;
   } lds;
-  const int h = blockIdx.x % c.kv_heads, unit = blockIdx.x / c.kv_heads;
-  if (!planned(plan, a, rows_of(Shape)) || unit >= plan.head()->units) return;
-  const Node& at = plan.nodes()[plan.units()[unit]];
-  Node x;
-  x.seq = uniform(at.seq), x.key0 = uniform(at.key0), x.keys = uniform(at.keys), x.tokens = uniform(at.tokens);
-  x.list = uniform(at.list), x.begin = uniform(at.begin), x.n = uniform(at.n), x.len = uniform(at.len);
-  x.unit = uniform(at.unit), x.chunks = uniform(at.chunks), x.tiles = uniform(at.tiles), x.rows = uniform(at.rows);
-  x.part = uniform(at.part);
-  const int group = a.q_heads / c.kv_heads, all = x.tokens * group;
-  const int rt = (unit - x.unit) / x.chunks, k = (unit - x.unit) % x.chunks, row0 = rt * x.rows, rows = min(x.rows, all - row0);
+  const Unit& at = plan.units()[blockIdx.x];
+  if (!planned(plan, a, rows_of(Shape)) || int(blockIdx.x) >= plan.head()->units) return;
+  Unit x;
+  x.seq = uniform(at.seq), x.key0 = uniform(at.key0), x.keys = uniform(at.keys), x.list = uniform(at.list);
+  x.begin = uniform(at.begin), x.n = uniform(at.n), x.len = uniform(at.len), x.all = uniform(at.all);
+  x.row0 = uniform(at.row0), x.rows = uniform(at.rows), x.h = uniform(at.h), x.M = uniform(at.M);
+  x.tile0 = uniform(at.tile0), x.tile1 = uniform(at.tile1), x.part = uniform(at.part);
+  const int group = a.q_heads / c.kv_heads, row0 = x.row0, rows = x.rows;
   const int32_t* table = c.table + int64_t(x.seq) * c.max_pages + (x.key0 >> c.page_shift);
   const int32_t* list = plan.tokens() + max(x.list, 0);
   const bool own = x.list < 0;  // keys of one sequence, its new rows among them
   if (own && x.n > a.max_new) return;
   FewTile t{};
-  t.h = h;
+  t.h = x.h;
   if (own) {
     t.q.begin = x.begin, t.q.n = x.n, t.q.len = x.len;
     t.tok0 = row0 / group, t.tok1 = (row0 + rows - 1) / group;
@@ -522,25 +555,25 @@ __global__ __launch_bounds__(kBlock, D == 256 ? 1 : 2) void nodes_kernel(KvCache
     t.q.len = t.limit = x.keys;
     t.tok0 = t.tok1 = -1;
   }
-  auto query = [&](int r) {
+  auto query = [&](int h, int r) {
     const int row = row0 + min(r, rows - 1), i = row / group;
     const int token = own ? x.begin + i : list[i];
     return int64_t(token) * a.ldq + int64_t(h * group + row % group) * D;
   };
   auto token = [&](int r) { return own && r < rows ? (row0 + r) / group : -1; };
   const Parts parts = plan.parts();
-  const int64_t part = part_row(c, x, group, rt, k, h);
-  auto emit = [&](int r, int column, f32x4 v, float top, float l) {
+  auto emit = [&](int h, int r, int column, f32x4 v, float top, float l) {
     if (r >= rows) return;
-    *reinterpret_cast<f32x4*>(parts.values + (part + r) * D + column) = v;
-    if (column == 0) parts.stats[part + r] = float2{top, l};
+    const int64_t part = x.part + (h - x.h) * rows + r;
+    *reinterpret_cast<f32x4*>(parts.values + part * D + column) = v;
+    if (column == 0) parts.stats[part] = float2{top, l};
   };
   auto tiles = [&](int keys) {  // key tiles of this many keys
-    t.kt0 = k * x.tiles * (kTile / keys);
-    t.kt1 = min(t.kt0 + x.tiles * (kTile / keys), (x.keys + keys - 1) / keys);
+    t.kt0 = x.tile0 * (kTile / keys);
+    t.kt1 = min(x.tile1 * (kTile / keys), (x.keys + keys - 1) / keys);
   };
   auto page_at = [&](int key) { return max(0, min(table[key >> c.page_shift], c.pages - 1)); };
-  if (Shape == kFew16 || x.rows == kSmall) {
+  if (Shape == kFew16 || x.M == kSmall) {
     tiles(Small::KW);
     Small::run(c, a, lds.small, t, page_at, query, token, emit);
   } else if constexpr (Shape == kFew32) {
@@ -548,7 +581,8 @@ __global__ __launch_bounds__(kBlock, D == 256 ? 1 : 2) void nodes_kernel(KvCache
     Large::run(c, a, lds.large, t, page_at, query, token, emit);
   } else if constexpr (Shape >= kMany64) {
     tiles(Large::KT);
-    Large::run(c, a, lds.large, t, table, query, token, emit);
+    Large::run(c, a, lds.large, t, table, [&](int r) { return query(x.h, r); }, token,
+               [&](int r, int column, f32x4 v, float top, float l) { emit(x.h, r, column, v, top, l); });
   }
 }
 
@@ -584,15 +618,24 @@ int shape(const KvCache& c, int32_t T, int32_t q_heads) {
   const int64_t rows = int64_t(T) * (q_heads / c.kv_heads);  // of a node, at most
   if (rows <= 16) return kFew16;
   if (c.dtype == TMS_F32) return c.head_dim < 256 ? kFew32 : kFew16;
-  return rows <= 32 && c.head_dim < 256 ? kFew32 : rows <= 64 ? kMany64 : kMany128;
+  return rows <= 32 && c.head_dim == 64 ? kFew32 : rows <= 64 ? kMany64 : kMany128;
+}
+
+// Key heads of a unit of a small node: as many as leave a unit for each slot.
+int small_heads(const KvCache& c, int32_t T) {
+  const int64_t nodes = int64_t(std::min(c.seqs, T)) * c.kv_heads;
+  return c.kv_heads % 4 == 0 && nodes >= 4 * kSlots ? 4 : c.kv_heads % 2 == 0 && nodes >= kSlots ? 2 : 1;
 }
 
 template <int DT, int D, int Shape>
 hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, hipStream_t s) {
-  const int64_t blocks = int64_t(plan.y.most_units) * c.kv_heads, rows = int64_t(a.T) * a.q_heads;
+  const int64_t blocks = plan.y.most_units, rows = int64_t(a.T) * a.q_heads;
   constexpr int kRows = kBlock * 4 / D;
   if (blocks >= (int64_t(1) << 32) / kBlock || rows >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  nodes_kernel<DT, D, Shape><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  const int heads = small_heads(c, a.T);
+  if (heads == 4) nodes_kernel<DT, D, Shape, 4><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  else if (heads == 2) nodes_kernel<DT, D, Shape, 2><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  else nodes_kernel<DT, D, Shape, 1><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   join_nodes_kernel<DT, D><<<unsigned((rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
   return hipGetLastError();
@@ -605,7 +648,7 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, int 
     if (shape == kMany64) return launch<DT, D, kMany64>(c, a, plan, s);
     if (shape == kMany128) return launch<DT, D, kMany128>(c, a, plan, s);
   }
-  if constexpr (D < 256) return launch<DT, D, kFew32>(c, a, plan, s);
+  if constexpr (D == 64 || (DT == 0 && D == 128)) return launch<DT, D, kFew32>(c, a, plan, s);
   return hipErrorInvalidValue;
 }
 
@@ -626,8 +669,8 @@ hipError_t launch_kv_share(const KvCache& c, const KvShared& sh, hipStream_t s) 
     meet_kernel<<<c.seqs, kWave, 0, s>>>(c, sh.a, plan);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (c.seqs <= kPlan) plan_kernel<1><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x));
-  else plan_kernel<kSeqs / kPlan><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x));
+  if (c.seqs <= kPlan) plan_kernel<1><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T));
+  else plan_kernel<kSeqs / kPlan><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T));
   return hipGetLastError();
 }
 
