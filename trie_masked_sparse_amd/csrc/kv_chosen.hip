@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kBlock) void join_chosen_kernel(KvAttention a, int 
   const int column = threadIdx.x % (D / 4) * 4;
   if (parts.stats[row].y < 0.f) return;
   PartSum sum;
-  sum.add<D>(parts, splits, column, [&](int i) { return i * all + row; });
+  sum.add<D, 8>(parts, splits, column, [&](int i) { return i * all + row; });
   store4<DT>(a.out, row * D + column, sum.x * (1.f / sum.l));
 }
 

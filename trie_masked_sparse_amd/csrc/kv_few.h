@@ -283,14 +283,13 @@ struct Parts {
 };
 
 // One row's 4 values from column `column` on over `count` parts: part i is row
-// at(i) of the parts.  A running maximum; kParts of them in flight.
+// at(i) of the parts.  A running maximum; kParts of them are in flight.
 struct PartSum {
   float top = -INFINITY, l = 0.f;
   f32x4 x{0.f, 0.f, 0.f, 0.f};
 
-  template <int D, class At>
+  template <int D, int kParts, class At>
   __device__ void add(const Parts& p, int count, int column, At at) {
-    constexpr int kParts = 8;
     for (int i = 0; i < count; i += kParts) {
       float2 s[kParts];
       f32x4 y[kParts];

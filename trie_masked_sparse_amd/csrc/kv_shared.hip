@@ -54,8 +54,13 @@ struct Head {
 };
 
 struct PlanSeq {
-  int32_t begin, n, len, levels;               // tokens, committed rows; nodes (-1: its outputs are NaN)
-  int32_t node[kLevels + 1], at[kLevels + 1];  // nodes, and where its tokens are among a node's
+  int32_t begin, n, len, levels;  // tokens, committed rows; nodes (-1: its outputs are NaN)
+  struct {
+    int32_t node, at;         // where its tokens are among a node's
+    int32_t all, M, chunks;   // of the node: rows, rows of a row tile, chunks, parts
+    int32_t pad;
+    int64_t part;
+  } of[kLevels + 1];
 };
 
 // Of a sequence: among those before it the first that has most pages in common
@@ -237,26 +242,22 @@ __device__ inline void each_value(bool on, int value, F f) {
   }
 }
 
-// First part row of row tile rt, chunk k of a node and key head: a chunk's parts
+// First part row of row tile rt, chunk k of a node's key head: a chunk's parts
 // are the tile's rows for head 0, then for head 1, ...
-__device__ inline int64_t part_row(const KvCache& c, const Node& x, int group, int rt, int k, int h) {
-  const int64_t all = int64_t(x.tokens) * group, first = int64_t(rt) * x.rows, rows = min(int64_t(x.rows), all - first);
-  return x.part + c.kv_heads * (first * x.chunks + k * rows) + h * rows;
+__device__ inline int64_t part_row(int64_t part, int kv_heads, int all, int M, int chunks, int rt, int k, int h) {
+  const int64_t first = int64_t(rt) * M, rows = min(int64_t(M), all - first);
+  return part + kv_heads * (first * chunks + k * rows) + h * rows;
 }
 
-// The units i, i + step, ... of a node whose first is `first`: heads next to each
-// other, then the chunks of a row tile.
-__device__ inline void write_units(const KvCache& c, const Plan& plan, const Node& x, int group, int row_tiles, int heads,
-                                   int64_t first, int i, int step) {
-  for (; i < row_tiles * x.chunks * heads; i += step) {
-    const int h = i % heads * (c.kv_heads / heads), k = i / heads % x.chunks, rt = i / heads / x.chunks;
-    Unit u{};
-    u.seq = x.seq, u.key0 = x.key0, u.keys = x.keys, u.list = x.list, u.begin = x.begin, u.n = x.n, u.len = x.len;
-    u.all = x.tokens * group, u.row0 = rt * x.rows, u.rows = min(x.rows, u.all - u.row0), u.h = h, u.M = x.rows;
-    u.tile0 = k * x.tiles, u.tile1 = u.tile0 + x.tiles;
-    u.part = part_row(c, x, group, rt, k, h);
-    plan.units()[first + i] = u;
-  }
+// Unit i of a node: heads next to each other, then the chunks of a row tile.
+__device__ inline Unit unit_of(const KvCache& c, const Node& x, int group, int heads, int i) {
+  const int h = i % heads * (c.kv_heads / heads), k = i / heads % x.chunks, rt = i / heads / x.chunks;
+  Unit u{};
+  u.seq = x.seq, u.key0 = x.key0, u.keys = x.keys, u.list = x.list, u.begin = x.begin, u.n = x.n, u.len = x.len;
+  u.all = x.tokens * group, u.row0 = rt * x.rows, u.rows = min(x.rows, u.all - u.row0), u.h = h, u.M = x.rows;
+  u.tile0 = k * x.tiles, u.tile1 = u.tile0 + x.tiles;
+  u.part = part_row(x.part, c.kv_heads, u.all, x.rows, x.chunks, rt, k, h);
+  return u;
 }
 
 // One workgroup.  In every round a group are the sequences that go through one
@@ -275,7 +276,14 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
   // of every sequence: the first of its group; tokens (0: none to share); its Meet.
   // Of a leader: the fewest pages that one of its group has in common with it, the
   // others' tokens, branches; its node's number and list
-  __shared__ int lead[kMost], with[kMost], pages[kMost], fewest[kMost], of_group[kMost], branches[kMost], place[kMost], whole[kMost];
+  __shared__ union {
+    struct {
+      int lead[kMost], with[kMost], pages[kMost], fewest[kMost], of_group[kMost], branches[kMost], place[kMost], whole[kMost];
+    } s;
+    int first_unit[kMost + kLevels * (kMost / 2) + 1];  // of every node, when the others are done with
+  } lds;
+  auto &lead = lds.s.lead, &with = lds.s.with, &pages = lds.s.pages, &fewest = lds.s.fewest, &of_group = lds.s.of_group,
+       &branches = lds.s.branches, &place = lds.s.place, &whole = lds.s.whole;
   __shared__ uint16_t count[kMost];
   __shared__ int nodes_s, list_s;
   __shared__ int64_t sums[3][kPlanWaves];
@@ -406,7 +414,7 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       for (int u = 0; u < count[s]; ++u) plan.tokens()[list + at + u] = p.begin + u;
 #pragma unroll
       for (int v = 0; v < kLevels; ++v)
-        if (p.levels == v) p.node[v] = node, p.at[v] = at;
+        if (p.levels == v) p.of[v].node = node, p.of[v].at = at;
       ++p.levels;
       if (s == l) {
         Node x{};
@@ -440,10 +448,9 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       plan.nodes()[node] = x;
 #pragma unroll
       for (int v = 0; v <= kLevels; ++v)
-        if (p.levels == v) p.node[v] = node, p.at[v] = 0;
+        if (p.levels == v) p.of[v].node = node, p.of[v].at = 0;
       ++p.levels;
     }
-    plan.seqs()[s] = p;
   }
   __syncthreads();
   // Chunks of the keys: of a unit's cost as much as a slot has, or less.
@@ -480,23 +487,37 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
   }
   threads_before(x_of, sums + 1, all);
   const bool fits = all[0] <= plan.y.most_units && all[1] <= plan.y.most_rows;
-  // (places of nodes with many units in LDS, for all threads to write them)
   for (int i = from; fits && i < to; ++i) {
     Node& x = plan.nodes()[i];
     const Size z = size(x);
     x.chunks = chunks(z), x.rows = z.rows, x.part = rows;
     x.tiles = (z.key_tiles + x.chunks - 1) / x.chunks;
-    if (i < kMost) place[i] = static_cast<int>(units);
-    else write_units(c, plan, x, group, z.row_tiles, z.heads, units, 0, 1);
+    lds.first_unit[i] = static_cast<int>(units);
     units += int64_t(z.row_tiles) * x.chunks * z.heads, rows += int64_t(x.tokens) * a.q_heads * x.chunks;
   }
   __syncthreads();
-  if (fits)
-    for (int i = wave; i < min(nodes, kMost); i += kPlanWaves) {
+  if (fits) {
+    for (int u = tid; u < all[0]; u += kPlan) {
+      int i = 0;
+      for (int step = 1 << (31 - __clz(nodes)); step; step /= 2)
+        if (i + step < nodes && lds.first_unit[i + step] <= u) i += step;
       const Node x = plan.nodes()[i];
-      const Size z = size(x);
-      write_units(c, plan, x, group, z.row_tiles, z.heads, place[i], lane, kWave);
+      plan.units()[u] = unit_of(c, x, group, size(x).heads, u - lds.first_unit[i]);
     }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {  // what the join has to know
+      const int s = tid + i * kPlan;
+      if (s >= n) continue;
+      PlanSeq& p = mine[i];
+#pragma unroll
+      for (int v = 0; v <= kLevels; ++v) {
+        if (v >= p.levels) continue;
+        const Node& x = plan.nodes()[p.of[v].node];
+        p.of[v].all = x.tokens * group, p.of[v].M = x.rows, p.of[v].chunks = x.chunks, p.of[v].part = x.part;
+      }
+      plan.seqs()[s] = p;
+    }
+  }
   if (tid == 0) *plan.head() = Head{fits ? kMagic : 0, a.T, a.q_heads, fits ? int(all[0]) : 0, nodes, M, {heads, 0}};
 }
 
@@ -586,32 +607,52 @@ __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ?
   }
 }
 
-// The parts of a token and query head over all its nodes: D / 4 threads to a row.
-template <int DT, int D>
+// The parts of a token and query head over all its nodes: D / 4 threads to a row,
+// or G times as many, each of which take every G-th chunk, where rows are few and
+// their chunks many.
+template <int DT, int D, int G>
 __global__ __launch_bounds__(kBlock) void join_nodes_kernel(KvCache c, KvAttention a, Plan plan, int M) {
-  const int64_t row = int64_t(blockIdx.x) * (kBlock * 4 / D) + threadIdx.x / (D / 4);
-  if (row >= int64_t(a.T) * a.q_heads) return;
-  const int column = threadIdx.x % (D / 4) * 4, t = static_cast<int>(row / a.q_heads), head = static_cast<int>(row % a.q_heads);
+  constexpr int kRow = D / 4, kRows = kBlock / (kRow * G);
+  __shared__ float2 stats[G > 1 ? kBlock : 1];
+  __shared__ f32x4 values[G > 1 ? kBlock : 1];
+  const int tid = threadIdx.x, g = tid / kRow % G, column = tid % kRow * 4;
+  const int64_t row = min(int64_t(blockIdx.x) * kRows + tid / (kRow * G), int64_t(a.T) * a.q_heads - 1);
+  const int t = static_cast<int>(row / a.q_heads), head = static_cast<int>(row % a.q_heads);
   const int group = a.q_heads / c.kv_heads, h = head / group;
-  f32x4 x{NAN, NAN, NAN, NAN};
-  if (planned(plan, a, M)) {
-    const int s = plan.owner()[t];
-    if (s < 0) return;  // a token of nobody: its outputs stay as they are
-    const PlanSeq& p = plan.seqs()[s];
-    // what the plan was made from
-    if (p.levels > 0 && c.status[s] == TMS_OK && p.len == c.length[s] && p.begin == a.start[s] && p.n <= a.max_new) {
-      PartSum sum;
-      for (int i = 0; i < p.levels; ++i) {
-        const Node& node = plan.nodes()[p.node[i]];
-        const int r = (p.at[i] + t - p.begin) * group + head % group, rt = r / node.rows;
-        const int64_t first = part_row(c, node, group, rt, 0, h) + r % node.rows;
-        const int64_t step = part_row(c, node, group, rt, 1, h) + r % node.rows - first;
-        sum.add<D>(plan.parts(), node.chunks, column, [&](int k) { return first + k * step; });
-      }
-      x = sum.x * (1.f / sum.l);
+  // (what is read from a plan that was not made is not used; the reads do not
+  // wait for each other)
+  const int s = plan.owner()[t], at = max(0, min(s, c.seqs - 1));
+  const PlanSeq p = plan.seqs()[at];
+  const bool made = planned(plan, a, M);
+  // what the plan was made from
+  const bool good = made && s >= 0 && p.levels > 0 && c.status[at] == TMS_OK && p.len == c.length[at] && p.begin == a.start[at] &&
+                    p.n <= a.max_new;
+  PartSum sum;
+  if (good) {
+#pragma unroll
+    for (int i = 0; i <= kLevels; ++i) {
+      if (i >= p.levels) break;
+      const auto& of = p.of[i];
+      const int r = (of.at + t - p.begin) * group + head % group, rt = r / of.M;
+      const int64_t first = part_row(of.part, c.kv_heads, of.all, of.M, of.chunks, rt, 0, h) + r % of.M;
+      const int64_t step = part_row(of.part, c.kv_heads, of.all, of.M, of.chunks, rt, 1, h) + r % of.M - first;
+      sum.add<D, G == 1 ? 4 : 8>(plan.parts(), (of.chunks - g + G - 1) / G, column, [&](int k) { return first + (g + k * G) * step; });
     }
   }
-  store4<DT>(a.out, row * D + column, x);
+  if constexpr (G > 1) {
+    stats[tid] = float2{sum.top, sum.l}, values[tid] = sum.x;
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+      const float2 y = stats[tid + i * kRow];
+      const float top = fmaxf(sum.top, y.x), base = top == -INFINITY ? 0.f : top;
+      const float mine = part_weight(sum.top - base), other = part_weight(y.x - base);
+      sum.l = sum.l * mine + y.y * other, sum.x = sum.x * mine + values[tid + i * kRow] * other, sum.top = top;
+    }
+  }
+  if (made && s < 0) return;  // a token of nobody: its outputs stay as they are
+  store4<DT>(a.out, row * D + column, good ? sum.x * (1.f / sum.l) : f32x4{NAN, NAN, NAN, NAN});
 }
 
 int shape(const KvCache& c, int32_t T, int32_t q_heads) {
@@ -621,23 +662,24 @@ int shape(const KvCache& c, int32_t T, int32_t q_heads) {
   return rows <= 32 && c.head_dim == 64 ? kFew32 : rows <= 64 ? kMany64 : kMany128;
 }
 
-// Key heads of a unit of a small node: as many as leave a unit for each slot.
+// Key heads of a unit of a small node: two where there are units enough (64 answers
+// 34 -> 31 us; four where they are four times as many 204 -> 214).
 int small_heads(const KvCache& c, int32_t T) {
-  const int64_t nodes = int64_t(std::min(c.seqs, T)) * c.kv_heads;
-  return c.kv_heads % 4 == 0 && nodes >= 4 * kSlots ? 4 : c.kv_heads % 2 == 0 && nodes >= kSlots ? 2 : 1;
+  return c.kv_heads % 2 == 0 && int64_t(std::min(c.seqs, T)) * c.kv_heads >= kSlots ? 2 : 1;
 }
 
 template <int DT, int D, int Shape>
 hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, hipStream_t s) {
   const int64_t blocks = plan.y.most_units, rows = int64_t(a.T) * a.q_heads;
-  constexpr int kRows = kBlock * 4 / D;
+  constexpr int kRows = kBlock * 4 / D;  // of a workgroup of the join
+  constexpr int64_t kFew = 2048;
   if (blocks >= (int64_t(1) << 32) / kBlock || rows >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
   const int heads = small_heads(c, a.T);
-  if (heads == 4) nodes_kernel<DT, D, Shape, 4><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
-  else if (heads == 2) nodes_kernel<DT, D, Shape, 2><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  if (heads == 2) nodes_kernel<DT, D, Shape, 2><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   else nodes_kernel<DT, D, Shape, 1><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  join_nodes_kernel<DT, D><<<unsigned((rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
+  if (rows <= kFew) join_nodes_kernel<DT, D, 4><<<unsigned((4 * rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
+  else join_nodes_kernel<DT, D, 1><<<unsigned((rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
   return hipGetLastError();
 }
 
