@@ -2,6 +2,8 @@
 // workgroup of the attention over chosen pages, and of the shared attention in
 // fp32, does.
 #pragma once
+#include <type_traits>
+
 #include "kv_tiles.h"
 
 namespace tms {
@@ -44,9 +46,15 @@ struct FewRows {
   // page_at(key): its page, clamped to the pool.  query(r): element of q of row r, in bounds for every r < M;
   // token(r): its token, -1 where there is none.  emit(h, r, column, x, top, l): 4
   // values of a row, not yet divided by the sum l of its weights relative to 2^top.
-  template <class PageAt, class Query, class Token, class Emit>
-  static __device__ inline void run(const KvCache& c, const KvAttention& a, Lds& lds, const FewTile& t, PageAt page_at,
-                                    Query query, Token token, Emit emit) {
+  // visible(key, r): whether row r sees key .. key + 3 (a multiple of 4), where that
+  // is not all that a.parent and the token say; rows then differ in keys that may
+  // hold anything, so where an output is not finite nothing is emitted: returns
+  // whether it was.
+  struct Everything {};
+  template <class PageAt, class Query, class Token, class Emit, class Visible = Everything>
+  static __device__ inline bool run(const KvCache& c, const KvAttention& a, Lds& lds, const FewTile& t, PageAt page_at,
+                                    Query query, Token token, Emit emit, Visible visible = Visible(), bool finite_only = false) {
+    constexpr bool kChosen = !std::is_same<Visible, Everything>::value;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int col = lane % 16, g = lane / 16, part = wave % Step, head = wave / Step, h = t.h + head;
     // a scale of 0 clears q instead: a masked score stays -inf
@@ -153,6 +161,16 @@ struct FewRows {
               for (int e = 0; e < 4; ++e) sc[m][i][e] = word >> (16 * i + e) & 1 ? sc[m][i][e] : -INFINITY;
           }
         }
+        if constexpr (kChosen) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < T::Sub; ++i) {
+              const bool on = visible(kt * KW + 16 * i + 4 * g, m * 16 + col);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[m][i][e] = on ? sc[m][i][e] : -INFINITY;
+            }
+        }
         u32x4 pw[MT], pl[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -218,11 +236,14 @@ struct FewRows {
       }
 
       float z = 0.f;
-      if (!again && end * KW > mixed.first)
+      if ((kChosen && finite_only) || (!again && end * KW > mixed.first))
 #pragma unroll
         for (int m = 0; m < MT; ++m) z = zero_or_nan(o[m], z);
       // every wavefront is done with its tiles
-      if (__syncthreads_or(z != z)) continue;
+      if (__syncthreads_or(z != z)) {
+        if (kChosen && finite_only) return false;
+        continue;
+      }
       // a head's wavefronts' parts joined; each ends with as many of the
       // columns
       f32x4* buf = reinterpret_cast<f32x4*>(lds.tiles);
@@ -270,7 +291,7 @@ struct FewRows {
           emit(h, r, 16 * d + 4 * g, x, top, l);
         }
       }
-      return;
+      return true;
     }
   }
 };
@@ -283,12 +304,13 @@ struct Parts {
 };
 
 // One row's 4 values from column `column` on over `count` parts: part i is row
-// at(i) of the parts.  A running maximum; kParts of them are in flight.
+// at(i) of the parts.  A running maximum; kParts of them are in flight.  Shared:
+// other workgroups of the launch have written them (part_store in kv_tiles.h).
 struct PartSum {
   float top = -INFINITY, l = 0.f;
   f32x4 x{0.f, 0.f, 0.f, 0.f};
 
-  template <int D, int kParts, class At>
+  template <int D, int kParts, bool Shared = false, class At>
   __device__ void add(const Parts& p, int count, int column, At at) {
     for (int i = 0; i < count; i += kParts) {
       float2 s[kParts];
@@ -298,8 +320,9 @@ struct PartSum {
         s[u] = float2{-INFINITY, 0.f}, y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (i + u < count) {
           const int64_t row = at(i + u);
-          s[u] = p.stats[row];
-          y[u] = *reinterpret_cast<const f32x4*>(p.values + row * D + column);
+          if constexpr (Shared) s[u] = float2{part_load<true>(&p.stats[row].x), part_load<true>(&p.stats[row].y)};
+          else s[u] = p.stats[row];
+          y[u] = part_load<Shared>(reinterpret_cast<const f32x4*>(p.values + row * D + column));
         }
       }
       float next = top;
