@@ -280,6 +280,47 @@ def test_shared_sequences_in_error_stale_plans_and_tokens_of_nobody():
     check_shared(b2, q2, out, 0.125, None, of=(0, 1))
 
 
+@pytest.mark.parametrize("n", [2, 3, 4, 15, 17, 40, 63, 64, 65, 100, 200, 1030])
+@pytest.mark.parametrize("prompts", [1, 2])
+def test_shared_pages_are_read_once(n, prompts):
+    """Pages of sequences other than the first of a prompt are replaced behind the
+    plan by one that holds NaN: whoever shares the first one's does not notice."""
+    rng = np.random.default_rng(n)
+    b = Branches(rng, BF, 1, 64, 16, [(((f"p{i % prompts}", 60),), i % 5, 1) for i in range(n)])
+    q = queries(rng, b, 2, 64, BF)
+    start = dev32(offsets(b.new))
+    plan = tms.SharedPlan(b.cache, n, 2)
+    tms.kv_share(b.cache, plan, start)
+    nobody = [p for p in range(b.cache.pages) if int(b.cache.refs[p]) == 0][0]
+    assert torch.isnan(b.cache.kv[0, nobody].float()).all()
+    b.cache.table[prompts:, :60] = nobody
+    out = run_shared(b, q, plan=plan)
+    alone = [s for s in range(n) if n // prompts < 2 or (n == 3 and prompts == 2 and s == 1)]
+    check_shared(b, q, out, 0.125, None, n, of=[s for s in range(n) if s < prompts or s not in alone])
+
+
+@pytest.mark.parametrize("branch", [3, 40])
+def test_shared_beginnings_of_prompts_are_read_once_where_it_pays(branch):
+    """Prompts of one beginning: a run of its own if it is long, else part of each
+    prompt's."""
+    rng = np.random.default_rng(branch)
+    b = Branches(rng, BF, 1, 64, 16, [((("a", branch), (f"p{i % 4}", 50)), 3, 1) for i in range(64)])
+    q = queries(rng, b, 2, 64, BF)
+    plan = tms.SharedPlan(b.cache, 64, 2)
+    tms.kv_share(b.cache, plan, dev32(offsets(b.new)))
+    nobody = [p for p in range(b.cache.pages) if int(b.cache.refs[p]) == 0][0]
+    keep = b.cache.table.clone()
+    b.cache.table[4:, :branch + 50] = nobody
+    check_shared(b, q, run_shared(b, q, plan=plan), 0.125, None, branch)
+    b.cache.table.copy_(keep)
+    b.cache.table[1:, :branch] = nobody
+    out = run_shared(b, q, plan=plan)
+    if branch == 40:
+        check_shared(b, q, out, 0.125, None, branch)
+    else:
+        assert torch.isfinite(out[0::4]).all() and torch.isnan(out[1::4]).all()
+
+
 def test_shared_starts_out_of_order_are_refused_without_harm():
     rng = np.random.default_rng(2)
     b = Branches(rng, BF, 2, 64, 16, [((("p", 40),), 0, 4)] * 4)

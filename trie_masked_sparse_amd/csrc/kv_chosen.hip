@@ -290,7 +290,7 @@ Parts parts_at(const KvCache& c, int64_t rows) {
 
 // Where the tiles of tokens and heads are fewer than the workgroups that the chip
 // holds at once, their pages are cut, to no less than kLeast keys a workgroup.
-constexpr int kFit = 512, kLeast = 256;
+constexpr int kFit = 512, kLeast = 128;
 static_assert(kFit * 4 <= kWorkCounts, "a counter for each tile that is cut");
 
 Cut cut(const KvCache& c, const KvChosen& ch) {

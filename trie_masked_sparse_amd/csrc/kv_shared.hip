@@ -231,7 +231,7 @@ __device__ inline int lanes_up_to(int x) {
 }
 
 // Calls f(value, lanes that have it), a value after the other, for the lanes
-// where `on`.
+// where `on`; all lanes of the wavefront are active.
 template <class F>
 __device__ inline void each_value(bool on, int value, F f) {
   for (uint64_t left = __ballot(on); left;) {
@@ -294,6 +294,12 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     for (int i = 0; i < kEach; ++i)
       if (tid + i * kPlan < n) f(i, tid + i * kPlan);
   };
+  // the same, by whole wavefronts: on, whether there is such a sequence (s is the last one where not)
+  auto each_lane = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (wave * kWave + i * kPlan < n) f(i, min(tid + i * kPlan, n - 1), tid + i * kPlan < n);
+  };
   a.max_new = INT_MAX;
   if (tid == 0) nodes_s = list_s = 0;
   for (int i = tid; i < a.T; i += kPlan) plan.owner()[i] = -1;
@@ -345,9 +351,9 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       fewest[s] = INT_MAX, of_group[s] = branches[s] = 0;
     });
     if (!__syncthreads_or(groups)) break;
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
+    each_lane([&](int i, int s, bool here) __attribute__((always_inline)) {
       const int l = lead[s];
-      each_value(l != s, l, [&](int v, uint64_t lanes) {
+      each_value(here && l != s, l, [&](int v, uint64_t lanes) {
         const bool on = lanes >> lane & 1;
         int least = on ? in_common[i] : INT_MAX;
         const int tokens = __builtin_amdgcn_readlane(lanes_up_to(on ? count[s] : 0), kWave - 1);
@@ -356,10 +362,10 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
       });
     });
     __syncthreads();
-    each_seq([&](int i, int s) __attribute__((always_inline)) {
+    each_lane([&](int i, int s, bool here) __attribute__((always_inline)) {
       const int l = lead[s], d = fewest[l];
       int unused;
-      each_value(d < INT_MAX && first_at(s, d, &unused) == s, l, [&](int v, uint64_t lanes) {
+      each_value(here && d < INT_MAX && first_at(s, d, &unused) == s, l, [&](int v, uint64_t lanes) {
         if (lane == __builtin_ctzll(lanes)) atomicAdd(&branches[v], __popcll(lanes));
       });
     });
