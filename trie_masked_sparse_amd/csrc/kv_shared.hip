@@ -24,11 +24,14 @@ constexpr int kPlan = 1024, kPlanWaves = kPlan / kWave;
 constexpr int kSlots = 512;     // workgroups that the chip holds at once
 constexpr int kTile = 64;       // keys that the plan counts in
 constexpr int kSmall = 16;      // rows of a small node
+constexpr int kMedium = 64;     // of one that takes a row tile half as high, where the others' have 128
 constexpr int kMagic = 0x73686172;
 
 // Sequences of more rows of a key head than this read their pages for
-// themselves: the products bound them, and many rows share a page's read already.
-constexpr int kMostRowsShared = 128;
+// themselves: the products bound them, and many rows share a page's read already
+// (5 to 31 drafts of 64 sequences behind prompts of 1201 to 2500 tokens: 2 rows a
+// draft, heads of 128 79 us alone, 57 shared; 4 rows, heads of 256 88 and 120).
+__host__ __device__ inline int most_rows_shared(const KvCache& c) { return c.head_dim == 256 ? 64 : 128; }
 
 // A node pays where the keys that are not read again (its keys, times the
 // readers that it saves) are more than these and what its rows' parts cost: a
@@ -47,7 +50,6 @@ constexpr int kLeastTiles = 4;
 constexpr int kOpenSmall = 20, kOpenLarge = 18, kTileSmall = 4, kTileLarge = 5;
 
 constexpr int kRounds = 16;  // branchings of the trie that are looked at, one behind the other
-
 
 struct Head {
   int32_t magic, T, q_heads, units, nodes, rows, pad[2];
@@ -99,7 +101,7 @@ int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 Layout layout(const KvCache& c, int32_t T, int32_t q_heads, int M) {
   Layout y{};
   const int64_t group = q_heads / c.kv_heads, n = std::min<int64_t>(c.seqs, T);
-  y.most_nodes = static_cast<int32_t>(n + kLevels * (n / 2));
+  y.most_nodes = static_cast<int32_t>(2 * n);  // the sequences' own, and places where the trie branches
   // A node's row tiles and heads, and what cuts add: a chunk costs a slot, less
   // one of its tiles, of which it has kLeastTiles or more.
   constexpr int kCuts = kSlots * (kLeastTiles + 1) / kLeastTiles;
@@ -135,7 +137,7 @@ struct Plan {
 
 // Whole pages of committed rows of a sequence that may be shared.
 __device__ inline int shared_pages(const KvCache& c, const KvAttention& a, const Seq& q) {
-  return q.n && !q.bad && int64_t(q.n) * (a.q_heads / c.kv_heads) <= kMostRowsShared ? q.len >> c.page_shift : 0;
+  return q.n && !q.bad && int64_t(q.n) * (a.q_heads / c.kv_heads) <= most_rows_shared(c) ? q.len >> c.page_shift : 0;
 }
 
 // Meet of sequence s, by one wavefront; whole(t): shared_pages of a sequence.  A
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
     struct {
       int lead[kMost], with[kMost], pages[kMost], fewest[kMost], of_group[kMost], branches[kMost], place[kMost], whole[kMost];
     } s;
-    int first_unit[kMost + kLevels * (kMost / 2) + 1];  // of every node, when the others are done with
+    int first_unit[2 * kMost];  // of every node, when the others are done with
   } lds;
   auto &lead = lds.s.lead, &with = lds.s.with, &pages = lds.s.pages, &fewest = lds.s.fewest, &of_group = lds.s.of_group,
        &branches = lds.s.branches, &place = lds.s.place, &whole = lds.s.whole;
@@ -469,7 +471,7 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, P
   auto size = [&](const Node& x) {
     const int64_t rows = int64_t(x.tokens) * group;
     const bool small = rows <= kSmall;
-    const int of = small ? kSmall : M;
+    const int of = small ? kSmall : rows <= kMedium ? min(M, kMedium) : M;
     return Size{of, static_cast<int>((rows + of - 1) / of), (x.keys + kTile - 1) / kTile, small ? c.kv_heads / heads : c.kv_heads,
                 small, small ? kOpenSmall : kOpenLarge, small ? kTileSmall * heads : kTileLarge};
   };
@@ -555,8 +557,10 @@ template <int DT, int D, int Shape, int Heads>
 __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
   using Small = FewRows<DT, D, 1, Heads>;
   using Large = typename Body<DT, D, Shape>::Type;
+  using Medium = typename Body<DT, D, Shape == kMany128 ? kMany64 : Shape>::Type;
   __shared__ union {
     typename Small::Lds small;
+    typename Medium::Lds medium;
     typename Large::Lds large;
   } lds;
   const Unit& at = plan.units()[blockIdx.x];
@@ -607,9 +611,14 @@ __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ?
     tiles(Large::KW);
     Large::run(c, a, lds.large, t, page_at, query, token, emit);
   } else if constexpr (Shape >= kMany64) {
-    tiles(Large::KT);
-    Large::run(c, a, lds.large, t, table, [&](int r) { return query(x.h, r); }, token,
-               [&](int r, int column, f32x4 v, float top, float l) { emit(x.h, r, column, v, top, l); });
+    auto many = [&](auto body, auto& in) __attribute__((always_inline)) {
+      using Rows = decltype(body);
+      tiles(Rows::KT);
+      Rows::run(c, a, in, t, table, [&](int r) { return query(x.h, r); }, token,
+                [&](int r, int column, f32x4 v, float top, float l) { emit(x.h, r, column, v, top, l); });
+    };
+    if (Shape == kMany128 && x.M == kMedium) many(Medium(), lds.medium);
+    else many(Large(), lds.large);
   }
 }
 
@@ -724,7 +733,7 @@ hipError_t launch_kv_share(const KvCache& c, const KvShared& sh, hipStream_t s) 
 
 hipError_t launch_kv_attention_shared(const KvCache& c, const KvShared& sh, hipStream_t s) {
   // where every sequence has many rows there is nothing to share
-  if (int64_t(sh.a.max_new) * (sh.a.q_heads / c.kv_heads) > kMostRowsShared) return launch_kv_attention(c, sh.a, s);
+  if (int64_t(sh.a.max_new) * (sh.a.q_heads / c.kv_heads) > most_rows_shared(c)) return launch_kv_attention(c, sh.a, s);
   const int x = shape(c, sh.a.T, sh.a.q_heads);
   const Plan plan = plan_of(c, sh, x);
   if (c.dtype == TMS_F32) {
