@@ -511,11 +511,13 @@ tms_status tms_kv_share_bytes(const tms_kv* c, int32_t T, int32_t q_heads, int64
 tms_status tms_kv_share(const tms_kv* c, const int32_t* start, int32_t T, int32_t q_heads, void* plan,
                         int64_t plan_bytes, void* stream);
 /* Arguments, errors and what unseen rows may hold as tms_kv_attention, which it
- * calls where max_new * q_heads / kv_heads is above 128 (many rows of one
- * sequence share the reads as it is; the plan is not used then).  In bf16 the
- * weights of the second product keep 16 bits.  NaN also for
+ * calls where max_new * q_heads / kv_heads is above 128 (64 with heads of 256):
+ * many rows of one sequence share the reads as it is, and the plan is not used
+ * then.  In bf16 the weights of the second product keep 16 bits in runs of up to
+ * 64 query rows of a key head, and are rounded to bf16 above.  NaN also for
  * sequences whose length, start or status is not the plan's, and for all tokens
- * where the plan is of another T or q_heads or was not made. */
+ * where the plan is of another T or q_heads or was not made.  A few short
+ * sequences are quicker with tms_kv_attention. */
 tms_status tms_kv_attention_shared(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
                                    const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,
                                    void* out, void* plan, int64_t plan_bytes, void* stream);
@@ -542,7 +544,7 @@ tms_status tms_kv_bounds(const tms_kv* c, const int32_t* n_new, int32_t max_new,
  * scores of a key of the page can add up to.  Of equal scores the lower page is
  * taken; NaN is above all, then come first and last; sums are fp64.  Where a
  * sequence has no more than k whole pages all are chosen, and -1 fills the rest
- * (also of a sequence in error).  k in [1, 8192]; first, last at least 0.  q as
+ * (also of a sequence in error or with more than max_new tokens).  k in [1, 8192]; first, last at least 0.  q as
  * for tms_kv_attention.  work: dev, 256-byte aligned, tms_kv_select_bytes for
  * this T or a larger one. */
 tms_status tms_kv_select_bytes(const tms_kv* c, int32_t T, int64_t* bytes);

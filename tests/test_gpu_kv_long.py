@@ -256,6 +256,9 @@ def test_shared_sequences_in_error_stale_plans_and_tokens_of_nobody():
     # a plan that is older than the lengths
     plan = tms.SharedPlan(b.cache, 4, 4)
     out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="made for 0"):
+        tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    plan._planned = 4  # (the library's own check)
     tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)  # never made
     assert torch.isnan(out).all()
     tms.kv_share(b.cache, plan, start)
@@ -265,6 +268,9 @@ def test_shared_sequences_in_error_stale_plans_and_tokens_of_nobody():
     b.cache.length[2] += 1
     # of other tokens
     tms.kv_share(b.cache, plan, dev32([0, 1, 2, 3, 3]), tokens=3)
+    with pytest.raises(ValueError, match="made for 3"):
+        tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    plan._planned = 4
     tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
     assert torch.isnan(out).all()
     out.fill_(7.0)
@@ -454,6 +460,53 @@ def test_select_equal_scores_and_values_that_are_not_finite(dtype):
     assert (run_select(cache, index, q, new, k)[1:] == -1).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pages,cut", [(40, False), (5000, False), (5000, True)], ids=["short", "past_lds", "cut"])
+def test_select_borders_among_nan_infinite_and_always_chosen_pages(dtype, pages, cut):
+    """Every place that the border can have: among NaN, among infinite scores and
+    the first and last pages (by place), among finite ones; more first and last
+    pages than are taken; equal scores at the border."""
+    rng = np.random.default_rng(pages)
+    # (a list is taken by one workgroup where there are many)
+    T = 1 if cut else 300 if pages > 1000 else 1
+    cache, _, _ = filled(rng, dtype, 1, 64, 8, [8 * pages + 2], [T])
+    index = tms.PageIndex(cache, tokens=T)
+    tms.kv_bounds(cache, index)
+    p = cache.table[0, :pages].long()
+    base = index.bounds[0, p].clone()
+    q = torch.from_numpy(np.abs(rng.standard_normal((1, 2, 64))).astype(np.float32)).to(dtype).cuda().expand(T, 2, 64).contiguous()
+    for nans, infs, same, low in ((0, 0, 0, 0), (3, 0, 0, 0), (20, 0, 0, 0), (0, 20, 0, 0), (4, 9, 0, 3), (0, 0, pages, 0), (2, 1, pages // 2, 1)):
+        b = base.clone()
+        where = torch.from_numpy(rng.permutation(pages)).cuda()
+        b[where[:same]] = base[0]
+        b[where[same // 2:same // 2 + nans], 0, 1, 3] = float("nan")
+        b[where[-infs - 1:-1] if infs else where[:0], 0, 1, 5] = float("inf")
+        b[where[5:5 + low], 0, 1, 7] = float("-inf")
+        index.bounds[0, p] = b
+        for k, first, last in ((1, 0, 0), (10, 0, 0), (10, 2, 3), (10, 7, 9), (pages - 1, 1, 1), (16, 0, 16)):
+            if k > 8192:
+                continue
+            chosen = run_select(cache, index, q, [T], k, None, first, last)
+            want = choice(q[0].double().cpu().numpy(), index.bounds[0, p].double().cpu().numpy(), k, 1.0, first, last)
+            assert (chosen == want[None]).all(), (nans, infs, same, low, k, first, last)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_select_gives_the_same_on_memory_that_holds_anything(dtype):
+    rng = np.random.default_rng(8)
+    lens, new = [9000, 40, 3000], [2, 1, 3]
+    cache, _, _ = filled(rng, dtype, 2, 128, 16, lens, new)
+    index = tms.PageIndex(cache, tokens=6)
+    tms.kv_bounds(cache, index)
+    q = torch.from_numpy(rng.standard_normal((6, 8, 128)).astype(np.float32)).to(dtype).cuda()
+    first = run_select(cache, index, q, new, 12)
+    check_select(cache, index, q, lens, new, 12, first)
+    index.memory.fill_(0xff)
+    cache.work[tms.KV_WORK_ZERO:].fill_(0xff)
+    assert (run_select(cache, index, q, new, 12) == first).all()
+    assert (cache.work[:tms.KV_WORK_ZERO] == 0).all()
+
+
 def test_select_leaves_tokens_of_nobody():
     rng = np.random.default_rng(5)
     cache, _, _ = filled(rng, BF, 2, 64, 16, [100, 200], [1, 1])
@@ -583,6 +636,85 @@ def test_pages_lists_that_are_wrong_give_nan():
     assert torch.isnan(out[:2]).all() and torch.isfinite(out[2]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(2, 2, 64), (16, 4, 128), (8, 1, 256), (20, 2, 64)], **ids)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_pages_of_drafts_in_every_kind_of_batch(dtype, heads, kind):
+    """Tokens of a sequence that share a workgroup: ones that do not fill a row
+    tile, sequences without tokens, lists with nothing in common, one list for
+    all, more pages than are held at once, sequences of many pages."""
+    hq, hkv, D = heads
+    for n, (page, lens, new, k, same) in enumerate([
+            (8, [700, 0, 90, 2000], [17, 3, 0, 40], 20, False), (16, [3000] * 3, [2, 16, 33], 30, True), (64, [5000, 64], [8, 7], 70, False),
+            (8, [20000], [20], 900, False), (8, [40] * 60, [int(x) for x in np.arange(60) % 4], 3, False)]):
+        if D == 256 and k > 100 or k > 100 and heads != (2, 2, 64) and dtype == F:
+            continue
+        print(f"pages of drafts {dtype} {heads} {kind} {n}", flush=True)
+        rng = np.random.default_rng(3 * n + D)
+        cache, ks, vs = filled(rng, dtype, hkv, D, page, lens, new)
+        q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+        parents = [tree(rng, x) for x in new] if kind == "tree" else None
+        chosen = lists(rng, lens, new, hkv, page, k)
+        if same:
+            at = offsets(new)
+            for s in range(len(new)):
+                chosen[at[s]:at[s + 1]] = chosen[at[s]]
+        out = run_pages(cache, q, new, chosen, parents)
+        check_pages(cache, q, out, ks, vs, lens, new, chosen, D ** -0.5, parents, n)
+        cache.work[tms.KV_WORK_ZERO:].fill_(0xff)
+        assert torch.equal(out, run_pages(cache, q, new, chosen, parents))
+        assert (cache.work[:tms.KV_WORK_ZERO] == 0).all()
+
+
+def test_pages_of_sequences_too_long_for_their_pages_to_be_counted_together():
+    """More than 32768 pages a sequence: tokens take workgroups of their own."""
+    rng = np.random.default_rng(1)
+    cache = tms.PagedCache.empty(1, 50, 2, 8, 64, 2, 40000, dtype=BF)
+    cache.kv.copy_(torch.randn(cache.kv.shape, device="cuda"))
+    table = cache.table
+    lens, new = [8 * 39990, 100], [3, 5]
+    table[0, :39995] = torch.from_numpy(rng.integers(0, 40, 39995).astype(np.int32)).cuda()
+    table[1, :14] = torch.arange(36, 50, dtype=torch.int32, device="cuda")
+    cache.length.copy_(dev32(lens))
+    cache.held.copy_(dev32([39995, 14]))
+    chosen = lists(rng, lens, new, 2, 8, 9)
+    q = torch.from_numpy(rng.standard_normal((8, 4, 64)).astype(np.float32)).to(BF).cuda()
+    out = run_pages(cache, q, new, chosen)
+    kv = cache.kv[0].double().cpu().numpy()
+    at = offsets(new)
+    for s in range(2):
+        rows = np.arange(lens[s] + new[s])
+        pages = table[s].cpu().numpy()[rows // 8]
+        ks, vs = kv[pages, 0, :, rows % 8], kv[pages, 1, :, rows % 8]
+        check_pages(cache, q[at[s]:at[s + 1]], out[at[s]:at[s + 1]], [ks], [vs], [lens[s]], [new[s]], chosen[at[s]:at[s + 1]], 0.125, None, s)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_pages_values_that_are_not_finite_in_pages_that_other_drafts_chose(dtype):
+    """In every split of the work."""
+    rng = np.random.default_rng(14)
+    lens, new, page, k = [8000], [7], 16, 40
+    cache, ks, vs = filled(rng, dtype, 2, 64, page, lens, new)
+    chosen = lists(rng, lens, new, 2, page, k)
+    q = 0.1 * torch.from_numpy(rng.standard_normal((7, 4, 64)).astype(np.float32)).to(dtype).cuda()
+    for t in range(7):
+        for h in range(2):
+            others = set(chosen[[u for u in range(7) if u != t], h].ravel().tolist())
+            alone = [p for p in chosen[t, h] if p >= 0 and p not in others]
+            if t % 2 and alone:
+                p = alone[t % len(alone)]
+                cache.kv[0, int(cache.table[0, p]), 1, h, 5, 9] = float("nan")
+                vs[0][p * page + 5, h, 9] = np.nan
+    out = run_pages(cache, q, new, chosen).double().cpu().numpy()
+    for t in range(7):
+        for h in range(2):
+            rows = [r for p in chosen[t, h] if p >= 0 for r in range(p * page, (p + 1) * page)] + list(range(8000, 8001 + t))
+            hit = np.isnan(vs[0][rows, h, 9]).any()
+            got = out[t, 2 * h:2 * h + 2]
+            assert np.isnan(got[:, 9]).all() == hit, (t, h)
+            assert np.isfinite(np.delete(got, 9, 1)).all(), (t, h)
+
+
 @pytest.mark.parametrize("k", [0, 3, 400])
 def test_pages_leave_tokens_of_nobody(k):
     rng = np.random.default_rng(12)
@@ -706,6 +838,7 @@ def test_binding_refusals_of_the_long_context_calls():
         tms.kv_attention_shared(cache, 0, q[:, :2], start, out, plan)
     with pytest.raises(tms.TmsError, match="plan_bytes"):
         tms.kv_share(cache, plan, start, tokens=20000)
+    tms.kv_share(cache, plan, start)
     with pytest.raises(tms.TmsError, match="layer"):
         tms.kv_attention_shared(cache, 1, q, start, out, plan)
     with pytest.raises(TypeError):
@@ -714,7 +847,14 @@ def test_binding_refusals_of_the_long_context_calls():
         tms.PageIndex(cache, torch.zeros((1, 3), device="cuda"))
     with pytest.raises(TypeError):
         tms.PageIndex(cache, index.bounds.float())
+    other, _, _ = filled(rng, BF, 2, 64, 16, [1000, 200], [1, 1])
+    with pytest.raises(ValueError, match="other sizes"):
+        tms.kv_bounds(other, index)
+    with pytest.raises(ValueError, match="other sizes"):
+        tms.kv_share(other, plan, start)
     chosen = torch.zeros((2, 2, 4), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="other sizes"):
+        tms.kv_select(other, 0, q, start, index, chosen)
     with pytest.raises(ValueError, match="chosen"):
         tms.kv_select(cache, 0, q, start, index, chosen[:1])
     with pytest.raises(ValueError, match="chosen"):

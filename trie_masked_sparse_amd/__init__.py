@@ -543,6 +543,7 @@ class PagedCache:
         self.work[:KV_WORK_ZERO].zero_()
         self._index = kv.device.index
         self._streams = set()  # that work on the cache
+        self._like = _sizes(self)
         d.work, d.work_bytes = self.work.data_ptr(), need.value
         self.d = d
         self.ref = C.byref(d)
@@ -696,6 +697,12 @@ def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = T
         _raise_kv_errors(cache, stream, "kv_commit")
 
 
+def _sizes(cache: PagedCache):
+    """What a plan or an index is made for."""
+    return cache.layers, cache.pages, cache.kv_heads, cache.page_tokens, cache.head_dim, cache.seqs, cache.max_pages, cache.dtype, \
+        cache._index
+
+
 class SharedPlan:
     """Work memory of the shared attention over a cache, for calls of up to
     `tokens` new tokens in all: what kv_share finds in the tables, and the parts
@@ -708,7 +715,7 @@ class SharedPlan:
         self.tokens, self.q_heads, self.bytes = tokens, q_heads, need.value
         self.memory = torch.empty(need.value, dtype=torch.uint8, device=cache.kv.device)
         self.memory[:256].zero_()  # not a plan yet
-        self._at, self._streams = self.memory.data_ptr(), set()
+        self._at, self._streams, self._cache, self._planned = self.memory.data_ptr(), set(), _sizes(cache), 0
 
 
 class PageIndex:
@@ -730,11 +737,14 @@ class PageIndex:
         _check(lib().tms_kv_select_bytes(cache.ref, tokens, C.byref(need)), "PageIndex")
         self.bounds, self.tokens, self.bytes = bounds, tokens, need.value
         self.memory = torch.empty(max(need.value, 256), dtype=torch.uint8, device=cache.kv.device)
-        self._at, self._streams = self.memory.data_ptr(), set()
+        self._at, self._streams, self._cache = self.memory.data_ptr(), set(), _sizes(cache)
 
 
 def _with_stream(cache: PagedCache, handle, stream):
-    """_kv_stream, told to the tensors of a plan or an index too."""
+    """_kv_stream, told to the tensors of a plan or an index too, which have to be
+    for caches like this one."""
+    if handle._cache != cache._like:
+        raise ValueError(f"the {type(handle).__name__} was made for a cache of other sizes")
     s = _kv_stream(cache, stream)
     if s not in handle._streams:
         on = torch.cuda.ExternalStream(s, device=cache.kv.device)
@@ -748,11 +758,13 @@ def _with_stream(cache: PagedCache, handle, stream):
 def kv_share(cache: PagedCache, plan: SharedPlan, start, tokens: int | None = None, stream=None):
     """Plan of the shared attention of `tokens` (default: plan.tokens) packed new
     tokens, from the cache's tables (tms_kv_share): after kv_reserve, once for all
-    layers.  Asynchronous."""
-    rc = cache._c[5](cache.ref, _sized(start, _int32, cache.seqs + 1, "start"), plan.tokens if tokens is None else tokens,
-                     plan.q_heads, plan._at, plan.bytes, _with_stream(cache, plan, stream))
+    layers; good until the next kv_fork, kv_reserve or kv_commit.  Asynchronous."""
+    T = plan.tokens if tokens is None else tokens
+    rc = cache._c[5](cache.ref, _sized(start, _int32, cache.seqs + 1, "start"), T, plan.q_heads, plan._at, plan.bytes,
+                     _with_stream(cache, plan, stream))
     if rc:
         _check(rc, "kv_share")
+    plan._planned = T
 
 
 def kv_attention_shared(cache: PagedCache, layer: int, q, start, out, plan: SharedPlan, scale: float | None = None,
@@ -766,6 +778,8 @@ def kv_attention_shared(cache: PagedCache, layer: int, q, start, out, plan: Shar
     at = _sized(start, _int32, cache.seqs + 1, "start")
     if hq != plan.q_heads:
         raise ValueError(f"q has {hq} heads, the plan is for {plan.q_heads}")
+    if T != plan._planned:
+        raise ValueError(f"q has {T} tokens, the plan was made for {plan._planned} (kv_share)")
     if max_new is None:
         max_new = _longest(cache, start, stream, T) if parent is not None and T > _MAX_TREE else T
     rc = cache._c[6](cache.ref, layer, qp, ldq, hq, at, T, max_new, None if parent is None else _sized(parent, _int32, T, "parent"),

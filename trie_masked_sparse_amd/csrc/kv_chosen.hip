@@ -21,7 +21,7 @@ constexpr int kHeld = 2048, kWords = 1024;  // pages of a workgroup, words of it
 // are some, a workgroup takes as many tokens of a sequence as fit a row tile, over
 // all pages that any of them has chosen (`together`, at most `held` for a
 // workgroup: tokens of 3 to 13 drafts of 16 sequences, 24 pages of 32 rows each,
-// 62 -> TODO us).
+// 62 -> 42 us).
 struct Cut {
   int64_t items;
   int splits, together, held, words;  // words of 32 pages in a sequence, at most
