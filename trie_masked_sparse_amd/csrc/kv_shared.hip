@@ -10,6 +10,12 @@
 //
 // Work memory ("plan"), made by plan_kernel from the cache's tables and used
 // for every layer: see Plan.
+//
+// Measured, a layer (us, MI355X; 32 query and 8 key heads of 128, bf16, pages of
+// 64): 64 tokens behind one prompt of 9000 rows and up to 400 of their own 37,
+// where kv_attention takes 264; 256 behind four prompts of 9000 to 24000 that share
+// 2048 rows and up to 1000 of their own 231 (2230).  The plan adds 12 to 36 once
+// for all layers, so four sequences of 150 rows are quicker without (14 and 10).
 #include <algorithm>
 #include <climits>
 
@@ -21,7 +27,7 @@ namespace {
 constexpr int kLevels = 3;      // nodes of a sequence beside its own
 constexpr int kSeqs = 4096;     // sequences of a cache, at most
 constexpr int kPlan = 1024, kPlanWaves = kPlan / kWave;
-constexpr int kSlots = 512;     // workgroups that the chip holds at once
+constexpr int kSlots = 512;     // workgroups that the chip holds at once (work cut for 768 to 2048: 64 answers 34 -> 39 to 44 us)
 constexpr int kTile = 64;       // keys that the plan counts in
 constexpr int kSmall = 16;      // rows of a small node
 constexpr int kMedium = 64;     // of one that takes a row tile half as high, where the others' have 128
@@ -184,7 +190,9 @@ __device__ inline Meet meet(const KvCache& c, int s, Whole whole) {
   return best;
 }
 
-// A wavefront for each sequence.
+// A wavefront for each sequence.  Bound by latency, 0.7 us a read: a sequence's
+// pages, the others' at one place, one other's pages, behind one another.  64
+// sequences 6 to 7 us, 256 of four prompts 8.
 __global__ __launch_bounds__(kWave) void meet_kernel(KvCache c, KvAttention a, Plan plan) {
   a.max_new = INT_MAX;
   const Meet m = meet(c, blockIdx.x, [&](int t) { return shared_pages(c, a, sequence(c, a, t, 1, 1)); });
@@ -268,9 +276,10 @@ __device__ inline Unit unit_of(const KvCache& c, const Node& x, int group, int h
 // without it every branch of the group (sequences that have the next page in
 // common too) would read them.  Behind them every branch is a group.
 //
-// Bound by latency: reads of global memory one after the other, and the code
-// itself, which is fetched for the first time in every call (kEach 4, for all
-// caches, is four times as much: 64 sequences 34 us instead of 27).
+// Bound by latency: reads of global memory one after the other, barriers, and the
+// code itself, which is fetched for the first time in every call (kEach 4, for all
+// caches, is four times as much: 64 sequences 34 us where kEach 1 took 27 then).
+// 4 sequences 13 us, 64 behind one prompt 15, 64 behind four that branch 20, 256 30.
 constexpr int kMeetHere = 16;  // sequences whose meets are found here: a launch less
 template <int kEach>
 __global__ __launch_bounds__(kPlan) void plan_kernel(KvCache c, KvAttention a, Plan plan, int M, int heads) {
@@ -553,6 +562,15 @@ struct Body<1, D, kMany128> {
 };
 
 // A unit of the plan.
+//
+// 64 tokens behind one prompt (shapes as above) 34 us a layer, 102 MB read: a tile
+// takes 1.8 us with two workgroups on a compute unit (128 rows x 64 keys: products,
+// maximum, exponentials, products, one behind the other in each wavefront; the matrix
+// cores are 13 to 22 % busy), and a unit 5 to 7 for its start and end.  256 tokens of
+// four prompts 192 us, 856 MB, 4.5 TB/s.  Tried and slower: equal shares of the cost,
+// a workgroup each, in a loop over their segments (34 -> 52, 64 trees 49 -> 60, 256
+// tokens 196 -> 235 us: registers go to scratch, and every segment starts anew), tiles
+// of 32 keys copied three ahead (32.1 -> 32.4, 46.9 -> 49.0, 198 -> 207).
 template <int DT, int D, int Shape, int Heads>
 __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
   using Small = FewRows<DT, D, 1, Heads>;
@@ -624,7 +642,8 @@ __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ?
 
 // The parts of a token and query head over all its nodes: D / 4 threads to a row,
 // or G times as many, each of which take every G-th chunk, where rows are few and
-// their chunks many.
+// their chunks many.  Bound by the chain plan, node, statistics, values: 64 tokens
+// of 32 heads 8 us for 16 MB, trees of 18 drafts 12 for 31 MB.
 template <int DT, int D, int G>
 __global__ __launch_bounds__(kBlock) void join_nodes_kernel(KvCache c, KvAttention a, Plan plan, int M) {
   constexpr int kRow = D / 4, kRows = kBlock / (kRow * G);
