@@ -868,3 +868,116 @@ def test_binding_refusals_of_the_long_context_calls():
                       torch.zeros((40000, 2, 4), dtype=torch.int32, device="cuda"))
     with pytest.raises(tms.TmsError, match="k must"):
         tms.kv_select(cache, 0, q, start, index, torch.zeros((2, 2, 0), dtype=torch.int32, device="cuda"))
+
+
+def test_shared_plans_older_than_the_tables_or_of_another_cache_are_refused():
+    """A fork may leave every length as it was, so the library cannot see it."""
+    rng = np.random.default_rng(30)
+    b = Branches(rng, BF, 2, 64, 16, [((("p", 40),), 3, 1), ((("p", 40),), 3, 1), ((("q", 40),), 3, 1)])
+    q = queries(rng, b, 4, 64, BF)
+    start, out = dev32(offsets(b.new)), torch.zeros_like(q)
+    plan = tms.SharedPlan(b.cache, 3, 4)
+    zero = dev32([0, 0, 0])
+    for change in (lambda: tms.kv_fork(b.cache, dev32([0, 1, 2])), lambda: tms.kv_reserve(b.cache, zero),
+                   lambda: tms.kv_commit(b.cache, dev32([-1, -1, -1]))):
+        tms.kv_share(b.cache, plan, start)
+        tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+        change()
+        with pytest.raises(ValueError, match="before the cache's last"):
+            tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    other = Branches(rng, BF, 2, 64, 16, [((("p", 40),), 3, 1), ((("p", 40),), 3, 1), ((("q", 40),), 3, 1)])
+    tms.kv_share(other.cache, plan, start)
+    with pytest.raises(ValueError, match="another cache"):
+        tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=1)
+    check_shared(other, q, run_shared(other, q, plan=plan), 0.125, None)
+
+
+def test_pools_past_32_bits_a_later_layer_another_stream_and_strided_queries():
+    """A pool of more than 2^32 elements a layer, pages at its end, bounds past 2^32
+    bytes; queries inside a wider row."""
+    rng = np.random.default_rng(31)
+    hq, hkv, D, page, pages = 16, 8, 128, 8, 272000  # 4.5 G elements a layer of keys and values, four layers
+    kv = torch.empty((4, pages, 2, hkv, page, D), dtype=BF, device="cuda")
+    index_of = torch.empty((4, pages, hkv, 2, D), dtype=BF, device="cuda")
+    assert kv[0].numel() > 2 ** 32 and index_of.numel() * 2 > 2 ** 32
+    lens, new, common = [500, 497], [1, 2], 60
+    table = np.full((2, 63), -1, np.int32)
+    table[0] = [pages - 1 - i if i % 2 else i for i in range(63)]
+    table[1] = table[0]
+    table[1, common:] = [pages - 100, 100, pages - 101]
+    refs = np.zeros(pages, np.int32)
+    for p in table.reshape(-1):
+        refs[p] += 1
+    used = torch.from_numpy(np.unique(table)).long().cuda()
+    kv[3, used] = torch.from_numpy(rng.standard_normal((len(used), 2, hkv, page, D)).astype(np.float32)).to(BF).cuda()
+    cache = tms.PagedCache(kv, dev32(table), dev32(lens), dev32([63, 63]), dev32(refs), dev32([0, 0]))
+    ks, vs = [], []
+    for s in range(2):
+        both = kv[3, torch.from_numpy(table[s]).long().cuda()].double().cpu().numpy().transpose(1, 0, 3, 2, 4).reshape(2, -1, hkv, D)
+        ks.append(both[0, :lens[s] + new[s]])
+        vs.append(both[1, :lens[s] + new[s]])
+    wide = torch.from_numpy(rng.standard_normal((3, hq + 9, D)).astype(np.float32)).to(BF).cuda()
+    q, start = wide[:, 5:5 + hq], dev32([0, 1, 3])
+    index, plan = tms.PageIndex(cache, index_of, tokens=3), tms.SharedPlan(cache, 3, hq)
+    chosen = torch.full((3, hkv, 6), 77, dtype=torch.int32, device="cuda")
+    shared, paged = torch.zeros((2, 3, hq, D), dtype=BF, device="cuda").unbind(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tms.kv_bounds(cache, index, stream=side)
+    tms.kv_share(cache, plan, start, stream=side)
+    tms.kv_attention_shared(cache, 3, q, start, shared, plan, max_new=2, stream=side)
+    tms.kv_select(cache, 3, q, start, index, chosen, max_new=2, stream=side)
+    tms.kv_attention_pages(cache, 3, q, start, chosen, paged, max_new=2, stream=side)
+    side.synchronize()
+    x, lists_of, at = q.double().cpu().numpy(), chosen.cpu().numpy(), offsets(new)
+    for s in range(2):
+        whole = lens[s] // page
+        bounds = np.stack([ks[s][:whole * page].reshape(whole, page, hkv, D).min(1),
+                           ks[s][:whole * page].reshape(whole, page, hkv, D).max(1)], 2)  # [pages][heads][2][D]
+        assert (index.bounds[3, torch.from_numpy(table[s, :whole]).long().cuda()].double().cpu().numpy() == bounds).all()
+        for t in range(at[s], at[s + 1]):
+            assert (lists_of[t] == choice(x[t], bounds, 6, 1.0, 1, 1)).all(), (s, t)
+        want, bound = attention(x[at[s]:at[s + 1]], ks[s], vs[s], lens[s], D ** -0.5, None, True)
+        assert (np.abs(shared[at[s]:at[s + 1]].double().cpu().numpy() - want) <= bound).all(), s
+    check_pages(cache, q, paged, ks, vs, lens, new, lists_of, D ** -0.5, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(4096, 1, 64), (256, 256, 64)], **ids)
+def test_the_most_heads(dtype, heads):
+    hq, hkv, D = heads
+    print(f"{dtype} {heads}", flush=True)
+    rng = np.random.default_rng(hq)
+    lens, new = [300, 77], [1, 1]
+    cache, ks, vs = filled(rng, dtype, hkv, D, 16, lens, new)
+    q = torch.from_numpy(rng.standard_normal((2, hq, D)).astype(np.float32)).to(dtype).cuda()
+    index, start = tms.PageIndex(cache, tokens=2), dev32([0, 1, 2])
+    tms.kv_bounds(cache, index)
+    chosen = run_select(cache, index, q, new, 6)
+    check_select(cache, index, q, lens, new, 6, chosen)
+    check_pages(cache, q, run_pages(cache, q, new, chosen), ks, vs, lens, new, chosen, 0.125, None)
+    plan, out = tms.SharedPlan(cache, 2, hq), torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    tms.kv_share(cache, plan, start)
+    tms.kv_attention_shared(cache, 0, q, start, out, plan, max_new=1)
+    x, out = q.double().cpu().numpy(), out.double().cpu().numpy()
+    for s in range(2):
+        want, bound = attention(x[s:s + 1], ks[s], vs[s], lens[s], 0.125, None, dtype == BF)
+        assert (np.abs(out[s:s + 1] - want) <= bound).all(), s
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_the_most_sequences(dtype):
+    """4096, of two prompts, most of them without a new token."""
+    rng = np.random.default_rng(33)
+    new = [0] * 4096
+    for s in rng.permutation(4096)[:60]:
+        new[s] = int(rng.integers(1, 4))
+    new[0] = new[4095] = 1
+    b = Branches(rng, dtype, 1, 64, 8, [(((f"p{s % 2}", 40),), s % 11, new[s]) for s in range(4096)])
+    q = queries(rng, b, 2, 64, dtype)
+    check_shared(b, q, run_shared(b, q), 0.125, None)
+    index = tms.PageIndex(b.cache, tokens=sum(new))
+    tms.kv_bounds(b.cache, index)
+    chosen = run_select(b.cache, index, q, new, 7)
+    check_select(b.cache, index, q, b.lens, new, 7, chosen)
+    check_pages(b.cache, q, run_pages(b.cache, q, new, chosen), b.ks[0], b.vs[0], b.lens, new, chosen, 0.125, None)

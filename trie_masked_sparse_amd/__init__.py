@@ -22,6 +22,7 @@ runtime (torch ships its own libamdhip64 with the same soname).
 from __future__ import annotations
 
 import ctypes as C
+import itertools
 import os
 
 import numpy as np
@@ -504,6 +505,9 @@ def _token_rows(t, dtype, dim: int, name: str):
     return t.data_ptr(), T, heads, row if T > 1 else heads * dim  # one token: no next row
 
 
+_changes = itertools.count(1)  # of any cache's tables
+
+
 class PagedCache:
     """Keys and values of a batch of sequences in shared pages: the caller's
     tensors, kept alive and changed in place by the kv_* calls, and the work
@@ -544,6 +548,7 @@ class PagedCache:
         self._index = kv.device.index
         self._streams = set()  # that work on the cache
         self._like = _sizes(self)
+        self._changed = next(_changes)  # by the last call that changed the tables
         d.work, d.work_bytes = self.work.data_ptr(), need.value
         self.d = d
         self.ref = C.byref(d)
@@ -596,6 +601,7 @@ def kv_fork(cache: PagedCache, src, stream=None, check: bool = True):
     -1: emptied).  check: synchronise and raise on device errors."""
     if check:
         _refuse_check_while_recording(check, stream, "kv_fork")
+    cache._changed = next(_changes)
     rc = cache._c[0](cache.ref, _sized(src, _int32, cache.seqs, "src"), _kv_stream(cache, stream))
     if rc:
         _check(rc, "kv_fork")
@@ -607,6 +613,7 @@ def kv_reserve(cache: PagedCache, n_new, stream=None, check: bool = True):
     """Pages for n_new[s] more rows of every sequence (int32 [seqs])."""
     if check:
         _refuse_check_while_recording(check, stream, "kv_reserve")
+    cache._changed = next(_changes)
     rc = cache._c[1](cache.ref, _sized(n_new, _int32, cache.seqs, "n_new"), _kv_stream(cache, stream))
     if rc:
         _check(rc, "kv_reserve")
@@ -690,6 +697,7 @@ def kv_commit(cache: PagedCache, n_keep, keep=None, stream=None, check: bool = T
         if keep.dim() != 2 or keep.shape[0] != cache.seqs:
             raise ValueError("keep must be [seqs][stride]")
         stride, at = keep.shape[1], _sized(keep, _int32, 1, "keep")
+    cache._changed = next(_changes)
     rc = cache._c[4](cache.ref, _sized(n_keep, _int32, cache.seqs, "n_keep"), at, stride, _kv_stream(cache, stream))
     if rc:
         _check(rc, "kv_commit")
@@ -716,6 +724,7 @@ class SharedPlan:
         self.memory = torch.empty(need.value, dtype=torch.uint8, device=cache.kv.device)
         self.memory[:256].zero_()  # not a plan yet
         self._at, self._streams, self._cache, self._planned = self.memory.data_ptr(), set(), _sizes(cache), 0
+        self._tables = cache._changed  # that it was made from
 
 
 class PageIndex:
@@ -758,21 +767,23 @@ def _with_stream(cache: PagedCache, handle, stream):
 def kv_share(cache: PagedCache, plan: SharedPlan, start, tokens: int | None = None, stream=None):
     """Plan of the shared attention of `tokens` (default: plan.tokens) packed new
     tokens, from the cache's tables (tms_kv_share): after kv_reserve, once for all
-    layers; good until the next kv_fork, kv_reserve or kv_commit.  Asynchronous."""
+    layers; good until the next kv_fork, kv_reserve or kv_commit, from which on
+    kv_attention_shared refuses it.  Asynchronous."""
     T = plan.tokens if tokens is None else tokens
     rc = cache._c[5](cache.ref, _sized(start, _int32, cache.seqs + 1, "start"), T, plan.q_heads, plan._at, plan.bytes,
                      _with_stream(cache, plan, stream))
     if rc:
         _check(rc, "kv_share")
-    plan._planned = T
+    plan._planned, plan._tables = T, cache._changed
 
 
 def kv_attention_shared(cache: PagedCache, layer: int, q, start, out, plan: SharedPlan, scale: float | None = None,
                         parent=None, max_new: int | None = None, stream=None):
     """kv_attention where sequences share pages, each read once
     (tms_kv_attention_shared): the same arguments, and the plan that kv_share has
-    made for these tokens.  Asynchronous, but for trees of more than 1024 tokens in
-    all without max_new."""
+    made for these tokens.  Give max_new: without it (T) a batch of single tokens
+    passes for one of long prompts, which share nothing.  Asynchronous, but for
+    trees of more than 1024 tokens in all without max_new."""
     dt, D = cache.dtype, cache.head_dim
     qp, T, hq, ldq = _token_rows(q, dt, D, "q")
     at = _sized(start, _int32, cache.seqs + 1, "start")
@@ -780,6 +791,8 @@ def kv_attention_shared(cache: PagedCache, layer: int, q, start, out, plan: Shar
         raise ValueError(f"q has {hq} heads, the plan is for {plan.q_heads}")
     if T != plan._planned:
         raise ValueError(f"q has {T} tokens, the plan was made for {plan._planned} (kv_share)")
+    if plan._tables != cache._changed:
+        raise ValueError("the plan was made before the cache's last kv_fork, kv_reserve or kv_commit, or for another cache (kv_share)")
     if max_new is None:
         max_new = _longest(cache, start, stream, T) if parent is not None and T > _MAX_TREE else T
     rc = cache._c[6](cache.ref, layer, qp, ldq, hq, at, T, max_new, None if parent is None else _sized(parent, _int32, T, "parent"),
