@@ -501,8 +501,9 @@ tms_status tms_kv_attention(const tms_kv* c, int32_t layer, const void* q, int64
  * tokens.  tms_kv_share finds such runs of pages in the tables and deals the
  * work; the plan is then good for every layer, until the next tms_kv_fork,
  * tms_kv_reserve or tms_kv_commit.  Call it after reserving, with the start and
- * T (at least 1) of the attention calls.  Up to three runs of a sequence are
- * shared, those that save most reads first.  plan: dev, 256-byte aligned,
+ * T (at least 1) of the attention calls.  Of a sequence the first
+ * three runs whose sharing saves more than it costs are shared (of the first 16
+ * places where tables part).  plan: dev, 256-byte aligned,
  * tms_kv_share_bytes (which needs the cache's sizes and dtype only) for this T
  * and q_heads; it holds the plan and the parts of the rows that are joined, so
  * calls that use one plan on several streams are ordered by the caller.  No

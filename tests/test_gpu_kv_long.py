@@ -981,3 +981,28 @@ def test_the_most_sequences(dtype):
     chosen = run_select(b.cache, index, q, new, 7)
     check_select(b.cache, index, q, b.lens, new, 7, chosen)
     check_pages(b.cache, q, run_pages(b.cache, q, new, chosen), b.ks[0], b.vs[0], b.lens, new, chosen, 0.125, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_pages_longest_lists_of_the_widest_heads(dtype):
+    """Lists and unions that take the most LDS, beside tiles that do: 8192 pages of a
+    workgroup, and 2048 of several tokens."""
+    rng = np.random.default_rng(34)
+    print(f"{dtype} 8192 pages a list", flush=True)
+    new, lens, page = [512], [8 * 8192 + 3], 8
+    cache, ks, vs = filled(rng, dtype, 1, 256, page, lens, new)
+    q = torch.from_numpy(rng.standard_normal((512, 16, 256)).astype(np.float32)).to(dtype).cuda()
+    chosen = np.tile(np.arange(8192, dtype=np.int32), (512, 1, 1))
+    out = run_pages(cache, q, new, chosen)
+    for t in (0, 1, 300, 511):
+        x = q[t:t + 1].double().cpu().numpy()
+        k, v = ks[0][:lens[0] + t + 1], vs[0][:lens[0] + t + 1]
+        want, bound = (attention_fine(x, k, v, len(k) - 1, 1 / 16, None) if dtype == BF else
+                       attention(x, k, v, len(k) - 1, 1 / 16, None, False))
+        assert (np.abs(out[t:t + 1].double().cpu().numpy() - want) <= bound).all(), t
+    print(f"{dtype} 2048 pages of several tokens", flush=True)
+    new, lens = [300, 300], [8 * 2010 + 1, 900]
+    cache, ks, vs = filled(rng, dtype, 8, 256, page, lens, new)
+    q = torch.from_numpy(rng.standard_normal((600, 8, 256)).astype(np.float32)).to(dtype).cuda()
+    chosen = lists(rng, lens, new, 8, page, 150)
+    check_pages(cache, q, run_pages(cache, q, new, chosen), ks, vs, lens, new, chosen, 1 / 16, None)
