@@ -1006,3 +1006,57 @@ def test_pages_longest_lists_of_the_widest_heads(dtype):
     q = torch.from_numpy(rng.standard_normal((600, 8, 256)).astype(np.float32)).to(dtype).cuda()
     chosen = lists(rng, lens, new, 8, page, 150)
     check_pages(cache, q, run_pages(cache, q, new, chosen), ks, vs, lens, new, chosen, 1 / 16, None)
+
+
+# ------------------------------------------------------------------ one prompt
+
+class OnePrompt:
+    """Sequences behind one prompt of whole pages, each with rows of its own and one
+    new token, without a 64-bit copy of the prompt for each: `want` puts the rows
+    of a sequence together where they are compared."""
+
+    def __init__(self, rng, dtype, kv_heads, dim, page, prompt, own, layers=1):
+        self.rows, self.page, seqs = prompt * page, page, len(own)
+        self.lens = [self.rows + x for x in own]
+        mine = [-(-(x + 1) // page) for x in own]
+        total = prompt + sum(mine) + 1
+        kv = torch.from_numpy(rng.standard_normal((layers, total, 2, kv_heads, page, dim)).astype(np.float32)).to(dtype)
+        order = rng.permutation(total)
+        table, refs, at = np.full((seqs, prompt + max(mine)), -1, np.int32), np.zeros(total, np.int32), prompt
+        for s in range(seqs):
+            table[s, :prompt] = order[:prompt]
+            table[s, prompt:prompt + mine[s]] = order[at:at + mine[s]]
+            at += mine[s]
+            np.add.at(refs, table[s, :prompt + mine[s]], 1)
+        self.kv, self.table = kv, table
+        self.cache = tms.PagedCache(kv.cuda(), dev32(table), dev32(self.lens), dev32([prompt + m for m in mine]), dev32(refs),
+                                    dev32([0] * seqs))
+        self.new = [1] * seqs
+
+    def check(self, q, out, of, layer=0, scale=None, fine=False):
+        bf16, scale = q.dtype == BF, q.shape[2] ** -0.5 if scale is None else scale
+        for s in of:
+            n = self.lens[s] + 1
+            both = self.kv[layer, self.table[s, :-(-n // self.page)].tolist()].double().numpy().transpose(1, 0, 3, 2, 4)
+            both = both.reshape(2, -1, both.shape[3], both.shape[4])[:, :n]
+            x = q[s:s + 1].double().cpu().numpy()
+            want, bound = attention_fine(x, both[0], both[1], n - 1, scale, None) if bf16 and fine else \
+                attention(x, both[0], both[1], n - 1, scale, None, bf16)
+            err = np.abs(out[s:s + 1].double().cpu().numpy() - want)
+            assert (err <= bound).all(), (s, n, float(np.nanmax(err / bound)), int((~(err <= bound)).sum()))
+
+
+@pytest.mark.parametrize("dtype,heads,seqs,prompt", [
+    (BF, (32, 32, 64), 16, 282), (F, (32, 32, 64), 16, 282), (BF, (32, 32, 128), 16, 288), (F, (32, 32, 256), 16, 192),
+    (BF, (128, 64, 64), 8, 282), (BF, (40, 40, 64), 16, 700)], ids=lambda x: str(x).replace("torch.", ""))
+def test_shared_plans_of_many_key_heads_and_few_rows_fit(dtype, heads, seqs, prompt):
+    """Units of two key heads whose row tiles have 16 rows: the parts of a long prompt's
+    chunks take twice the rows of one head's."""
+    hq, hkv, D = heads
+    print(f"{dtype} {heads} {seqs} sequences behind {prompt} pages", flush=True)
+    rng = np.random.default_rng(prompt)
+    b = OnePrompt(rng, dtype, hkv, D, 32, prompt, [20 + s % 3 for s in range(seqs)])
+    q = queries(rng, b, hq, D, dtype)
+    out = run_shared(b, q)
+    assert torch.isfinite(out).all()
+    b.check(q, out, (0, seqs // 2, seqs - 1))

@@ -13,6 +13,7 @@ constexpr int kLevels = 3;      // nodes of a sequence beside its own
 constexpr int kSlots = 512;     // workgroups that the chip holds at once (work cut for 768 to 2048: 64 answers 34 -> 39 to 44 us)
 constexpr int kTile = 64;       // keys that the plan counts in
 constexpr int kSmall = 16;      // rows of a small node
+constexpr int kMostHeads = 2;   // key heads of a unit of one, at most
 constexpr int kMedium = 64;     // of one that takes a row tile half as high, where the others' have 128
 
 // Key tiles of a chunk, at least.
@@ -75,11 +76,13 @@ inline Layout layout(const KvCache& c, int32_t T, int32_t q_heads, int M) {
   const int64_t group = q_heads / c.kv_heads, n = std::min<int64_t>(c.seqs, T);
   y.most_nodes = static_cast<int32_t>(2 * n);  // the sequences' own, and places where the trie branches
   // A node's row tiles and heads, and what cuts add: a chunk costs a slot, less
-  // one of its tiles, of which it has kLeastTiles or more.
+  // one of its tiles, of which it has kLeastTiles or more.  A unit has the rows of
+  // a row tile for each of its heads: 32 for the two of a small one, whatever M (and
+  // whether there are two, so that more tokens never need less).
   constexpr int kCuts = kSlots * (kLeastTiles + 1) / kLeastTiles;
   const int64_t tiles = (kLevels + 1) * (int64_t(T) * group / std::max(M, kSmall)) + y.most_nodes;
   y.most_units = tiles * c.kv_heads + kCuts;
-  y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + kCuts * int64_t(M);
+  y.most_rows = (kLevels + 1) * int64_t(T) * q_heads + kCuts * std::max<int64_t>(M, kMostHeads * kSmall);
   y.seqs = up(sizeof(Head));
   y.meets = up(y.seqs + c.seqs * int64_t(sizeof(PlanSeq)));
   y.nodes = up(y.meets + c.seqs * int64_t(sizeof(Meet)));
