@@ -1,6 +1,7 @@
 // The arithmetic of the shared attention's plan (trie_masked_sparse_amd/csrc/
 // kv_plan.h) over batches of every kind, without a GPU: the units and part rows of
-// a batch fit the memory that its layout has for them.  Prints "ok <batches>".
+// a batch fit the memory that its layout has for them, and a unit is worked on by
+// as many key heads as it was cut for.  Prints "ok <batches>".
 #include <cstdio>
 #include <vector>
 
@@ -37,7 +38,14 @@ Batch batch(int dtype, int dim, int kv_heads, int group, int seqs, int n, const 
 }
 
 bool fits(const Batch& b) {
-  const int M = rows_of(shape(b.c, b.T, b.q_heads)), heads = small_heads(b.c, b.T), group = b.q_heads / b.c.kv_heads;
+  const int M = rows_of(shape(b.c, b.T, b.q_heads)), heads = small_heads(b.c, b.T, b.q_heads), group = b.q_heads / b.c.kv_heads;
+  for (const Node& x : b.nodes) {
+    const Size z = size_of(x, group, b.c.kv_heads, M, heads);
+    if (z.heads * unit_heads(shape(b.c, b.T, b.q_heads), z.rows, heads) == b.c.kv_heads) continue;
+    std::printf("dtype %d heads %d/%d of %d, %d sequences, %d tokens, a node of %d: %d units of %d key heads\n", b.c.dtype, b.q_heads,
+                b.c.kv_heads, b.c.head_dim, b.c.seqs, b.T, x.tokens, z.heads, unit_heads(shape(b.c, b.T, b.q_heads), z.rows, heads));
+    return false;
+  }
   const Layout y = layout(b.c, b.T, b.q_heads, M);
   int64_t work = 0, units = 0, rows = 0;
   for (const Node& x : b.nodes) work += cost_of(size_of(x, group, b.c.kv_heads, M, heads));

@@ -1060,3 +1060,18 @@ def test_shared_plans_of_many_key_heads_and_few_rows_fit(dtype, heads, seqs, pro
     out = run_shared(b, q)
     assert torch.isfinite(out).all()
     b.check(q, out, (0, seqs // 2, seqs - 1))
+
+
+@pytest.mark.parametrize("heads,seqs,prompt,own", [((8, 2, 256), 256, 40, 3), ((32, 8, 256), 64, 30, 40), ((2, 2, 256), 300, 25, 0)])
+def test_shared_wide_heads_in_fp32_of_many_sequences(heads, seqs, prompt, own):
+    """Row tiles of 16 for nodes of any size: the shared run is worked on a key head a
+    unit, however many units there are."""
+    hq, hkv, D = heads
+    print(f"{heads} {seqs} sequences", flush=True)
+    rng = np.random.default_rng(seqs)
+    b = OnePrompt(rng, F, hkv, D, 16, prompt, [own + s % 2 for s in range(seqs)], layers=2)
+    q = queries(rng, b, hq, D, F)
+    out = run_shared(b, q, layer=1)
+    assert torch.equal(out, run_shared(b, q, layer=1))
+    b.check(q, out, range(0, seqs, 5), layer=1)
+    assert torch.isfinite(out).all()

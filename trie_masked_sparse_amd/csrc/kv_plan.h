@@ -129,10 +129,18 @@ inline int shape(const KvCache& c, int32_t T, int32_t q_heads) {
   return rows <= 32 && c.head_dim == 64 ? kFew32 : rows <= 64 ? kMany64 : kMany128;
 }
 
+// Whether units of row tiles of M rows are worked on as those of small nodes are,
+// and by how many key heads at once.
+constexpr __host__ __device__ bool few_rows(int shape, int M) { return shape == kFew16 || M == kSmall; }
+inline int unit_heads(int shape, int M, int heads) { return few_rows(shape, M) ? heads : 1; }
+
 // Key heads of a unit of a small node: two where there are units enough (64 answers
-// 34 -> 31 us; four where they are four times as many 204 -> 214).
-inline int small_heads(const KvCache& c, int32_t T) {
-  return c.kv_heads % 2 == 0 && int64_t(std::min(c.seqs, T)) * c.kv_heads >= kSlots ? 2 : 1;
+// 34 -> 31 us; four where they are four times as many 204 -> 214), and where the
+// nodes that are not small have taller row tiles (few_rows tells them apart by
+// these) or there are none.
+inline int small_heads(const KvCache& c, int32_t T, int32_t q_heads) {
+  const bool alike = shape(c, T, q_heads) == kFew16 && int64_t(T) * (q_heads / c.kv_heads) > kSmall;
+  return !alike && c.kv_heads % 2 == 0 && int64_t(std::min(c.seqs, T)) * c.kv_heads >= kSlots ? kMostHeads : 1;
 }
 
 }  // namespace

@@ -518,7 +518,7 @@ __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ?
     t.kt1 = min(x.tile1 * (kTile / keys), (x.keys + keys - 1) / keys);
   };
   auto page_at = [&](int key) { return max(0, min(table[key >> c.page_shift], c.pages - 1)); };
-  if (Shape == kFew16 || x.M == kSmall) {
+  if (few_rows(Shape, x.M)) {
     tiles(Small::KW);
     Small::run(c, a, lds.small, t, page_at, query, token, emit);
   } else if constexpr (Shape == kFew32) {
@@ -591,8 +591,8 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const Plan& plan, hipS
   constexpr int kRows = kBlock * 4 / D;  // of a workgroup of the join
   constexpr int64_t kFew = 2048;
   if (blocks >= (int64_t(1) << 32) / kBlock || rows >= (int64_t(1) << 32) / kBlock) return hipErrorInvalidValue;
-  const int heads = small_heads(c, a.T);
-  if (heads == 2) nodes_kernel<DT, D, Shape, 2><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
+  const int heads = small_heads(c, a.T, a.q_heads);
+  if (heads == kMostHeads) nodes_kernel<DT, D, Shape, kMostHeads><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   else nodes_kernel<DT, D, Shape, 1><<<unsigned(blocks), kBlock, 0, s>>>(c, a, plan);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (rows <= kFew) join_nodes_kernel<DT, D, 4><<<unsigned((4 * rows + kRows - 1) / kRows), kBlock, 0, s>>>(c, a, plan, rows_of(Shape));
@@ -628,8 +628,8 @@ hipError_t launch_kv_share(const KvCache& c, const KvShared& sh, hipStream_t s) 
     meet_kernel<<<c.seqs, kWave, 0, s>>>(c, sh.a, plan);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (c.seqs <= kPlan) plan_kernel<1><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T));
-  else plan_kernel<kSeqs / kPlan><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T));
+  if (c.seqs <= kPlan) plan_kernel<1><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T, sh.a.q_heads));
+  else plan_kernel<kSeqs / kPlan><<<1, kPlan, 0, s>>>(c, sh.a, plan, rows_of(x), small_heads(c, sh.a.T, sh.a.q_heads));
   return hipGetLastError();
 }
 
