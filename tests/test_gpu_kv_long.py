@@ -1075,3 +1075,40 @@ def test_shared_wide_heads_in_fp32_of_many_sequences(heads, seqs, prompt, own):
     assert torch.equal(out, run_shared(b, q, layer=1))
     b.check(q, out, range(0, seqs, 5), layer=1)
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads,new", [((4, 2, 64), [1, 1, 1]), ((40, 2, 128), [2, 1, 3]), ((8, 1, 256), [1, 0, 1])], ids=["one", "wide", "256"])
+@pytest.mark.parametrize("k", [4, 37, 200])
+def test_pages_wrong_lists_of_tokens_that_are_alone_in_a_workgroup(dtype, heads, new, k):
+    """Entries that are out of order, equal, out of range or behind a negative one, in
+    every part of a list: NaN for their token and head, and nothing changes for the
+    others."""
+    hq, hkv, D = heads
+    print(f"{dtype} {heads} {k}", flush=True)
+    rng = np.random.default_rng(k)
+    lens, page = [16 * 300 + 5, 700, 16 * 260], 16
+    cache, ks, vs = filled(rng, dtype, hkv, D, page, lens, new)
+    q = torch.from_numpy(rng.standard_normal((sum(new), hq, D)).astype(np.float32)).to(dtype).cuda()
+    good = lists(rng, lens, new, hkv, page, k)
+    t, h = sum(new) - 1, hkv - 1  # of the last sequence, which has 260 whole pages
+    good[t, h] = np.arange(k)
+    right = run_pages(cache, q, new, good)
+    check_pages(cache, q, right, ks, vs, lens, new, good, D ** -0.5, None)
+    mine = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    mine[t, h * hq // hkv:(h + 1) * hq // hkv] = True
+    for at in sorted({1, 2, k // 3, k // 2, k - 2, k - 1} - {0}):
+        for entry in (at - 1, max(at - 2, 0), 259 if at < k - 1 else 260, 300, 2 ** 31 - 1, -1, -2 ** 31):
+            wrong = good.copy()
+            wrong[t, h, at] = entry
+            if entry < 0 and at == k - 1:  # the list ends there
+                continue
+            out = run_pages(cache, q, new, wrong)
+            assert torch.isnan(out[mine]).all(), (at, entry)
+            assert torch.equal(out[~mine], right[~mine]), (at, entry)
+    for first in (260, -1, 2 ** 31 - 1):  # the first entry
+        wrong = good.copy()
+        wrong[t, h, 0] = first
+        out = run_pages(cache, q, new, wrong)
+        assert torch.isnan(out[mine]).all() and torch.equal(out[~mine], right[~mine]), first
+    assert (cache.work[:tms.KV_WORK_ZERO] == 0).all()

@@ -152,7 +152,10 @@ __global__ __launch_bounds__(kBlock, D == 256 ? 1 : 2) void chosen_kernel(KvCach
     int n = 0;  // entries are a run from the first on
     for (int e = e0 + tid; e < e1; e += kBlock) {
       const int v = entry(0, e);
-      if (v >= 0) listed.page[e - e0] = max(0, min(table[v], c.pages - 1)), n = max(n, e - e0 + 1);
+      // (of a refused entry any page: a good one may follow, and the keys up to it are
+      // read, though the outputs are NaN)
+      listed.page[e - e0] = v >= 0 ? max(0, min(table[v], c.pages - 1)) : 0;
+      if (v >= 0) n = max(n, e - e0 + 1);
     }
     if (n) atomicMax(&count, n);
     __syncthreads();
