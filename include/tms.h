@@ -514,10 +514,9 @@ tms_status tms_kv_share(const tms_kv* c, const int32_t* start, int32_t T, int32_
 /* Arguments, errors and what unseen rows may hold as tms_kv_attention, which it
  * calls where max_new * q_heads / kv_heads is above 128 (64 with heads of 256):
  * many rows of one sequence share the reads as it is, and the plan is not used
- * then.  In bf16 the weights of the second product keep 16 bits in runs of up to
- * 64 query rows of a key head, and are rounded to bf16 above.  NaN also for
- * sequences whose length, start or status is not the plan's, and for all tokens
- * where the plan is of another T or q_heads or was not made.  A few short
+ * then.  Else, in bf16, the weights of the second product keep 16 bits.  NaN also
+ * for sequences whose length, start or status is not the plan's, and for all
+ * tokens where the plan is of another T or q_heads or was not made.  A few short
  * sequences are quicker with tms_kv_attention. */
 tms_status tms_kv_attention_shared(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
                                    const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent, float scale,

@@ -1112,3 +1112,22 @@ def test_pages_wrong_lists_of_tokens_that_are_alone_in_a_workgroup(dtype, heads,
         out = run_pages(cache, q, new, wrong)
         assert torch.isnan(out[mine]).all() and torch.equal(out[~mine], right[~mine]), first
     assert (cache.work[:tms.KV_WORK_ZERO] == 0).all()
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 4, 128), (8, 2, 256)], **ids)
+@pytest.mark.parametrize("seqs,kind", [(64, "token"), (24, "tree")])
+def test_shared_weights_keep_16_bits_however_many_rows_share_a_run(heads, seqs, kind):
+    """Runs of more than 64 query rows of a key head, whose weights are those of single
+    tokens: what a token gets does not depend on how many others share its prompt.
+    A peaked softmax: weights of 8 bits are off by 1.1 to 3.7 of the bound."""
+    hq, hkv, D = heads
+    rng = np.random.default_rng(seqs + D)
+    b = Branches(rng, BF, hkv, D, 16, [((("p", 20),), s % 7, 1 if kind == "token" else 5 + s % 3) for s in range(seqs)])
+    q = 2 * queries(rng, b, hq, D, BF)
+    parents = [tree(rng, n) for n in b.new] if kind == "tree" else None
+    out, at = run_shared(b, q, parents).double().cpu().numpy(), offsets(b.new)
+    x = q.double().cpu().numpy()
+    for s in range(seqs):
+        want, bound = attention_fine(x[at[s]:at[s + 1]], b.ks[0][s], b.vs[0][s], b.lens[s], D ** -0.5, None if parents is None else parents[s])
+        err = np.abs(out[at[s]:at[s + 1]] - want)
+        assert (err <= bound).all(), (s, float((err / bound).max()), int((err > bound).sum()))

@@ -9,16 +9,19 @@ namespace {
 
 // RW x KS wavefronts: each holds 32 rows and takes 1 / KS of the keys of every
 // tile of 64; K and V tiles are copied from the cache straight into LDS, one tile
-// ahead of the products.  Where the keys are split (KS 2) the rows are few and
-// memory bounds the loop, so the weights go into the second product as two bf16
-// parts (16 bits); else as one.  A tile of 64 keys takes a wavefront 1.8 us where
-// two workgroups of 128 rows share a compute unit: the chain from scores to weights,
-// not the copies (tiles of 32 keys three ahead took no less).  Heads of 256, 64
-// answers over 9000 rows: 128 rows of a workgroup 44 us, 64 rows 58.
+// ahead of the products.  The weights go into the second product as two bf16 parts
+// (16 bits), so that what a token gets does not depend on how many others share its
+// pages: of 128 rows, one part was quicker (64 answers behind one prompt 103.4 ->
+// 105.2 us for plan and two layers, trees of 5 to 31 drafts 138 -> 150, 256 answers
+// 238 -> 245), and off by up to 2^-8 of each weight.  Their sum is taken from the
+// fp32 weights (by products with ones, of both parts: 106.2, 153, 248).  A tile of 64
+// keys took a wavefront 1.8 us, weights of one part, where two workgroups of 128 rows
+// share a compute unit: the chain from scores to weights, not the copies (tiles of 32
+// keys three ahead took no less).  Heads of 256, 64 answers over 9000 rows: 128 rows
+// of a workgroup 44 us, 64 rows 58.
 template <int D, int RW, int KS>
 struct ManyRows {
   static constexpr int W = RW * KS, M = 32 * RW, CH = D / 8, KK = D / 16, DB = D / 32, Threads = W * kWave;
-  static constexpr bool Fine = KS == 2;
   static constexpr int KT = 64, TileWords = KT * CH;       // keys of a tile, its 16-byte words
   static constexpr int NB = KT / 32 / KS;                  // 32-key blocks of a tile for each wavefront
   static constexpr int Bufs = 2;
@@ -66,11 +69,8 @@ struct ManyRows {
         for (int i = 0; i < KK; ++i) qr[i] = p[2 * i + hi2];
       }
       const f32x16 zero = {};
-      f32x16 o[DB], sc[NB], total_w;  // total_w: a row's sum of weights, in every register
-      float mx = -INFINITY;
-      const bf16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
-#pragma unroll
-      for (int e = 0; e < 16; ++e) total_w[e] = 0.f;
+      f32x16 o[DB], sc[NB];
+      float mx = -INFINITY, sum = 0.f;  // sum: of this lane's weights
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -185,7 +185,7 @@ struct ManyRows {
         if (__any(top > mx + 8.f)) {
           const float next = fmaxf(mx, top), turn = next == -INFINITY ? 1.f : exp2_fast(mx - next);
           mx = next;
-          total_w *= turn;
+          sum *= turn;
 #pragma unroll
           for (int d = 0; d < DB; ++d) o[d] *= turn;
         }
@@ -197,9 +197,11 @@ struct ManyRows {
         for (int j = 0; j < 2 * NB; ++j) {
           float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = exp2_fast(fmaf(sc[j / 2][j % 2 * 8 + e], scale, -at));
-          if constexpr (Fine) split_bf16(w, &pw[j], &pl[j]);
-          else pw[j] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+          for (int e = 0; e < 8; ++e) {
+            w[e] = exp2_fast(fmaf(sc[j / 2][j % 2 * 8 + e], scale, -at));
+            sum += w[e];
+          }
+          split_bf16(w, &pw[j], &pl[j]);
 #pragma unroll
           for (int i = j * P / NB; i < (j + 1) * P / NB; ++i) ask(kt, i);
           __builtin_amdgcn_sched_barrier(0);
@@ -239,11 +241,7 @@ struct ManyRows {
           __builtin_amdgcn_sched_barrier(0);
           if (i < PV) {
             const int j = i / DB, d = i % DB;
-            if constexpr (Fine) {
-              if (d == 0) total_w = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, __builtin_bit_cast(bf16x8, pl[j]), total_w, 0, 0, 0);
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % Ahead], __builtin_bit_cast(bf16x8, pl[j]), o[d], 0, 0, 0);
-            }
-            if (d == 0) total_w = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, __builtin_bit_cast(bf16x8, pw[j]), total_w, 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % Ahead], __builtin_bit_cast(bf16x8, pl[j]), o[d], 0, 0, 0);
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % Ahead], __builtin_bit_cast(bf16x8, pw[j]), o[d], 0, 0, 0);
           } else {
             const int j = (i - PV) / NB, k = (i - PV) % NB;
@@ -262,7 +260,10 @@ struct ManyRows {
         const float z = zero_or_nan(o);
         if (__syncthreads_or(z != z)) continue;
       }
-      float sum = total_w[0];
+      {
+        auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+        sum = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+      }
       if constexpr (KS == 2) {  // the two halves of the keys joined
         static_assert(KS == 1 || RW * DB * 4 * kWave <= 2 * Bufs * TileWords, "the outputs of one half fit the tiles");
         f32x4* buf = reinterpret_cast<f32x4*>(lds.tiles);
