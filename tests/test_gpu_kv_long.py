@@ -1131,3 +1131,28 @@ def test_shared_weights_keep_16_bits_however_many_rows_share_a_run(heads, seqs, 
         want, bound = attention_fine(x[at[s]:at[s + 1]], b.ks[0][s], b.vs[0][s], b.lens[s], D ** -0.5, None if parents is None else parents[s])
         err = np.abs(out[at[s]:at[s + 1]] - want)
         assert (err <= bound).all(), (s, float((err / bound).max()), int((err > bound).sum()))
+
+
+def test_an_index_of_another_cache_is_refused():
+    """Of the same sizes too: its bounds would be of other keys."""
+    rng = np.random.default_rng(40)
+    cache, _, _ = filled(rng, BF, 2, 64, 16, [100, 200], [1, 1])
+    other, _, _ = filled(rng, BF, 2, 64, 16, [100, 200], [1, 1])
+    index, start = tms.PageIndex(cache, tokens=2), dev32([0, 1, 2])
+    tms.kv_bounds(cache, index)
+    before = index.bounds.clone()
+    q = torch.zeros((2, 4, 64), dtype=BF, device="cuda")
+    chosen = torch.full((2, 2, 4), 77, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="another cache"):
+        tms.kv_select(other, 0, q, start, index, chosen, max_new=1)
+    with pytest.raises(ValueError, match="another cache"):
+        tms.kv_bounds(other, index)
+    assert (chosen == 77).all() and torch.equal(index.bounds, before)
+    # the same tensors in a cache made anew are the same keys
+    again = tms.PagedCache(cache.kv, cache.table, cache.length, cache.held, cache.refs, cache.status_codes)
+    tms.kv_select(again, 0, q, start, index, chosen, max_new=1)
+    assert (chosen >= 0).all()
+    # bounds that were kept may be given to an index for the cache that they are of
+    del other
+    tms.kv_select(cache, 0, q, start, tms.PageIndex(cache, before, tokens=2), chosen, max_new=1)
+    assert (chosen >= 0).all()

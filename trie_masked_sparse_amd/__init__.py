@@ -24,6 +24,7 @@ from __future__ import annotations
 import ctypes as C
 import itertools
 import os
+import weakref
 
 import numpy as np
 import torch
@@ -729,7 +730,8 @@ class SharedPlan:
 
 class PageIndex:
     """Bounds of the keys of a cache's whole pages, kept by kv_bounds, and the
-    work memory of kv_select for calls of up to `tokens` new tokens in all.
+    work memory of kv_select for calls of up to `tokens` new tokens in all.  It
+    goes with the cache's kv tensor: calls with another cache are refused.
     bounds [layers][pages][kv_heads][2][head_dim] of the cache's dtype (lowest,
     highest); made here if it is not given."""
 
@@ -747,13 +749,16 @@ class PageIndex:
         self.bounds, self.tokens, self.bytes = bounds, tokens, need.value
         self.memory = torch.empty(max(need.value, 256), dtype=torch.uint8, device=cache.kv.device)
         self._at, self._streams, self._cache = self.memory.data_ptr(), set(), _sizes(cache)
+        self._kv = weakref.ref(cache.kv)  # whose keys the bounds are of
 
 
 def _with_stream(cache: PagedCache, handle, stream):
     """_kv_stream, told to the tensors of a plan or an index too, which have to be
-    for caches like this one."""
+    for caches like this one, an index for these pages."""
     if handle._cache != cache._like:
         raise ValueError(f"the {type(handle).__name__} was made for a cache of other sizes")
+    if isinstance(handle, PageIndex) and handle._kv() is not cache.kv:
+        raise ValueError("the PageIndex was made for another cache: its bounds are of other keys")
     s = _kv_stream(cache, stream)
     if s not in handle._streams:
         on = torch.cuda.ExternalStream(s, device=cache.kv.device)
