@@ -1156,3 +1156,22 @@ def test_an_index_of_another_cache_is_refused():
     del other
     tms.kv_select(cache, 0, q, start, tms.PageIndex(cache, before, tokens=2), chosen, max_new=1)
     assert (chosen >= 0).all()
+
+
+def test_shared_plans_of_tokens_that_two_sequences_claim_give_nan():
+    """And leave the plan's memory good for the next plan."""
+    rng = np.random.default_rng(41)
+    b = Branches(rng, BF, 2, 64, 16, [((("p", 40),), 0, 4)] * 4)
+    q = queries(rng, b, 4, 64, BF)
+    held = b.cache.held.clone()
+    b.cache.held.fill_(44)
+    plan = tms.SharedPlan(b.cache, 16, 4)
+    for bad in ([0, 10, 4, 14, 16], [0, 16, 0, 16, 16], [0, 9, 8, 16, 16]):
+        out, start = torch.full(q.shape, 7.0, dtype=BF, device="cuda"), dev32(bad)
+        tms.kv_share(b.cache, plan, start)
+        tms.kv_attention_shared(b.cache, 0, q, start, out, plan, max_new=16)
+        assert torch.isnan(out).all(), bad
+    b.cache.held.copy_(held)
+    start = dev32(offsets(b.new))
+    tms.kv_share(b.cache, plan, start)
+    check_shared(b, q, run_shared(b, q, plan=plan), 0.125, None)
