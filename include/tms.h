@@ -555,10 +555,12 @@ tms_status tms_kv_select(const tms_kv* c, int32_t layer, const void* q, int64_t 
 /* tms_kv_attention over chosen pages: a token's query heads see the committed
  * rows of the pages in its list for their key head (dev int32 [T][kv_heads][k],
  * as tms_kv_select makes it: whole pages of committed rows in ascending order,
- * up to the first negative entry), the committed rows behind the last whole
- * page, and of the new rows the same as in tms_kv_attention.  k in [0, 8192].  In
- * bf16 the weights of the second product keep 16 bits.  The outputs of a token
- * with an entry that is out of range or not in order are NaN. */
+ * and behind the last of them negative entries only), the committed rows behind
+ * the last whole page, and of the new rows the same as in tms_kv_attention.  k in
+ * [0, 8192].  In bf16 the weights of the second product keep 16 bits.  Where a
+ * list has an entry that is not a whole page, or not above the one before it, or
+ * that comes behind a negative one, the outputs of its token and key head are
+ * NaN. */
 tms_status tms_kv_attention_pages(const tms_kv* c, int32_t layer, const void* q, int64_t ldq, int32_t q_heads,
                                   const int32_t* start, int32_t T, int32_t max_new, const int32_t* parent,
                                   const int32_t* chosen, int32_t k, float scale, void* out, void* stream);

@@ -773,7 +773,8 @@ def kv_share(cache: PagedCache, plan: SharedPlan, start, tokens: int | None = No
     """Plan of the shared attention of `tokens` (default: plan.tokens) packed new
     tokens, from the cache's tables (tms_kv_share): after kv_reserve, once for all
     layers; good until the next kv_fork, kv_reserve or kv_commit, from which on
-    kv_attention_shared refuses it.  Asynchronous."""
+    kv_attention_shared refuses it.  Of changes that a replayed graph makes it does
+    not know: plan within the graph, or again behind it.  Asynchronous."""
     T = plan.tokens if tokens is None else tokens
     rc = cache._c[5](cache.ref, _sized(start, _int32, cache.seqs + 1, "start"), T, plan.q_heads, plan._at, plan.bytes,
                      _with_stream(cache, plan, stream))

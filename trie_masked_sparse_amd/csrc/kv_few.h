@@ -1,6 +1,6 @@
 // One tile of up to 16 MT query rows of one key head over a run of keys: what a
-// workgroup of the attention over chosen pages, and of the shared attention in
-// fp32, does.
+// workgroup of the attention over chosen pages does, and of the shared attention
+// in fp32 or, in bf16, where the rows are few (up to 16; 32 with heads of 64).
 #pragma once
 #include <type_traits>
 
