@@ -12,10 +12,11 @@
 // for every layer: see Plan.
 //
 // Measured, a layer (us, MI355X; 32 query and 8 key heads of 128, bf16, pages of
-// 64): 64 tokens behind one prompt of 9000 rows and up to 400 of their own 37,
-// where kv_attention takes 264; 256 behind four prompts of 9000 to 24000 that share
-// 2048 rows and up to 1000 of their own 231 (2230).  The plan adds 12 to 36 once
-// for all layers, so four sequences of 150 rows are quicker without (14 and 10).
+// 64; four batches of other inputs in turn): 64 tokens behind one prompt of 9000
+// rows and up to 400 of their own 45, where kv_attention takes 265; 256 behind four
+// prompts of 9000 to 24000 that share 2048 rows and up to 1000 of their own 229
+// (2222).  The plan adds 12 to 34 once for all layers, so four sequences of 150 rows
+// are quicker without (14 and 10).
 #include <algorithm>
 #include <climits>
 
@@ -459,14 +460,15 @@ struct Body<1, D, kMany128> {
 
 // A unit of the plan.
 //
-// 64 tokens behind one prompt (shapes as above) 34 us a layer, 102 MB read: a tile
-// takes 1.8 us with two workgroups on a compute unit (128 rows x 64 keys: products,
-// maximum, exponentials, products, one behind the other in each wavefront; the matrix
-// cores are 13 to 22 % busy), and a unit 5 to 7 for its start and end.  256 tokens of
-// four prompts 192 us, 856 MB, 4.5 TB/s.  Tried and slower: equal shares of the cost,
-// a workgroup each, in a loop over their segments (34 -> 52, 64 trees 49 -> 60, 256
-// tokens 196 -> 235 us: registers go to scratch, and every segment starts anew), tiles
-// of 32 keys copied three ahead (32.1 -> 32.4, 46.9 -> 49.0, 198 -> 207).
+// 64 tokens behind one prompt (shapes as above) 34 us a layer, 103 MB read, 64 trees
+// of drafts 51: a tile of 128 rows x 64 keys is products, maximum, exponentials,
+// products, one behind the other in each wavefront, with two workgroups on a compute
+// unit (the matrix cores are 16 to 27 % busy), and a unit takes 5 to 7 us for its
+// start and end.  256 tokens of four prompts 203 us, 841 MB, 4.1 TB/s.  Tried and
+// slower, with weights of one part: equal shares of the cost, a workgroup each, in a
+// loop over their segments (34 -> 52, trees 49 -> 60, 256 tokens 196 -> 235 us:
+// registers go to scratch, and every segment starts anew), tiles of 32 keys copied
+// three ahead (32.1 -> 32.4, 46.9 -> 49.0, 198 -> 207).
 template <int DT, int D, int Shape, int Heads>
 __global__ __launch_bounds__(kBlock, D == 256 || (D == 128 && Shape == kFew32) ? 1 : 2) void nodes_kernel(KvCache c, KvAttention a, Plan plan) {
   using Small = FewRows<DT, D, 1, Heads>;
